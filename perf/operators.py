@@ -288,10 +288,10 @@ def run_own(s):
         if s["kind"] == "weights":
             q, sc = fme.quantize_fp8_block128_weights(s["x"])
             return as_values(q), sc
-        q, sc = fme.quantize_fp8_block128(s["x"])
         if s["kind"] == "rows":
+            q, sc = fme.quantize_fp8_block128(s["x"])
             return as_values(q), sc
-        qc, scc, padded = fme.quantize_fp8_block128(s["x"], fme.COLWISE, s["offsets"])
+        (q, sc), (qc, scc, padded) = fme.quantize_fp8_block128_rowcol(s["x"], s["offsets"])
         return as_values(q), sc, as_values(qc), scc, padded
     if op == "gate":
         ids, w = fme.moe_gate(s["logits"], s["top_k"], score=s["score"], bias=s["bias_t"], normalize=s["norm"],
