@@ -19,13 +19,13 @@ def listed():
     return [
         # One token of a decode step: its 8 experts of 32, the gate/up product (n = 2 x 2048) from bf16 hidden states.
         # What counts is how fast the chosen experts' weights are read.
-        {"name": "product, one token", "op": "fwd", "tokens": 1, "top_k": 8, "experts": 32, "n": 4096, "k": 7168},
+        {"name": "product one token", "op": "fwd", "tokens": 1, "top_k": 8, "experts": 32, "n": 4096, "k": 7168},
         # A prefill or training batch: 8192 tokens x 8, experts of very different loads, some without tokens.
-        {"name": "product, 65536 rows", "op": "fwd", "tokens": 8192, "top_k": 8, "experts": 32, "n": 4096, "k": 7168},
+        {"name": "product 65536 rows", "op": "fwd", "tokens": 8192, "top_k": 8, "experts": 32, "n": 4096, "k": 7168},
         # The two gradients of a projection, small experts of odd sizes that fill no tile (fp32 weight gradient).
-        {"name": "gradients, 1999 rows", "op": "bwd", "rows": 1999, "experts": 8, "n": 1040, "k": 1392, "dw": "fp32"},
+        {"name": "gradients 1999 rows", "op": "bwd", "rows": 1999, "experts": 8, "n": 1040, "k": 1392, "dw": "fp32"},
         # The down projection's gradients of a long batch, bf16 weight gradient.
-        {"name": "gradients, 65536 rows", "op": "bwd", "rows": 65536, "experts": 32, "n": 7168, "k": 2048,
+        {"name": "gradients 65536 rows", "op": "bwd", "rows": 65536, "experts": 32, "n": 7168, "k": 2048,
          "dw": "bf16"},
         # A few experts' weights requantized after an optimizer step.
         {"name": "quantize weights", "op": "quant", "kind": "weights", "rows": 4, "experts": 4, "n": 2048, "k": 7168},
@@ -33,21 +33,21 @@ def listed():
         {"name": "quantize both ways", "op": "quant", "kind": "both", "rows": 65536, "experts": 32, "n": 1,
          "k": 7168},
         # The router of a small decode batch: latency.
-        {"name": "gate, 16 tokens", "op": "gate", "tokens": 16, "experts": 32, "top_k": 8, "score": "sigmoid",
+        {"name": "gate 16 tokens", "op": "gate", "tokens": 16, "experts": 32, "top_k": 8, "score": "sigmoid",
          "norm": True, "bias": True, "dtype": "bf16", "grad": False},
         # The router of a training step with its gradient.
-        {"name": "gate, 32768 tokens", "op": "gate", "tokens": 32768, "experts": 256, "top_k": 8, "score": "softmax",
+        {"name": "gate 32768 tokens", "op": "gate", "tokens": 32768, "experts": 256, "top_k": 8, "score": "softmax",
          "norm": True, "bias": False, "dtype": "fp32", "grad": True},
         # The balance loss of a short batch, one sequence.
-        {"name": "balance, 1023 tokens", "op": "balance", "tokens": 1023, "experts": 32, "top_k": 4, "seqs": 1,
+        {"name": "balance 1023 tokens", "op": "balance", "tokens": 1023, "experts": 32, "top_k": 4, "seqs": 1,
          "score": "softmax", "mask": False, "dtype": "fp32"},
         # The balance loss of packed sequences of odd lengths with padding tokens.
-        {"name": "balance, 32768 tokens", "op": "balance", "tokens": 32768, "experts": 256, "top_k": 8, "seqs": 13,
+        {"name": "balance 32768 tokens", "op": "balance", "tokens": 32768, "experts": 256, "top_k": 8, "seqs": 13,
          "score": "sigmoid", "mask": True, "dtype": "bf16"},
         # The combine's gradient, a short batch of a narrow model with two experts a token.
-        {"name": "combine grad, 300 tokens", "op": "combine", "tokens": 300, "top_k": 2, "experts": 8, "n": 1000},
+        {"name": "combine grad 300 tokens", "op": "combine", "tokens": 300, "top_k": 2, "experts": 8, "n": 1000},
         # The combine's gradient of a training batch.
-        {"name": "combine grad, 16384 tokens", "op": "combine", "tokens": 16384, "top_k": 8, "experts": 32, "n": 7168},
+        {"name": "combine grad 16384 tokens", "op": "combine", "tokens": 16384, "top_k": 8, "experts": 32, "n": 7168},
     ]
 
 
