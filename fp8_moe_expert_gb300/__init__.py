@@ -19,6 +19,9 @@ ROWWISE = 0
 COLWISE = 1
 MAX_GROUPS = 1024
 MX_SCALE_CEIL = 0x100
+DW_BF16 = 0
+DW_FP32 = 1
+DW_FP32_ADD = 2
 DEV_TIMEOUT = 0x1
 DEV_BAD_OFFSETS = 0x2
 DEV_BAD_INDEX = 0x4
@@ -94,6 +97,14 @@ SYMBOLS = {
     "moe_combine": ("i32", ["p", "i64", "p", "p", "i64", "i32", "i64", "p", "p", "p"]),
     "grouped_gemm_wgrad_mxfp8_accumulate": ("i32", ["p", "p", "i64", "p", "p", "i64", "p", "i32", "i64", "i64", "p",
                                                     "p", "p"]),
+    "quantize_fp8_block128": ("i32", ["p", "i64", "i64", "i32", "p", "i32", "p", "p", "p", "p", "p"]),
+    "quantize_fp8_block128_rowcol": ("i32", ["p", "i64", "i64", "p", "i32", "p", "p", "p", "p", "p", "p", "p"]),
+    "permute_quantize_fp8_block128": ("i32", ["p", "i64", "i64", "p", "i32", "p", "p", "p", "p"]),
+    "quantize_fp8_block128_weights": ("i32", ["p", "i32", "i64", "i64", "p", "p", "p"]),
+    "grouped_gemm_fwd_fp8_block128": ("i32", ["p", "p", "p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
+    "grouped_gemm_dgrad_fp8_block128": ("i32", ["p", "p", "p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
+    "grouped_gemm_wgrad_fp8_block128": ("i32", ["p", "p", "p", "p", "i64", "p", "i32", "i64", "i64", "p", "i32", "p",
+                                                "p"]),
     "fme_route_workspace_bytes": ("i64", ["i64", "i32", "i32"]),
     "fme_sf_padded_rows": ("i64", ["i64", "i32"]),
     "fme_sf_bytes": ("i64", ["i64", "i64", "i32", "i32"]),
@@ -161,6 +172,21 @@ def _empty(shape, dtype, device):
     import torch
 
     return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _need(where, name, t, dtype, shape):
+    """Raise unless t is a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor of {dtype} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ' (not contiguous)'}")
+
+
+def _out(where, name, t, dtype, shape, device):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return _empty(shape, dtype, device)
+    _need(where, name, t, dtype, shape)
+    return t
 
 
 # --------------------------------------------------------------- the five calls --
@@ -508,6 +534,153 @@ def grouped_gemm_wgrad_mxfp8_accumulate(a_codes, a_sf, lda, b_codes, b_sf, ldb, 
                                                    _stream(stream))
     _check(st, "grouped_gemm_wgrad_mxfp8_accumulate")
     return dw_acc
+
+
+# ------------------------------------------------------------ FP8 block-128 --
+def quantize_fp8_block128(x, axis=ROWWISE, offsets=None, num_groups=None, *, src_row=None, top_k=1, codes=None,
+                          scale=None, padded_offsets=None, status=None, stream=None):
+    """FP8 (E4M3) of bf16 x [rows, cols] with one fp32 scale per 128 values.
+
+    ROWWISE -> (codes [rows, cols] u8, scale [ceil(cols/128), rows] f32); with src_row
+    (int32 [tokens*top_k], from moe_route) the rows are x[src_row // top_k].
+    COLWISE -> (codes [ld, cols] u8, scale [ld/128, cols] f32, padded_offsets [G+1] i32),
+    blocks along each group's rows, each group padded with zeros to a multiple of 128."""
+    import torch
+
+    where = "quantize_fp8_block128"
+    rows, cols = x.shape
+    dev = x.device
+    _need(where, "x", x, torch.bfloat16, x.shape)
+    if axis == ROWWISE:
+        if src_row is not None:
+            _need(where, "src_row", src_row, torch.int32, (rows * top_k,))
+        out = rows * top_k if src_row is not None else rows
+        codes = _out(where, "codes", codes, torch.uint8, (out, cols), dev)
+        scale = _out(where, "scale", scale, torch.float32, ((cols + 127) // 128, out), dev)
+        if src_row is not None:
+            st = lib().permute_quantize_fp8_block128(_ptr(x), rows, cols, _ptr(src_row), top_k, _ptr(codes),
+                                                     _ptr(scale), _ptr(status), _stream(stream))
+        else:
+            st = lib().quantize_fp8_block128(_ptr(x), rows, cols, axis, None, 1, _ptr(codes), _ptr(scale), None,
+                                             _ptr(status), _stream(stream))
+        _check(st, where)
+        return codes, scale
+    if src_row is not None:
+        raise ValueError(f"{where}: src_row is for ROWWISE only")
+    offsets, g = _groups(offsets, num_groups)
+    if offsets is not None:
+        _need(where, "offsets", offsets, torch.int32, (g + 1,))
+    ld = colwise_ld(rows, g)
+    codes = _out(where, "codes", codes, torch.uint8, (ld, cols), dev)
+    scale = _out(where, "scale", scale, torch.float32, (ld // 128, cols), dev)
+    padded_offsets = _out(where, "padded_offsets", padded_offsets, torch.int32, (g + 1,), dev)
+    st = lib().quantize_fp8_block128(_ptr(x), rows, cols, axis, _ptr(offsets), g, _ptr(codes), _ptr(scale),
+                                     _ptr(padded_offsets), _ptr(status), _stream(stream))
+    _check(st, where)
+    return codes, scale, padded_offsets
+
+
+def quantize_fp8_block128_rowcol(x, offsets=None, num_groups=None, *, row_codes=None, row_scale=None, col_codes=None,
+                                 col_scale=None, padded_offsets=None, status=None, stream=None):
+    """Both layouts of quantize_fp8_block128 from one read of x ->
+    ((row_codes, row_scale), (col_codes, col_scale, padded_offsets))."""
+    import torch
+
+    where = "quantize_fp8_block128_rowcol"
+    rows, cols = x.shape
+    dev = x.device
+    _need(where, "x", x, torch.bfloat16, x.shape)
+    offsets, g = _groups(offsets, num_groups)
+    if offsets is not None:
+        _need(where, "offsets", offsets, torch.int32, (g + 1,))
+    ld = colwise_ld(rows, g)
+    row_codes = _out(where, "row_codes", row_codes, torch.uint8, (rows, cols), dev)
+    row_scale = _out(where, "row_scale", row_scale, torch.float32, ((cols + 127) // 128, rows), dev)
+    col_codes = _out(where, "col_codes", col_codes, torch.uint8, (ld, cols), dev)
+    col_scale = _out(where, "col_scale", col_scale, torch.float32, (ld // 128, cols), dev)
+    padded_offsets = _out(where, "padded_offsets", padded_offsets, torch.int32, (g + 1,), dev)
+    st = lib().quantize_fp8_block128_rowcol(_ptr(x), rows, cols, _ptr(offsets), g, _ptr(row_codes), _ptr(row_scale),
+                                            _ptr(col_codes), _ptr(col_scale), _ptr(padded_offsets), _ptr(status),
+                                            _stream(stream))
+    _check(st, where)
+    return (row_codes, row_scale), (col_codes, col_scale, padded_offsets)
+
+
+def quantize_fp8_block128_weights(w, *, codes=None, scale=None, stream=None):
+    """FP8 of expert weights w [E, n, k] (bf16) with one fp32 scale per 128 x 128 block ->
+    (codes [E, n, k] u8, scale [E, ceil(n/128), ceil(k/128)] f32)."""
+    import torch
+
+    where = "quantize_fp8_block128_weights"
+    e, n, k = w.shape
+    _need(where, "w", w, torch.bfloat16, w.shape)
+    codes = _out(where, "codes", codes, torch.uint8, (e, n, k), w.device)
+    scale = _out(where, "scale", scale, torch.float32, (e, (n + 127) // 128, (k + 127) // 128), w.device)
+    st = lib().quantize_fp8_block128_weights(_ptr(w), e, n, k, _ptr(codes), _ptr(scale), _stream(stream))
+    _check(st, where)
+    return codes, scale
+
+
+def _block128_rows_gemm(where, a_codes, a_scale, w_codes, w_scale, offsets, inner, out_cols, y, status, stream):
+    import torch
+
+    e, n, k = w_codes.shape
+    m = a_codes.shape[0]
+    _need(where, "a_codes", a_codes, torch.uint8, (m, inner))
+    _need(where, "a_scale", a_scale, torch.float32, ((inner + 127) // 128, m))
+    _need(where, "w_codes", w_codes, torch.uint8, (e, n, k))
+    _need(where, "w_scale", w_scale, torch.float32, (e, (n + 127) // 128, (k + 127) // 128))
+    _need(where, "offsets", offsets, torch.int32, (e + 1,))
+    y = _out(where, "y", y, torch.bfloat16, (m, out_cols), a_codes.device)
+    st = getattr(lib(), where)(_ptr(a_codes), _ptr(a_scale), _ptr(w_codes), _ptr(w_scale), _ptr(offsets), e, m, n, k,
+                               _ptr(y), _ptr(status), _stream(stream))
+    _check(st, where)
+    return y
+
+
+def grouped_gemm_fwd_fp8_block128(a_codes, a_scale, w_codes, w_scale, offsets, *, y=None, status=None, stream=None):
+    """Y [m, n] (bf16) = X_e W_e^T per expert, from quantize_fp8_block128(ROWWISE) of
+    X [m, k] and quantize_fp8_block128_weights of W [E, n, k]."""
+    _, n, k = w_codes.shape
+    return _block128_rows_gemm("grouped_gemm_fwd_fp8_block128", a_codes, a_scale, w_codes, w_scale, offsets, k, n, y,
+                               status, stream)
+
+
+def grouped_gemm_dgrad_fp8_block128(dy_codes, dy_scale, w_codes, w_scale, offsets, *, dx=None, status=None,
+                                    stream=None):
+    """dX [m, k] (bf16) = dY_e W_e per expert, from quantize_fp8_block128(ROWWISE) of
+    dY [m, n] and the forward's weight codes."""
+    _, n, k = w_codes.shape
+    return _block128_rows_gemm("grouped_gemm_dgrad_fp8_block128", dy_codes, dy_scale, w_codes, w_scale, offsets, n, k,
+                               dx, status, stream)
+
+
+def grouped_gemm_wgrad_fp8_block128(dy_codes, dy_scale, x_codes, x_scale, padded_offsets, *, dw=None, dtype=None,
+                                    accumulate=False, status=None, stream=None):
+    """dW [E, n, k] = dY_e^T X_e per expert, from quantize_fp8_block128(COLWISE) of dY [rows, n]
+    and X [rows, k] with the same offsets.  dtype bfloat16 (default) or float32; with accumulate
+    the result is added into dw (float32)."""
+    import torch
+
+    where = "grouped_gemm_wgrad_fp8_block128"
+    ld, n = dy_codes.shape
+    k = x_codes.shape[1]
+    e = padded_offsets.shape[0] - 1
+    dtype = dtype or (dw.dtype if dw is not None else torch.bfloat16)
+    if dtype not in (torch.bfloat16, torch.float32) or (accumulate and (dw is None or dtype != torch.float32)):
+        raise ValueError(f"{where}: dw is bfloat16 or float32, and a given float32 tensor to accumulate into")
+    _need(where, "dy_codes", dy_codes, torch.uint8, (ld, n))
+    _need(where, "dy_scale", dy_scale, torch.float32, (ld // 128, n))
+    _need(where, "x_codes", x_codes, torch.uint8, (ld, k))
+    _need(where, "x_scale", x_scale, torch.float32, (ld // 128, k))
+    _need(where, "padded_offsets", padded_offsets, torch.int32, (e + 1,))
+    dw = _out(where, "dw", dw, dtype, (e, n, k), dy_codes.device)
+    mode = DW_BF16 if dtype == torch.bfloat16 else DW_FP32_ADD if accumulate else DW_FP32
+    st = lib().grouped_gemm_wgrad_fp8_block128(_ptr(dy_codes), _ptr(dy_scale), _ptr(x_codes), _ptr(x_scale), ld,
+                                               _ptr(padded_offsets), e, n, k, _ptr(dw), mode, _ptr(status),
+                                               _stream(stream))
+    _check(st, where)
+    return dw
 
 
 def read_device_status(status, stream=None) -> tuple[int, int]:

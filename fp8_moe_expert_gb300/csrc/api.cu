@@ -673,4 +673,236 @@ fme_status grouped_gemm_wgrad_mxfp8_accumulate(const uint8_t *a_codes, const uin
                     dev_status, stream, "grouped_gemm_wgrad_mxfp8_accumulate launch");
 }
 
+// ------------------------------------------------------------ FP8 block-128 --
+namespace {
+
+// Columns of an FP8 block-128 tensor: its code rows are a multiple of 16 bytes.
+bool block128_cols(int64_t c) { return c >= 16 && c <= 65536 && c % 16 == 0; }
+
+// 3-D uint8 weights [experts][n][k], box {128, 128, 1}, 128-byte swizzle, zero fill past each
+// expert's n and k.
+fme_status encode_u8_weights(CUtensorMap *map, const void *base, uint64_t experts, uint64_t n, uint64_t k) {
+  EncodeTiledFn fn;
+  fme_status st = get_encoder(&fn);
+  if (st != FME_OK) return st;
+  cuuint64_t dims[3] = {k, n, experts};
+  cuuint64_t strides[2] = {k, n * k};
+  cuuint32_t box[3] = {128, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[96];
+    std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled (weights) failed (CUresult %d)", static_cast<int>(r));
+    g_last_cuda_error = buf;
+    return FME_ERR_CUDA;
+  }
+  return FME_OK;
+}
+
+// 128 x 128 tiles of a [rows x cols] tensor fit one launch.
+bool tiles_fit(int64_t row_chunks, int64_t cols) {
+  return row_chunks * ((cols + 127) / 128) <= (int64_t(1) << 31) - 1;
+}
+
+fme_status fp8_rows(const void *x, int64_t x_rows, int64_t rows, int64_t cols, const int32_t *src_row, int32_t top_k,
+                    uint8_t *codes, float *scale, int32_t *dev_status, void *stream, const char *what) {
+  if (!block128_cols(cols) || rows > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return FME_OK;
+  if (!x || !codes || !scale) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scale) || !aligned16(src_row)) return FME_ERR_MISALIGNED;
+  fme::LaunchFp8Quant a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.codes = codes;
+  a.scale = scale;
+  a.gather = src_row;
+  a.gather_div = top_k;
+  a.gather_limit = x_rows;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_fp8_block128_rows(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, what);
+}
+
+fme_status fp8_cols(const void *x, int64_t rows, int64_t cols, const int32_t *offsets, int32_t num_groups,
+                    uint8_t *row_codes, float *row_scale, uint8_t *codes, float *scale, int32_t *padded_offsets,
+                    int32_t *dev_status, void *stream, const char *what) {
+  const int64_t ld = fme_colwise_ld(rows, num_groups);
+  if (!block128_cols(cols) || ld > (int64_t(1) << 31) - 1 || !tiles_fit(ld / 128, cols))
+    return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!padded_offsets || (ld > 0 && (!codes || !scale)) || (rows > 0 && !x)) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scale) || !aligned16(row_codes) || !aligned16(row_scale) ||
+      !aligned16(padded_offsets))
+    return FME_ERR_MISALIGNED;
+  fme::LaunchFp8Quant a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.offsets = offsets;
+  a.num_groups = num_groups;
+  a.codes = codes;
+  a.scale = scale;
+  a.padded_offsets = padded_offsets;
+  a.ld = ld;
+  a.row_codes = row_codes;
+  a.row_scale = row_scale;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_fp8_block128_cols(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, what);
+}
+
+// The forward (out = n columns, contraction k) and dgrad (out = k columns, contraction n).
+fme_status block128_rows_gemm(bool dgrad, const uint8_t *a_codes, const float *a_scale, const uint8_t *w_codes,
+                              const float *w_scale, const int32_t *offsets, int32_t num_experts, int64_t m, int64_t n,
+                              int64_t k, void *y, int32_t *dev_status, void *stream, const char *what) {
+  if (m < 0 || n < 0 || k < 0 || check_groups(num_experts) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (!block128_cols(n) || !block128_cols(k)) return FME_ERR_UNSUPPORTED_SHAPE;
+  // row coordinates of the last, partly empty tiles stay in 32 bits
+  if (m > (int64_t(1) << 31) - 1 - 256) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets) return FME_ERR_INVALID_ARGUMENT;
+  if (m == 0) return FME_OK;
+  if (!a_codes || !a_scale || !w_codes || !w_scale || !y) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(a_codes) || !aligned16(a_scale) || !aligned16(w_codes) || !aligned16(w_scale) || !aligned16(y) ||
+      !aligned16(offsets))
+    return FME_ERR_MISALIGNED;
+  fme::LaunchBlock128 a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  a.k = dgrad ? n : k;
+  a.n = dgrad ? k : n;
+  if ((st = encode_u8_2d(&a.map_a, a_codes, a.k, m, a.k, 128)) != FME_OK) return st;
+  if ((st = encode_u8_weights(&a.map_b, w_codes, num_experts, n, k)) != FME_OK) return st;
+  if ((st = encode_bf16_out(&a.map_y, y, a.n, m)) != FME_OK) return st;
+  a.a_scale = a_scale;
+  a.b_scale = w_scale;
+  a.offsets = offsets;
+  a.num_experts = num_experts;
+  a.m = m;
+  a.y = y;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = dgrad ? fme::launch_block128_dgrad(a) : fme::launch_block128_fwd(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, what);
+}
+
+}  // namespace
+
+fme_status quantize_fp8_block128(const void *x, int64_t rows, int64_t cols, int32_t axis, const int32_t *offsets,
+                                 int32_t num_groups, uint8_t *codes, float *scale, int32_t *padded_offsets,
+                                 int32_t *dev_status, void *stream) {
+  if (rows < 0 || cols < 0 || check_groups(num_groups) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (offsets == nullptr && num_groups != 1) return FME_ERR_INVALID_ARGUMENT;
+  if (axis == FME_ROWWISE) {
+    if (padded_offsets != nullptr) return FME_ERR_INVALID_ARGUMENT;
+    return fp8_rows(x, rows, rows, cols, nullptr, 1, codes, scale, dev_status, stream, "quantize_fp8_block128 launch");
+  }
+  if (axis != FME_COLWISE) return FME_ERR_INVALID_ARGUMENT;
+  return fp8_cols(x, rows, cols, offsets, num_groups, nullptr, nullptr, codes, scale, padded_offsets, dev_status,
+                  stream, "quantize_fp8_block128 launch");
+}
+
+fme_status quantize_fp8_block128_rowcol(const void *x, int64_t rows, int64_t cols, const int32_t *offsets,
+                                        int32_t num_groups, uint8_t *row_codes, float *row_scale, uint8_t *col_codes,
+                                        float *col_scale, int32_t *padded_offsets, int32_t *dev_status,
+                                        void *stream) {
+  if (rows < 0 || cols < 0 || check_groups(num_groups) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (offsets == nullptr && num_groups != 1) return FME_ERR_INVALID_ARGUMENT;
+  if (rows > 0 && (!row_codes || !row_scale)) return FME_ERR_INVALID_ARGUMENT;
+  return fp8_cols(x, rows, cols, offsets, num_groups, rows > 0 ? row_codes : nullptr, row_scale, col_codes, col_scale,
+                  padded_offsets, dev_status, stream, "quantize_fp8_block128_rowcol launch");
+}
+
+fme_status permute_quantize_fp8_block128(const void *x, int64_t tokens, int64_t cols, const int32_t *src_row,
+                                         int32_t top_k, uint8_t *codes, float *scale, int32_t *dev_status,
+                                         void *stream) {
+  if (tokens < 0 || cols < 0 || top_k < 1 || top_k > 64) return FME_ERR_INVALID_ARGUMENT;
+  if (tokens > 0 && !src_row) return FME_ERR_INVALID_ARGUMENT;
+  return fp8_rows(x, tokens, tokens * top_k, cols, src_row, top_k, codes, scale, dev_status, stream,
+                  "permute_quantize_fp8_block128 launch");
+}
+
+fme_status quantize_fp8_block128_weights(const void *w, int32_t num_experts, int64_t n, int64_t k, uint8_t *codes,
+                                         float *scale, void *stream) {
+  if (n < 0 || k < 0 || check_groups(num_experts) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (!block128_cols(n) || !block128_cols(k) || !tiles_fit(num_experts * ((n + 127) / 128), k))
+    return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!w || !codes || !scale) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(w) || !aligned16(codes) || !aligned16(scale)) return FME_ERR_MISALIGNED;
+  fme::LaunchFp8Quant a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  a.x = w;
+  a.rows = n;
+  a.cols = k;
+  a.num_groups = num_experts;
+  a.codes = codes;
+  a.scale = scale;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_fp8_block128_weights(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "quantize_fp8_block128_weights launch");
+}
+
+fme_status grouped_gemm_fwd_fp8_block128(const uint8_t *a_codes, const float *a_scale, const uint8_t *w_codes,
+                                         const float *w_scale, const int32_t *offsets, int32_t num_experts, int64_t m,
+                                         int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream) {
+  return block128_rows_gemm(false, a_codes, a_scale, w_codes, w_scale, offsets, num_experts, m, n, k, y, dev_status,
+                            stream, "grouped_gemm_fwd_fp8_block128 launch");
+}
+
+fme_status grouped_gemm_dgrad_fp8_block128(const uint8_t *dy_codes, const float *dy_scale, const uint8_t *w_codes,
+                                           const float *w_scale, const int32_t *offsets, int32_t num_experts,
+                                           int64_t m, int64_t n, int64_t k, void *dx, int32_t *dev_status,
+                                           void *stream) {
+  return block128_rows_gemm(true, dy_codes, dy_scale, w_codes, w_scale, offsets, num_experts, m, n, k, dx, dev_status,
+                            stream, "grouped_gemm_dgrad_fp8_block128 launch");
+}
+
+fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float *dy_scale, const uint8_t *x_codes,
+                                           const float *x_scale, int64_t positions, const int32_t *padded_offsets,
+                                           int32_t num_experts, int64_t n, int64_t k, void *dw, int32_t dw_mode,
+                                           int32_t *dev_status, void *stream) {
+  if (n < 0 || k < 0 || positions < 0 || check_groups(num_experts) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (dw_mode != FME_DW_BF16 && dw_mode != FME_DW_FP32 && dw_mode != FME_DW_FP32_ADD) return FME_ERR_INVALID_ARGUMENT;
+  if (!block128_cols(n) || !block128_cols(k) || positions % 128 != 0 || positions > (int64_t(1) << 31) - 1)
+    return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!padded_offsets || !dw) return FME_ERR_INVALID_ARGUMENT;
+  if (positions > 0 && (!dy_codes || !dy_scale || !x_codes || !x_scale)) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(dy_codes) || !aligned16(dy_scale) || !aligned16(x_codes) || !aligned16(x_scale) || !aligned16(dw) ||
+      !aligned16(padded_offsets))
+    return FME_ERR_MISALIGNED;
+  fme::LaunchBlock128 a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  // without positions every expert is empty and the operands' maps are never used
+  const void *abase = positions ? static_cast<const void *>(dy_codes) : dw;
+  const void *bbase = positions ? static_cast<const void *>(x_codes) : dw;
+  const int64_t extent = positions ? positions : 1;
+  if ((st = encode_u8_2d(&a.map_a, abase, n, extent, n, 128)) != FME_OK) return st;
+  if ((st = encode_u8_2d(&a.map_b, bbase, k, extent, k, 128)) != FME_OK) return st;
+  if (dw_mode == FME_DW_BF16 && (st = encode_bf16_out(&a.map_y, dw, k, static_cast<uint64_t>(num_experts) * n)) != FME_OK)
+    return st;
+  a.a_scale = dy_scale;
+  a.b_scale = x_scale;
+  a.offsets = padded_offsets;
+  a.num_experts = num_experts;
+  a.m = n;
+  a.n = k;
+  a.positions = positions;
+  a.y = dw;
+  a.out_fp32 = dw_mode != FME_DW_BF16;
+  a.accumulate = dw_mode == FME_DW_FP32_ADD;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_block128_wgrad(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "grouped_gemm_wgrad_fp8_block128 launch");
+}
+
 }  // extern "C"

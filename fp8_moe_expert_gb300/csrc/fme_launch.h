@@ -97,6 +97,48 @@ struct LaunchGemm {
   bool accumulate = false;  // wgrad only: y is fp32 and receives y += result
 };
 
+// FP8 block-128 quantizers (quant_block128.cu).
+struct LaunchFp8Quant {
+  const void *x;
+  int64_t rows, cols;       // weights: rows of one expert
+  const int32_t *offsets;   // column-wise
+  int32_t num_groups;       // column-wise: groups; weights: experts
+  uint8_t *codes;
+  float *scale;
+  int32_t *padded_offsets;  // column-wise
+  int64_t ld;               // column-wise: padded positions
+  uint8_t *row_codes;       // column-wise: also row-wise (or NULL)
+  float *row_scale;
+  const int32_t *gather;    // row-wise: row r reads row gather[r] / gather_div of gather_limit (or NULL)
+  int32_t gather_div;
+  int64_t gather_limit;
+  int32_t *status;
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_fp8_block128_rows(const LaunchFp8Quant &a);
+cudaError_t launch_fp8_block128_cols(const LaunchFp8Quant &a);
+cudaError_t launch_fp8_block128_weights(const LaunchFp8Quant &a);
+
+// FP8 block-128 grouped GEMMs (gemm_block128.cu).
+struct LaunchBlock128 {
+  CUtensorMap map_a, map_b;  // codes, 128 x 128-byte boxes, 128-byte swizzle (map_b 3-D [experts][n][k] but for wgrad)
+  CUtensorMap map_y;         // bf16 output, 32 x 32 boxes, 64-byte swizzle
+  const float *a_scale, *b_scale;
+  const int32_t *offsets;  // rows (forward, dgrad) or padded positions (wgrad) of each expert
+  int32_t num_experts;
+  int64_t m, n, k;    // output rows (wgrad: of one expert) and columns; contraction (not wgrad)
+  int64_t positions;  // wgrad: padded positions of the operands
+  void *y;
+  bool out_fp32, accumulate;  // wgrad
+  int32_t *status;
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_block128_fwd(const LaunchBlock128 &a);
+cudaError_t launch_block128_dgrad(const LaunchBlock128 &a);
+cudaError_t launch_block128_wgrad(const LaunchBlock128 &a);
+
 cudaError_t launch_quantize_nvfp4(const LaunchNvfp4 &a);
 // Standard NVFP4 (one FP32 scale for the whole tensor): zero *tensor_amax, reduce
 // max |x| into it, then quantize every row with it in place of the row's amax.

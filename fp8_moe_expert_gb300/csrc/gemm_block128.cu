@@ -1,0 +1,564 @@
+// gemm_block128.cu -- grouped GEMMs on FP8 operands with an fp32 scale per block of
+// 128 along the contraction (forward, dgrad, wgrad), on tcgen05, CTA pairs.
+//
+//   forward  Y[t,n]    = sum_b sx[b,t]  sw[e,n/128,b]  sum_{k in b} qx[t,k]  qw[e,n,k]
+//   dgrad    dX[t,k]   = sum_b sdy[b,t] sw[e,b,k/128]  sum_{n in b} qdy[t,n] qw[e,n,k]
+//   wgrad    dW[e,n,k] = sum_b sdy[b,n] sx[b,k]        sum_{t in b} qdy[t,n] qx[t,k]
+//
+// The tensor core sums the 128 products of a block in tensor memory (four K = 32
+// kind::f8f6f4 MMAs from zero); the scales are no powers of two, so each block's
+// partial sum is multiplied by its scale and added to fp32 sums in registers.  That
+// is 128 x 256 fused multiply-adds a block and CTA, 256 cycles of the FMA pipe against
+// about 600 of the tensor pipe (measured for a pair's M = 256, N = 256, K = 32 FP8 MMA:
+// 151 cycles), so with two accumulators in tensor memory (2 x 256 of its 512 columns;
+// there are no block scales to keep there) the two overlap.  wgrad's scale differs for
+// every output element: one multiply more each.
+//
+// One set of weight codes serves both directions: blocks are 128 x 128, and dgrad reads
+// the same [n x k] codes as an MN-major operand (its contraction runs down the rows).
+// wgrad reads both token-major operands MN-major, so no quantizer transposes anything.
+//
+// Tiles are 256 x 256 a pair, walked round-robin (see gemm_common.cuh); every ragged edge
+// is cut by the tensor maps (zero fill) and the stores, so n and k only have to be
+// multiples of 16.  No split over the contraction: a row's result does not depend on the
+// other rows.  12 warps a CTA:
+//   warp 0      TMA producer: A and B into a ring of 32 KB stages, completing on the leader's
+//               barriers; one commit per two stages frees both;
+//   warp 1      allocates tensor memory; in the leader one thread issues the MMAs, a commit per
+//               block hands the accumulator to both CTAs' epilogues;
+//   warps 4-11  epilogue: 32 rows x 128 columns each, sums in 128 registers a thread.
+#include <algorithm>
+
+#include "block128.cuh"
+#include "gemm_common.cuh"
+
+namespace fme {
+
+namespace {
+
+constexpr int kThreads128 = 384;
+constexpr int kEpiWarp0 = 4;
+constexpr int kGroupBars128 = 4;
+constexpr int kStageBytes128 = kABytes + kBBytes;
+constexpr int kStages128 = 6;
+constexpr int kColScaleBytes = 2 * 128 * 4;  // wgrad: two blocks' column scales of a warp
+constexpr int kStageOut = 8 * (kOutBoxBytes + kColScaleBytes);
+
+enum class Kind128 { kFwd, kDgrad, kWgrad };
+
+struct Shared128 {
+  uint64_t full[kStages128];
+  uint64_t grp_done[kGroupBars128];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint64_t peer_fills_bar;
+  uint32_t peer_fills;
+  uint32_t tmem_base;
+  int abort_flag;
+  int ok_flag;
+};
+
+// D = A B^T (+ D), E4M3 x E4M3 -> fp32, M = 256 over the pair.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor: fp32 accumulator (bit 4), E4M3 operands (0), the operands'
+// major-ness (bits 15, 16: 1 = MN-major), N / 8 and M / 16.
+constexpr uint32_t idesc_f8(bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled tile.  K-major: rows of 128 bytes of K,
+// 8-row atoms 1024 bytes apart.  MN-major: rows of 128 M or N values, one row for each k,
+// 8-k atoms 1024 bytes apart (a CTA's 128 values are one atom wide, so the other stride
+// is not used and holds the same value).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, bool mn) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
+  d |= static_cast<uint64_t>((mn ? 1024 : 16) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster_addr,
+                                                 int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// tcgen05.wait::ld that the 32 loaded registers depend on, so that no use of them can be
+// moved before it.
+__device__ __forceinline__ void tmem_wait_ld_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Expert tables in shared memory: first row and first 256-row block of each expert (forward,
+// dgrad), or padded offsets and experts by decreasing work (wgrad).
+struct Tables {
+  int32_t *off;
+  int32_t *aux;
+};
+
+struct Tile128 {
+  int32_t e;
+  int32_t nk;          // contraction blocks
+  int32_t row0;        // this CTA's first output row: of all rows (fwd, dgrad) or of the expert's (wgrad)
+  int32_t rows_valid;  // of its 128
+  int32_t col0;        // first output column of the tile
+  int32_t p0;          // wgrad: first padded position
+};
+
+template <Kind128 K>
+__device__ __forceinline__ Tile128 tile128(const LaunchBlock128 &p, const Tables &s, int64_t t, int rank) {
+  Tile128 tl;
+  const int64_t nb = (p.n + kBN - 1) / kBN;
+  if constexpr (K == Kind128::kWgrad) {
+    const int64_t mb = (p.m + kPairM - 1) / kPairM;
+    const int64_t order = t / (mb * nb);
+    const int64_t rem = t - order * (mb * nb);
+    const int64_t row = rem / nb;
+    tl.e = s.aux[order];
+    tl.p0 = s.off[tl.e];
+    tl.nk = (s.off[tl.e + 1] - tl.p0) >> 7;
+    tl.row0 = static_cast<int32_t>(row * kPairM + rank * kBM);
+    tl.rows_valid = static_cast<int32_t>(min(int64_t(kBM), p.m - tl.row0));
+    tl.col0 = static_cast<int32_t>((rem - row * nb) * kBN);
+  } else {
+    const int64_t g = t / nb;
+    tl.col0 = static_cast<int32_t>((t - g * nb) * kBN);
+    tl.e = find_group(s.aux, p.num_experts, g);
+    const int32_t first = static_cast<int32_t>(g - s.aux[tl.e]) * kPairM + rank * kBM;
+    tl.row0 = s.off[tl.e] + first;
+    tl.rows_valid = min(kBM, s.off[tl.e + 1] - s.off[tl.e] - first);
+    tl.nk = static_cast<int32_t>((p.k + 127) >> 7);
+    tl.p0 = 0;
+  }
+  return tl;
+}
+
+// 32 rows x 32 columns of sums to global memory.  `ld` output columns a row; columns at or
+// past `cols_left` and rows at or past `rows_valid` are not written.
+__device__ __forceinline__ void store_block_cut(__nv_bfloat16 *dst, int64_t ld, int rows_valid, int cols_left,
+                                                uint8_t *stage, int lane, const uint32_t (&packed)[16]) {
+  uint8_t *row = stage + lane * 64;
+  const int x = (lane >> 1) & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4 *>(row + 16 * (j ^ x)) =
+        make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+  __syncwarp();
+  const int j = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + 16 * (j ^ ((r >> 1) & 3)));
+    if (r < rows_valid && 8 * j < cols_left) *reinterpret_cast<uint4 *>(dst + r * ld + 8 * j) = v;
+  }
+  __syncwarp();
+}
+
+// The same for 16 fp32 columns, written or added (one unfused add an element).
+__device__ __forceinline__ void store_fp32_cut(float *dst, int64_t ld, int rows_valid, int cols_left, bool add,
+                                               uint8_t *stage, int lane, const float2 *v) {
+  uint8_t *row = stage + lane * 64;
+  const int x = (lane >> 1) & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<float4 *>(row + 16 * (j ^ x)) = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+  __syncwarp();
+  const int j = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    float4 o = *reinterpret_cast<const float4 *>(stage + r * 64 + 16 * (j ^ ((r >> 1) & 3)));
+    if (r < rows_valid && 4 * j < cols_left) {
+      float4 *at = reinterpret_cast<float4 *>(dst + r * ld + 4 * j);
+      if (add) {
+        const float4 b = *at;
+        o = make_float4(__fadd_rn(b.x, o.x), __fadd_rn(b.y, o.y), __fadd_rn(b.z, o.z), __fadd_rn(b.w, o.w));
+      }
+      *at = o;
+    }
+  }
+  __syncwarp();
+}
+
+template <Kind128 K>
+__global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __grid_constant__ LaunchBlock128 p) {
+  constexpr bool kAmn = K == Kind128::kWgrad;
+  constexpr bool kBmn = K != Kind128::kFwd;
+  __shared__ Shared128 s;
+  extern __shared__ uint8_t dyn_smem[];
+  constexpr int S = kStages128;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem_a = smem;
+  uint8_t *smem_b = smem_a + S * kABytes;
+  uint8_t *smem_out = smem + S * kStageBytes128;
+  int32_t *gmem = reinterpret_cast<int32_t *>(smem_out + kStageOut);
+  const Tables tab{gmem, gmem + (p.num_experts + 1)};
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(pair::cta_rank());
+  const int64_t pair_id = blockIdx.x >> 1;
+  const int64_t pairs = gridDim.x >> 1;
+
+  // ---- tables (both CTAs of a pair see the same offsets and take the same way out)
+  if constexpr (K == Kind128::kWgrad) {
+    if (warp == 0) {
+      bool ok = true;
+      for (int e = lane; e <= p.num_experts; e += 32) {
+        const int32_t v = __ldg(p.offsets + e);
+        const int32_t before = e ? __ldg(p.offsets + e - 1) : 0;
+        if ((e == 0 && v != 0) || v < before || (v & 127) != 0 || v > p.positions) ok = false;
+        tab.off[e] = v;
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (lane == 0) s.ok_flag = ok;
+    }
+    __syncthreads();
+    if (s.ok_flag) {
+      for (int e = threadIdx.x; e < p.num_experts; e += kThreads128) {
+        const int32_t w = tab.off[e + 1] - tab.off[e];
+        int order = 0;
+        for (int f = 0; f < p.num_experts; ++f) {
+          const int32_t wf = tab.off[f + 1] - tab.off[f];
+          order += (wf > w) || (wf == w && f < e);
+        }
+        tab.aux[order] = e;
+      }
+    }
+  } else if (warp == 0) {
+    const int32_t total = scan_groups(p.offsets, p.num_experts, p.m, kPairM,
+                                      [&](int g, int32_t lo, int32_t, int32_t first) {
+                                        tab.off[g] = lo;
+                                        tab.aux[g] = first;
+                                      });
+    if (lane == 0) {
+      tab.off[p.num_experts] = static_cast<int32_t>(p.m);
+      tab.aux[p.num_experts] = total;
+      s.ok_flag = total >= 0;
+    }
+  }
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < S; ++i) mbar_init(&s.full[i], 1);
+    for (int i = 0; i < kGroupBars128; ++i) mbar_init(&s.grp_done[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], kAccEmptyArrivals);
+    }
+    mbar_init(&s.drain, 1);
+    mbar_init(&s.peer_fills_bar, 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    prefetch_tensormap(&p.map_a);
+    prefetch_tensormap(&p.map_b);
+  }
+  __syncthreads();
+  if (!s.ok_flag) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
+    return;
+  }
+  if (warp == 1) {
+    pair::tmem_alloc(&s.tmem_base, kTmemCols);
+    pair::tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  pair::cluster_sync();  // both CTAs' barriers exist before any copy or arrive crosses the pair
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  volatile int *abort_flag = &s.abort_flag;
+  const int64_t nb = (p.n + kBN - 1) / kBN;
+  const int64_t total = K == Kind128::kWgrad ? p.num_experts * ((p.m + kPairM - 1) / kPairM) * nb
+                                             : static_cast<int64_t>(tab.aux[p.num_experts]) * nb;
+
+  if (warp < kEpiWarp0) {
+    // 128 threads x 56 + 256 x 224 registers = the launch's 384 x 168
+    regs_dec<56>();
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------------- producer
+      uint32_t stage = 0, filled = 0;
+      bool stop = false;
+      for (int64_t t = pair_id; t < total && !stop; t += pairs) {
+        const Tile128 tl = tile128<K>(p, tab, t, rank);
+        for (int i = 0; i < tl.nk; ++i) {
+          if (filled >= S) {
+            const uint32_t c = (filled - S) >> 1;
+            if (!mbar_wait<true>(&s.grp_done[c % kGroupBars128], (c / kGroupBars128) & 1, abort_flag, p.status)) {
+              stop = true;
+              break;
+            }
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytes128);
+          const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
+          uint8_t *a = smem_a + stage * kABytes, *b = smem_b + stage * kBBytes;
+          const int32_t bcol = tl.col0 + rank * kHalfN;
+          if constexpr (K == Kind128::kWgrad) {
+            pair::tma_load_2d(a, &p.map_a, bar, tl.row0, tl.p0 + i * 128);
+            pair::tma_load_2d(b, &p.map_b, bar, bcol, tl.p0 + i * 128);
+          } else {
+            pair::tma_load_2d(a, &p.map_a, bar, i * 128, tl.row0);
+            if constexpr (K == Kind128::kFwd)
+              tma_load_3d_pair(b, &p.map_b, bar, i * 128, bcol, tl.e);
+            else
+              tma_load_3d_pair(b, &p.map_b, bar, bcol, i * 128, tl.e);
+          }
+          ++filled;
+          if (++stage == S) stage = 0;
+        }
+      }
+      const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
+      if (rank == 0) drain_pair_ring(s.full, S, filled, peer, kStageBytes128);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------------------------------------------- MMA issuer (leader)
+      constexpr uint32_t idesc = idesc_f8(kAmn, kBmn);
+      uint32_t stage = 0, phase = 0, fill = 0;
+      bool stop = false;
+      for (int64_t t = pair_id; t < total && !stop; t += pairs) {
+        const int nk = tile128<K>(p, tab, t, 0).nk;
+        for (int i = 0; i < nk; ++i) {
+          const uint32_t b = fill & 1;
+          if (!mbar_wait<true>(&s.acc_empty[b], ((fill >> 1) & 1) ^ 1, abort_flag, p.status) ||
+              !mbar_wait<true>(&s.full[stage], phase, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_s = smem_u32(smem_a + stage * kABytes);
+          const uint32_t b_s = smem_u32(smem_b + stage * kBBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 of K: 32 bytes along a K-major row, 32 rows of an MN-major tile
+            mma_f8(tmem + b * kBN, desc_sw128(a_s + kk * (kAmn ? 4096 : 32), kAmn),
+                   desc_sw128(b_s + kk * (kBmn ? 4096 : 32), kBmn), idesc, kk > 0);
+          pair::commit_both(&s.acc_full[b]);
+          if (fill & 1) pair::commit_both(&s.grp_done[(fill >> 1) % kGroupBars128]);
+          ++fill;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      pair::commit_local(&s.drain);
+      mbar_drain(&s.drain, 0);
+    }
+  } else {
+    // ----------------------------------------------------------------- epilogue
+    regs_inc<224>();
+    const int ew = warp - kEpiWarp0;
+    const int q = warp & 3;         // tensor-memory lane quarter
+    const int half = ew >> 2;       // column half of the tile
+    const int r = q * 32 + lane;    // row of the CTA's 128
+    uint8_t *stage_blk = smem_out + ew * kOutBoxBytes;
+    float *colsc = reinterpret_cast<float *>(smem_out + 8 * kOutBoxBytes + ew * kColScaleBytes);
+    const uint32_t leader_empty[2] = {pair::map_to_rank(&s.acc_empty[0], 0), pair::map_to_rank(&s.acc_empty[1], 0)};
+    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    const int64_t kb_count = (p.k + 127) >> 7;   // contraction blocks (fwd, dgrad)
+    const int64_t nb128 = (p.n + 127) >> 7;      // output column blocks
+    uint32_t g = 0;
+    bool stop = false;
+    for (int64_t t = pair_id; t < total && !stop; t += pairs) {
+      const Tile128 tl = tile128<K>(p, tab, t, rank);
+      const int c0 = tl.col0 + half * 128;
+      const bool valid = r < tl.rows_valid;
+      // scale of this thread's row for block i, and of the warp's columns
+      const float *sa_ptr;
+      int64_t sa_step;
+      if constexpr (K == Kind128::kWgrad) {
+        sa_ptr = p.a_scale + static_cast<int64_t>(tl.p0 >> 7) * p.m + tl.row0 + r;
+        sa_step = p.m;
+      } else {
+        sa_ptr = p.a_scale + tl.row0 + r;
+        sa_step = p.m;
+      }
+      const float *sb_ptr;
+      int64_t sb_step;
+      const bool in_cols = c0 < p.n;
+      if constexpr (K == Kind128::kFwd) {
+        sb_ptr = p.b_scale + (tl.e * nb128 + (c0 >> 7)) * kb_count;
+        sb_step = 1;
+      } else if constexpr (K == Kind128::kDgrad) {
+        sb_ptr = p.b_scale + tl.e * kb_count * nb128 + (c0 >> 7);
+        sb_step = nb128;
+      } else {
+        sb_ptr = p.b_scale + static_cast<int64_t>(tl.p0 >> 7) * p.n + c0 + 4 * lane;
+        sb_step = p.n;
+      }
+      const bool lane_cols = c0 + 4 * lane < p.n;  // wgrad: n is a multiple of 16
+      auto load_a = [&](int i) { return valid && i < tl.nk ? __ldg(sa_ptr + i * sa_step) : 0.0f; };
+      auto load_b = [&](int i) { return in_cols && i < tl.nk ? __ldg(sb_ptr + i * sb_step) : 0.0f; };
+      auto load_b4 = [&](int i) {
+        return lane_cols && i < tl.nk ? __ldg(reinterpret_cast<const float4 *>(sb_ptr + i * sb_step))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+      // scales of the next blocks, on their way while this one is summed
+      float fa0 = load_a(0), fa1 = load_a(1), fa2 = load_a(2);
+      float fb0 = 0.f, fb1 = 0.f, fb2 = 0.f;
+      float4 fc0, fc1;
+      if constexpr (K == Kind128::kWgrad) {
+        fc0 = load_b4(0);
+        fc1 = load_b4(1);
+      } else {
+        fb0 = load_b(0);
+        fb1 = load_b(1);
+        fb2 = load_b(2);
+      }
+#pragma unroll 1
+      for (int i = 0; i < tl.nk; ++i) {
+        const uint32_t b = g & 1;
+        const float *cs = colsc + (i & 1) * 128;
+        float v = fa0;
+        if constexpr (K == Kind128::kWgrad) {
+          reinterpret_cast<float4 *>(colsc + (i & 1) * 128)[lane] = fc0;
+          fc0 = fc1;
+          fc1 = load_b4(i + 2);
+          __syncwarp();
+        } else {
+          v *= fb0;
+          fb0 = fb1;
+          fb1 = fb2;
+          fb2 = load_b(i + 3);
+        }
+        fa0 = fa1;
+        fa1 = fa2;
+        fa2 = load_a(i + 3);
+        const float2 f = make_float2(v, v);
+        if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        auto add = [&](int c, const uint32_t(&d)[32]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+            float2 w = f;
+            if constexpr (K == Kind128::kWgrad) w = __fmul2_rn(*reinterpret_cast<const float2 *>(cs + 32 * c + 2 * j), f);
+            acc[16 * c + j] = __ffma2_rn(x, w, acc[16 * c + j]);
+          }
+        };
+        const uint32_t tb = tq + b * kBN;
+        uint32_t va[32], vb[32];
+        tmem_ld_32x32(tb, va);
+        tmem_wait_ld_for(va);
+        tmem_ld_32x32(tb + 32, vb);
+        add(0, va);
+        tmem_wait_ld_for(vb);
+        tmem_ld_32x32(tb + 64, va);
+        add(1, vb);
+        tmem_wait_ld_for(va);
+        tmem_ld_32x32(tb + 96, vb);
+        add(2, va);
+        tmem_wait_ld_for(vb);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair::arrive_remote_relaxed(leader_empty[b]);
+        add(3, vb);
+        ++g;
+      }
+      if (stop) break;
+      // ---- the tile's sums out
+      const int warp_rows = tl.rows_valid - 32 * q;
+      if (warp_rows <= 0 || !in_cols) continue;
+      const int64_t out_row = (K == Kind128::kWgrad ? tl.e * p.m : int64_t(0)) + tl.row0 + 32 * q;
+      if (K == Kind128::kWgrad && p.out_fp32) {
+        if (tl.nk == 0 && p.accumulate) continue;
+        float *dst = static_cast<float *>(p.y) + out_row * p.n + c0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          store_fp32_cut(dst + 16 * c, p.n, warp_rows, static_cast<int>(p.n - c0 - 16 * c), p.accumulate, stage_blk,
+                         lane, acc + 8 * c);
+      } else {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.y) + out_row * p.n + c0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int left = static_cast<int>(p.n) - c0 - 32 * c;
+          uint32_t packed[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * c + j].x, acc[16 * c + j].y);
+            packed[j] = *reinterpret_cast<const uint32_t *>(&h);
+          }
+          if (left <= 0) break;
+          if (warp_rows >= 32 && left >= 32) {
+            store_block_tma(&p.map_y, c0 + 32 * c, static_cast<int32_t>(out_row), stage_blk, lane, packed);
+          } else {
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+            store_block_cut(dst + 32 * c, p.n, warp_rows, left, stage_blk, lane, packed);
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  pair::cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    pair::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <Kind128 K>
+cudaError_t launch128(const LaunchBlock128 &a) {
+  const int smem = 1024 + kStages128 * kStageBytes128 + kStageOut + 8 * (a.num_experts + 1);
+  auto kernel = gemm_block128_kernel<K>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  const int64_t nb = (a.n + kBN - 1) / kBN;
+  const int64_t bound = K == Kind128::kWgrad ? a.num_experts * ((a.m + kPairM - 1) / kPairM) * nb
+                                             : (a.m / kPairM + std::min<int64_t>(a.num_experts, a.m)) * nb;
+  int64_t pairs = a.num_sms / 2;
+  if (bound < pairs) pairs = bound;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(kThreads128, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_block128_fwd(const LaunchBlock128 &a) { return launch128<Kind128::kFwd>(a); }
+cudaError_t launch_block128_dgrad(const LaunchBlock128 &a) { return launch128<Kind128::kDgrad>(a); }
+cudaError_t launch_block128_wgrad(const LaunchBlock128 &a) { return launch128<Kind128::kWgrad>(a); }
+
+}  // namespace fme

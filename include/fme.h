@@ -23,6 +23,13 @@
  *   grouped_gemm_dgrad_mxfp8  dX_e = dY_e W_e per expert, bf16 out.
  *   grouped_gemm_wgrad_mxfp8  dW_e = dY_e^T H_e per expert, bf16 out (or added into
  *                             fp32: grouped_gemm_wgrad_mxfp8_accumulate).
+ * And the same projections in FP8 with an fp32 scale per block of 128:
+ *   quantize_fp8_block128 (quantize_fp8_block128_rowcol, permute_quantize_fp8_block128),
+ *   quantize_fp8_block128_weights   E4M3 codes, one fp32 scale per 128 values along
+ *                             the contraction, or per 128 x 128 weights.
+ *   grouped_gemm_fwd_fp8_block128, grouped_gemm_dgrad_fp8_block128,
+ *   grouped_gemm_wgrad_fp8_block128   the products; one set of weight codes for both
+ *                             directions, n and k any multiples of 16.
  *
  * Source passages ("Composer 2 Technical Report", papercache.org summary,
  * section 6.1): the NVFP4-variant paragraph (E2M1, E4M3 per block of 16, FP32
@@ -469,6 +476,88 @@ fme_status grouped_gemm_wgrad_mxfp8_accumulate(const uint8_t *a_codes, const uin
                                                const uint8_t *b_codes, const uint8_t *b_sf, int64_t ldb,
                                                const int32_t *padded_offsets, int32_t num_experts, int64_t m,
                                                int64_t n, float *dw_acc, int32_t *dev_status, void *stream);
+
+/*
+ * quantize_fp8_block128 -- FP8 with one fp32 scale per block of 128 values.
+ *
+ * For a block with largest magnitude a: A = max(a, 2^-100), scale = fl32(A / 448),
+ * r = fl32(448 / A) (both IEEE divisions), code = E4M3(fl32(x r)), round to nearest
+ * even, saturating.  Dequantized value = code * scale.
+ * ("Scaling and Optimizing Frontier Model Training": DeepSeek-V3-class experts, which
+ * are stored and trained in this format; the floor 2^-100 is this library's choice.)
+ *
+ *   x            device bf16 [rows x cols]
+ *   rows, cols   rows >= 0; cols a multiple of 16, 16 .. 65536; CB = ceil(cols / 128)
+ *   axis         FME_ROWWISE: blocks along a row.  codes uint8 [rows x cols], scale float
+ *                [CB x rows] (block-major); offsets are not read, padded_offsets NULL.
+ *                FME_COLWISE: blocks along each group's rows.  Group g starts at padded
+ *                position P_g = 128 * sum_{g'<g} ceil(n_g' / 128); ld = fme_colwise_ld(rows,
+ *                num_groups) positions.  codes uint8 [ld x cols] (not transposed), scale
+ *                float [ld / 128 x cols]; every position that holds no row, to the end, gets
+ *                codes 0.  padded_offsets int32 [num_groups + 1] receives P_0 .. P_G.
+ *   offsets      device int32 [num_groups + 1] or NULL (one group)
+ */
+fme_status quantize_fp8_block128(const void *x, int64_t rows, int64_t cols, int32_t axis, const int32_t *offsets,
+                                 int32_t num_groups, uint8_t *codes, float *scale, int32_t *padded_offsets,
+                                 int32_t *dev_status, void *stream);
+
+/* quantize_fp8_block128_rowcol -- both layouts of one tensor from one read of it (the
+ * output gradient: rows for dgrad, columns for wgrad); byte for byte the two calls. */
+fme_status quantize_fp8_block128_rowcol(const void *x, int64_t rows, int64_t cols, const int32_t *offsets,
+                                        int32_t num_groups, uint8_t *row_codes, float *row_scale, uint8_t *col_codes,
+                                        float *col_scale, int32_t *padded_offsets, int32_t *dev_status,
+                                        void *stream);
+
+/* permute_quantize_fp8_block128 -- the row-wise quantization of the grouped rows
+ * x[src_row[r] / top_k], r < tokens * top_k (src_row from moe_route; x bf16 [tokens x cols]).
+ * An index outside [0, tokens * top_k) sets FME_DEV_BAD_INDEX and reads row 0. */
+fme_status permute_quantize_fp8_block128(const void *x, int64_t tokens, int64_t cols, const int32_t *src_row,
+                                         int32_t top_k, uint8_t *codes, float *scale, int32_t *dev_status,
+                                         void *stream);
+
+/* quantize_fp8_block128_weights -- one scale per 128 x 128 block of each expert's
+ * w [num_experts][n][k] (bf16): codes uint8 of the same shape, scale float
+ * [num_experts][ceil(n / 128)][ceil(k / 128)].  n, k multiples of 16, 16 .. 65536. */
+fme_status quantize_fp8_block128_weights(const void *w, int32_t num_experts, int64_t n, int64_t k, uint8_t *codes,
+                                         float *scale, void *stream);
+
+/*
+ * grouped_gemm_fwd_fp8_block128 -- Y[t, n] = sum_b a_scale[b][t] w_scale[e][n / 128][b]
+ * sum_{k in block b} a[t, k] w[e, n, k] for every row t of expert e; the inner sums on the
+ * tensor cores, the outer ones in fp32 registers in order of b, one rounding to bf16.
+ * No split over k: a row's output does not depend on any other row.
+ *
+ *   a_codes, a_scale   quantize_fp8_block128(ROWWISE) (or permute_..) of X [m x k]
+ *   w_codes, w_scale   quantize_fp8_block128_weights of W [num_experts][n][k]
+ *   offsets            device int32 [num_experts + 1], rows of X per expert
+ *   m, n, k            n and k multiples of 16, 16 .. 65536
+ *   y                  device bf16 [m x n]
+ */
+fme_status grouped_gemm_fwd_fp8_block128(const uint8_t *a_codes, const float *a_scale, const uint8_t *w_codes,
+                                         const float *w_scale, const int32_t *offsets, int32_t num_experts, int64_t m,
+                                         int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream);
+
+/* grouped_gemm_dgrad_fp8_block128 -- dX[t, :] = dY[t, :] W_e from the row-wise codes of
+ * dY [m x n] and the same weight codes as the forward; dx bf16 [m x k]. */
+fme_status grouped_gemm_dgrad_fp8_block128(const uint8_t *dy_codes, const float *dy_scale, const uint8_t *w_codes,
+                                           const float *w_scale, const int32_t *offsets, int32_t num_experts,
+                                           int64_t m, int64_t n, int64_t k, void *dx, int32_t *dev_status,
+                                           void *stream);
+
+/* grouped_gemm_wgrad_fp8_block128 -- dW_e = dY_e^T X_e from the column-wise codes of
+ * dY [rows x n] and X [rows x k], quantized with the same offsets.
+ *   positions       padded positions of both (fme_colwise_ld), a multiple of 128
+ *   padded_offsets  device int32 [num_experts + 1] written by the quantizer
+ *   dw, dw_mode     FME_DW_BF16: bf16 [num_experts][n][k]; FME_DW_FP32: fp32;
+ *                   FME_DW_FP32_ADD: added into fp32, one unfused add an element.
+ * An expert with no rows gets zeros (nothing is added). */
+#define FME_DW_BF16 0
+#define FME_DW_FP32 1
+#define FME_DW_FP32_ADD 2
+fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float *dy_scale, const uint8_t *x_codes,
+                                           const float *x_scale, int64_t positions, const int32_t *padded_offsets,
+                                           int32_t num_experts, int64_t n, int64_t k, void *dw, int32_t dw_mode,
+                                           int32_t *dev_status, void *stream);
 
 /* Rows of the padded scale layout for `rows` rows in `num_groups` groups: an
  * upper bound of 128 * sum ceil(n_g / 128) that needs no offsets. */
