@@ -105,6 +105,14 @@ SYMBOLS = {
     "grouped_gemm_dgrad_fp8_block128": ("i32", ["p", "p", "p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
     "grouped_gemm_wgrad_fp8_block128": ("i32", ["p", "p", "p", "p", "i64", "p", "i32", "i64", "i64", "p", "i32", "p",
                                                 "p"]),
+    "moe_gate": ("i32", ["p", "i32", "i64", "i32", "i32", "i32", "i32", "f32", "p", "p", "p", "p"]),
+    "moe_gate_backward": ("i32", ["p", "i32", "p", "p", "i64", "i32", "i32", "i32", "i32", "f32", "p", "p", "p"]),
+    "moe_balance_loss": ("i32", ["p", "i32", "p", "i64", "i32", "i32", "i32", "f32", "p", "i64", "p", "p", "p", "p",
+                                 "p", "i64", "p", "p"]),
+    "moe_balance_loss_backward": ("i32", ["p", "i32", "p", "p", "p", "i64", "i32", "i32", "i32", "f32", "p", "i64",
+                                          "p", "p", "i32", "p"]),
+    "moe_combine_backward": ("i32", ["p", "p", "i64", "p", "p", "i64", "i32", "i64", "p", "p", "p", "p"]),
+    "fme_balance_workspace_bytes": ("i64", ["i64", "i64", "i32"]),
     "fme_route_workspace_bytes": ("i64", ["i64", "i32", "i32"]),
     "fme_sf_padded_rows": ("i64", ["i64", "i32"]),
     "fme_sf_bytes": ("i64", ["i64", "i64", "i32", "i32"]),
@@ -115,7 +123,7 @@ SYMBOLS = {
     "fme_version": ("s", []),
 }
 
-_CT = {"i32": ctypes.c_int32, "i64": ctypes.c_int64, "p": ctypes.c_void_p, "s": ctypes.c_char_p}
+_CT = {"f32": ctypes.c_float, "i32": ctypes.c_int32, "i64": ctypes.c_int64, "p": ctypes.c_void_p, "s": ctypes.c_char_p}
 
 
 def _declare(handle):
@@ -681,6 +689,146 @@ def grouped_gemm_wgrad_fp8_block128(dy_codes, dy_scale, x_codes, x_scale, padded
                                                _stream(stream))
     _check(st, where)
     return dw
+
+
+# ------------------------------------------------------------------- router --
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _router(where, logits, top_k, score):
+    """(tokens, experts, dtype code, score code) of checked router arguments."""
+    import torch
+
+    tokens, experts = logits.shape
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{where}: logits must be bfloat16 or float32, got {logits.dtype}")
+    _need(where, "logits", logits, logits.dtype, logits.shape)
+    if score not in SCORES:
+        raise ValueError(f"{where}: score must be 'softmax' or 'sigmoid', got {score!r}")
+    return tokens, experts, 0 if logits.dtype == torch.bfloat16 else 1, SCORES[score]
+
+
+def _sequences(where, tokens, seq_offsets, token_mask):
+    import torch
+
+    if seq_offsets is not None:
+        _need(where, "seq_offsets", seq_offsets, torch.int32, (seq_offsets.shape[0],))
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"{where}: token_mask must be bool or uint8, got {token_mask.dtype}")
+        _need(where, "token_mask", token_mask, token_mask.dtype, (tokens,))
+    return 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+
+
+def moe_gate(logits, top_k, *, score="softmax", bias=None, normalize=True, scale=1.0, ids=None, weights=None,
+             stream=None):
+    """The top_k experts of each token by logits [tokens, E] (+ bias [E]), largest first, and
+    their weights, scale * s / sum of the chosen s (normalize) or scale * s, s the softmax or
+    sigmoid of the logits -> (ids [tokens, top_k] int32, weights [tokens, top_k] f32)."""
+    import torch
+
+    where = "moe_gate"
+    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
+    if bias is not None:
+        _need(where, "bias", bias, torch.float32, (experts,))
+    ids = _out(where, "ids", ids, torch.int32, (tokens, top_k), logits.device)
+    weights = _out(where, "weights", weights, torch.float32, (tokens, top_k), logits.device)
+    st = lib().moe_gate(_ptr(logits), dtype, tokens, experts, top_k, kind, int(normalize), scale, _ptr(bias), _ptr(ids),
+                        _ptr(weights), _stream(stream))
+    _check(st, where)
+    return ids, weights
+
+
+def moe_gate_backward(logits, ids, d_weights, *, score="softmax", normalize=True, scale=1.0, d_logits=None, status=None,
+                      stream=None):
+    """The gradient of moe_gate's weights -> d_logits [tokens, E] in the logits' type."""
+    import torch
+
+    where = "moe_gate_backward"
+    top_k = ids.shape[1]
+    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
+    _need(where, "ids", ids, torch.int32, (tokens, top_k))
+    _need(where, "d_weights", d_weights, torch.float32, (tokens, top_k))
+    d_logits = _out(where, "d_logits", d_logits, logits.dtype, (tokens, experts), logits.device)
+    st = lib().moe_gate_backward(_ptr(logits), dtype, _ptr(ids), _ptr(d_weights), tokens, experts, top_k, kind,
+                                 int(normalize), scale, _ptr(d_logits), _ptr(status), _stream(stream))
+    _check(st, where)
+    return d_logits
+
+
+def balance_workspace_bytes(tokens: int, num_seqs: int, num_experts: int) -> int:
+    return int(lib().fme_balance_workspace_bytes(tokens, num_seqs, num_experts))
+
+
+def moe_balance_loss(logits, ids, *, score="softmax", alpha=1.0, seq_offsets=None, token_mask=None, loss=None,
+                     counts=None, seq_tokens=None, workspace=None, status=None, stream=None):
+    """alpha times the sequence-wise load-balance loss of routing logits [tokens, E] to ids
+    [tokens, top_k] -> (loss [1] f32, counts [S, E] int32, seq_tokens [S] int32).
+
+    seq_offsets: int32 [S+1], rising from 0 to tokens (None: one sequence); token_mask: bool or
+    uint8 [tokens], the tokens that count (None: all)."""
+    import torch
+
+    where = "moe_balance_loss"
+    top_k = ids.shape[1]
+    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
+    _need(where, "ids", ids, torch.int32, (tokens, top_k))
+    seqs = _sequences(where, tokens, seq_offsets, token_mask)
+    dev = logits.device
+    loss = _out(where, "loss", loss, torch.float32, (1,), dev)
+    counts = _out(where, "counts", counts, torch.int32, (seqs, experts), dev)
+    seq_tokens = _out(where, "seq_tokens", seq_tokens, torch.int32, (seqs,), dev)
+    if workspace is None:
+        workspace = _empty((balance_workspace_bytes(tokens, seqs, experts),), torch.uint8, dev)
+        if stream is not None:
+            workspace.record_stream(stream)  # it is released when this call returns
+    st = lib().moe_balance_loss(_ptr(logits), dtype, _ptr(ids), tokens, experts, top_k, kind, alpha, _ptr(seq_offsets),
+                                seqs, _ptr(token_mask), _ptr(loss), _ptr(counts), _ptr(seq_tokens), _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check(st, where)
+    return loss, counts, seq_tokens
+
+
+def moe_balance_loss_backward(logits, counts, seq_tokens, d_loss, top_k, *, score="softmax", alpha=1.0,
+                              seq_offsets=None, token_mask=None, d_logits=None, accumulate=False, stream=None):
+    """The gradient of d_loss [1] times moe_balance_loss -> d_logits [tokens, E] in the logits'
+    type; with accumulate it is added to the given d_logits."""
+    import torch
+
+    where = "moe_balance_loss_backward"
+    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
+    seqs = _sequences(where, tokens, seq_offsets, token_mask)
+    _need(where, "counts", counts, torch.int32, (seqs, experts))
+    _need(where, "seq_tokens", seq_tokens, torch.int32, (seqs,))
+    _need(where, "d_loss", d_loss, torch.float32, (1,))
+    if accumulate and d_logits is None:
+        raise ValueError(f"{where}: accumulate needs the d_logits to add to")
+    d_logits = _out(where, "d_logits", d_logits, logits.dtype, (tokens, experts), logits.device)
+    st = lib().moe_balance_loss_backward(_ptr(logits), dtype, _ptr(counts), _ptr(seq_tokens), _ptr(d_loss), tokens,
+                                         experts, top_k, kind, alpha, _ptr(seq_offsets), seqs, _ptr(token_mask),
+                                         _ptr(d_logits), int(accumulate), _stream(stream))
+    _check(st, where)
+    return d_logits
+
+
+def moe_combine_backward(d_out, y, row_of, weights, *, d_y=None, d_weights=None, status=None, stream=None):
+    """The gradient of moe_combine for d_out [tokens, n] bf16 -> (d_y [rows_y, n] bf16,
+    d_weights [tokens, top_k] f32)."""
+    import torch
+
+    where = "moe_combine_backward"
+    rows_y, n = y.shape
+    tokens, top_k = row_of.shape
+    _need(where, "d_out", d_out, torch.bfloat16, (tokens, n))
+    _need(where, "y", y, torch.bfloat16, (rows_y, n))
+    _need(where, "row_of", row_of, torch.int32, (tokens, top_k))
+    _need(where, "weights", weights, torch.float32, (tokens, top_k))
+    d_y = _out(where, "d_y", d_y, torch.bfloat16, (rows_y, n), y.device)
+    d_weights = _out(where, "d_weights", d_weights, torch.float32, (tokens, top_k), y.device)
+    st = lib().moe_combine_backward(_ptr(d_out), _ptr(y), rows_y, _ptr(row_of), _ptr(weights), tokens, top_k, n,
+                                    _ptr(d_y), _ptr(d_weights), _ptr(status), _stream(stream))
+    _check(st, where)
+    return d_y, d_weights
 
 
 def read_device_status(status, stream=None) -> tuple[int, int]:

@@ -20,7 +20,7 @@ ROOT = os.path.dirname(HERE)
 LIBRARY = os.path.join(HERE, "libfme.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quant_nvfp4.cu", "quant_mxfp8.cu", "gemm.cu", "gemm_nvfp4.cu", "route.cu",
-           "quant_block128.cu", "gemm_block128.cu"]
+           "quant_block128.cu", "gemm_block128.cu", "gate.cu"]
 HEADERS = ["fme_device.cuh", "fme_launch.h", "gemm_common.cuh", "block128.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -905,4 +905,206 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
   return err == cudaSuccess ? FME_OK : cuda_fail(err, "grouped_gemm_wgrad_fp8_block128 launch");
 }
 
+// ------------------------------------------------------------------ router --
+namespace {
+
+// Tokens of one sequence are summed by `slices` CTAs: two CTAs for every SM at most, 16 tokens at
+// least for each.  A function of the sizes alone, so that the workspace and the order of the
+// sums do not depend on the device.
+int32_t balance_slices(int64_t tokens, int64_t num_seqs) {
+  const int64_t by_size = (tokens + 16 * num_seqs - 1) / (16 * num_seqs);
+  int64_t s = 304 / num_seqs;
+  if (s > by_size) s = by_size;
+  return static_cast<int32_t>(s < 1 ? 1 : s);
+}
+
+int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
+
+struct BalanceWorkspace {
+  int64_t sums, counts, tokens, term, done, bytes;
+};
+BalanceWorkspace balance_workspace(int64_t tokens, int64_t num_seqs, int32_t num_experts) {
+  const int64_t parts = num_seqs * balance_slices(tokens, num_seqs);
+  BalanceWorkspace w;
+  w.sums = 0;
+  w.counts = w.sums + round16(parts * num_experts * 4);
+  w.tokens = w.counts + round16(parts * num_experts * 4);
+  w.term = w.tokens + round16(parts * 4);
+  w.done = w.term + round16(num_seqs * 4);
+  w.bytes = w.done + 16;
+  return w;
+}
+
+bool router_dtype(int32_t d) { return d == FME_BF16 || d == FME_FP32; }
+bool router_score(int32_t s) { return s == FME_SCORE_SOFTMAX || s == FME_SCORE_SIGMOID; }
+
+// Sizes common to the router's calls.
+fme_status check_router(int64_t tokens, int32_t num_experts, int32_t top_k, int32_t dtype, int32_t score) {
+  if (tokens < 0 || num_experts < 1 || top_k < 1 || top_k > num_experts) return FME_ERR_INVALID_ARGUMENT;
+  if (!router_dtype(dtype) || !router_score(score)) return FME_ERR_INVALID_ARGUMENT;
+  if (num_experts > FME_MAX_GROUPS || top_k > 32 || tokens > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
+  return FME_OK;
+}
+
+}  // namespace
+
+int64_t fme_balance_workspace_bytes(int64_t tokens, int64_t num_seqs, int32_t num_experts) {
+  if (tokens < 0 || num_seqs < 1 || num_experts < 1) return 0;
+  return balance_workspace(tokens, num_seqs, num_experts).bytes;
+}
+
+fme_status moe_gate(const void *logits, int32_t dtype, int64_t tokens, int32_t num_experts, int32_t top_k, int32_t score,
+                    int32_t normalize, float scale, const float *bias, int32_t *ids, float *weights, void *stream) {
+  fme_status st = check_router(tokens, num_experts, top_k, dtype, score);
+  if (st != FME_OK) return st;
+  if (tokens == 0) return FME_OK;
+  if (!logits || !ids || !weights) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return FME_ERR_MISALIGNED;
+  int sms = 0;
+  if ((st = current_device(&sms)) != FME_OK) return st;
+  fme::LaunchGate a{};
+  a.logits = logits;
+  a.bf16 = dtype == FME_BF16;
+  a.tokens = tokens;
+  a.num_experts = num_experts;
+  a.top_k = top_k;
+  a.softmax = score == FME_SCORE_SOFTMAX;
+  a.normalize = normalize != 0;
+  a.scale = scale;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_gate(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_gate launch");
+}
+
+fme_status moe_gate_backward(const void *logits, int32_t dtype, const int32_t *ids, const float *d_weights,
+                             int64_t tokens, int32_t num_experts, int32_t top_k, int32_t score, int32_t normalize,
+                             float scale, void *d_logits, int32_t *dev_status, void *stream) {
+  fme_status st = check_router(tokens, num_experts, top_k, dtype, score);
+  if (st != FME_OK) return st;
+  if (tokens == 0) return FME_OK;
+  if (!logits || !ids || !d_weights || !d_logits) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(logits) || !aligned16(ids) || !aligned16(d_weights) || !aligned16(d_logits)) return FME_ERR_MISALIGNED;
+  int sms = 0;
+  if ((st = current_device(&sms)) != FME_OK) return st;
+  fme::LaunchGate a{};
+  a.logits = logits;
+  a.bf16 = dtype == FME_BF16;
+  a.tokens = tokens;
+  a.num_experts = num_experts;
+  a.top_k = top_k;
+  a.softmax = score == FME_SCORE_SOFTMAX;
+  a.normalize = normalize != 0;
+  a.scale = scale;
+  a.ids = const_cast<int32_t *>(ids);
+  a.d_weights = d_weights;
+  a.d_logits = d_logits;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_gate_backward(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_gate_backward launch");
+}
+
+fme_status moe_balance_loss(const void *logits, int32_t dtype, const int32_t *ids, int64_t tokens, int32_t num_experts,
+                            int32_t top_k, int32_t score, float alpha, const int32_t *seq_offsets, int64_t num_seqs,
+                            const uint8_t *token_mask, float *loss, int32_t *counts, int32_t *seq_tokens,
+                            void *workspace, int64_t workspace_bytes, int32_t *dev_status, void *stream) {
+  fme_status st = check_router(tokens, num_experts, top_k, dtype, score);
+  if (st != FME_OK) return st;
+  if (num_seqs < 1 || (!seq_offsets && num_seqs != 1)) return FME_ERR_INVALID_ARGUMENT;
+  if (num_seqs > (int64_t(1) << 24)) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!loss || !counts || !seq_tokens || !workspace || (tokens > 0 && (!logits || !ids))) return FME_ERR_INVALID_ARGUMENT;
+  const BalanceWorkspace w = balance_workspace(tokens, num_seqs, num_experts);
+  if (workspace_bytes < w.bytes) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(logits) || !aligned16(ids) || !aligned16(seq_offsets) || !aligned16(token_mask) || !aligned16(loss) ||
+      !aligned16(counts) || !aligned16(seq_tokens) || !aligned16(workspace))
+    return FME_ERR_MISALIGNED;
+  int sms = 0;
+  if ((st = current_device(&sms)) != FME_OK) return st;
+  fme::LaunchBalance a{};
+  a.logits = logits;
+  a.bf16 = dtype == FME_BF16;
+  a.tokens = tokens;
+  a.num_experts = num_experts;
+  a.top_k = top_k;
+  a.softmax = score == FME_SCORE_SOFTMAX;
+  a.alpha = alpha;
+  a.ids = ids;
+  a.seq_offsets = seq_offsets;
+  a.num_seqs = num_seqs;
+  a.token_mask = token_mask;
+  a.loss = loss;
+  a.counts = counts;
+  a.seq_tokens = seq_tokens;
+  a.slices = balance_slices(tokens, num_seqs);
+  uint8_t *base = static_cast<uint8_t *>(workspace);
+  a.part_sum = reinterpret_cast<float *>(base + w.sums);
+  a.part_count = reinterpret_cast<int32_t *>(base + w.counts);
+  a.part_tokens = reinterpret_cast<int32_t *>(base + w.tokens);
+  a.term = reinterpret_cast<float *>(base + w.term);
+  a.done = reinterpret_cast<int32_t *>(base + w.done);
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_balance_loss(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_balance_loss launch");
+}
+
+fme_status moe_balance_loss_backward(const void *logits, int32_t dtype, const int32_t *counts, const int32_t *seq_tokens,
+                                     const float *d_loss, int64_t tokens, int32_t num_experts, int32_t top_k,
+                                     int32_t score, float alpha, const int32_t *seq_offsets, int64_t num_seqs,
+                                     const uint8_t *token_mask, void *d_logits, int32_t accumulate, void *stream) {
+  fme_status st = check_router(tokens, num_experts, top_k, dtype, score);
+  if (st != FME_OK) return st;
+  if (num_seqs < 1 || (!seq_offsets && num_seqs != 1)) return FME_ERR_INVALID_ARGUMENT;
+  if (num_seqs > (int64_t(1) << 24)) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (tokens == 0) return FME_OK;
+  if (!logits || !counts || !seq_tokens || !d_loss || !d_logits) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(logits) || !aligned16(counts) || !aligned16(seq_tokens) || !aligned16(d_loss) ||
+      !aligned16(seq_offsets) || !aligned16(token_mask) || !aligned16(d_logits))
+    return FME_ERR_MISALIGNED;
+  int sms = 0;
+  if ((st = current_device(&sms)) != FME_OK) return st;
+  fme::LaunchBalance a{};
+  a.logits = logits;
+  a.bf16 = dtype == FME_BF16;
+  a.tokens = tokens;
+  a.num_experts = num_experts;
+  a.top_k = top_k;
+  a.softmax = score == FME_SCORE_SOFTMAX;
+  a.alpha = alpha;
+  a.seq_offsets = seq_offsets;
+  a.num_seqs = num_seqs;
+  a.token_mask = token_mask;
+  a.counts = const_cast<int32_t *>(counts);
+  a.seq_tokens = const_cast<int32_t *>(seq_tokens);
+  a.d_loss = d_loss;
+  a.d_logits = d_logits;
+  a.accumulate = accumulate != 0;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_balance_backward(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_balance_loss_backward launch");
+}
+
+fme_status moe_combine_backward(const void *d_out, const void *y, int64_t rows_y, const int32_t *row_of,
+                                const float *weights, int64_t tokens, int32_t top_k, int64_t n, void *d_y,
+                                float *d_weights, int32_t *dev_status, void *stream) {
+  if (tokens < 0 || rows_y < 0 || top_k < 1 || top_k > 64 || n < 0) return FME_ERR_INVALID_ARGUMENT;
+  if (n % 8 != 0 || n == 0 || n > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (tokens > ((int64_t(1) << 31) - 1) / top_k || rows_y > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (tokens == 0) return FME_OK;
+  if (!d_out || !row_of || !weights || !d_weights || (rows_y > 0 && (!y || !d_y))) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(d_out) || !aligned16(y) || !aligned16(row_of) || !aligned16(weights) || !aligned16(d_y) ||
+      !aligned16(d_weights))
+    return FME_ERR_MISALIGNED;
+  int sms = 0;
+  fme_status st = current_device(&sms);
+  if (st != FME_OK) return st;
+  fme::LaunchCombineBackward c{d_out, y, row_of, weights, tokens, top_k, n, rows_y, d_y, d_weights, dev_status,
+                               static_cast<cudaStream_t>(stream)};
+  cudaError_t err = fme::launch_combine_backward(c);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_combine_backward launch");
+}
+
 }  // extern "C"

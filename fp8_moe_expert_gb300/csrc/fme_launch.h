@@ -139,6 +139,65 @@ cudaError_t launch_block128_fwd(const LaunchBlock128 &a);
 cudaError_t launch_block128_dgrad(const LaunchBlock128 &a);
 cudaError_t launch_block128_wgrad(const LaunchBlock128 &a);
 
+// The router (gate.cu).
+struct LaunchGate {
+  const void *logits;  // [tokens x num_experts], bf16 or fp32
+  bool bf16;
+  int64_t tokens;
+  int32_t num_experts, top_k;
+  bool softmax, normalize;
+  float scale;
+  const float *bias;  // or NULL
+  int32_t *ids;       // read by the gradient
+  float *weights;
+  const float *d_weights;
+  void *d_logits;
+  int32_t *status;
+  cudaStream_t stream;
+};
+struct LaunchBalance {
+  const void *logits;
+  bool bf16;
+  int64_t tokens;
+  int32_t num_experts, top_k;
+  bool softmax;
+  float alpha;
+  const int32_t *ids;
+  const int32_t *seq_offsets;  // [num_seqs + 1] or NULL
+  int64_t num_seqs;
+  const uint8_t *token_mask;  // or NULL
+  float *loss;
+  int32_t *counts, *seq_tokens;
+  // workspace
+  int32_t slices;
+  float *part_sum, *term;
+  int32_t *part_count, *part_tokens, *done;
+  // gradient
+  const float *d_loss;
+  void *d_logits;
+  bool accumulate;
+  int32_t *status;
+  cudaStream_t stream;
+};
+cudaError_t launch_gate(const LaunchGate &a);
+cudaError_t launch_gate_backward(const LaunchGate &a);
+cudaError_t launch_balance_loss(const LaunchBalance &a);
+cudaError_t launch_balance_backward(const LaunchBalance &a);
+
+struct LaunchCombineBackward {
+  const void *d_out, *y;
+  const int32_t *row_of;
+  const float *weights;
+  int64_t tokens;
+  int32_t top_k;
+  int64_t n, rows_y;
+  void *d_y;
+  float *d_weights;
+  int32_t *status;
+  cudaStream_t stream;
+};
+cudaError_t launch_combine_backward(const LaunchCombineBackward &c);
+
 cudaError_t launch_quantize_nvfp4(const LaunchNvfp4 &a);
 // Standard NVFP4 (one FP32 scale for the whole tensor): zero *tensor_amax, reduce
 // max |x| into it, then quantize every row with it in place of the row's amax.

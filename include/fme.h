@@ -30,6 +30,10 @@
  *   grouped_gemm_fwd_fp8_block128, grouped_gemm_dgrad_fp8_block128,
  *   grouped_gemm_wgrad_fp8_block128   the products; one set of weight codes for both
  *                             directions, n and k any multiples of 16.
+ * And the router around them:
+ *   moe_gate, moe_gate_backward   experts and weights of each token from its logits.
+ *   moe_balance_loss, moe_balance_loss_backward   load balance and per-expert counts.
+ *   moe_combine_backward      the gradient of moe_combine.
  *
  * Source passages ("Composer 2 Technical Report", papercache.org summary,
  * section 6.1): the NVFP4-variant paragraph (E2M1, E4M3 per block of 16, FP32
@@ -558,6 +562,86 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
                                            const float *x_scale, int64_t positions, const int32_t *padded_offsets,
                                            int32_t num_experts, int64_t n, int64_t k, void *dw, int32_t dw_mode,
                                            int32_t *dev_status, void *stream);
+
+/*
+ * moe_gate -- the top_k experts of each token and their weights, from router logits.
+ *
+ * key[t, e] = fl32(logits[t, e] + bias[e]); ids[t, :] = the top_k largest keys, largest first,
+ * equal keys by the lower expert (a NaN is lowest).  The choice is one fp32 addition and
+ * comparisons: the same on every run and machine, so it can be replayed
+ * ("Composer 2 Technical Report", section 6.2).  With s = softmax over the token's
+ * experts or sigmoid, of the logits without bias:
+ *   weights[t, i] = scale s_i / sum of s over the choices (normalize), or scale s_i.
+ * All arithmetic in fp32.  A token whose chosen logits (without normalize: all its logits)
+ * are -inf gets weights 0; +inf under softmax, or a NaN, gives weights NaN.
+ *
+ *   logits     device bf16 (FME_BF16) or float (FME_FP32) [tokens x num_experts]
+ *   top_k      1 .. min(num_experts, 32); num_experts <= FME_MAX_GROUPS
+ *   bias       device float [num_experts] or NULL; steers the choice alone
+ *   ids        device int32 [tokens x top_k] (moe_route's topk_ids)
+ *   weights    device float [tokens x top_k] (moe_combine's weights)
+ */
+#define FME_BF16 0
+#define FME_FP32 1
+#define FME_SCORE_SOFTMAX 0
+#define FME_SCORE_SIGMOID 1
+fme_status moe_gate(const void *logits, int32_t dtype, int64_t tokens, int32_t num_experts, int32_t top_k, int32_t score,
+                    int32_t normalize, float scale, const float *bias, int32_t *ids, float *weights, void *stream);
+
+/* moe_gate_backward -- d_logits [tokens x num_experts], in the logits' type, from d_weights
+ * float [tokens x top_k] and the forward's ids (distinct within a token); every element is
+ * written, experts that were not chosen get 0 (softmax without normalize: their share).  An id
+ * outside [0, num_experts) sets FME_DEV_BAD_INDEX and is left out. */
+fme_status moe_gate_backward(const void *logits, int32_t dtype, const int32_t *ids, const float *d_weights,
+                             int64_t tokens, int32_t num_experts, int32_t top_k, int32_t score, int32_t normalize,
+                             float scale, void *d_logits, int32_t *dev_status, void *stream);
+
+/*
+ * moe_balance_loss -- sequence-wise load balance of the routed tokens.
+ *
+ * p[t, :] = softmax of the token's logits, or its sigmoids divided by their sum.  With T_q
+ * counted tokens in sequence q, count[q, e] of their choices going to expert e, and S
+ * sequences with tokens:
+ *   loss = alpha / S  sum_q  E / (top_k T_q^2)  sum_e count[q, e] sum_t p[t, e]
+ * (1 x alpha when the choices and probabilities are uniform); 0 without any counted token.
+ *
+ *   ids          device int32 [tokens x top_k]; one outside [0, num_experts) is not
+ *                counted and sets FME_DEV_BAD_INDEX
+ *   seq_offsets  device int32 [num_seqs + 1], rising from 0 to tokens, or NULL (one sequence);
+ *                a malformed sequence counts no token and sets FME_DEV_BAD_OFFSETS
+ *   token_mask   device uint8 [tokens], non-zero = counted, or NULL (all); the logits and ids of
+ *                a token that is not counted are not used
+ *   loss         device float [1]
+ *   counts       device int32 [num_seqs x num_experts]
+ *   seq_tokens   device int32 [num_seqs], T_q
+ *   workspace    fme_balance_workspace_bytes(tokens, num_seqs, num_experts) bytes; any contents
+ * Every sum is made in a fixed order: the same inputs give the same bits.
+ */
+fme_status moe_balance_loss(const void *logits, int32_t dtype, const int32_t *ids, int64_t tokens, int32_t num_experts,
+                            int32_t top_k, int32_t score, float alpha, const int32_t *seq_offsets, int64_t num_seqs,
+                            const uint8_t *token_mask, float *loss, int32_t *counts, int32_t *seq_tokens,
+                            void *workspace, int64_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* moe_balance_loss_backward -- d_logits (in the logits' type) of d_loss float [1] times the
+ * loss; the counts are constants to it.  counts, seq_tokens: as moe_balance_loss wrote them for
+ * the same seq_offsets and mask.  Tokens that are not counted get 0.  With accumulate the
+ * gradient is added to d_logits (after moe_gate_backward), rounded once. */
+fme_status moe_balance_loss_backward(const void *logits, int32_t dtype, const int32_t *counts, const int32_t *seq_tokens,
+                                     const float *d_loss, int64_t tokens, int32_t num_experts, int32_t top_k,
+                                     int32_t score, float alpha, const int32_t *seq_offsets, int64_t num_seqs,
+                                     const uint8_t *token_mask, void *d_logits, int32_t accumulate, void *stream);
+
+/* moe_combine_backward -- the gradient of moe_combine: for every assignment (t, k) with row
+ * r = row_of[t, k] >= 0, d_y[r, :] = bf16(weights[t, k] d_out[t, :]) and d_weights[t, k] =
+ * sum_c d_out[t, c] y[r, c] (fp32).  An assignment without a row gets d_weights 0; rows of
+ * d_y that no assignment has are not written; row_of >= rows_y sets FME_DEV_BAD_INDEX.
+ * Sizes as moe_combine; y, d_y bf16 [rows_y x n], d_out bf16 [tokens x n]. */
+fme_status moe_combine_backward(const void *d_out, const void *y, int64_t rows_y, const int32_t *row_of,
+                                const float *weights, int64_t tokens, int32_t top_k, int64_t n, void *d_y,
+                                float *d_weights, int32_t *dev_status, void *stream);
+
+/* Bytes of moe_balance_loss's workspace. */
+int64_t fme_balance_workspace_bytes(int64_t tokens, int64_t num_seqs, int32_t num_experts);
 
 /* Rows of the padded scale layout for `rows` rows in `num_groups` groups: an
  * upper bound of 128 * sum ceil(n_g / 128) that needs no offsets. */
