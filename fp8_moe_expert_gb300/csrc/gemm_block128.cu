@@ -26,6 +26,9 @@
 //               barriers; one commit per two stages frees both;
 //   warp 1      allocates tensor memory; in the leader one thread issues the MMAs, a commit per
 //               block hands the accumulator to both CTAs' epilogues;
+//   warps 2-3   bring the blocks' scales into shared memory, one block each in turn (loads by
+//               the epilogue threads themselves, a few blocks ahead in registers, kept them
+//               waiting on the loads: 2.09 -> @@ ms for 65536 x 4096 x 7168);
 //   warps 4-11  epilogue: 32 rows x 128 columns each, sums in 128 registers a thread.
 #include <algorithm>
 
@@ -41,8 +44,10 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kGroupBars128 = 4;
 constexpr int kStageBytes128 = kABytes + kBBytes;
 constexpr int kStages128 = 6;
-constexpr int kColScaleBytes = 2 * 128 * 4;  // wgrad: two blocks' column scales of a warp
-constexpr int kStageOut = 8 * (kOutBoxBytes + kColScaleBytes);
+constexpr int kScaleWarp0 = 2;                // and 3
+constexpr int kScaleSlots = 4;                // blocks whose scales are in shared memory
+constexpr int kScaleSlotFloats = 128 + kBN;  // of the CTA's rows and the tile's columns (see scale_slot)
+constexpr int kStageOut = 8 * kOutBoxBytes + kScaleSlots * kScaleSlotFloats * 4;
 
 enum class Kind128 { kFwd, kDgrad, kWgrad };
 
@@ -51,6 +56,8 @@ struct Shared128 {
   uint64_t grp_done[kGroupBars128];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t sc_full[kScaleSlots];
+  uint64_t sc_empty[kScaleSlots];
   uint64_t drain;
   uint64_t peer_fills_bar;
   uint32_t peer_fills;
@@ -213,6 +220,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
   uint8_t *smem_a = smem;
   uint8_t *smem_b = smem_a + S * kABytes;
   uint8_t *smem_out = smem + S * kStageBytes128;
+  float *scales = reinterpret_cast<float *>(smem_out + 8 * kOutBoxBytes);
   int32_t *gmem = reinterpret_cast<int32_t *>(smem_out + kStageOut);
   const Tables tab{gmem, gmem + (p.num_experts + 1)};
 
@@ -265,6 +273,10 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.acc_full[i], 1);
       mbar_init(&s.acc_empty[i], kAccEmptyArrivals);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&s.sc_full[i], 1);
+      mbar_init(&s.sc_empty[i], 8);
     }
     mbar_init(&s.drain, 1);
     mbar_init(&s.peer_fills_bar, 1);
@@ -363,6 +375,61 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       }
       pair::commit_local(&s.drain);
       mbar_drain(&s.drain, 0);
+    } else if (warp >= kScaleWarp0) {
+      // ------------------------------------------------------------------ scales
+      // Forward, dgrad: slot[half][row] = scale of the row times that of the weight block of
+      // the column half.  wgrad: slot[0][row], then the tile's 256 column scales.
+      uint32_t g = 0;  // blocks so far; this warp takes every other one
+      bool stop = false;
+      const int64_t kb_count = (p.k + 127) >> 7;
+      const int64_t nb128 = (p.n + 127) >> 7;
+      for (int64_t t = pair_id; t < total && !stop; t += pairs) {
+        const Tile128 tl = tile128<K>(p, tab, t, rank);
+        const float *a = p.a_scale + (K == Kind128::kWgrad ? (tl.p0 >> 7) * p.m : int64_t(0)) + tl.row0;
+        for (int i = 0; i < tl.nk; ++i, ++g) {
+          if ((g & 1) != (warp & 1)) continue;
+          const uint32_t slot = g % kScaleSlots;
+          float *dst = scales + slot * kScaleSlotFloats;
+          float ra[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = lane + 32 * j;
+            ra[j] = r < tl.rows_valid ? __ldg(a + i * p.m + r) : 0.0f;
+          }
+          float cb[K == Kind128::kWgrad ? 8 : 2];
+          if constexpr (K == Kind128::kWgrad) {
+            const float *b = p.b_scale + ((tl.p0 >> 7) + i) * p.n + tl.col0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cb[j] = tl.col0 + lane + 32 * j < p.n ? __ldg(b + lane + 32 * j) : 0.0f;
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int64_t c = (tl.col0 >> 7) + h;
+              const int64_t at = K == Kind128::kFwd ? (tl.e * nb128 + c) * kb_count + i : (tl.e * kb_count + i) * nb128 + c;
+              cb[h] = c < nb128 ? __ldg(p.b_scale + at) : 0.0f;
+            }
+          }
+          if (!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (K == Kind128::kWgrad) {
+              dst[lane + 32 * j] = ra[j];
+            } else {
+              dst[lane + 32 * j] = ra[j] * cb[0];
+              dst[128 + lane + 32 * j] = ra[j] * cb[1];
+            }
+          }
+          if constexpr (K == Kind128::kWgrad) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[128 + lane + 32 * j] = cb[j];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.sc_full[slot]);
+        }
+      }
     }
   } else {
     // ----------------------------------------------------------------- epilogue
@@ -372,81 +439,28 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
     const int half = ew >> 2;       // column half of the tile
     const int r = q * 32 + lane;    // row of the CTA's 128
     uint8_t *stage_blk = smem_out + ew * kOutBoxBytes;
-    float *colsc = reinterpret_cast<float *>(smem_out + 8 * kOutBoxBytes + ew * kColScaleBytes);
     const uint32_t leader_empty[2] = {pair::map_to_rank(&s.acc_empty[0], 0), pair::map_to_rank(&s.acc_empty[1], 0)};
     const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
-    const int64_t kb_count = (p.k + 127) >> 7;   // contraction blocks (fwd, dgrad)
-    const int64_t nb128 = (p.n + 127) >> 7;      // output column blocks
     uint32_t g = 0;
     bool stop = false;
     for (int64_t t = pair_id; t < total && !stop; t += pairs) {
       const Tile128 tl = tile128<K>(p, tab, t, rank);
       const int c0 = tl.col0 + half * 128;
-      const bool valid = r < tl.rows_valid;
-      // scale of this thread's row for block i, and of the warp's columns
-      const float *sa_ptr;
-      int64_t sa_step;
-      if constexpr (K == Kind128::kWgrad) {
-        sa_ptr = p.a_scale + static_cast<int64_t>(tl.p0 >> 7) * p.m + tl.row0 + r;
-        sa_step = p.m;
-      } else {
-        sa_ptr = p.a_scale + tl.row0 + r;
-        sa_step = p.m;
-      }
-      const float *sb_ptr;
-      int64_t sb_step;
       const bool in_cols = c0 < p.n;
-      if constexpr (K == Kind128::kFwd) {
-        sb_ptr = p.b_scale + (tl.e * nb128 + (c0 >> 7)) * kb_count;
-        sb_step = 1;
-      } else if constexpr (K == Kind128::kDgrad) {
-        sb_ptr = p.b_scale + tl.e * kb_count * nb128 + (c0 >> 7);
-        sb_step = nb128;
-      } else {
-        sb_ptr = p.b_scale + static_cast<int64_t>(tl.p0 >> 7) * p.n + c0 + 4 * lane;
-        sb_step = p.n;
-      }
-      const bool lane_cols = c0 + 4 * lane < p.n;  // wgrad: n is a multiple of 16
-      auto load_a = [&](int i) { return valid && i < tl.nk ? __ldg(sa_ptr + i * sa_step) : 0.0f; };
-      auto load_b = [&](int i) { return in_cols && i < tl.nk ? __ldg(sb_ptr + i * sb_step) : 0.0f; };
-      auto load_b4 = [&](int i) {
-        return lane_cols && i < tl.nk ? __ldg(reinterpret_cast<const float4 *>(sb_ptr + i * sb_step))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-      };
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      // scales of the next blocks, on their way while this one is summed
-      float fa0 = load_a(0), fa1 = load_a(1), fa2 = load_a(2);
-      float fb0 = 0.f, fb1 = 0.f, fb2 = 0.f;
-      float4 fc0, fc1;
-      if constexpr (K == Kind128::kWgrad) {
-        fc0 = load_b4(0);
-        fc1 = load_b4(1);
-      } else {
-        fb0 = load_b(0);
-        fb1 = load_b(1);
-        fb2 = load_b(2);
-      }
 #pragma unroll 1
       for (int i = 0; i < tl.nk; ++i) {
         const uint32_t b = g & 1;
-        const float *cs = colsc + (i & 1) * 128;
-        float v = fa0;
-        if constexpr (K == Kind128::kWgrad) {
-          reinterpret_cast<float4 *>(colsc + (i & 1) * 128)[lane] = fc0;
-          fc0 = fc1;
-          fc1 = load_b4(i + 2);
-          __syncwarp();
-        } else {
-          v *= fb0;
-          fb0 = fb1;
-          fb1 = fb2;
-          fb2 = load_b(i + 3);
+        const uint32_t slot = g % kScaleSlots;
+        if (!mbar_wait(&s.sc_full[slot], (g / kScaleSlots) & 1, abort_flag, p.status)) {
+          stop = true;
+          break;
         }
-        fa0 = fa1;
-        fa1 = fa2;
-        fa2 = load_a(i + 3);
+        const float *sc = scales + slot * kScaleSlotFloats;
+        const float *cs = sc + 128 + half * 128;  // wgrad
+        const float v = K == Kind128::kWgrad ? sc[r] : sc[half * 128 + r];
         const float2 f = make_float2(v, v);
         if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) {
           stop = true;
@@ -479,6 +493,8 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
         __syncwarp();
         if (lane == 0) pair::arrive_remote_relaxed(leader_empty[b]);
         add(3, vb);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.sc_empty[slot]);
         ++g;
       }
       if (stop) break;
