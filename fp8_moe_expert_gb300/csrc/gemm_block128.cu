@@ -23,7 +23,7 @@
 // multiples of 16.  No split over the contraction: a row's result does not depend on the
 // other rows.  12 warps a CTA:
 //   warp 0      TMA producer: A and B into a ring of 32 KB stages, completing on the leader's
-//               barriers; one commit per two stages frees both;
+//               barriers; the epilogue frees a stage when it sees the block's MMAs done;
 //   warp 1      allocates tensor memory; in the leader one thread issues the MMAs, a commit per
 //               block hands the accumulator to both CTAs' epilogues;
 //   warps 2-3   bring the blocks' scales into shared memory, one block each in turn (loads by
@@ -41,7 +41,6 @@ namespace {
 
 constexpr int kThreads128 = 384;
 constexpr int kEpiWarp0 = 4;
-constexpr int kGroupBars128 = 4;
 constexpr int kStageBytes128 = kABytes + kBBytes;
 constexpr int kStages128 = 6;
 constexpr int kScaleWarp0 = 2;                // and 3
@@ -53,7 +52,7 @@ enum class Kind128 { kFwd, kDgrad, kWgrad };
 
 struct Shared128 {
   uint64_t full[kStages128];
-  uint64_t grp_done[kGroupBars128];
+  uint64_t freed[kStages128];  // the stage's MMAs are done (own CTA)
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t sc_full[kScaleSlots];
@@ -66,16 +65,38 @@ struct Shared128 {
   int ok_flag;
 };
 
-// D = A B^T (+ D), E4M3 x E4M3 -> fp32, M = 256 over the pair.
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// One block of 128 of the contraction: D = A B^T over four K = 32 steps, E4M3 x E4M3 -> fp32,
+// M = 256 over the pair, then a commit to the barrier at the same shared address in both CTAs.
+// kA, kB: distance of the steps in the operands' descriptors (16-byte units).  One asm statement,
+// issued by one elected lane of a converged warp: as single MMAs under `lane == 0` the issuing
+// thread itself took about 900 cycles a block, more than the MMAs.
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void mma_block(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred z, o;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.u32 z, 0, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
+      "add.s64 a1, %1, %5;\n\tadd.s64 a2, %1, 2 * %5;\n\tadd.s64 a3, %1, 3 * %5;\n\t"
+      "add.s64 b1, %2, %6;\n\tadd.s64 b2, %2, 2 * %6;\n\tadd.s64 b3, %2, 3 * %6;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, z;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, o;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, o;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, o;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %7;\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(smem_u32(bar)), "n"(kA), "n"(kB), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-      "}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 
 // Instruction descriptor: fp32 accumulator (bit 4), E4M3 operands (0), the operands'
@@ -268,8 +289,10 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
     }
   }
   if (threadIdx.x == 32) {
-    for (int i = 0; i < S; ++i) mbar_init(&s.full[i], 1);
-    for (int i = 0; i < kGroupBars128; ++i) mbar_init(&s.grp_done[i], 1);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.freed[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.acc_full[i], 1);
       mbar_init(&s.acc_empty[i], kAccEmptyArrivals);
@@ -316,12 +339,9 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       for (int64_t t = pair_id; t < total && !stop; t += pairs) {
         const Tile128 tl = tile128<K>(p, tab, t, rank);
         for (int i = 0; i < tl.nk; ++i) {
-          if (filled >= S) {
-            const uint32_t c = (filled - S) >> 1;
-            if (!mbar_wait<true>(&s.grp_done[c % kGroupBars128], (c / kGroupBars128) & 1, abort_flag, p.status)) {
-              stop = true;
-              break;
-            }
+          if (!mbar_wait<true>(&s.freed[stage], ((filled / S) & 1) ^ 1, abort_flag, p.status)) {
+            stop = true;
+            break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytes128);
           const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
@@ -343,29 +363,28 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       }
       const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
       if (rank == 0) drain_pair_ring(s.full, S, filled, peer, kStageBytes128);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-      // ---------------------------------------------------- MMA issuer (leader)
+    } else if (warp == 1 && rank == 0) {
+      // ------------------------------------------- MMA issuer (leader, whole warp)
       constexpr uint32_t idesc = idesc_f8(kAmn, kBmn);
+      const uint64_t a_desc = desc_sw128(smem_u32(smem_a), kAmn), b_desc = desc_sw128(smem_u32(smem_b), kBmn);
       uint32_t stage = 0, phase = 0, fill = 0;
       bool stop = false;
       for (int64_t t = pair_id; t < total && !stop; t += pairs) {
         const int nk = tile128<K>(p, tab, t, 0).nk;
         for (int i = 0; i < nk; ++i) {
           const uint32_t b = fill & 1;
-          if (!mbar_wait<true>(&s.acc_empty[b], ((fill >> 1) & 1) ^ 1, abort_flag, p.status) ||
-              !mbar_wait<true>(&s.full[stage], phase, abort_flag, p.status)) {
+          if (!mbar_wait(&s.full[stage], phase, abort_flag, p.status) ||
+              !mbar_wait(&s.acc_empty[b], ((fill >> 1) & 1) ^ 1, abort_flag, p.status)) {
             stop = true;
-            break;
           }
+          stop = __any_sync(0xFFFFFFFFu, stop);
+          if (stop) break;
           tc_fence_after();
-          const uint32_t a_s = smem_u32(smem_a + stage * kABytes);
-          const uint32_t b_s = smem_u32(smem_b + stage * kBBytes);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 of K: 32 bytes along a K-major row, 32 rows of an MN-major tile
-            mma_f8(tmem + b * kBN, desc_sw128(a_s + kk * (kAmn ? 4096 : 32), kAmn),
-                   desc_sw128(b_s + kk * (kBmn ? 4096 : 32), kBmn), idesc, kk > 0);
-          pair::commit_both(&s.acc_full[b]);
-          if (fill & 1) pair::commit_both(&s.grp_done[(fill >> 1) % kGroupBars128]);
+          // 32 of K: 32 bytes along a K-major row, 32 rows of an MN-major tile
+          if (elect_one())
+            mma_block<(kAmn ? 4096 : 32) / 16, (kBmn ? 4096 : 32) / 16>(
+                tmem + b * kBN, a_desc + stage * (kABytes / 16), b_desc + stage * (kBBytes / 16), idesc, &s.acc_full[b]);
+          __syncwarp();
           ++fill;
           if (++stage == S) {
             stage = 0;
@@ -373,8 +392,12 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
           }
         }
       }
-      pair::commit_local(&s.drain);
-      mbar_drain(&s.drain, 0);
+      __syncwarp();
+      if (elect_one()) {
+        pair::commit_local(&s.drain);
+        mbar_drain(&s.drain, 0);
+      }
+      __syncwarp();
     } else if (warp >= kScaleWarp0) {
       // ------------------------------------------------------------------ scales
       // Forward, dgrad: slot[half][row] = scale of the row times that of the weight block of
@@ -466,6 +489,8 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
           stop = true;
           break;
         }
+        // the block's MMAs are done: its operands' stage is free
+        if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
         tc_fence_after();
         auto add = [&](int c, const uint32_t(&d)[32]) {
 #pragma unroll
