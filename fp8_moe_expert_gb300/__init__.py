@@ -63,6 +63,8 @@ def ensure_built() -> str:
 def lib() -> ctypes.CDLL:
     """The loaded CUDA library.  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIBRARY):
@@ -152,15 +154,16 @@ def route_workspace_bytes(tokens: int, top_k: int, num_experts: int) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
 
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    # the current device's current stream, without a Stream object (3 us a call on a Grace core)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(status: int, where: str):

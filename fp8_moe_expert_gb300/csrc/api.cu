@@ -930,7 +930,7 @@ BalanceWorkspace balance_workspace(int64_t tokens, int64_t num_seqs, int32_t num
   w.counts = w.sums + round16(parts * num_experts * 4);
   w.tokens = w.counts + round16(parts * num_experts * 4);
   w.term = w.tokens + round16(parts * 4);
-  w.done = w.term + round16(num_seqs * 4);
+  w.done = w.term + round16(num_seqs * ((num_experts + 31) / 32) * 4);
   w.bytes = w.done + 16;
   return w;
 }
@@ -1014,7 +1014,7 @@ fme_status moe_balance_loss(const void *logits, int32_t dtype, const int32_t *id
   fme_status st = check_router(tokens, num_experts, top_k, dtype, score);
   if (st != FME_OK) return st;
   if (num_seqs < 1 || (!seq_offsets && num_seqs != 1)) return FME_ERR_INVALID_ARGUMENT;
-  if (num_seqs > (int64_t(1) << 24)) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (num_seqs > (int64_t(1) << 24)) return FME_ERR_UNSUPPORTED_SHAPE;  // CTAs: times ceil(1024 / 32)
   if (!loss || !counts || !seq_tokens || !workspace || (tokens > 0 && (!logits || !ids))) return FME_ERR_INVALID_ARGUMENT;
   const BalanceWorkspace w = balance_workspace(tokens, num_seqs, num_experts);
   if (workspace_bytes < w.bytes) return FME_ERR_INVALID_ARGUMENT;

@@ -20,8 +20,9 @@
 //   a_e = dL alpha / S  E / (K T_q^2) count_qe,   softmax: dl_e = p_e (a_e - sum_j p_j a_j),
 //   sigmoid: dl_e = s_e (1 - s_e) / Z (a_e - sum_j p_j a_j).
 //
-// One warp a token, expert e in lane e % 32, so that loads are contiguous; all sums fp32.
-// Reads the logits once: HBM-bound when there are many tokens, launch-bound when few.
+// One warp a token, V experts a lane, VEC of them neighbours (one load of up to 16 bytes); all
+// sums fp32.  Reads the logits once.  Few tokens: launch-bound.  Many: the instructions of the
+// selection and of the exponentials, a few hundred a token, take longer than its bytes.
 #include "block128.cuh"
 
 namespace fme {
@@ -31,10 +32,57 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kGateWarps = 8;
 
-__device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
-__device__ __forceinline__ float load_logit(const __nv_bfloat16 *p) { return __bfloat162float(__ldg(p)); }
-__device__ __forceinline__ void store_grad(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_grad(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_float(float v) {
+  if constexpr (sizeof(T) == 2)
+    return __float2bfloat16_rn(v);
+  else
+    return v;
+}
+
+template <typename T, int VEC>
+struct alignas(VEC * sizeof(T)) Pack {
+  T v[VEC];
+};
+
+// Expert of a lane's j-th value.
+template <int VEC>
+__device__ __forceinline__ int expert_of(int j, int lane) {
+  return (j / VEC) * (32 * VEC) + lane * VEC + j % VEC;
+}
+
+// A token's row, V values a lane; -inf past the experts (a multiple of VEC).
+template <typename T, int V, int VEC>
+__device__ __forceinline__ void load_row(const T *row, int experts, int lane, float (&l)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += VEC) {
+    const int e = expert_of<VEC>(j, lane);
+    if (e < experts) {
+      const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC> *>(row + e);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) l[j + c] = to_float(p.v[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) l[j + c] = -INFINITY;
+    }
+  }
+}
+
+template <typename T, int V, int VEC>
+__device__ __forceinline__ void store_row(T *row, int experts, int lane, const float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; j += VEC) {
+    const int e = expert_of<VEC>(j, lane);
+    if (e < experts) {
+      Pack<T, VEC> p;
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) p.v[c] = from_float<T>(v[j + c]);
+      *reinterpret_cast<Pack<T, VEC> *>(row + e) = p;
+    }
+  }
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -47,20 +95,30 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+// sigmoid(l) and 1 - sigmoid(l) = sigmoid(-l) from one exponential that cannot overflow,
+// t = e^-|l|: 1 / (1 + t) and t / (1 + t).
+__device__ __forceinline__ void sigmoids(float l, float &s, float &rest) {
+  const float t = __expf(-fabsf(l));
+  const float r = rcp_approx(1.0f + t);
+  s = l != l ? l : l >= 0.0f ? r : t * r;
+  rest = l != l ? l : l >= 0.0f ? t * r : r;
+}
+__device__ __forceinline__ float sigmoid(float l) {
+  float s, rest;
+  sigmoids(l, s, rest);
+  return s;
+}
 
-// Order of keys as unsigned integers: larger float, larger integer; -0 as +0; a NaN counts as
-// the lowest.  0 is below every key (no expert here, or already taken).
+// Order of keys as unsigned integers: larger float, larger integer, none 0; -0 as +0, a NaN as -inf.
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f != f) return 1u;
-  const uint32_t b = __float_as_uint(f + 0.0f);
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  const int32_t b = __float_as_int(fmaxf(f, -INFINITY) + 0.0f);
+  return static_cast<uint32_t>(b) ^ (static_cast<uint32_t>(b >> 31) | 0x80000000u);
 }
 
 // exp(l - max) of a row held V values a lane; a row without a finite maximum gets zeros (all
 // -inf: nothing is left of the row) or NaN (+inf or NaN among them).
 template <int V>
-__device__ __forceinline__ float exp_row(const float (&l)[V], float (&x)[V], int experts, int lane) {
+__device__ __forceinline__ float exp_row(const float (&l)[V], float (&x)[V]) {
   float m = -INFINITY, bad = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -71,81 +129,121 @@ __device__ __forceinline__ float exp_row(const float (&l)[V], float (&x)[V], int
   float sum = bad;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    x[j] = m == -INFINITY ? 0.0f : expf(l[j] - m);
-    if (lane + 32 * j < experts) sum += x[j];
+    x[j] = m == -INFINITY ? 0.0f : __expf(l[j] - m);  // lanes past the experts hold -inf
+    sum += x[j];
   }
   return warp_sum(sum);
 }
 
-template <typename T, int V>
+template <typename T, int V, int VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const T *__restrict__ logits, int64_t tokens,
                                                                int experts, int top_k, bool softmax, bool normalize,
                                                                float scale, const float *__restrict__ bias,
                                                                int32_t *__restrict__ ids,
                                                                float *__restrict__ weights) {
+  // candidates: key, then the lower expert first
+  __shared__ uint64_t cand[kGateWarps][32];
   const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   if (t >= tokens) return;
+  const T *row = logits + t * experts;
   float l[V];
+  load_row<T, V, VEC>(row, experts, lane, l);
+  float denom = 1.0f, m_all = 0.0f;  // softmax over all experts, only where the weights need it
+  if (softmax && !normalize) {
+    float x[V];
+    denom = exp_row<V>(l, x);
+    m_all = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < V; ++j) m_all = fmaxf(m_all, l[j]);
+    m_all = warp_max(m_all);
+  }
   uint32_t key[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = lane + 32 * j;
-    l[j] = e < experts ? load_logit(logits + t * experts + e) : -INFINITY;
-    key[j] = e < experts ? order_key(bias ? l[j] + __ldg(bias + e) : l[j]) : 0u;
+    const int e = expert_of<VEC>(j, lane);
+    if (bias && e < experts) l[j] += __ldg(bias + e);
+    key[j] = e < experts ? order_key(l[j]) : 0u;
   }
-  float denom = 1.0f;  // softmax over all experts, only where the weights need it
-  float m = 0.0f;
-  if (softmax && !normalize) {
-    float x[V];
-    denom = exp_row<V>(l, x, experts, lane);
-    m = -INFINITY;
+  // A lower bound of the top_k-th key: the top_k-th largest of the lanes' largest keys (equal ones
+  // taken together, which only lowers it).
+  uint32_t bound = 1;
+  if constexpr (V > 1) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
-    m = warp_max(m);
+    for (int j = 0; j < V; ++j) m = max(m, key[j]);
+    for (int i = 0; i < top_k; ++i) {
+      bound = __reduce_max_sync(kAll, m);
+      if (m == bound) m = 0;
+    }
+    bound = max(bound, 1u);
   }
-  int my_id = 0;
-  float my_l = -INFINITY;
-  for (int i = 0; i < top_k; ++i) {
-    uint32_t best = 0;
+  // The keys at or above it, in any order: how many in the lanes before this one, by the bits of
+  // the lanes' counts.
+  int mine_n = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) best = max(best, key[j]);
-    best = __reduce_max_sync(kAll, best);
-    int at = INT32_MAX;
+  for (int j = 0; j < V; ++j) mine_n += key[j] >= bound ? 1 : 0;
+  int at = 0, n = 0;
 #pragma unroll
-    for (int j = V - 1; j >= 0; --j)
-      if (key[j] == best) at = lane + 32 * j;
-    at = __reduce_min_sync(kAll, at);
-    float lv = 0.0f;
+  for (int b = 1; b <= V; b <<= 1) {
+    const uint32_t has = __ballot_sync(kAll, mine_n & b);
+    at += __popc(has & ((1u << lane) - 1)) * b;
+    n += __popc(has) * b;
+  }
+  int pos = top_k, my_id = 0;  // this lane's choice: number and expert; none if pos >= top_k
+  if (n <= 32) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (at == lane + 32 * j) {
-        key[j] = 0;
-        lv = l[j];
+      if (key[j] >= bound)
+        cand[warp][at++] = (static_cast<uint64_t>(key[j]) << 32) | static_cast<uint32_t>(~expert_of<VEC>(j, lane));
+    __syncwarp();
+    // every candidate counts those before it
+    if (lane < n) {
+      const uint64_t me = cand[warp][lane];
+      pos = 0;
+#pragma unroll 4
+      for (int q = 0; q < n; ++q) pos += cand[warp][q] > me ? 1 : 0;
+      my_id = static_cast<int>(~static_cast<uint32_t>(me));
+    }
+  } else {
+    // many equal keys: one choice after the other
+    for (int i = 0; i < top_k; ++i) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) best = max(best, key[j]);
+      best = __reduce_max_sync(kAll, best);
+      int e = INT32_MAX;
+#pragma unroll
+      for (int j = V - 1; j >= 0; --j)
+        if (key[j] == best) e = expert_of<VEC>(j, lane);
+      e = __reduce_min_sync(kAll, e);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (e == expert_of<VEC>(j, lane)) key[j] = 0;
+      if (lane == i) {
+        pos = i;
+        my_id = e;
       }
-    lv = __shfl_sync(kAll, lv, at & 31);
-    if (lane == (i & 31)) {
-      my_id = at;
-      my_l = lv;
     }
   }
-  // lane i holds choice i (top_k <= 32)
-  const bool mine = lane < top_k;
+  const bool mine = pos < top_k;
+  const float my_l = mine ? to_float(row[my_id]) : -INFINITY;  // without the bias
   float s;
   if (softmax) {
-    const float ref = normalize ? warp_max(mine ? my_l : -INFINITY) : m;
-    s = !mine ? 0.0f : my_l != my_l ? my_l : ref == -INFINITY ? 0.0f : expf(my_l - ref);
+    const float ref = normalize ? warp_max(my_l) : m_all;
+    s = !mine ? 0.0f : my_l != my_l ? my_l : ref == -INFINITY ? 0.0f : __expf(my_l - ref);
   } else {
     s = mine ? sigmoid(my_l) : 0.0f;
   }
   if (normalize) denom = warp_sum(s);
   if (mine) {
-    ids[t * top_k + lane] = my_id;
-    weights[t * top_k + lane] = denom == 0.0f ? 0.0f : scale * s / denom;
+    ids[t * top_k + pos] = my_id;
+    weights[t * top_k + pos] = denom == 0.0f ? 0.0f : scale * s / denom;
   }
 }
 
-template <typename T, int V>
+template <typename T, int V, int VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_kernel(
     const T *__restrict__ logits, const int32_t *__restrict__ ids, const float *__restrict__ d_weights, int64_t tokens,
     int experts, int top_k, bool softmax, bool normalize, float scale, T *__restrict__ d_logits, int32_t *status) {
@@ -161,32 +259,28 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_kernel(
   }
   const bool live = id >= 0;
   const float g = live ? scale * __ldg(d_weights + t * top_k + lane) : 0.0f;
-  const float my_l = live ? load_logit(row + id) : -INFINITY;
+  const float my_l = live ? to_float(row[id]) : -INFINITY;
   float l[V], x[V];
   float d_mine, inner = 0.0f, denom = 1.0f;
   if (softmax && !normalize) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = lane + 32 * j;
-      l[j] = e < experts ? load_logit(row + e) : -INFINITY;
-    }
-    denom = exp_row<V>(l, x, experts, lane);
+    load_row<T, V, VEC>(row, experts, lane, l);
+    denom = exp_row<V>(l, x);
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
     m = warp_max(m);
-    const float p = !live ? 0.0f : denom == 0.0f ? 0.0f : expf(my_l - m) / denom;
+    const float p = !live ? 0.0f : denom == 0.0f ? 0.0f : __expf(my_l - m) / denom;
     inner = warp_sum(p * g);
     d_mine = g;  // times p_e below
   } else if (softmax) {
     const float ref = warp_max(my_l);
-    const float s = !live || ref == -INFINITY ? 0.0f : expf(my_l - ref);
+    const float s = !live || ref == -INFINITY ? 0.0f : __expf(my_l - ref);
     const float total = warp_sum(s);
     const float p = total == 0.0f ? 0.0f : s / total;
     d_mine = p * (g - warp_sum(p * g));
   } else {
-    const float s = live ? sigmoid(my_l) : 0.0f;
-    const float rest = live ? sigmoid(-my_l) : 0.0f;
+    float s = 0.0f, rest = 0.0f;
+    if (live) sigmoids(my_l, s, rest);
     if (normalize) {
       const float total = warp_sum(s);
       const float mean = total == 0.0f ? 0.0f : warp_sum(s * g) / total;
@@ -195,56 +289,55 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_kernel(
       d_mine = g * s * rest;
     }
   }
-  float out[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) out[j] = 0.0f;
-  for (int i = 0; i < top_k; ++i) {
-    const int e = __shfl_sync(kAll, id, i);
-    const float v = __shfl_sync(kAll, d_mine, i);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (e == lane + 32 * j) out[j] = v;
-  }
+  T *out_row = d_logits + t * experts;
   if (softmax && !normalize) {
+    // every expert has its share: -p_e sum_j p_j g_j, and p_e g_e where it was chosen
+    const float r = denom == 0.0f ? 0.0f : 1.0f / denom;
 #pragma unroll
-    for (int j = 0; j < V; ++j) out[j] = denom == 0.0f ? 0.0f : x[j] / denom * (out[j] - inner);
-  }
+    for (int j = 0; j < V; ++j) l[j] = 0.0f;  // the choices' g
+    for (int i = 0; i < top_k; ++i) {
+      const int e = __shfl_sync(kAll, id, i);
+      const float v = __shfl_sync(kAll, d_mine, i);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane + 32 * j;
-    if (e < experts) store_grad(d_logits + t * experts + e, out[j]);
+      for (int j = 0; j < V; ++j)
+        if (e == expert_of<VEC>(j, lane)) l[j] = v;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = x[j] * r * (l[j] - inner);
+    store_row<T, V, VEC>(out_row, experts, lane, l);
+    return;
   }
+  // zeros, then the choices' values over them
+  float zero[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) zero[j] = 0.0f;
+  store_row<T, V, VEC>(out_row, experts, lane, zero);
+  __syncwarp();
+  if (live) out_row[id] = from_float<T>(d_mine);
 }
 
 // ------------------------------------------------------------- balance loss --
 // Probabilities of one token's row, V a lane; also s and 1 - s scaled for the gradient.
-template <typename T, int V>
-__device__ __forceinline__ void probabilities(const T *row, int experts, int lane, bool softmax, float (&p)[V],
-                                              float (&slope)[V]) {
-  float l[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane + 32 * j;
-    l[j] = e < experts ? load_logit(row + e) : -INFINITY;
-  }
+template <int V>
+__device__ __forceinline__ void probabilities(const float (&l)[V], bool softmax, float (&p)[V], float (&slope)[V]) {
   if (softmax) {
-    const float z = exp_row<V>(l, p, experts, lane);
+    const float z = exp_row<V>(l, p);
     const float r = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
     for (int j = 0; j < V; ++j) slope[j] = p[j] = p[j] * r;
   } else {
-    float z = 0.0f;
+    float z = 0.0f;  // lanes past the experts hold -inf: sigmoid 0
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      p[j] = lane + 32 * j < experts ? sigmoid(l[j]) : 0.0f;
+      sigmoids(l[j], p[j], slope[j]);
       z += p[j];
     }
     z = warp_sum(z);
     const float r = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      slope[j] = lane + 32 * j < experts ? p[j] * sigmoid(-l[j]) * r : 0.0f;
       p[j] *= r;
+      slope[j] *= p[j];
     }
   }
 }
@@ -253,7 +346,7 @@ __device__ __forceinline__ void probabilities(const T *row, int experts, int lan
 // the workspace, [sequence][slice][experts] each.  The order of every sum is fixed.
 constexpr int kPartWarps = 16;
 
-template <typename T, int V>
+template <typename T, int V, int VEC>
 __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(LaunchBalance a) {
   extern __shared__ float smem[];  // [kPartWarps / 2][experts] sums, then [experts] counts
   constexpr int kHalf = kPartWarps / 2;
@@ -280,10 +373,16 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
 #pragma unroll
   for (int j = 0; j < V; ++j) sum[j] = 0.0f;
   int mine = 0;
+  const T *logits = static_cast<const T *>(a.logits);
+  float next[V];  // the next token's row, loaded while this one is summed
+  if (t0 + warp < t1) load_row<T, V, VEC>(logits + (t0 + warp) * experts, experts, lane, next);
   for (int64_t t = t0 + warp; t < t1; t += kPartWarps) {
+    float l[V], p[V], slope[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = next[j];
+    if (t + kPartWarps < t1) load_row<T, V, VEC>(logits + (t + kPartWarps) * experts, experts, lane, next);
     if (a.token_mask && !__ldg(a.token_mask + t)) continue;
-    float p[V], slope[V];
-    probabilities<T, V>(static_cast<const T *>(a.logits) + t * experts, experts, lane, a.softmax, p, slope);
+    probabilities<V>(l, a.softmax, p, slope);
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] += p[j];
     ++mine;
@@ -299,13 +398,13 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
   if (warp >= kHalf) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (lane + 32 * j < experts) smem[(warp - kHalf) * experts + lane + 32 * j] = sum[j];
+      if (expert_of<VEC>(j, lane) < experts) smem[(warp - kHalf) * experts + expert_of<VEC>(j, lane)] = sum[j];
   }
   __syncthreads();
   if (warp < kHalf) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (lane + 32 * j < experts) smem[warp * experts + lane + 32 * j] += sum[j];
+      if (expert_of<VEC>(j, lane) < experts) smem[warp * experts + expert_of<VEC>(j, lane)] += sum[j];
   }
   __syncthreads();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * experts;
@@ -319,6 +418,11 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
   if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = n_tokens;
 }
 
+// Launched with programmatic serialization: starts while the kernel before it ends, and waits
+// here for all of its writes.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Sum over a CTA of 1024 threads, in every thread.
 __device__ __forceinline__ float block_sum(float v, float *part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   v = warp_sum(v);
@@ -328,193 +432,238 @@ __device__ __forceinline__ float block_sum(float v, float *part) {
   return warp_sum(part[lane]);
 }
 
-// One CTA of 1024 threads a sequence: thread (part, e) adds every parts-th slice, the parts are
-// added in order; then the sequence's term.  The last CTA to finish adds the terms.
+// One CTA for 32 experts of a sequence: lane = expert, each warp adds every 32nd slice, the warps'
+// sums are added in order; then the experts' part of the sequence's term.  The last CTA to finish adds
+// all parts in order.
 __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
-  __shared__ float sums[1024];
-  __shared__ int32_t cnts[1024];
+  __shared__ float sums[32][33];
+  __shared__ int32_t cnts[32][33];
   __shared__ float red[32];
   __shared__ int last;
   __shared__ int32_t total_tokens;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int experts = a.num_experts;
-  const int width = (experts + 31) & ~31;
-  const int parts = 1024 / width;
-  const int64_t s = blockIdx.x;
-  const int e = tid % width, part = tid / width;
+  const int groups = (experts + 31) >> 5;
+  const int64_t s = blockIdx.x / groups;
+  const int e = static_cast<int>(blockIdx.x - s * groups) * 32 + lane;
+  if (tid == 0) total_tokens = 0;
+  wait_for_previous_kernel();
   float v = 0.0f;
   int32_t c = 0;
-  if (part < parts && e < experts) {
-#pragma unroll 8
-    for (int i = part; i < a.slices; i += parts) {
+  if (e < experts) {
+#pragma unroll 4
+    for (int i = warp; i < a.slices; i += 32) {
       const int64_t at = (s * a.slices + i) * experts + e;
       v += a.part_sum[at];
       c += a.part_count[at];
     }
   }
-  sums[tid] = v;
-  cnts[tid] = c;
+  sums[warp][lane] = v;
+  cnts[warp][lane] = c;
   int32_t n = 0;
   for (int i = tid; i < a.slices; i += 1024) n += a.part_tokens[s * a.slices + i];
-  if (tid == 0) total_tokens = 0;
   __syncthreads();
   if (n) atomicAdd(&total_tokens, n);
-  float term = 0.0f;
-  if (tid < experts) {
+  __syncthreads();
+  if (warp == 0) {
     v = 0.0f;
     c = 0;
-    for (int i = 0; i < parts; ++i) {
-      v += sums[i * width + tid];
-      c += cnts[i * width + tid];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v += sums[i][lane];
+      c += cnts[i][lane];
     }
-    a.counts[s * experts + tid] = c;
-    term = static_cast<float>(c) * v;
-  }
-  term = block_sum(term, red);
-  if (tid == 0) {
-    const int32_t t = total_tokens;
-    const float tf = static_cast<float>(t);
-    a.seq_tokens[s] = t;
-    a.term[s] = t > 0 ? term / tf * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tf)) : 0.0f;
-    __threadfence();
-    last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+    if (e < experts) a.counts[s * experts + e] = c;
+    const float term = warp_sum(e < experts ? static_cast<float>(c) * v : 0.0f);
+    if (lane == 0) {
+      const int32_t t = total_tokens;
+      const float tf = static_cast<float>(t);
+      if (e < 32) a.seq_tokens[s] = t;
+      a.term[blockIdx.x] = t > 0 ? term / tf * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tf)) : 0.0f;
+      __threadfence();
+      last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+    }
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
   float all = 0.0f, live = 0.0f;
-  for (int64_t i = tid; i < a.num_seqs; i += 1024) {
-    all += __ldcg(a.term + i);
-    live += __ldcg(a.seq_tokens + i) > 0 ? 1.0f : 0.0f;
-  }
+  for (int64_t i = tid; i < gridDim.x; i += 1024) all += __ldcg(a.term + i);
+  for (int64_t i = tid; i < a.num_seqs; i += 1024) live += __ldcg(a.seq_tokens + i) > 0 ? 1.0f : 0.0f;
   all = block_sum(all, red);
   live = block_sum(live, red);
   if (tid == 0) a.loss[0] = live > 0.0f ? a.alpha * all / live : 0.0f;
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * kGateWarps) balance_backward_kernel(LaunchBalance a) {
+// A warp takes `per_warp` consecutive tokens; the sequence's coefficients stay in registers from
+// one token to the next.
+template <typename T, int V, int VEC>
+__global__ void __launch_bounds__(32 * kGateWarps) balance_backward_kernel(LaunchBalance a, int per_warp) {
   const int lane = threadIdx.x & 31;
   const int experts = a.num_experts;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
-  // sequences with tokens
-  int live = 0;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5)) * per_warp;
+  if (t0 >= a.tokens) return;
+  const int64_t t1 = min(a.tokens, t0 + per_warp);
+  const T *logits = static_cast<const T *>(a.logits);
+  float l[V], w[V];
+  load_row<T, V, VEC>(logits + t0 * experts, experts, lane, l);
+  int live = 0;  // sequences with tokens
   for (int64_t s = lane; s < a.num_seqs; s += 32) live += __ldg(a.seq_tokens + s) > 0;
   live = __reduce_add_sync(kAll, live);
-  if (t >= a.tokens) return;
-  int64_t seq = 0;
-  if (a.seq_offsets) {  // the last sequence that starts at or before t
+  // the last sequence that starts at or before t0: halving down to 32, then all at once
+  int64_t seq = 0, next_start = a.tokens;
+  if (a.seq_offsets) {
     int64_t lo = 0, hi = a.num_seqs;
-    while (hi - lo > 1) {
+    while (hi - lo > 32) {
       const int64_t mid = (lo + hi) >> 1;
-      if (__ldg(a.seq_offsets + mid) <= t)
+      if (__ldg(a.seq_offsets + mid) <= t0)
         lo = mid;
       else
         hi = mid;
     }
-    seq = lo;
+    const int64_t mine = lo + 1 + lane;
+    seq = lo + __popc(__ballot_sync(kAll, mine < hi && __ldg(a.seq_offsets + mine) <= t0));
+    next_start = seq + 1 < a.num_seqs ? __ldg(a.seq_offsets + seq + 1) : a.tokens;
   }
-  T *out = static_cast<T *>(a.d_logits) + t * experts;
-  const bool on = !a.token_mask || __ldg(a.token_mask + t);
-  const int32_t n = __ldg(a.seq_tokens + seq);
-  if (!on || n <= 0) {
-    if (!a.accumulate)
-      for (int e = lane; e < experts; e += 32) store_grad(out + e, 0.0f);
-    return;
-  }
-  const float tn = static_cast<float>(n);
-  const float c = __ldg(a.d_loss) * a.alpha / static_cast<float>(live) *
-                  (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tn)) / tn;
-  float p[V], slope[V], w[V];
-  probabilities<T, V>(static_cast<const T *>(a.logits) + t * experts, experts, lane, a.softmax, p, slope);
-  float dot = 0.0f;
+  const float up = __ldg(a.d_loss) * a.alpha / static_cast<float>(live);
+  int64_t loaded = -1;  // the sequence that w belongs to
+  for (int64_t t = t0; t < t1; ++t) {
+    while (t >= next_start && seq + 1 < a.num_seqs) {
+      ++seq;
+      next_start = seq + 1 < a.num_seqs ? __ldg(a.seq_offsets + seq + 1) : a.tokens;
+    }
+    const int32_t n = __ldg(a.seq_tokens + seq);
+    if (seq != loaded) {
+      const float tn = static_cast<float>(n);
+      const float c = n > 0 ? up * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tn)) / tn : 0.0f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane + 32 * j;
-    w[j] = e < experts ? c * static_cast<float>(__ldg(a.counts + seq * experts + e)) : 0.0f;
-    dot += p[j] * w[j];
-  }
-  dot = warp_sum(dot);
+      for (int j = 0; j < V; ++j) {
+        const int e = expert_of<VEC>(j, lane);
+        w[j] = e < experts ? c * static_cast<float>(__ldg(a.counts + seq * experts + e)) : 0.0f;
+      }
+      loaded = seq;
+    }
+    float cur[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane + 32 * j;
-    if (e >= experts) continue;
-    float d = slope[j] * (w[j] - dot);
-    if (a.accumulate) d += load_logit(out + e);
-    store_grad(out + e, d);
+    for (int j = 0; j < V; ++j) cur[j] = l[j];
+    if (t + 1 < t1) load_row<T, V, VEC>(logits + (t + 1) * experts, experts, lane, l);
+    T *out = static_cast<T *>(a.d_logits) + t * experts;
+    if ((a.token_mask && !__ldg(a.token_mask + t)) || n <= 0) {
+      if (!a.accumulate) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) cur[j] = 0.0f;
+        store_row<T, V, VEC>(out, experts, lane, cur);
+      }
+      continue;
+    }
+    float p[V], slope[V];
+    probabilities<V>(cur, a.softmax, p, slope);
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) dot += p[j] * w[j];
+    dot = warp_sum(dot);
+    if (a.accumulate) {
+      load_row<T, V, VEC>(out, experts, lane, cur);
+#pragma unroll
+      for (int j = 0; j < V; ++j) cur[j] += slope[j] * (w[j] - dot);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) cur[j] = slope[j] * (w[j] - dot);
+    }
+    store_row<T, V, VEC>(out, experts, lane, cur);
   }
 }
 
-template <typename F>
+// Calls f with the values a lane holds, V, and how many are neighbours: as many as fit a 16-byte
+// load where the experts divide by it, else one.
+template <typename T, typename F>
 cudaError_t by_width(int experts, F f) {
-  if (experts <= 32) return f(std::integral_constant<int, 1>{});
-  if (experts <= 64) return f(std::integral_constant<int, 2>{});
-  if (experts <= 128) return f(std::integral_constant<int, 4>{});
-  if (experts <= 256) return f(std::integral_constant<int, 8>{});
-  if (experts <= 512) return f(std::integral_constant<int, 16>{});
-  return f(std::integral_constant<int, 32>{});
+  auto with = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    constexpr int kVec = V < 16 / static_cast<int>(sizeof(T)) ? V : 16 / static_cast<int>(sizeof(T));
+    if (experts % kVec == 0) return f(v, std::integral_constant<int, kVec>{});
+    return f(v, std::integral_constant<int, 1>{});
+  };
+  if (experts <= 32) return with(std::integral_constant<int, 1>{});
+  if (experts <= 64) return with(std::integral_constant<int, 2>{});
+  if (experts <= 128) return with(std::integral_constant<int, 4>{});
+  if (experts <= 256) return with(std::integral_constant<int, 8>{});
+  if (experts <= 512) return with(std::integral_constant<int, 16>{});
+  return with(std::integral_constant<int, 32>{});
+}
+
+template <typename T>
+cudaError_t gate(const LaunchGate &a) {
+  const unsigned blocks = static_cast<unsigned>((a.tokens + kGateWarps - 1) / kGateWarps);
+  return by_width<T>(a.num_experts, [&](auto v, auto vec) {
+    gate_kernel<T, decltype(v)::value, decltype(vec)::value><<<blocks, 32 * kGateWarps, 0, a.stream>>>(
+        static_cast<const T *>(a.logits), a.tokens, a.num_experts, a.top_k, a.softmax, a.normalize, a.scale, a.bias,
+        a.ids, a.weights);
+    return cudaGetLastError();
+  });
+}
+
+template <typename T>
+cudaError_t gate_backward(const LaunchGate &a) {
+  const unsigned blocks = static_cast<unsigned>((a.tokens + kGateWarps - 1) / kGateWarps);
+  return by_width<T>(a.num_experts, [&](auto v, auto vec) {
+    gate_backward_kernel<T, decltype(v)::value, decltype(vec)::value><<<blocks, 32 * kGateWarps, 0, a.stream>>>(
+        static_cast<const T *>(a.logits), a.ids, a.d_weights, a.tokens, a.num_experts, a.top_k, a.softmax, a.normalize,
+        a.scale, static_cast<T *>(a.d_logits), a.status);
+    return cudaGetLastError();
+  });
+}
+
+template <typename T>
+cudaError_t balance_partial(const LaunchBalance &a) {
+  const unsigned blocks = static_cast<unsigned>(a.num_seqs * a.slices);
+  const size_t smem = static_cast<size_t>(kPartWarps / 2 + 1) * a.num_experts * 4;
+  return by_width<T>(a.num_experts, [&](auto v, auto vec) {
+    balance_partial_kernel<T, decltype(v)::value, decltype(vec)::value>
+        <<<blocks, 32 * kPartWarps, smem, a.stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+template <typename T>
+cudaError_t balance_backward(const LaunchBalance &a) {
+  // up to four tokens a warp, as long as that leaves about 32 warps an SM
+  const int64_t fit = a.tokens / 4864;
+  const int per_warp = static_cast<int>(fit < 1 ? 1 : fit > 4 ? 4 : fit);
+  const int64_t warps = (a.tokens + per_warp - 1) / per_warp;
+  const unsigned blocks = static_cast<unsigned>((warps + kGateWarps - 1) / kGateWarps);
+  return by_width<T>(a.num_experts, [&](auto v, auto vec) {
+    balance_backward_kernel<T, decltype(v)::value, decltype(vec)::value>
+        <<<blocks, 32 * kGateWarps, 0, a.stream>>>(a, per_warp);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace
 
-cudaError_t launch_gate(const LaunchGate &a) {
-  const unsigned blocks = static_cast<unsigned>((a.tokens + kGateWarps - 1) / kGateWarps);
-  return by_width(a.num_experts, [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    if (a.bf16)
-      gate_kernel<__nv_bfloat16, V><<<blocks, 32 * kGateWarps, 0, a.stream>>>(
-          static_cast<const __nv_bfloat16 *>(a.logits), a.tokens, a.num_experts, a.top_k, a.softmax, a.normalize, a.scale,
-          a.bias, a.ids, a.weights);
-    else
-      gate_kernel<float, V><<<blocks, 32 * kGateWarps, 0, a.stream>>>(static_cast<const float *>(a.logits), a.tokens,
-                                                                     a.num_experts, a.top_k, a.softmax, a.normalize,
-                                                                     a.scale, a.bias, a.ids, a.weights);
-    return cudaGetLastError();
-  });
-}
+cudaError_t launch_gate(const LaunchGate &a) { return a.bf16 ? gate<__nv_bfloat16>(a) : gate<float>(a); }
 
 cudaError_t launch_gate_backward(const LaunchGate &a) {
-  const unsigned blocks = static_cast<unsigned>((a.tokens + kGateWarps - 1) / kGateWarps);
-  return by_width(a.num_experts, [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    if (a.bf16)
-      gate_backward_kernel<__nv_bfloat16, V><<<blocks, 32 * kGateWarps, 0, a.stream>>>(
-          static_cast<const __nv_bfloat16 *>(a.logits), a.ids, a.d_weights, a.tokens, a.num_experts, a.top_k, a.softmax,
-          a.normalize, a.scale, static_cast<__nv_bfloat16 *>(a.d_logits), a.status);
-    else
-      gate_backward_kernel<float, V><<<blocks, 32 * kGateWarps, 0, a.stream>>>(
-          static_cast<const float *>(a.logits), a.ids, a.d_weights, a.tokens, a.num_experts, a.top_k, a.softmax,
-          a.normalize, a.scale, static_cast<float *>(a.d_logits), a.status);
-    return cudaGetLastError();
-  });
+  return a.bf16 ? gate_backward<__nv_bfloat16>(a) : gate_backward<float>(a);
 }
 
 cudaError_t launch_balance_loss(const LaunchBalance &a) {
-  const unsigned blocks = static_cast<unsigned>(a.num_seqs * a.slices);
-  const size_t smem = static_cast<size_t>(kPartWarps / 2 + 1) * a.num_experts * 4;
-  cudaError_t err = by_width(a.num_experts, [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    if (a.bf16)
-      balance_partial_kernel<__nv_bfloat16, V><<<blocks, 32 * kPartWarps, smem, a.stream>>>(a);
-    else
-      balance_partial_kernel<float, V><<<blocks, 32 * kPartWarps, smem, a.stream>>>(a);
-    return cudaGetLastError();
-  });
+  cudaError_t err = a.bf16 ? balance_partial<__nv_bfloat16>(a) : balance_partial<float>(a);
   if (err != cudaSuccess) return err;
-  balance_final_kernel<<<static_cast<unsigned>(a.num_seqs), 1024, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs * ((a.num_experts + 31) / 32)), 1, 1);
+  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, balance_final_kernel, a);
 }
 
 cudaError_t launch_balance_backward(const LaunchBalance &a) {
-  const unsigned blocks = static_cast<unsigned>((a.tokens + kGateWarps - 1) / kGateWarps);
-  return by_width(a.num_experts, [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    if (a.bf16)
-      balance_backward_kernel<__nv_bfloat16, V><<<blocks, 32 * kGateWarps, 0, a.stream>>>(a);
-    else
-      balance_backward_kernel<float, V><<<blocks, 32 * kGateWarps, 0, a.stream>>>(a);
-    return cudaGetLastError();
-  });
+  return a.bf16 ? balance_backward<__nv_bfloat16>(a) : balance_backward<float>(a);
 }
 
 }  // namespace fme

@@ -567,7 +567,7 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
  * moe_gate -- the top_k experts of each token and their weights, from router logits.
  *
  * key[t, e] = fl32(logits[t, e] + bias[e]); ids[t, :] = the top_k largest keys, largest first,
- * equal keys by the lower expert (a NaN is lowest).  The choice is one fp32 addition and
+ * equal keys by the lower expert (a NaN counts as -inf).  The choice is one fp32 addition and
  * comparisons: the same on every run and machine, so it can be replayed
  * ("Composer 2 Technical Report", section 6.2).  With s = softmax over the token's
  * experts or sigmoid, of the logits without bias:
