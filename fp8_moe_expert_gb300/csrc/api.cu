@@ -778,8 +778,10 @@ fme_status block128_rows_gemm(bool dgrad, const uint8_t *a_codes, const float *a
   if (st != FME_OK) return st;
   a.k = dgrad ? n : k;
   a.n = dgrad ? k : n;
-  if ((st = encode_u8_2d(&a.map_a, a_codes, a.k, m, a.k, 128)) != FME_OK) return st;
-  if ((st = encode_u8_weights(&a.map_b, w_codes, num_experts, n, k)) != FME_OK) return st;
+  const bool few = !dgrad && fme::block128_few_rows(m, num_experts);
+  CUtensorMap &rows_map = few ? a.map_b : a.map_a, &w_map = few ? a.map_a : a.map_b;
+  if ((st = encode_u8_2d(&rows_map, a_codes, a.k, m, a.k, few ? 16 : 128)) != FME_OK) return st;
+  if ((st = encode_u8_weights(&w_map, w_codes, num_experts, n, k)) != FME_OK) return st;
   if ((st = encode_bf16_out(&a.map_y, y, a.n, m)) != FME_OK) return st;
   a.a_scale = a_scale;
   a.b_scale = w_scale;

@@ -570,6 +570,326 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
   }
 }
 
+// ------------------------------------------------- forward, few rows an expert --
+// The same sums with the operands exchanged: an item is 128 rows of W_e (the MMA's M) and up to 64
+// of the expert's tokens (its N, in steps of 16), one CTA an item.  With few tokens the time is that
+// of reading the weights once, and 256-row token tiles would leave all but a few rows of the MMAs
+// empty and put the weights on half as many SMs.  Each block's 16 KB of codes go through a ring of
+// eight stages; the sums of up to four blocks are in tensor memory; thread = row of W, its
+// tokens' sums in registers, scaled by sx[b,t] sw[e,n/128,b] exactly as above, in the same order of
+// b: a row's bits are the same in both forms.
+//   warp 0 producer, warp 1 MMA issuer, warps 2-3 scales (two blocks each in turn), warps 4-7 epilogue.
+constexpr int kFewTokens = 64;
+constexpr int kFewStages = 8;
+constexpr int kFewAccs = 4;
+constexpr int kFewSlots = 8;
+constexpr int kFewThreads = 256;
+constexpr int kFewBBytes = kFewTokens * kStageKBytes;
+constexpr int kFewStageBytes = kABytes + kFewBBytes;
+constexpr uint32_t kFewTmemCols = kFewAccs * kFewTokens;
+
+struct SharedFew {
+  uint64_t full[kFewStages];
+  uint64_t freed[kFewStages];
+  uint64_t acc_full[kFewAccs];
+  uint64_t acc_empty[kFewAccs];
+  uint64_t sc_full[kFewSlots];
+  uint64_t sc_empty[kFewSlots];
+  uint64_t drain;
+  alignas(16) float scales[kFewSlots][kFewTokens];  // read as float4
+  uint32_t tmem_base;
+  int abort_flag;
+  int ok_flag;
+};
+
+__device__ __forceinline__ void tma_load_2d_own(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_own(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y,
+                                                int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// One block on one CTA (M = 128), both operands K-major, and its commit.
+__device__ __forceinline__ void mma_block_own(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred z, o;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.u32 z, 0, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, z;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, o;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, o;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, o;\n\t"
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 32 lanes x 16 columns, and the wait for them.
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])::"memory");
+}
+
+struct ItemFew {
+  int32_t e;
+  int32_t row0;    // first token row
+  int32_t tokens;  // 1 .. 64
+  int32_t n0;      // first row of W_e = output column
+};
+__device__ __forceinline__ ItemFew item_few(const LaunchBlock128 &p, const Tables &s, int64_t t) {
+  const int64_t nb = (p.n + kBM - 1) / kBM;
+  const int64_t g = t / nb;
+  ItemFew it;
+  it.n0 = static_cast<int32_t>((t - g * nb) * kBM);
+  it.e = find_group(s.aux, p.num_experts, g);
+  const int32_t first = static_cast<int32_t>(g - s.aux[it.e]) * kFewTokens;
+  it.row0 = s.off[it.e] + first;
+  it.tokens = min(kFewTokens, s.off[it.e + 1] - s.off[it.e] - first);
+  return it;
+}
+
+__global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const __grid_constant__ LaunchBlock128 p) {
+  __shared__ SharedFew s;
+  extern __shared__ uint8_t dyn_smem[];
+  constexpr int S = kFewStages;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem_a = smem;
+  uint8_t *smem_b = smem_a + S * kABytes;
+  int32_t *gmem = reinterpret_cast<int32_t *>(smem + S * kFewStageBytes);
+  const Tables tab{gmem, gmem + (p.num_experts + 1)};
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (warp == 0) {
+    const int32_t total = scan_groups(p.offsets, p.num_experts, p.m, kFewTokens,
+                                      [&](int g, int32_t lo, int32_t, int32_t first) {
+                                        tab.off[g] = lo;
+                                        tab.aux[g] = first;
+                                      });
+    if (lane == 0) {
+      tab.off[p.num_experts] = static_cast<int32_t>(p.m);
+      tab.aux[p.num_experts] = total;
+      s.ok_flag = total >= 0;
+    }
+  } else if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem_base)),
+                 "r"(kFewTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (threadIdx.x == 64) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.freed[i], 1);
+    }
+    for (int i = 0; i < kFewAccs; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 4);
+    }
+    for (int i = 0; i < kFewSlots; ++i) {
+      mbar_init(&s.sc_full[i], 1);
+      mbar_init(&s.sc_empty[i], 4);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    prefetch_tensormap(&p.map_a);
+    prefetch_tensormap(&p.map_b);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  volatile int *abort_flag = &s.abort_flag;
+  const int nk = static_cast<int>((p.k + 127) >> 7);
+  const int64_t nb = (p.n + kBM - 1) / kBM;
+  // malformed offsets: no item, straight to the end
+  const int64_t total = s.ok_flag ? static_cast<int64_t>(tab.aux[p.num_experts]) * nb : 0;
+  if (!s.ok_flag && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- producer
+      uint32_t stage = 0, filled = 0;
+      bool stop = false;
+      for (int64_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
+        const ItemFew it = item_few(p, tab, t);
+        const int groups = (it.tokens + 15) >> 4;
+        for (int i = 0; i < nk; ++i) {
+          if (!mbar_wait<true>(&s.freed[stage], ((filled / S) & 1) ^ 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&s.full[stage], kABytes + groups * 16 * kStageKBytes);
+          tma_load_3d_own(smem_a + stage * kABytes, &p.map_a, &s.full[stage], i * 128, it.n0, it.e);
+          for (int j = 0; j < groups; ++j)
+            tma_load_2d_own(smem_b + stage * kFewBBytes + j * 16 * kStageKBytes, &p.map_b, &s.full[stage], i * 128,
+                            it.row0 + 16 * j);
+          ++filled;
+          if (++stage == S) stage = 0;
+        }
+      }
+      // every copy has landed before the CTA can exit
+      for (uint32_t j = 0; j < S && j < filled; ++j) {
+        const uint32_t f = j + S * ((filled - 1 - j) / S);
+        mbar_drain(&s.full[j], (f / S) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------- MMA issuer (whole warp)
+    const uint64_t a_desc = desc_sw128(smem_u32(smem_a), false), b_desc = desc_sw128(smem_u32(smem_b), false);
+    uint32_t stage = 0, phase = 0, fill = 0;
+    bool stop = false;
+    for (int64_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
+      const uint32_t cols = (item_few(p, tab, t).tokens + 15) & ~15;
+      const uint32_t idesc = (1u << 4) | ((cols >> 3) << 17) | ((128u >> 4) << 24);
+      for (int i = 0; i < nk; ++i) {
+        const uint32_t b = fill % kFewAccs;
+        if (!mbar_wait(&s.full[stage], phase, abort_flag, p.status) ||
+            !mbar_wait(&s.acc_empty[b], ((fill / kFewAccs) & 1) ^ 1, abort_flag, p.status))
+          stop = true;
+        stop = __any_sync(0xFFFFFFFFu, stop);
+        if (stop) break;
+        tc_fence_after();
+        if (elect_one())
+          mma_block_own(tmem + b * kFewTokens, a_desc + stage * (kABytes / 16), b_desc + stage * (kFewBBytes / 16), idesc,
+                        &s.acc_full[b]);
+        __syncwarp();
+        ++fill;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+    if (elect_one()) {
+      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       smem_u32(&s.drain))
+                   : "memory");
+      mbar_drain(&s.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < kEpiWarp0) {
+    // -------------------------------------------------------------------- scales
+    const int which = warp - kScaleWarp0;  // of every four blocks, this warp's first is 2 * which
+    uint32_t g = 0;                        // blocks of earlier items
+    bool stop = false;
+    for (int64_t t = blockIdx.x; t < total && !stop; t += gridDim.x, g += nk) {
+      const ItemFew it = item_few(p, tab, t);
+      const float *a = p.a_scale + it.row0;
+      const float *b = p.b_scale + (it.e * nb + (it.n0 >> 7)) * nk;
+      for (int i0 = 2 * which; i0 < nk && !stop; i0 += 4) {
+        float v[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int i = i0 + u;
+          const float w = i < nk ? __ldg(b + i) : 0.0f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int tok = lane + 32 * h;
+            v[u][h] = i < nk && tok < it.tokens ? __ldg(a + i * p.m + tok) * w : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (i0 + u >= nk) break;
+          const uint32_t q = g + i0 + u, slot = q % kFewSlots;
+          if (!mbar_wait<true>(&s.sc_empty[slot], ((q / kFewSlots) & 1) ^ 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          s.scales[slot][lane] = v[u][0];
+          s.scales[slot][lane + 32] = v[u][1];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.sc_full[slot]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t g = 0;
+    bool stop = false;
+    for (int64_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
+      const ItemFew it = item_few(p, tab, t);
+      float acc[kFewTokens];
+#pragma unroll
+      for (int j = 0; j < kFewTokens; ++j) acc[j] = 0.0f;
+#pragma unroll 1
+      for (int i = 0; i < nk; ++i, ++g) {
+        const uint32_t b = g % kFewAccs, slot = g % kFewSlots;
+        if (!mbar_wait(&s.sc_full[slot], (g / kFewSlots) & 1, abort_flag, p.status) ||
+            !mbar_wait(&s.acc_full[b], (g / kFewAccs) & 1, abort_flag, p.status)) {
+          stop = true;
+          break;
+        }
+        if (warp == kEpiWarp0 && lane == 0) mbar_arrive(&s.freed[g % S]);  // the block's MMAs are done
+        tc_fence_after();
+        const float4 *f = reinterpret_cast<const float4 *>(s.scales[slot]);
+#pragma unroll
+        for (int c = 0; c < kFewTokens / 16; ++c) {
+          if (16 * c < it.tokens) {
+            uint32_t v[16];
+            tmem_ld_32x16(tq + b * kFewTokens + 16 * c, v);
+            tmem_wait_ld_for(v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 w = f[4 * c + j];
+              acc[16 * c + 4 * j] = __fmaf_rn(__uint_as_float(v[4 * j]), w.x, acc[16 * c + 4 * j]);
+              acc[16 * c + 4 * j + 1] = __fmaf_rn(__uint_as_float(v[4 * j + 1]), w.y, acc[16 * c + 4 * j + 1]);
+              acc[16 * c + 4 * j + 2] = __fmaf_rn(__uint_as_float(v[4 * j + 2]), w.z, acc[16 * c + 4 * j + 2]);
+              acc[16 * c + 4 * j + 3] = __fmaf_rn(__uint_as_float(v[4 * j + 3]), w.w, acc[16 * c + 4 * j + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s.acc_empty[b]);
+          mbar_arrive(&s.sc_empty[slot]);
+        }
+      }
+      if (stop) break;
+      const int64_t col = it.n0 + q * 32 + lane;
+      if (col < p.n) {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + static_cast<int64_t>(it.row0) * p.n + col;
+#pragma unroll
+        for (int j = 0; j < kFewTokens; ++j)
+          if (j < it.tokens) y[j * p.n] = __float2bfloat16_rn(acc[j]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFewTmemCols) : "memory");
+}
+
 template <Kind128 K>
 cudaError_t launch128(const LaunchBlock128 &a) {
   const int smem = 1024 + kStages128 * kStageBytes128 + kStageOut + 8 * (a.num_experts + 1);
@@ -596,9 +916,22 @@ cudaError_t launch128(const LaunchBlock128 &a) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+cudaError_t launch_few(const LaunchBlock128 &a) {
+  const int smem = 1024 + kFewStages * kFewStageBytes + 8 * (a.num_experts + 1);
+  cudaError_t err =
+      cudaFuncSetAttribute(gemm_block128_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  const int64_t items = (a.m / kFewTokens + std::min<int64_t>(a.num_experts, a.m)) * ((a.n + kBM - 1) / kBM);
+  gemm_block128_few_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.num_sms, items)), kFewThreads, smem, a.stream>>>(
+      a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_block128_fwd(const LaunchBlock128 &a) { return launch128<Kind128::kFwd>(a); }
+cudaError_t launch_block128_fwd(const LaunchBlock128 &a) {
+  return block128_few_rows(a.m, a.num_experts) ? launch_few(a) : launch128<Kind128::kFwd>(a);
+}
 cudaError_t launch_block128_dgrad(const LaunchBlock128 &a) { return launch128<Kind128::kDgrad>(a); }
 cudaError_t launch_block128_wgrad(const LaunchBlock128 &a) { return launch128<Kind128::kWgrad>(a); }
 

@@ -181,3 +181,66 @@ def test_wgrad(rows, e, n, k, status):
         a, b = dy[p[i]:p[i + 1]], x[p[i]:p[i + 1]]
         check(dw32[i], a.t() @ b, a.abs().t() @ b.abs(), p[i + 1] - p[i], 0.0)
     assert not any(bool(dw32[i].any()) for i in range(e) if off[i] == off[i + 1])
+
+
+@pytest.mark.parametrize("n,k", [(4096, 7168), (400, 656)])
+def test_forward_rows_do_not_depend_on_the_batch(n, k, status):
+    """The rows of a small batch, alone and inside a large one of the same experts: the same bits."""
+    e = 3
+    w = fme.quantize_fp8_block128_weights(torch.stack([ref.normal((n, k), 0.02, i) for i in range(e)]))
+    x = outliers((3000, k), 9)
+    big = [0, 1500, 1600, 3000]
+    y = fme.grouped_gemm_fwd_fp8_block128(*fme.quantize_fp8_block128(x), *w, i32(big), status=status)
+    for take in ([1, 0, 1], [70, 100, 3], [0, 17, 0], [128, 64, 150]):
+        off = np.concatenate([[0], np.cumsum(take)]).tolist()
+        rows = torch.cat([torch.arange(big[i], big[i] + take[i], device=DEV) for i in range(e)])
+        small = fme.grouped_gemm_fwd_fp8_block128(*fme.quantize_fp8_block128(x[rows].contiguous()), *w, i32(off),
+                                                  status=status)
+        assert torch.equal(small, y[rows])
+
+
+@pytest.mark.parametrize("rows", [10, 2000])
+@pytest.mark.parametrize("bad", [[1, 0, 0], [0, 1, 0], [0, 0, 1], [0, 5000, 0], [0, -3000, 0]])
+def test_products_malformed_offsets_write_nothing(rows, bad):
+    n = k = 256
+    w = fme.quantize_fp8_block128_weights(torch.stack([ref.normal((n, k), 0.02, i) for i in range(2)]))
+    a = fme.quantize_fp8_block128(outliers((rows, k), 1))
+    off = i32([bad[0], rows // 2 + bad[1] if bad[1] != 1 else rows + 1, rows + bad[2]])
+    for call in (fme.grouped_gemm_fwd_fp8_block128, fme.grouped_gemm_dgrad_fp8_block128):
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = torch.full((rows, 256), 3.0, dtype=torch.bfloat16, device=DEV)
+        call(*a, *w, off, status=st, **{"y" if call is fme.grouped_gemm_fwd_fp8_block128 else "dx": out})
+        assert fme.read_device_status(st)[0] == fme.ERR_DEVICE_BAD_OFFSETS
+        assert bool((out == 3.0).all())
+
+
+@pytest.mark.parametrize("po", [[128, 256, 384], [0, 100, 384], [0, 256, 128], [0, 256, 512]])
+def test_wgrad_malformed_offsets_write_nothing(po):
+    c = torch.zeros((384, 128), dtype=torch.uint8, device=DEV)
+    s = torch.ones((3, 128), device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dw = torch.full((2, 128, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    fme.grouped_gemm_wgrad_fp8_block128(c, s, c, s, i32(po), dw=dw, status=st)
+    assert fme.read_device_status(st)[0] == fme.ERR_DEVICE_BAD_OFFSETS and bool((dw == 3.0).all())
+
+
+def test_nan_codes_of_one_expert_and_row_stay_there(status):
+    """0x7F codes (NaN) in one expert's weights and in one row reach no other expert or row, also where
+    n and k end inside a tile."""
+    n, k = 144, 272
+    w, ws = fme.quantize_fp8_block128_weights(torch.stack([ref.normal((n, k), 0.02, i) for i in range(3)]))
+    w[1] = 0x7F
+    for rows in (30, 900):
+        off = [0, rows // 3, 2 * rows // 3, rows]
+        a, s = fme.quantize_fp8_block128(ref.normal((rows, k), 1.0, 4))
+        a[0] = 0x7F
+        y = fme.grouped_gemm_fwd_fp8_block128(a, s, w, ws, i32(off), status=status)
+        bad = torch.isnan(y).all(dim=1)
+        want = torch.zeros(rows, dtype=torch.bool, device=DEV)
+        want[off[1]:off[2]] = True
+        want[0] = True
+        assert torch.equal(bad, want) and torch.equal(torch.isnan(y).any(dim=1), want)
+        d, ds = fme.quantize_fp8_block128(ref.normal((rows, n), 1.0, 4))
+        dx = fme.grouped_gemm_dgrad_fp8_block128(d, ds, w, ws, i32(off), status=status)
+        want[0] = False
+        assert torch.equal(torch.isnan(dx).any(dim=1), want)
