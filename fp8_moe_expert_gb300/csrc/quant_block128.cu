@@ -34,9 +34,22 @@ __device__ __forceinline__ uint32_t absmax_halves(uint32_t m) { return max(m & 0
 struct BlockScale {
   float s, r;
 };
+// Both quotients correctly rounded, by one step of P. Markstein's fused-multiply-add refinement (IBM J.
+// Res. Dev. 34(1), 1990): q + (n - d q) / d with the reciprocal in place of the last division.  A is
+// taken times 2^-14 in the second, so that neither it nor its reciprocal leaves the normal range.
+// Equal to IEEE division for every bf16 A from the floor up, and for reciprocals up to two ulps off
+// (checked with exact rational arithmetic); two IEEE divisions a block were a fifth of the row-wise
+// kernel's instructions.
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
   const float a = fmaxf(bf16_bits_to_float(amax_bits), kAmaxFloor);
-  return {__fdiv_rn(a, 448.0f), __fdiv_rn(448.0f, a)};
+  constexpr float kInv = 1.0f / 448.0f;
+  const float q = __fmul_rn(a, kInv);
+  const float s = __fmaf_rn(__fmaf_rn(-448.0f, q, a), kInv, q);
+  const float d = __fmul_rn(a, 0x1p-14f);
+  const float t = rcp_approx(d);
+  const float u = __fmul_rn(448.0f * 0x1p-14f, t);
+  const float r = __fmaf_rn(__fmaf_rn(-d, u, 448.0f * 0x1p-14f), t, u);
+  return {s, r};
 }
 
 // The four bf16 of words a, b times (r0, r1, r2, r3) -> four E4M3 codes in order.
@@ -106,8 +119,9 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const uint16_t *__restric
       const BlockScale f = block_scale(absmax_halves(m));
       const float2 r = make_float2(f.r, f.r);
       if (col < c_hi) {
-        *reinterpret_cast<uint4 *>(qr + col) = make_uint4(codes4(a.x, a.y, r, r), codes4(a.z, a.w, r, r),
-                                                          codes4(b.x, b.y, r, r), codes4(b.z, b.w, r, r));
+        // streaming: the codes do not push the tokens out of L2
+        __stcs(reinterpret_cast<uint4 *>(qr + col), make_uint4(codes4(a.x, a.y, r, r), codes4(a.z, a.w, r, r),
+                                                               codes4(b.x, b.y, r, r), codes4(b.z, b.w, r, r)));
         if ((lane & 7) == 0) scale[static_cast<int64_t>(col >> 7) * rows + row] = f.s;
       }
     }
@@ -274,6 +288,9 @@ cudaError_t launch_fp8_block128_rows(const LaunchFp8Quant &a) {
   const int steps = (a.cols + kUnroll * kChunkCols - 1) / (kUnroll * kChunkCols);
   int splits = 1;
   while (splits < steps && groups * splits < a.num_sms) ++splits;
+  // a token's row is read once for each of its experts: 2048 columns of all rows at a time, so that
+  // those columns of the tokens stay in L2 between (8192 tokens x 7168, top 8: 184 -> 147 us)
+  if (a.gather_div > 1 && splits < (steps + 1) / 2) splits = (steps + 1) / 2;
   const int per = (steps + splits - 1) / splits * (kUnroll * kChunkCols);
   const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>((a.cols + per - 1) / per));
   auto kernel = a.gather ? fp8_rows_kernel<true> : fp8_rows_kernel<false>;

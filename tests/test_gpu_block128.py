@@ -65,6 +65,20 @@ def test_rows(rows, cols, make, status):
     same(codes, v)
 
 
+def test_every_magnitude(status):
+    """A row for each positive finite bf16 value as its block's magnitude, the rest random fractions of it."""
+    bits = torch.arange(1, 255 << 7, device=DEV, dtype=torch.int32)
+    top = (bits << 16).view(torch.float32)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    x = (top[:, None] * (2 * torch.rand((len(top), 128), generator=g, device=DEV) - 1)).to(torch.bfloat16)
+    x[:, 77] = top.to(torch.bfloat16)
+    codes, scale = fme.quantize_fp8_block128(x, status=status)
+    v, s = ref.quantize_rows(x)
+    assert torch.equal(scale, s)
+    same(codes, v)
+
+
 @pytest.mark.parametrize("tokens,top_k,cols", [(1, 8, 7168), (33, 3, 272), (500, 1, 128)])
 def test_gathered_rows_equal_the_quantized_copy(tokens, top_k, cols, status):
     x = outliers((tokens, cols), 5)
