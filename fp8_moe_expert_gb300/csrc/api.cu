@@ -103,17 +103,17 @@ fme_status encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint
   return FME_OK;
 }
 
-// bf16 matrix [rows x cols] (row stride cols * 2 bytes) for bulk tensor stores of
-// 32 x 32 boxes with the 64-byte swizzle.
-fme_status encode_bf16_out(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows) {
+// bf16 (or fp32) matrix [rows x cols] (row stride cols * 2 or 4 bytes) for bulk tensor stores
+// of boxes of 32 rows x 64 bytes with the 64-byte swizzle.
+fme_status encode_bf16_out(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, bool fp32 = false) {
   EncodeTiledFn fn;
   fme_status st = get_encoder(&fn);
   if (st != FME_OK) return st;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {32, 32};
+  cuuint64_t strides[1] = {cols * (fp32 ? 4 : 2)};
+  cuuint32_t box[2] = {fp32 ? 16u : 32u, 32};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+  CUresult r = fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -889,7 +889,7 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
   const int64_t extent = positions ? positions : 1;
   if ((st = encode_u8_2d(&a.map_a, abase, n, extent, n, 128)) != FME_OK) return st;
   if ((st = encode_u8_2d(&a.map_b, bbase, k, extent, k, 128)) != FME_OK) return st;
-  if (dw_mode == FME_DW_BF16 && (st = encode_bf16_out(&a.map_y, dw, k, static_cast<uint64_t>(num_experts) * n)) != FME_OK)
+  if ((st = encode_bf16_out(&a.map_y, dw, k, static_cast<uint64_t>(num_experts) * n, dw_mode != FME_DW_BF16)) != FME_OK)
     return st;
   a.a_scale = dy_scale;
   a.b_scale = x_scale;

@@ -42,11 +42,12 @@ namespace {
 constexpr int kThreads128 = 384;
 constexpr int kEpiWarp0 = 4;
 constexpr int kStageBytes128 = kABytes + kBBytes;
-constexpr int kStages128 = 6;
+constexpr int kStages128 = 4;
+constexpr int kOutBlocks = 4;                // 2 KB staging blocks a warp: its 32 x 128 bf16 outputs of a tile
 constexpr int kScaleWarp0 = 2;                // and 3
 constexpr int kScaleSlots = 4;                // blocks whose scales are in shared memory
 constexpr int kScaleSlotFloats = 128 + kBN;  // of the CTA's rows and the tile's columns (see scale_slot)
-constexpr int kStageOut = 8 * kOutBoxBytes + kScaleSlots * kScaleSlotFloats * 4;
+constexpr int kStageOut = 8 * kOutBlocks * kOutBoxBytes + kScaleSlots * kScaleSlotFloats * 4;
 
 enum class Kind128 { kFwd, kDgrad, kWgrad };
 
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
   uint8_t *smem_a = smem;
   uint8_t *smem_b = smem_a + S * kABytes;
   uint8_t *smem_out = smem + S * kStageBytes128;
-  float *scales = reinterpret_cast<float *>(smem_out + 8 * kOutBoxBytes);
+  float *scales = reinterpret_cast<float *>(smem_out + 8 * kOutBlocks * kOutBoxBytes);
   int32_t *gmem = reinterpret_cast<int32_t *>(smem_out + kStageOut);
   const Tables tab{gmem, gmem + (p.num_experts + 1)};
 
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
     const int q = warp & 3;         // tensor-memory lane quarter
     const int half = ew >> 2;       // column half of the tile
     const int r = q * 32 + lane;    // row of the CTA's 128
-    uint8_t *stage_blk = smem_out + ew * kOutBoxBytes;
+    uint8_t *stage_blks = smem_out + ew * kOutBlocks * kOutBoxBytes;
     const uint32_t leader_empty[2] = {pair::map_to_rank(&s.acc_empty[0], 0), pair::map_to_rank(&s.acc_empty[1], 0)};
     const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     uint32_t g = 0;
@@ -527,31 +528,73 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       const int warp_rows = tl.rows_valid - 32 * q;
       if (warp_rows <= 0 || !in_cols) continue;
       const int64_t out_row = (K == Kind128::kWgrad ? tl.e * p.m : int64_t(0)) + tl.row0 + 32 * q;
-      if (K == Kind128::kWgrad && p.out_fp32) {
-        if (tl.nk == 0 && p.accumulate) continue;
-        float *dst = static_cast<float *>(p.y) + out_row * p.n + c0;
+      // 2 KB blocks of 32 rows x 32 bf16 or 16 fp32 columns in the warp's staging area.  A
+      // whole one leaves by a bulk store: four blocks are written, made visible and stored together
+      // (one wait, one fence); one cut by the output's edge, and sums added to dW, by plain stores.
+      const int xs = (lane >> 1) & 3;  // the 64-byte swizzle of this lane's row
+      auto await_staging = [&] {
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+      };
+      const bool fp32 = K == Kind128::kWgrad && p.out_fp32;
+      if (fp32 && tl.nk == 0 && p.accumulate) continue;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          store_fp32_cut(dst + 16 * c, p.n, warp_rows, static_cast<int>(p.n - c0 - 16 * c), p.accumulate, stage_blk,
-                         lane, acc + 8 * c);
-      } else {
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.y) + out_row * p.n + c0;
+      for (int half_tile = 0; half_tile < (K == Kind128::kWgrad ? 2 : 1); ++half_tile) {
+        if (!fp32 && half_tile == 1) break;
+        const int wide = fp32 ? 16 : 32;  // columns of a block
+        const int base = c0 + half_tile * 64;
+        const int whole = fp32 && p.accumulate ? 0 : warp_rows >= 32 ? min(4, max(0, static_cast<int>(p.n) - base) / wide) : 0;
+        if (base >= p.n) break;
+        await_staging();
+        if (whole > 0) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int left = static_cast<int>(p.n) - c0 - 32 * c;
-          uint32_t packed[16];
+          for (int c = 0; c < 4; ++c) {
+            uint4 *row = reinterpret_cast<uint4 *>(stage_blks + c * kOutBoxBytes + lane * 64);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * c + j].x, acc[16 * c + j].y);
-            packed[j] = *reinterpret_cast<const uint32_t *>(&h);
+            for (int j = 0; j < 4; ++j) {
+              uint4 v;
+              if (fp32) {
+                const float2 lo = acc[32 * half_tile + 8 * c + 2 * j], hi = acc[32 * half_tile + 8 * c + 2 * j + 1];
+                v = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
+              } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * c + 4 * j + i].x, acc[16 * c + 4 * j + i].y);
+                  w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                v = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+              row[j ^ xs] = v;
+            }
           }
-          if (left <= 0) break;
-          if (warp_rows >= 32 && left >= 32) {
-            store_block_tma(&p.map_y, c0 + 32 * c, static_cast<int32_t>(out_row), stage_blk, lane, packed);
-          } else {
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-            store_block_cut(dst + 32 * c, p.n, warp_rows, left, stage_blk, lane, packed);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            for (int c = 0; c < whole; ++c)
+              tma_store_2d(&p.map_y, base + wide * c, static_cast<int32_t>(out_row), stage_blks + c * kOutBoxBytes);
+            bulk_commit();
+          }
+        }
+        if (whole < 4 && base + wide * whole < p.n) {
+          await_staging();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col = base + wide * c;
+            if (c < whole || col >= p.n) continue;
+            if (fp32) {
+              store_fp32_cut(static_cast<float *>(p.y) + out_row * p.n + col, p.n, warp_rows, 16, p.accumulate,
+                             stage_blks, lane, acc + 32 * half_tile + 8 * c);
+            } else {
+              uint32_t packed[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * c + j].x, acc[16 * c + j].y);
+                packed[j] = *reinterpret_cast<const uint32_t *>(&h);
+              }
+              store_block_cut(static_cast<__nv_bfloat16 *>(p.y) + out_row * p.n + col, p.n, warp_rows,
+                              static_cast<int>(p.n) - col, stage_blks, lane, packed);
+            }
           }
         }
       }
