@@ -103,19 +103,22 @@ fme_status encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint
   return FME_OK;
 }
 
-// bf16 (or fp32) matrix [rows x cols] (row stride cols * 2 or 4 bytes) for bulk tensor stores
-// of boxes of 32 rows x 64 bytes with the 64-byte swizzle.
-fme_status encode_bf16_out(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, bool fp32 = false) {
+// bf16 matrix [rows x cols] (row stride cols * 2 bytes) for bulk tensor stores of
+// 32 x 32 boxes with the 64-byte swizzle.  kWide..: boxes of 32 rows x 128 bytes with the
+// 128-byte swizzle, bf16 or fp32.
+enum class OutBox { kBf16, kWideBf16, kWideFp32 };
+fme_status encode_bf16_out(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, OutBox kind = OutBox::kBf16) {
   EncodeTiledFn fn;
   fme_status st = get_encoder(&fn);
   if (st != FME_OK) return st;
+  const bool fp32 = kind == OutBox::kWideFp32, wide = kind != OutBox::kBf16;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * (fp32 ? 4 : 2)};
-  cuuint32_t box[2] = {fp32 ? 16u : 32u, 32};
+  cuuint32_t box[2] = {kind == OutBox::kWideBf16 ? 64u : 32u, 32};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     char buf[96];
     std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled (output) failed (CUresult %d)", static_cast<int>(r));
@@ -765,8 +768,9 @@ fme_status block128_rows_gemm(bool dgrad, const uint8_t *a_codes, const float *a
                               int64_t k, void *y, int32_t *dev_status, void *stream, const char *what) {
   if (m < 0 || n < 0 || k < 0 || check_groups(num_experts) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
   if (!block128_cols(n) || !block128_cols(k)) return FME_ERR_UNSUPPORTED_SHAPE;
-  // row coordinates of the last, partly empty tiles stay in 32 bits
+  // row coordinates of the last, partly empty tiles and the number of tiles stay in 32 bits
   if (m > (int64_t(1) << 31) - 1 - 256) return FME_ERR_UNSUPPORTED_SHAPE;
+  if ((m / 64 + num_experts) * (((dgrad ? k : n) + 127) / 128) > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
   if (!offsets) return FME_ERR_INVALID_ARGUMENT;
   if (m == 0) return FME_OK;
   if (!a_codes || !a_scale || !w_codes || !w_scale || !y) return FME_ERR_INVALID_ARGUMENT;
@@ -782,7 +786,7 @@ fme_status block128_rows_gemm(bool dgrad, const uint8_t *a_codes, const float *a
   CUtensorMap &rows_map = few ? a.map_b : a.map_a, &w_map = few ? a.map_a : a.map_b;
   if ((st = encode_u8_2d(&rows_map, a_codes, a.k, m, a.k, few ? 16 : 128)) != FME_OK) return st;
   if ((st = encode_u8_weights(&w_map, w_codes, num_experts, n, k)) != FME_OK) return st;
-  if ((st = encode_bf16_out(&a.map_y, y, a.n, m)) != FME_OK) return st;
+  if ((st = encode_bf16_out(&a.map_y, y, a.n, m, OutBox::kWideBf16)) != FME_OK) return st;
   a.a_scale = a_scale;
   a.b_scale = w_scale;
   a.offsets = offsets;
@@ -875,6 +879,9 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
   if (dw_mode != FME_DW_BF16 && dw_mode != FME_DW_FP32 && dw_mode != FME_DW_FP32_ADD) return FME_ERR_INVALID_ARGUMENT;
   if (!block128_cols(n) || !block128_cols(k) || positions % 128 != 0 || positions > (int64_t(1) << 31) - 1)
     return FME_ERR_UNSUPPORTED_SHAPE;
+  if (num_experts * ((n + 255) / 256) * ((k + 255) / 256) > (int64_t(1) << 31) - 1 ||
+      num_experts * n > (int64_t(1) << 31) - 1 - 256)
+    return FME_ERR_UNSUPPORTED_SHAPE;
   if (!padded_offsets || !dw) return FME_ERR_INVALID_ARGUMENT;
   if (positions > 0 && (!dy_codes || !dy_scale || !x_codes || !x_scale)) return FME_ERR_INVALID_ARGUMENT;
   if (!aligned16(dy_codes) || !aligned16(dy_scale) || !aligned16(x_codes) || !aligned16(x_scale) || !aligned16(dw) ||
@@ -889,7 +896,8 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
   const int64_t extent = positions ? positions : 1;
   if ((st = encode_u8_2d(&a.map_a, abase, n, extent, n, 128)) != FME_OK) return st;
   if ((st = encode_u8_2d(&a.map_b, bbase, k, extent, k, 128)) != FME_OK) return st;
-  if ((st = encode_bf16_out(&a.map_y, dw, k, static_cast<uint64_t>(num_experts) * n, dw_mode != FME_DW_BF16)) != FME_OK)
+  if ((st = encode_bf16_out(&a.map_y, dw, k, static_cast<uint64_t>(num_experts) * n,
+                            dw_mode == FME_DW_BF16 ? OutBox::kWideBf16 : OutBox::kWideFp32)) != FME_OK)
     return st;
   a.a_scale = dy_scale;
   a.b_scale = x_scale;

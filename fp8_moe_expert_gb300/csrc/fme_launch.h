@@ -123,7 +123,7 @@ cudaError_t launch_fp8_block128_weights(const LaunchFp8Quant &a);
 // FP8 block-128 grouped GEMMs (gemm_block128.cu).
 struct LaunchBlock128 {
   CUtensorMap map_a, map_b;  // codes, 128 x 128-byte boxes, 128-byte swizzle (map_b 3-D [experts][n][k] but for wgrad)
-  CUtensorMap map_y;         // output, boxes of 32 rows x 64 bytes, 64-byte swizzle
+  CUtensorMap map_y;         // output, boxes of 32 rows x 128 bytes, 128-byte swizzle
   const float *a_scale, *b_scale;
   const int32_t *offsets;  // rows (forward, dgrad) or padded positions (wgrad) of each expert
   int32_t num_experts;

@@ -43,11 +43,12 @@ constexpr int kThreads128 = 384;
 constexpr int kEpiWarp0 = 4;
 constexpr int kStageBytes128 = kABytes + kBBytes;
 constexpr int kStages128 = 4;
-constexpr int kOutBlocks = 4;                // 2 KB staging blocks a warp: its 32 x 128 bf16 outputs of a tile
+constexpr int kOutBlocks = 2;                // staging blocks a warp: its 32 x 128 bf16 outputs of a tile
+constexpr int kOutBlockBytes = 32 * 128;
 constexpr int kScaleWarp0 = 2;                // and 3
 constexpr int kScaleSlots = 4;                // blocks whose scales are in shared memory
 constexpr int kScaleSlotFloats = 128 + kBN;  // of the CTA's rows and the tile's columns (see scale_slot)
-constexpr int kStageOut = 8 * kOutBlocks * kOutBoxBytes + kScaleSlots * kScaleSlotFloats * 4;
+constexpr int kStageOut = 8 * kOutBlocks * kOutBlockBytes + kScaleSlots * kScaleSlotFloats * 4;
 
 enum class Kind128 { kFwd, kDgrad, kWgrad };
 
@@ -156,26 +157,27 @@ struct Tile128 {
   int32_t p0;          // wgrad: first padded position
 };
 
+// Tiles and their counts are in 32 bits (checked on the host).
 template <Kind128 K>
-__device__ __forceinline__ Tile128 tile128(const LaunchBlock128 &p, const Tables &s, int64_t t, int rank) {
+__device__ __forceinline__ Tile128 tile128(const LaunchBlock128 &p, const Tables &s, uint32_t t, int rank) {
   Tile128 tl;
-  const int64_t nb = (p.n + kBN - 1) / kBN;
+  const uint32_t nb = (static_cast<uint32_t>(p.n) + kBN - 1) / kBN;
   if constexpr (K == Kind128::kWgrad) {
-    const int64_t mb = (p.m + kPairM - 1) / kPairM;
-    const int64_t order = t / (mb * nb);
-    const int64_t rem = t - order * (mb * nb);
-    const int64_t row = rem / nb;
+    const uint32_t per = (static_cast<uint32_t>(p.m) + kPairM - 1) / kPairM * nb;
+    const uint32_t order = t / per;
+    const uint32_t rem = t - order * per;
+    const uint32_t row = rem / nb;
     tl.e = s.aux[order];
     tl.p0 = s.off[tl.e];
     tl.nk = (s.off[tl.e + 1] - tl.p0) >> 7;
     tl.row0 = static_cast<int32_t>(row * kPairM + rank * kBM);
-    tl.rows_valid = static_cast<int32_t>(min(int64_t(kBM), p.m - tl.row0));
+    tl.rows_valid = min(kBM, static_cast<int32_t>(p.m) - tl.row0);
     tl.col0 = static_cast<int32_t>((rem - row * nb) * kBN);
   } else {
-    const int64_t g = t / nb;
+    const uint32_t g = t / nb;
     tl.col0 = static_cast<int32_t>((t - g * nb) * kBN);
     tl.e = find_group(s.aux, p.num_experts, g);
-    const int32_t first = static_cast<int32_t>(g - s.aux[tl.e]) * kPairM + rank * kBM;
+    const int32_t first = (static_cast<int32_t>(g) - s.aux[tl.e]) * kPairM + rank * kBM;
     tl.row0 = s.off[tl.e] + first;
     tl.rows_valid = min(kBM, s.off[tl.e + 1] - s.off[tl.e] - first);
     tl.nk = static_cast<int32_t>((p.k + 127) >> 7);
@@ -242,15 +244,15 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
   uint8_t *smem_a = smem;
   uint8_t *smem_b = smem_a + S * kABytes;
   uint8_t *smem_out = smem + S * kStageBytes128;
-  float *scales = reinterpret_cast<float *>(smem_out + 8 * kOutBlocks * kOutBoxBytes);
+  float *scales = reinterpret_cast<float *>(smem_out + 8 * kOutBlocks * kOutBlockBytes);
   int32_t *gmem = reinterpret_cast<int32_t *>(smem_out + kStageOut);
   const Tables tab{gmem, gmem + (p.num_experts + 1)};
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(pair::cta_rank());
-  const int64_t pair_id = blockIdx.x >> 1;
-  const int64_t pairs = gridDim.x >> 1;
+  const uint32_t pair_id = blockIdx.x >> 1;
+  const uint32_t pairs = gridDim.x >> 1;
 
   // ---- tables (both CTAs of a pair see the same offsets and take the same way out)
   if constexpr (K == Kind128::kWgrad) {
@@ -326,9 +328,10 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   volatile int *abort_flag = &s.abort_flag;
-  const int64_t nb = (p.n + kBN - 1) / kBN;
-  const int64_t total = K == Kind128::kWgrad ? p.num_experts * ((p.m + kPairM - 1) / kPairM) * nb
-                                             : static_cast<int64_t>(tab.aux[p.num_experts]) * nb;
+  const uint32_t nb = static_cast<uint32_t>((p.n + kBN - 1) / kBN);
+  const uint32_t total =
+      (K == Kind128::kWgrad ? p.num_experts * static_cast<uint32_t>((p.m + kPairM - 1) / kPairM) : tab.aux[p.num_experts]) *
+      nb;
 
   if (warp < kEpiWarp0) {
     // 128 threads x 56 + 256 x 224 registers = the launch's 384 x 168
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       // -------------------------------------------------------------- producer
       uint32_t stage = 0, filled = 0;
       bool stop = false;
-      for (int64_t t = pair_id; t < total && !stop; t += pairs) {
+      for (uint32_t t = pair_id; t < total && !stop; t += pairs) {
         const Tile128 tl = tile128<K>(p, tab, t, rank);
         for (int i = 0; i < tl.nk; ++i) {
           if (!mbar_wait<true>(&s.freed[stage], ((filled / S) & 1) ^ 1, abort_flag, p.status)) {
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       const uint64_t a_desc = desc_sw128(smem_u32(smem_a), kAmn), b_desc = desc_sw128(smem_u32(smem_b), kBmn);
       uint32_t stage = 0, phase = 0, fill = 0;
       bool stop = false;
-      for (int64_t t = pair_id; t < total && !stop; t += pairs) {
+      for (uint32_t t = pair_id; t < total && !stop; t += pairs) {
         const int nk = tile128<K>(p, tab, t, 0).nk;
         for (int i = 0; i < nk; ++i) {
           const uint32_t b = fill & 1;
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       bool stop = false;
       const int64_t kb_count = (p.k + 127) >> 7;
       const int64_t nb128 = (p.n + 127) >> 7;
-      for (int64_t t = pair_id; t < total && !stop; t += pairs) {
+      for (uint32_t t = pair_id; t < total && !stop; t += pairs) {
         const Tile128 tl = tile128<K>(p, tab, t, rank);
         const float *a = p.a_scale + (K == Kind128::kWgrad ? (tl.p0 >> 7) * p.m : int64_t(0)) + tl.row0;
         for (int i = 0; i < tl.nk; ++i, ++g) {
@@ -462,13 +465,16 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
     const int q = warp & 3;         // tensor-memory lane quarter
     const int half = ew >> 2;       // column half of the tile
     const int r = q * 32 + lane;    // row of the CTA's 128
-    uint8_t *stage_blks = smem_out + ew * kOutBlocks * kOutBoxBytes;
+    uint8_t *stage_blks = smem_out + ew * kOutBlocks * kOutBlockBytes;
     const uint32_t leader_empty[2] = {pair::map_to_rank(&s.acc_empty[0], 0), pair::map_to_rank(&s.acc_empty[1], 0)};
     const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     uint32_t g = 0;
     bool stop = false;
-    for (int64_t t = pair_id; t < total && !stop; t += pairs) {
-      const Tile128 tl = tile128<K>(p, tab, t, rank);
+    Tile128 next{};
+    if (pair_id < total) next = tile128<K>(p, tab, pair_id, rank);
+    for (uint32_t t = pair_id; t < total && !stop; t += pairs) {
+      const Tile128 tl = next;
+      if (t + pairs < total) next = tile128<K>(p, tab, t + pairs, rank);  // while the MMAs of this one run
       const int c0 = tl.col0 + half * 128;
       const bool in_cols = c0 < p.n;
       float2 acc[64];
@@ -528,10 +534,11 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       const int warp_rows = tl.rows_valid - 32 * q;
       if (warp_rows <= 0 || !in_cols) continue;
       const int64_t out_row = (K == Kind128::kWgrad ? tl.e * p.m : int64_t(0)) + tl.row0 + 32 * q;
-      // 2 KB blocks of 32 rows x 32 bf16 or 16 fp32 columns in the warp's staging area.  A
-      // whole one leaves by a bulk store: four blocks are written, made visible and stored together
-      // (one wait, one fence); one cut by the output's edge, and sums added to dW, by plain stores.
-      const int xs = (lane >> 1) & 3;  // the 64-byte swizzle of this lane's row
+      // 4 KB blocks of 32 rows x 64 bf16 or 32 fp32 columns in the warp's staging area.  A whole
+      // one leaves by a bulk store: two blocks are written, made visible and stored together (one
+      // wait, one fence, two stores: issuing a store takes a few hundred cycles next to the loads); one
+      // cut by the output's edge, and sums added to dW, by plain stores.
+      const int xs = lane & 7;  // the 128-byte swizzle of this lane's row
       auto await_staging = [&] {
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
@@ -541,26 +548,26 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
 #pragma unroll
       for (int half_tile = 0; half_tile < (K == Kind128::kWgrad ? 2 : 1); ++half_tile) {
         if (!fp32 && half_tile == 1) break;
-        const int wide = fp32 ? 16 : 32;  // columns of a block
+        const int wide = fp32 ? 32 : 64;  // columns of a block
         const int base = c0 + half_tile * 64;
-        const int whole = fp32 && p.accumulate ? 0 : warp_rows >= 32 ? min(4, max(0, static_cast<int>(p.n) - base) / wide) : 0;
         if (base >= p.n) break;
+        const int whole = (fp32 && p.accumulate) || warp_rows < 32 ? 0 : min(2, (static_cast<int>(p.n) - base) / wide);
         await_staging();
         if (whole > 0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint4 *row = reinterpret_cast<uint4 *>(stage_blks + c * kOutBoxBytes + lane * 64);
+          for (int c = 0; c < 2; ++c) {
+            uint4 *row = reinterpret_cast<uint4 *>(stage_blks + c * kOutBlockBytes + lane * 128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
               uint4 v;
               if (fp32) {
-                const float2 lo = acc[32 * half_tile + 8 * c + 2 * j], hi = acc[32 * half_tile + 8 * c + 2 * j + 1];
+                const float2 lo = acc[32 * half_tile + 16 * c + 2 * j], hi = acc[32 * half_tile + 16 * c + 2 * j + 1];
                 v = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
               } else {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * c + 4 * j + i].x, acc[16 * c + 4 * j + i].y);
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(acc[32 * c + 4 * j + i].x, acc[32 * c + 4 * j + i].y);
                   w[i] = *reinterpret_cast<const uint32_t *>(&h);
                 }
                 v = make_uint4(w[0], w[1], w[2], w[3]);
@@ -572,20 +579,26 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
           __syncwarp();
           if (lane == 0) {
             for (int c = 0; c < whole; ++c)
-              tma_store_2d(&p.map_y, base + wide * c, static_cast<int32_t>(out_row), stage_blks + c * kOutBoxBytes);
+              tma_store_2d(&p.map_y, base + wide * c, static_cast<int32_t>(out_row), stage_blks + c * kOutBlockBytes);
             bulk_commit();
           }
         }
-        if (whole < 4 && base + wide * whole < p.n) {
+        if (whole < 2 && base + wide * whole < p.n) {
           await_staging();
+          const int done = base + wide * whole;  // columns before it are stored
+          if (fp32) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int col = base + wide * c;
-            if (c < whole || col >= p.n) continue;
-            if (fp32) {
-              store_fp32_cut(static_cast<float *>(p.y) + out_row * p.n + col, p.n, warp_rows, 16, p.accumulate,
-                             stage_blks, lane, acc + 32 * half_tile + 8 * c);
-            } else {
+            for (int c = 0; c < 4; ++c) {
+              const int col = base + 16 * c;
+              if (col >= done && col < p.n)
+                store_fp32_cut(static_cast<float *>(p.y) + out_row * p.n + col, p.n, warp_rows, 16, p.accumulate,
+                               stage_blks, lane, acc + 32 * half_tile + 8 * c);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int col = base + 32 * c;
+              if (col < done || col >= p.n) continue;
               uint32_t packed[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
