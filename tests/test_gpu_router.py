@@ -220,10 +220,11 @@ def test_balance_loss_and_gradient(tokens, experts, top_k, seqs, score, masked, 
     assert fme.read_device_status(st)[0] == 0
     clean = torch.where(on[:, None], l, torch.zeros_like(l)).double().requires_grad_(True)
     loss64, counts64, n64 = balance64(clean, ids, score, 0.3, host, on)
+    value64 = float(loss64.detach())
     assert torch.equal(counts.long(), counts64) and n.tolist() == n64
     # all terms are positive: their sums are within (tokens + experts + sequences) u of themselves at most
     tol = slack(experts, clean.detach()) + (tokens + experts + seqs) * 2.0 ** -24
-    assert abs(loss.item() - float(loss64)) <= tol * abs(float(loss64))
+    assert abs(loss.item() - value64) <= tol * abs(value64)
 
     again = fme.moe_balance_loss(l, ids, **kw)
     assert torch.equal(loss, again[0])
