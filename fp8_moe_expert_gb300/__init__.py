@@ -1,10 +1,12 @@
 """GB300-native low-precision MoE expert path: NVFP4 per-token forward, MXFP8 backward.
 
-A thin ctypes binding over ``libfme.so`` (C ABI in ``include/fme.h``).  Every
-step of the path runs in the library's CUDA kernels; this module only turns
-torch tensors into pointers, allocates outputs with torch when the caller does
-not pass them, and turns status codes into exceptions.  There is no fallback:
-if the library is missing or the device is not a GB300, calls raise.
+A thin binding over ``libfme.so`` (C ABI in ``include/fme.h``): ctypes, and a compiled
+module for the FP8 block-128 and router calls, whose host side would outlast
+their kernels in Python.  Every step of the path runs in the library's CUDA
+kernels; the binding only turns torch tensors into pointers, allocates outputs
+with torch when the caller does not pass them, and turns status codes into
+exceptions.  There is no fallback: if the library is missing or the device is not
+a GB300, calls raise.
 """
 from __future__ import annotations
 
@@ -183,21 +185,6 @@ def _empty(shape, dtype, device):
     import torch
 
     return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _need(where, name, t, dtype, shape):
-    """Raise unless t is a contiguous CUDA tensor of this dtype and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor of {dtype} {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ' (not contiguous)'}")
-
-
-def _out(where, name, t, dtype, shape, device):
-    """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return _empty(shape, dtype, device)
-    _need(where, name, t, dtype, shape)
-    return t
 
 
 # --------------------------------------------------------------- the five calls --
@@ -548,6 +535,31 @@ def grouped_gemm_wgrad_mxfp8_accumulate(a_codes, a_sf, lda, b_codes, b_sf, ldb, 
 
 
 # ------------------------------------------------------------ FP8 block-128 --
+_native = None
+
+
+def _bind():
+    """The compiled half of the binding (csrc/binding.cpp): checks the tensors (ValueError), allocates outputs, calls
+    the library.  Raises if it has not been built."""
+    global _native
+    if _native is None:
+        lib()
+        import torch  # noqa: F401  (the module's symbols come from torch's libraries)
+
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the binding is missing or was built for another torch: build it with "
+                               "`python -m fp8_moe_expert_gb300.build`") from e
+        _binding.set_error(FmeError)
+        _native = _binding
+    return _native
+
+
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
+
+
 def quantize_fp8_block128(x, axis=ROWWISE, offsets=None, num_groups=None, *, src_row=None, top_k=1, codes=None,
                           scale=None, padded_offsets=None, status=None, stream=None):
     """FP8 (E4M3) of bf16 x [rows, cols] with one fp32 scale per 128 values.
@@ -556,114 +568,41 @@ def quantize_fp8_block128(x, axis=ROWWISE, offsets=None, num_groups=None, *, src
     (int32 [tokens*top_k], from moe_route) the rows are x[src_row // top_k].
     COLWISE -> (codes [ld, cols] u8, scale [ld/128, cols] f32, padded_offsets [G+1] i32),
     blocks along each group's rows, each group padded with zeros to a multiple of 128."""
-    import torch
-
-    where = "quantize_fp8_block128"
-    rows, cols = x.shape
-    dev = x.device
-    _need(where, "x", x, torch.bfloat16, x.shape)
     if axis == ROWWISE:
-        if src_row is not None:
-            _need(where, "src_row", src_row, torch.int32, (rows * top_k,))
-        out = rows * top_k if src_row is not None else rows
-        codes = _out(where, "codes", codes, torch.uint8, (out, cols), dev)
-        scale = _out(where, "scale", scale, torch.float32, ((cols + 127) // 128, out), dev)
-        if src_row is not None:
-            st = lib().permute_quantize_fp8_block128(_ptr(x), rows, cols, _ptr(src_row), top_k, _ptr(codes),
-                                                     _ptr(scale), _ptr(status), _stream(stream))
-        else:
-            st = lib().quantize_fp8_block128(_ptr(x), rows, cols, axis, None, 1, _ptr(codes), _ptr(scale), None,
-                                             _ptr(status), _stream(stream))
-        _check(st, where)
-        return codes, scale
+        return _bind().quantize_rows(x, src_row, top_k, codes, scale, status, _raw(stream))
+    if axis != COLWISE:
+        raise FmeError(ERR_INVALID_ARGUMENT, "quantize_fp8_block128")
     if src_row is not None:
-        raise ValueError(f"{where}: src_row is for ROWWISE only")
-    offsets, g = _groups(offsets, num_groups)
-    if offsets is not None:
-        _need(where, "offsets", offsets, torch.int32, (g + 1,))
-    ld = colwise_ld(rows, g)
-    codes = _out(where, "codes", codes, torch.uint8, (ld, cols), dev)
-    scale = _out(where, "scale", scale, torch.float32, (ld // 128, cols), dev)
-    padded_offsets = _out(where, "padded_offsets", padded_offsets, torch.int32, (g + 1,), dev)
-    st = lib().quantize_fp8_block128(_ptr(x), rows, cols, axis, _ptr(offsets), g, _ptr(codes), _ptr(scale),
-                                     _ptr(padded_offsets), _ptr(status), _stream(stream))
-    _check(st, where)
-    return codes, scale, padded_offsets
+        raise ValueError("quantize_fp8_block128: src_row is for ROWWISE only")
+    return _bind().quantize_cols(x, offsets, num_groups, codes, scale, padded_offsets, status, _raw(stream))
 
 
 def quantize_fp8_block128_rowcol(x, offsets=None, num_groups=None, *, row_codes=None, row_scale=None, col_codes=None,
                                  col_scale=None, padded_offsets=None, status=None, stream=None):
     """Both layouts of quantize_fp8_block128 from one read of x ->
     ((row_codes, row_scale), (col_codes, col_scale, padded_offsets))."""
-    import torch
-
-    where = "quantize_fp8_block128_rowcol"
-    rows, cols = x.shape
-    dev = x.device
-    _need(where, "x", x, torch.bfloat16, x.shape)
-    offsets, g = _groups(offsets, num_groups)
-    if offsets is not None:
-        _need(where, "offsets", offsets, torch.int32, (g + 1,))
-    ld = colwise_ld(rows, g)
-    row_codes = _out(where, "row_codes", row_codes, torch.uint8, (rows, cols), dev)
-    row_scale = _out(where, "row_scale", row_scale, torch.float32, ((cols + 127) // 128, rows), dev)
-    col_codes = _out(where, "col_codes", col_codes, torch.uint8, (ld, cols), dev)
-    col_scale = _out(where, "col_scale", col_scale, torch.float32, (ld // 128, cols), dev)
-    padded_offsets = _out(where, "padded_offsets", padded_offsets, torch.int32, (g + 1,), dev)
-    st = lib().quantize_fp8_block128_rowcol(_ptr(x), rows, cols, _ptr(offsets), g, _ptr(row_codes), _ptr(row_scale),
-                                            _ptr(col_codes), _ptr(col_scale), _ptr(padded_offsets), _ptr(status),
-                                            _stream(stream))
-    _check(st, where)
-    return (row_codes, row_scale), (col_codes, col_scale, padded_offsets)
+    r = _bind().quantize_rowcol(x, offsets, num_groups, row_codes, row_scale, col_codes, col_scale, padded_offsets,
+                                status, _raw(stream))
+    return r[:2], r[2:]
 
 
 def quantize_fp8_block128_weights(w, *, codes=None, scale=None, stream=None):
     """FP8 of expert weights w [E, n, k] (bf16) with one fp32 scale per 128 x 128 block ->
     (codes [E, n, k] u8, scale [E, ceil(n/128), ceil(k/128)] f32)."""
-    import torch
-
-    where = "quantize_fp8_block128_weights"
-    e, n, k = w.shape
-    _need(where, "w", w, torch.bfloat16, w.shape)
-    codes = _out(where, "codes", codes, torch.uint8, (e, n, k), w.device)
-    scale = _out(where, "scale", scale, torch.float32, (e, (n + 127) // 128, (k + 127) // 128), w.device)
-    st = lib().quantize_fp8_block128_weights(_ptr(w), e, n, k, _ptr(codes), _ptr(scale), _stream(stream))
-    _check(st, where)
-    return codes, scale
-
-
-def _block128_rows_gemm(where, a_codes, a_scale, w_codes, w_scale, offsets, inner, out_cols, y, status, stream):
-    import torch
-
-    e, n, k = w_codes.shape
-    m = a_codes.shape[0]
-    _need(where, "a_codes", a_codes, torch.uint8, (m, inner))
-    _need(where, "a_scale", a_scale, torch.float32, ((inner + 127) // 128, m))
-    _need(where, "w_codes", w_codes, torch.uint8, (e, n, k))
-    _need(where, "w_scale", w_scale, torch.float32, (e, (n + 127) // 128, (k + 127) // 128))
-    _need(where, "offsets", offsets, torch.int32, (e + 1,))
-    y = _out(where, "y", y, torch.bfloat16, (m, out_cols), a_codes.device)
-    st = getattr(lib(), where)(_ptr(a_codes), _ptr(a_scale), _ptr(w_codes), _ptr(w_scale), _ptr(offsets), e, m, n, k,
-                               _ptr(y), _ptr(status), _stream(stream))
-    _check(st, where)
-    return y
+    return _bind().quantize_weights(w, codes, scale, _raw(stream))
 
 
 def grouped_gemm_fwd_fp8_block128(a_codes, a_scale, w_codes, w_scale, offsets, *, y=None, status=None, stream=None):
     """Y [m, n] (bf16) = X_e W_e^T per expert, from quantize_fp8_block128(ROWWISE) of
     X [m, k] and quantize_fp8_block128_weights of W [E, n, k]."""
-    _, n, k = w_codes.shape
-    return _block128_rows_gemm("grouped_gemm_fwd_fp8_block128", a_codes, a_scale, w_codes, w_scale, offsets, k, n, y,
-                               status, stream)
+    return _bind().fwd(a_codes, a_scale, w_codes, w_scale, offsets, y, status, _raw(stream))
 
 
 def grouped_gemm_dgrad_fp8_block128(dy_codes, dy_scale, w_codes, w_scale, offsets, *, dx=None, status=None,
                                     stream=None):
     """dX [m, k] (bf16) = dY_e W_e per expert, from quantize_fp8_block128(ROWWISE) of
     dY [m, n] and the forward's weight codes."""
-    _, n, k = w_codes.shape
-    return _block128_rows_gemm("grouped_gemm_dgrad_fp8_block128", dy_codes, dy_scale, w_codes, w_scale, offsets, n, k,
-                               dx, status, stream)
+    return _bind().dgrad(dy_codes, dy_scale, w_codes, w_scale, offsets, dx, status, _raw(stream))
 
 
 def grouped_gemm_wgrad_fp8_block128(dy_codes, dy_scale, x_codes, x_scale, padded_offsets, *, dw=None, dtype=None,
@@ -673,90 +612,28 @@ def grouped_gemm_wgrad_fp8_block128(dy_codes, dy_scale, x_codes, x_scale, padded
     the result is added into dw (float32)."""
     import torch
 
-    where = "grouped_gemm_wgrad_fp8_block128"
-    ld, n = dy_codes.shape
-    k = x_codes.shape[1]
-    e = padded_offsets.shape[0] - 1
-    dtype = dtype or (dw.dtype if dw is not None else torch.bfloat16)
+    if dtype is None:
+        dtype = torch.bfloat16 if dw is None else dw.dtype
     if dtype not in (torch.bfloat16, torch.float32) or (accumulate and (dw is None or dtype != torch.float32)):
-        raise ValueError(f"{where}: dw is bfloat16 or float32, and a given float32 tensor to accumulate into")
-    _need(where, "dy_codes", dy_codes, torch.uint8, (ld, n))
-    _need(where, "dy_scale", dy_scale, torch.float32, (ld // 128, n))
-    _need(where, "x_codes", x_codes, torch.uint8, (ld, k))
-    _need(where, "x_scale", x_scale, torch.float32, (ld // 128, k))
-    _need(where, "padded_offsets", padded_offsets, torch.int32, (e + 1,))
-    dw = _out(where, "dw", dw, dtype, (e, n, k), dy_codes.device)
+        raise ValueError("grouped_gemm_wgrad_fp8_block128: dw is bfloat16 or float32, and a given float32 tensor to "
+                         "accumulate into")
     mode = DW_BF16 if dtype == torch.bfloat16 else DW_FP32_ADD if accumulate else DW_FP32
-    st = lib().grouped_gemm_wgrad_fp8_block128(_ptr(dy_codes), _ptr(dy_scale), _ptr(x_codes), _ptr(x_scale), ld,
-                                               _ptr(padded_offsets), e, n, k, _ptr(dw), mode, _ptr(status),
-                                               _stream(stream))
-    _check(st, where)
-    return dw
+    return _bind().wgrad(dy_codes, dy_scale, x_codes, x_scale, padded_offsets, dw, mode, status, _raw(stream))
 
 
 # ------------------------------------------------------------------- router --
-SCORES = {"softmax": 0, "sigmoid": 1}
-
-
-def _router(where, logits, top_k, score):
-    """(tokens, experts, dtype code, score code) of checked router arguments."""
-    import torch
-
-    tokens, experts = logits.shape
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{where}: logits must be bfloat16 or float32, got {logits.dtype}")
-    _need(where, "logits", logits, logits.dtype, logits.shape)
-    if score not in SCORES:
-        raise ValueError(f"{where}: score must be 'softmax' or 'sigmoid', got {score!r}")
-    return tokens, experts, 0 if logits.dtype == torch.bfloat16 else 1, SCORES[score]
-
-
-def _sequences(where, tokens, seq_offsets, token_mask):
-    import torch
-
-    if seq_offsets is not None:
-        _need(where, "seq_offsets", seq_offsets, torch.int32, (seq_offsets.shape[0],))
-    if token_mask is not None:
-        if token_mask.dtype not in (torch.bool, torch.uint8):
-            raise ValueError(f"{where}: token_mask must be bool or uint8, got {token_mask.dtype}")
-        _need(where, "token_mask", token_mask, token_mask.dtype, (tokens,))
-    return 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-
-
 def moe_gate(logits, top_k, *, score="softmax", bias=None, normalize=True, scale=1.0, ids=None, weights=None,
              stream=None):
     """The top_k experts of each token by logits [tokens, E] (+ bias [E]), largest first, and
     their weights, scale * s / sum of the chosen s (normalize) or scale * s, s the softmax or
     sigmoid of the logits -> (ids [tokens, top_k] int32, weights [tokens, top_k] f32)."""
-    import torch
-
-    where = "moe_gate"
-    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
-    if bias is not None:
-        _need(where, "bias", bias, torch.float32, (experts,))
-    ids = _out(where, "ids", ids, torch.int32, (tokens, top_k), logits.device)
-    weights = _out(where, "weights", weights, torch.float32, (tokens, top_k), logits.device)
-    st = lib().moe_gate(_ptr(logits), dtype, tokens, experts, top_k, kind, int(normalize), scale, _ptr(bias), _ptr(ids),
-                        _ptr(weights), _stream(stream))
-    _check(st, where)
-    return ids, weights
+    return _bind().gate(logits, top_k, score, bias, normalize, scale, ids, weights, _raw(stream))
 
 
 def moe_gate_backward(logits, ids, d_weights, *, score="softmax", normalize=True, scale=1.0, d_logits=None, status=None,
                       stream=None):
     """The gradient of moe_gate's weights -> d_logits [tokens, E] in the logits' type."""
-    import torch
-
-    where = "moe_gate_backward"
-    top_k = ids.shape[1]
-    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
-    _need(where, "ids", ids, torch.int32, (tokens, top_k))
-    _need(where, "d_weights", d_weights, torch.float32, (tokens, top_k))
-    d_logits = _out(where, "d_logits", d_logits, logits.dtype, (tokens, experts), logits.device)
-    st = lib().moe_gate_backward(_ptr(logits), dtype, _ptr(ids), _ptr(d_weights), tokens, experts, top_k, kind,
-                                 int(normalize), scale, _ptr(d_logits), _ptr(status), _stream(stream))
-    _check(st, where)
-    return d_logits
+    return _bind().gate_backward(logits, ids, d_weights, score, normalize, scale, d_logits, status, _raw(stream))
 
 
 def balance_workspace_bytes(tokens: int, num_seqs: int, num_experts: int) -> int:
@@ -770,68 +647,29 @@ def moe_balance_loss(logits, ids, *, score="softmax", alpha=1.0, seq_offsets=Non
 
     seq_offsets: int32 [S+1], rising from 0 to tokens (None: one sequence); token_mask: bool or
     uint8 [tokens], the tokens that count (None: all)."""
-    import torch
+    if stream is not None and workspace is None:
+        seqs = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+        import torch
 
-    where = "moe_balance_loss"
-    top_k = ids.shape[1]
-    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
-    _need(where, "ids", ids, torch.int32, (tokens, top_k))
-    seqs = _sequences(where, tokens, seq_offsets, token_mask)
-    dev = logits.device
-    loss = _out(where, "loss", loss, torch.float32, (1,), dev)
-    counts = _out(where, "counts", counts, torch.int32, (seqs, experts), dev)
-    seq_tokens = _out(where, "seq_tokens", seq_tokens, torch.int32, (seqs,), dev)
-    if workspace is None:
-        workspace = _empty((balance_workspace_bytes(tokens, seqs, experts),), torch.uint8, dev)
-        if stream is not None:
-            workspace.record_stream(stream)  # it is released when this call returns
-    st = lib().moe_balance_loss(_ptr(logits), dtype, _ptr(ids), tokens, experts, top_k, kind, alpha, _ptr(seq_offsets),
-                                seqs, _ptr(token_mask), _ptr(loss), _ptr(counts), _ptr(seq_tokens), _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
-    _check(st, where)
-    return loss, counts, seq_tokens
+        workspace = _empty((balance_workspace_bytes(logits.shape[0], seqs, logits.shape[1]),), torch.uint8,
+                           logits.device)
+        workspace.record_stream(stream)  # it is released when this call returns
+    return _bind().balance_loss(logits, ids, score, alpha, seq_offsets, token_mask, loss, counts, seq_tokens, workspace,
+                                status, _raw(stream))
 
 
 def moe_balance_loss_backward(logits, counts, seq_tokens, d_loss, top_k, *, score="softmax", alpha=1.0,
                               seq_offsets=None, token_mask=None, d_logits=None, accumulate=False, stream=None):
     """The gradient of d_loss [1] times moe_balance_loss -> d_logits [tokens, E] in the logits'
     type; with accumulate it is added to the given d_logits."""
-    import torch
-
-    where = "moe_balance_loss_backward"
-    tokens, experts, dtype, kind = _router(where, logits, top_k, score)
-    seqs = _sequences(where, tokens, seq_offsets, token_mask)
-    _need(where, "counts", counts, torch.int32, (seqs, experts))
-    _need(where, "seq_tokens", seq_tokens, torch.int32, (seqs,))
-    _need(where, "d_loss", d_loss, torch.float32, (1,))
-    if accumulate and d_logits is None:
-        raise ValueError(f"{where}: accumulate needs the d_logits to add to")
-    d_logits = _out(where, "d_logits", d_logits, logits.dtype, (tokens, experts), logits.device)
-    st = lib().moe_balance_loss_backward(_ptr(logits), dtype, _ptr(counts), _ptr(seq_tokens), _ptr(d_loss), tokens,
-                                         experts, top_k, kind, alpha, _ptr(seq_offsets), seqs, _ptr(token_mask),
-                                         _ptr(d_logits), int(accumulate), _stream(stream))
-    _check(st, where)
-    return d_logits
+    return _bind().balance_loss_backward(logits, counts, seq_tokens, d_loss, top_k, score, alpha, seq_offsets, token_mask,
+                                         d_logits, accumulate, _raw(stream))
 
 
 def moe_combine_backward(d_out, y, row_of, weights, *, d_y=None, d_weights=None, status=None, stream=None):
     """The gradient of moe_combine for d_out [tokens, n] bf16 -> (d_y [rows_y, n] bf16,
     d_weights [tokens, top_k] f32)."""
-    import torch
-
-    where = "moe_combine_backward"
-    rows_y, n = y.shape
-    tokens, top_k = row_of.shape
-    _need(where, "d_out", d_out, torch.bfloat16, (tokens, n))
-    _need(where, "y", y, torch.bfloat16, (rows_y, n))
-    _need(where, "row_of", row_of, torch.int32, (tokens, top_k))
-    _need(where, "weights", weights, torch.float32, (tokens, top_k))
-    d_y = _out(where, "d_y", d_y, torch.bfloat16, (rows_y, n), y.device)
-    d_weights = _out(where, "d_weights", d_weights, torch.float32, (tokens, top_k), y.device)
-    st = lib().moe_combine_backward(_ptr(d_out), _ptr(y), rows_y, _ptr(row_of), _ptr(weights), tokens, top_k, n,
-                                    _ptr(d_y), _ptr(d_weights), _ptr(status), _stream(stream))
-    _check(st, where)
-    return d_y, d_weights
+    return _bind().combine_backward(d_out, y, row_of, weights, d_y, d_weights, status, _raw(stream))
 
 
 def read_device_status(status, stream=None) -> tuple[int, int]:

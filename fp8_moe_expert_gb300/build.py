@@ -1,4 +1,5 @@
-"""Build libfme.so (the CUDA library behind include/fme.h) for sm_103a with nvcc.
+"""Build libfme.so (the CUDA library behind include/fme.h) for sm_103a with nvcc, and
+the compiled half of its Python binding (csrc/binding.cpp) with the host compiler.
 
 Every translation unit is compiled in parallel, then linked into
 ``fp8_moe_expert_gb300/libfme.so`` (git-ignored, rebuilt on each machine: the
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -18,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIBRARY = os.path.join(HERE, "libfme.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quant_nvfp4.cu", "quant_mxfp8.cu", "gemm.cu", "gemm_nvfp4.cu", "route.cu",
            "quant_block128.cu", "gemm_block128.cu", "gate.cu"]
@@ -40,15 +43,52 @@ def _inputs() -> list[str]:
     return files
 
 
-def stale(output: str = LIBRARY) -> bool:
+def _older(output: str, inputs: list[str]) -> bool:
     if not os.path.exists(output):
         return True
     t = os.path.getmtime(output)
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return any(os.path.getmtime(f) > t for f in inputs)
+
+
+def _binding_inputs() -> list[str]:
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "fme.h")]
+
+
+def stale(output: str = LIBRARY) -> bool:
+    return _older(output, _inputs()) or (output == LIBRARY and _older(BINDING, _binding_inputs()))
+
+
+def _torch_dir() -> str:
+    import torch
+
+    return os.path.dirname(torch.__file__)
+
+
+def _build_binding_object(obj: str, env: dict) -> None:
+    """binding.cpp against the installed torch's headers (about 20 s)."""
+    include = [os.path.join(_torch_dir(), "include"), sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-DNDEBUG",
+           *(f"-I{p}" for p in include), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True, env=env)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
+
+
+def _link_binding(obj: str, env: dict) -> None:
+    tmp_out = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp_out, obj, LIBRARY, "-Wl,-rpath,$ORIGIN",
+           "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True, env=env)
+    if res.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp_out, BINDING)
 
 
 def build(output: str = LIBRARY, extra_flags: list[str] | None = None, verbose: bool = False) -> str:
-    """Compile and link the library; returns its path."""
+    """Compile and link the library (and, for the package's own, the binding); returns its path."""
+    binding = output == LIBRARY and _older(BINDING, _binding_inputs())
     flags = NVCC_FLAGS + (extra_flags or [])
     tool = nvcc()
     # objects and nvcc's own intermediates stay inside the package tree (git-ignored)
@@ -67,14 +107,20 @@ def build(output: str = LIBRARY, extra_flags: list[str] | None = None, verbose: 
                 sys.stderr.write(res.stdout + res.stderr)
             return obj
 
-        with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+        binding_obj = os.path.join(tmp, "binding.o")
+        with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+            pending = pool.submit(_build_binding_object, binding_obj, env) if binding else None
             objs = list(pool.map(compile_one, SOURCES))
+            if pending:
+                pending.result()
         tmp_out = output + ".tmp"
-        cmd = [tool, *ARCH, "-shared", "-o", tmp_out, *objs]
+        cmd = [tool, *ARCH, "-shared", "-Xlinker", "-soname=libfme.so", "-o", tmp_out, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True, env=env)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp_out, output)
+        if binding:
+            _link_binding(binding_obj, env)
     return output
 
 
