@@ -918,30 +918,29 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
 // ------------------------------------------------------------------ router --
 namespace {
 
-// Tokens of one sequence are summed by `slices` CTAs: two CTAs for every SM at most, 16 tokens at
-// least for each.  A function of the sizes alone, so that the workspace and the order of the
-// sums do not depend on the device.
-int32_t balance_slices(int64_t tokens, int64_t num_seqs) {
-  const int64_t by_size = (tokens + 16 * num_seqs - 1) / (16 * num_seqs);
-  int64_t s = 304 / num_seqs;
-  if (s > by_size) s = by_size;
-  return static_cast<int32_t>(s < 1 ? 1 : s);
+// Tokens are summed in equal chunks, a CTA each: two CTAs for every SM at most, 16 tokens (one a
+// warp) at least.  A function of the sizes alone, so that the workspace and the order of the sums do
+// not depend on the device.
+int64_t balance_chunk(int64_t tokens) {
+  const int64_t c = (tokens + 303) / 304;
+  return c < 16 ? 16 : c;
 }
 
 int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 
 struct BalanceWorkspace {
-  int64_t sums, counts, tokens, term, done, bytes;
+  int64_t sums, counts, tokens, term, flags, bytes;
 };
 BalanceWorkspace balance_workspace(int64_t tokens, int64_t num_seqs, int32_t num_experts) {
-  const int64_t parts = num_seqs * balance_slices(tokens, num_seqs);
+  const int64_t chunk = balance_chunk(tokens);
+  const int64_t slots = (tokens + chunk - 1) / chunk + num_seqs;
   BalanceWorkspace w;
   w.sums = 0;
-  w.counts = w.sums + round16(parts * num_experts * 4);
-  w.tokens = w.counts + round16(parts * num_experts * 4);
-  w.term = w.tokens + round16(parts * 4);
-  w.done = w.term + round16(num_seqs * ((num_experts + 31) / 32) * 4);
-  w.bytes = w.done + 16;
+  w.counts = w.sums + round16(slots * num_experts * 4);
+  w.tokens = w.counts + round16(slots * num_experts * 4);
+  w.term = w.tokens + round16(slots * 4);
+  w.flags = w.term + round16(num_seqs * ((num_experts + 31) / 32) * 4);
+  w.bytes = w.flags + 16;
   return w;
 }
 
@@ -1048,13 +1047,13 @@ fme_status moe_balance_loss(const void *logits, int32_t dtype, const int32_t *id
   a.loss = loss;
   a.counts = counts;
   a.seq_tokens = seq_tokens;
-  a.slices = balance_slices(tokens, num_seqs);
+  a.chunk = balance_chunk(tokens);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   a.part_sum = reinterpret_cast<float *>(base + w.sums);
   a.part_count = reinterpret_cast<int32_t *>(base + w.counts);
   a.part_tokens = reinterpret_cast<int32_t *>(base + w.tokens);
   a.term = reinterpret_cast<float *>(base + w.term);
-  a.done = reinterpret_cast<int32_t *>(base + w.done);
+  a.flags = reinterpret_cast<int32_t *>(base + w.flags);
   a.status = dev_status;
   a.stream = static_cast<cudaStream_t>(stream);
   cudaError_t err = fme::launch_balance_loss(a);

@@ -178,9 +178,9 @@ struct LaunchBalance {
   float *loss;
   int32_t *counts, *seq_tokens;
   // workspace
-  int32_t slices;
+  int64_t chunk;  // tokens a CTA
   float *part_sum, *term;
-  int32_t *part_count, *part_tokens, *done;
+  int32_t *part_count, *part_tokens, *flags;
   // gradient
   const float *d_loss;
   void *d_logits;

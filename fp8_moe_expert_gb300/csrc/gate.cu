@@ -342,8 +342,26 @@ __device__ __forceinline__ void probabilities(const float (&l)[V], bool softmax,
   }
 }
 
-// One CTA for each (sequence, slice): sums of p and counts of the slice's counted tokens into
-// the workspace, [sequence][slice][experts] each.  The order of every sum is fixed.
+// The last sequence that starts at or before token t (so empty ones are passed over): halving down
+// to 32 candidates, then all at once.  The whole warp calls it.
+__device__ __forceinline__ int64_t find_sequence(const int32_t *offsets, int64_t num_seqs, int64_t t, int lane) {
+  int64_t lo = 0, hi = num_seqs;
+  while (hi - lo > 32) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (__ldg(offsets + mid) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int64_t mine = lo + 1 + lane;
+  return lo + __popc(__ballot_sync(kAll, mine < hi && __ldg(offsets + mine) <= t));
+}
+
+// One CTA for `chunk` consecutive tokens: for each sequence that has some of them, the sums of p and
+// the counts of its counted tokens go to the workspace's slot chunk + sequence (along the tokens one
+// of the two grows from piece to piece, so no two pieces share a slot).  Equal chunks of tokens
+// rather than slices of each sequence, whose lengths may differ a hundredfold.  The order of every
+// sum is fixed.
 constexpr int kPartWarps = 16;
 
 template <typename T, int V, int VEC>
@@ -354,68 +372,83 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
   int32_t *cnt = reinterpret_cast<int32_t *>(smem + kHalf * experts);
   __shared__ int32_t n_tokens;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t seq = blockIdx.x / a.slices;
-  const int slice = static_cast<int>(blockIdx.x - seq * a.slices);
-  const int64_t lo = a.seq_offsets ? __ldg(a.seq_offsets + seq) : 0;
-  const int64_t hi = a.seq_offsets ? __ldg(a.seq_offsets + seq + 1) : a.tokens;
-  const bool bad = lo < 0 || hi < lo || hi > a.tokens || (seq == 0 && lo != 0) ||
-                   (seq == a.num_seqs - 1 && hi != a.tokens);
-  if (bad && threadIdx.x == 0) report(a.status, kDevBadOffsets);
-  for (int e = threadIdx.x; e < experts; e += blockDim.x) cnt[e] = 0;
-  if (threadIdx.x == 0) {
-    n_tokens = 0;
-    if (blockIdx.x == 0) *a.done = 0;  // of balance_final_kernel
-  }
-  __syncthreads();
-  const int64_t per = (hi - lo + a.slices - 1) / a.slices;
-  const int64_t t0 = lo + slice * per, t1 = bad ? t0 : min(hi, t0 + per);
-  float sum[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) sum[j] = 0.0f;
-  int mine = 0;
-  const T *logits = static_cast<const T *>(a.logits);
-  float next[V];  // the next token's row, loaded while this one is summed
-  if (t0 + warp < t1) load_row<T, V, VEC>(logits + (t0 + warp) * experts, experts, lane, next);
-  for (int64_t t = t0 + warp; t < t1; t += kPartWarps) {
-    float l[V], p[V], slope[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = next[j];
-    if (t + kPartWarps < t1) load_row<T, V, VEC>(logits + (t + kPartWarps) * experts, experts, lane, next);
-    if (a.token_mask && !__ldg(a.token_mask + t)) continue;
-    probabilities<V>(l, a.softmax, p, slope);
-#pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] += p[j];
-    ++mine;
-    if (lane < a.top_k) {
-      const int32_t e = __ldg(a.ids + t * a.top_k + lane);
-      if (e >= 0 && e < experts)
-        atomicAdd(&cnt[e], 1);
-      else
-        report(a.status, kDevBadIndex);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+  const int64_t c1 = min(a.tokens, c0 + a.chunk);
+  if (blockIdx.x == 0) {  // once: are the sequences well formed?
+    bool bad = false;
+    if (a.seq_offsets)
+      for (int64_t s = threadIdx.x; s <= a.num_seqs; s += blockDim.x) {
+        const int32_t v = __ldg(a.seq_offsets + s);
+        bad |= s == 0 ? v != 0 : v < __ldg(a.seq_offsets + s - 1);
+        bad |= s == a.num_seqs && v != a.tokens;
+      }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+      a.flags[0] = 0;  // CTAs of balance_final_kernel that are done
+      a.flags[1] = bad;
+      if (bad) report(a.status, kDevBadOffsets);
     }
   }
-  if (lane == 0 && mine) atomicAdd(&n_tokens, mine);
-  if (warp >= kHalf) {
+  const T *logits = static_cast<const T *>(a.logits);
+  float next[V];  // the next token's row, loaded while this one is summed
+  for (int64_t t0 = c0; t0 < c1;) {
+    int64_t seq = 0, t1 = c1;
+    if (a.seq_offsets) {
+      seq = find_sequence(a.seq_offsets, a.num_seqs, t0, lane);
+      t1 = min(c1, static_cast<int64_t>(__ldg(a.seq_offsets + seq + 1)));
+      if (t1 <= t0) break;  // malformed: no sequence holds t0
+    }
+    if (t0 + warp < t1) load_row<T, V, VEC>(logits + (t0 + warp) * experts, experts, lane, next);
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) cnt[e] = 0;
+    if (threadIdx.x == 0) n_tokens = 0;
+    __syncthreads();
+    float sum[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (expert_of<VEC>(j, lane) < experts) smem[(warp - kHalf) * experts + expert_of<VEC>(j, lane)] = sum[j];
-  }
-  __syncthreads();
-  if (warp < kHalf) {
+    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+    int mine = 0;
+    for (int64_t t = t0 + warp; t < t1; t += kPartWarps) {
+      float l[V], p[V], slope[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (expert_of<VEC>(j, lane) < experts) smem[warp * experts + expert_of<VEC>(j, lane)] += sum[j];
-  }
-  __syncthreads();
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * experts;
-  for (int e = threadIdx.x; e < experts; e += blockDim.x) {
-    float v = 0.0f;
+      for (int j = 0; j < V; ++j) l[j] = next[j];
+      if (t + kPartWarps < t1) load_row<T, V, VEC>(logits + (t + kPartWarps) * experts, experts, lane, next);
+      if (a.token_mask && !__ldg(a.token_mask + t)) continue;
+      if (lane < a.top_k) {
+        const int32_t e = __ldg(a.ids + t * a.top_k + lane);
+        if (e >= 0 && e < experts)
+          atomicAdd(&cnt[e], 1);
+        else
+          report(a.status, kDevBadIndex);
+      }
+      probabilities<V>(l, a.softmax, p, slope);
 #pragma unroll
-    for (int w = 0; w < kHalf; ++w) v += smem[w * experts + e];
-    a.part_sum[at + e] = v;
-    a.part_count[at + e] = cnt[e];
+      for (int j = 0; j < V; ++j) sum[j] += p[j];
+      ++mine;
+    }
+    if (lane == 0 && mine) atomicAdd(&n_tokens, mine);
+    if (warp >= kHalf) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (expert_of<VEC>(j, lane) < experts) smem[(warp - kHalf) * experts + expert_of<VEC>(j, lane)] = sum[j];
+    }
+    __syncthreads();
+    if (warp < kHalf) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (expert_of<VEC>(j, lane) < experts) smem[warp * experts + expert_of<VEC>(j, lane)] += sum[j];
+    }
+    __syncthreads();
+    const int64_t slot = blockIdx.x + seq;
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kHalf; ++w) v += smem[w * experts + e];
+      a.part_sum[slot * experts + e] = v;
+      a.part_count[slot * experts + e] = cnt[e];
+    }
+    if (threadIdx.x == 0) a.part_tokens[slot] = n_tokens;
+    t0 = t1;
+    __syncthreads();  // before the next piece clears what was just read
   }
-  if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = n_tokens;
 }
 
 // Launched with programmatic serialization: starts while the kernel before it ends, and waits
@@ -432,7 +465,7 @@ __device__ __forceinline__ float block_sum(float v, float *part) {
   return warp_sum(part[lane]);
 }
 
-// One CTA for 32 experts of a sequence: lane = expert, each warp adds every 32nd slice, the warps'
+// One CTA for 32 experts of a sequence: lane = expert, each warp adds every 32nd piece, the warps'
 // sums are added in order; then the experts' part of the sequence's term.  The last CTA to finish adds
 // all parts in order.
 __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
@@ -447,21 +480,26 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
   const int64_t s = blockIdx.x / groups;
   const int e = static_cast<int>(blockIdx.x - s * groups) * 32 + lane;
   if (tid == 0) total_tokens = 0;
+  // the sequence's pieces: slots first .. last
+  const int64_t lo = a.seq_offsets ? __ldg(a.seq_offsets + s) : 0;
+  const int64_t hi = a.seq_offsets ? __ldg(a.seq_offsets + s + 1) : a.tokens;
   wait_for_previous_kernel();
+  const bool none = a.tokens == 0 || hi <= lo || __ldcg(a.flags + 1) != 0;  // malformed sequences count no token
+  const int64_t first = none ? 0 : lo / a.chunk + s;
+  const int64_t last_slot = none ? -1 : (hi - 1) / a.chunk + s;
   float v = 0.0f;
   int32_t c = 0;
   if (e < experts) {
 #pragma unroll 4
-    for (int i = warp; i < a.slices; i += 32) {
-      const int64_t at = (s * a.slices + i) * experts + e;
-      v += a.part_sum[at];
-      c += a.part_count[at];
+    for (int64_t i = first + warp; i <= last_slot; i += 32) {
+      v += a.part_sum[i * experts + e];
+      c += a.part_count[i * experts + e];
     }
   }
   sums[warp][lane] = v;
   cnts[warp][lane] = c;
   int32_t n = 0;
-  for (int i = tid; i < a.slices; i += 1024) n += a.part_tokens[s * a.slices + i];
+  for (int64_t i = first + tid; i <= last_slot; i += 1024) n += a.part_tokens[i];
   __syncthreads();
   if (n) atomicAdd(&total_tokens, n);
   __syncthreads();
@@ -481,7 +519,7 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
       if (e < 32) a.seq_tokens[s] = t;
       a.term[blockIdx.x] = t > 0 ? term / tf * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tf)) : 0.0f;
       __threadfence();
-      last = atomicAdd(a.done, 1) == static_cast<int>(gridDim.x) - 1;
+      last = atomicAdd(a.flags, 1) == static_cast<int>(gridDim.x) - 1;
     }
   }
   __syncthreads();
@@ -510,19 +548,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) balance_backward_kernel(Launc
   int live = 0;  // sequences with tokens
   for (int64_t s = lane; s < a.num_seqs; s += 32) live += __ldg(a.seq_tokens + s) > 0;
   live = __reduce_add_sync(kAll, live);
-  // the last sequence that starts at or before t0: halving down to 32, then all at once
   int64_t seq = 0, next_start = a.tokens;
   if (a.seq_offsets) {
-    int64_t lo = 0, hi = a.num_seqs;
-    while (hi - lo > 32) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (__ldg(a.seq_offsets + mid) <= t0)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int64_t mine = lo + 1 + lane;
-    seq = lo + __popc(__ballot_sync(kAll, mine < hi && __ldg(a.seq_offsets + mine) <= t0));
+    seq = find_sequence(a.seq_offsets, a.num_seqs, t0, lane);
     next_start = seq + 1 < a.num_seqs ? __ldg(a.seq_offsets + seq + 1) : a.tokens;
   }
   const float up = __ldg(a.d_loss) * a.alpha / static_cast<float>(live);
@@ -616,7 +644,7 @@ cudaError_t gate_backward(const LaunchGate &a) {
 
 template <typename T>
 cudaError_t balance_partial(const LaunchBalance &a) {
-  const unsigned blocks = static_cast<unsigned>(a.num_seqs * a.slices);
+  const unsigned blocks = static_cast<unsigned>(a.tokens > 0 ? (a.tokens + a.chunk - 1) / a.chunk : 1);
   const size_t smem = static_cast<size_t>(kPartWarps / 2 + 1) * a.num_experts * 4;
   return by_width<T>(a.num_experts, [&](auto v, auto vec) {
     balance_partial_kernel<T, decltype(v)::value, decltype(vec)::value>

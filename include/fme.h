@@ -608,7 +608,7 @@ fme_status moe_gate_backward(const void *logits, int32_t dtype, const int32_t *i
  *   ids          device int32 [tokens x top_k]; one outside [0, num_experts) is not
  *                counted and sets FME_DEV_BAD_INDEX
  *   seq_offsets  device int32 [num_seqs + 1], rising from 0 to tokens, or NULL (one sequence);
- *                a malformed sequence counts no token and sets FME_DEV_BAD_OFFSETS
+ *                malformed ones set FME_DEV_BAD_OFFSETS and no token is counted (loss 0)
  *   token_mask   device uint8 [tokens], non-zero = counted, or NULL (all); the logits and ids of
  *                a token that is not counted are not used
  *   loss         device float [1]
