@@ -26,9 +26,11 @@
 //               barriers; the epilogue frees a stage when it sees the block's MMAs done;
 //   warp 1      allocates tensor memory; in the leader one thread issues the MMAs, a commit per
 //               block hands the accumulator to both CTAs' epilogues;
-//   warps 2-3   bring the blocks' scales into shared memory, one block each in turn (loads by
-//               the epilogue threads themselves, a few blocks ahead in registers, kept them
-//               waiting on the loads: 2.09 -> @@ ms for 65536 x 4096 x 7168);
+//   warps 2-3   bring the blocks' scales into shared memory, in turn (loads by the epilogue
+//               threads themselves, a few blocks ahead in registers, kept them waiting on the loads:
+//               2.09 -> 1.48 ms for 65536 x 4096 x 7168).  Four blocks' together where a row's scale is one
+//               product a block: the MMAs' operands take nearly all of shared memory's bandwidth (80 KB a
+//               block and SM in 632 cycles), so every access of the epilogue waits (1.42 -> 1.36 ms);
 //   warps 4-11  epilogue: 32 rows x 128 columns each, sums in 128 registers a thread.
 #include <algorithm>
 
@@ -46,8 +48,10 @@ constexpr int kStages128 = 4;
 constexpr int kOutBlocks = 2;                // staging blocks a warp: its 32 x 128 bf16 outputs of a tile
 constexpr int kOutBlockBytes = 32 * 128;
 constexpr int kScaleWarp0 = 2;                // and 3
-constexpr int kScaleSlots = 4;                // blocks whose scales are in shared memory
-constexpr int kScaleSlotFloats = 128 + kBN;  // of the CTA's rows and the tile's columns (see scale_slot)
+constexpr int kScaleSlots = 4;                // slots of blocks' scales in shared memory
+constexpr int kScaleGroup = 4;                // blocks of a slot (forward, dgrad); wgrad's holds one
+constexpr int kScaleSlotFloats = kScaleGroup * 2 * 128;  // forward, dgrad: [column half][row][block]
+constexpr int kScaleSlotFloatsW = 128 + kBN;             // wgrad: [row], [column]
 constexpr int kStageOut = 8 * kOutBlocks * kOutBlockBytes + kScaleSlots * kScaleSlotFloats * 4;
 
 enum class Kind128 { kFwd, kDgrad, kWgrad };
@@ -404,57 +408,78 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       __syncwarp();
     } else if (warp >= kScaleWarp0) {
       // ------------------------------------------------------------------ scales
-      // Forward, dgrad: slot[half][row] = scale of the row times that of the weight block of
-      // the column half.  wgrad: slot[0][row], then the tile's 256 column scales.
-      uint32_t g = 0;  // blocks so far; this warp takes every other one
+      // Forward, dgrad: slot[half][row][block] = scale of the row times that of the weight block of the
+      // column half, four blocks a slot.  wgrad: slot[row], then the tile's 256 column scales, one block
+      // a slot.  Each of the two warps takes every other slot.
+      uint32_t g = 0;
       bool stop = false;
       const int64_t kb_count = (p.k + 127) >> 7;
       const int64_t nb128 = (p.n + 127) >> 7;
       for (uint32_t t = pair_id; t < total && !stop; t += pairs) {
         const Tile128 tl = tile128<K>(p, tab, t, rank);
-        const float *a = p.a_scale + (K == Kind128::kWgrad ? (tl.p0 >> 7) * p.m : int64_t(0)) + tl.row0;
-        for (int i = 0; i < tl.nk; ++i, ++g) {
-          if ((g & 1) != (warp & 1)) continue;
-          const uint32_t slot = g % kScaleSlots;
-          float *dst = scales + slot * kScaleSlotFloats;
-          float ra[4];
+        if constexpr (K == Kind128::kWgrad) {
+          const float *a = p.a_scale + (tl.p0 >> 7) * p.m + tl.row0;
+          for (int i = 0; i < tl.nk; ++i, ++g) {
+            if ((g & 1) != (warp & 1)) continue;
+            const uint32_t slot = g % kScaleSlots;
+            float *dst = scales + slot * kScaleSlotFloatsW;
+            float ra[4], cb[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = lane + 32 * j;
-            ra[j] = r < tl.rows_valid ? __ldg(a + i * p.m + r) : 0.0f;
-          }
-          float cb[K == Kind128::kWgrad ? 8 : 2];
-          if constexpr (K == Kind128::kWgrad) {
+            for (int j = 0; j < 4; ++j) {
+              const int r = lane + 32 * j;
+              ra[j] = r < tl.rows_valid ? __ldg(a + i * p.m + r) : 0.0f;
+            }
             const float *b = p.b_scale + ((tl.p0 >> 7) + i) * p.n + tl.col0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) cb[j] = tl.col0 + lane + 32 * j < p.n ? __ldg(b + lane + 32 * j) : 0.0f;
-          } else {
+            if (!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status)) {
+              stop = true;
+              break;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = ra[j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[128 + lane + 32 * j] = cb[j];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.sc_full[slot]);
+          }
+        } else {
+          const float *a = p.a_scale + tl.row0;
+          for (int i0 = 0; i0 < tl.nk; i0 += kScaleGroup, ++g) {
+            if ((g & 1) != (warp & 1)) continue;
+            const uint32_t slot = g % kScaleSlots;
+            float4 *dst = reinterpret_cast<float4 *>(scales + slot * kScaleSlotFloats);
+            float ra[4][kScaleGroup], cb[2][kScaleGroup];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = lane + 32 * j;
+#pragma unroll
+              for (int u = 0; u < kScaleGroup; ++u)
+                ra[j][u] = r < tl.rows_valid && i0 + u < tl.nk ? __ldg(a + (i0 + u) * p.m + r) : 0.0f;
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int64_t c = (tl.col0 >> 7) + h;
-              const int64_t at = K == Kind128::kFwd ? (tl.e * nb128 + c) * kb_count + i : (tl.e * kb_count + i) * nb128 + c;
-              cb[h] = c < nb128 ? __ldg(p.b_scale + at) : 0.0f;
-            }
-          }
-          if (!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status)) {
-            stop = true;
-            break;
-          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (K == Kind128::kWgrad) {
-              dst[lane + 32 * j] = ra[j];
-            } else {
-              dst[lane + 32 * j] = ra[j] * cb[0];
-              dst[128 + lane + 32 * j] = ra[j] * cb[1];
+              for (int u = 0; u < kScaleGroup; ++u) {
+                const int64_t i = i0 + u;
+                const int64_t at = K == Kind128::kFwd ? (tl.e * nb128 + c) * kb_count + i : (tl.e * kb_count + i) * nb128 + c;
+                cb[h][u] = c < nb128 && i < tl.nk ? __ldg(p.b_scale + at) : 0.0f;
+              }
             }
-          }
-          if constexpr (K == Kind128::kWgrad) {
+            if (!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status)) {
+              stop = true;
+              break;
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[128 + lane + 32 * j] = cb[j];
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                dst[h * 128 + lane + 32 * j] =
+                    make_float4(ra[j][0] * cb[h][0], ra[j][1] * cb[h][1], ra[j][2] * cb[h][2], ra[j][3] * cb[h][3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.sc_full[slot]);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.sc_full[slot]);
         }
       }
     }
@@ -468,7 +493,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
     uint8_t *stage_blks = smem_out + ew * kOutBlocks * kOutBlockBytes;
     const uint32_t leader_empty[2] = {pair::map_to_rank(&s.acc_empty[0], 0), pair::map_to_rank(&s.acc_empty[1], 0)};
     const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
-    uint32_t g = 0;
+    uint32_t g = 0, sg = 0;  // blocks and scale groups so far
     bool stop = false;
     Tile128 next{};
     if (pair_id < total) next = tile128<K>(p, tab, pair_id, rank);
@@ -480,34 +505,9 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-#pragma unroll 1
-      for (int i = 0; i < tl.nk; ++i) {
-        const uint32_t b = g & 1;
-        const uint32_t slot = g % kScaleSlots;
-        if (!mbar_wait(&s.sc_full[slot], (g / kScaleSlots) & 1, abort_flag, p.status)) {
-          stop = true;
-          break;
-        }
-        const float *sc = scales + slot * kScaleSlotFloats;
-        const float *cs = sc + 128 + half * 128;  // wgrad
-        const float v = K == Kind128::kWgrad ? sc[r] : sc[half * 128 + r];
-        const float2 f = make_float2(v, v);
-        if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) {
-          stop = true;
-          break;
-        }
-        // the block's MMAs are done: its operands' stage is free
-        if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
-        tc_fence_after();
-        auto add = [&](int c, const uint32_t(&d)[32]) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 x = make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
-            float2 w = f;
-            if constexpr (K == Kind128::kWgrad) w = __fmul2_rn(*reinterpret_cast<const float2 *>(cs + 32 * c + 2 * j), f);
-            acc[16 * c + j] = __ffma2_rn(x, w, acc[16 * c + j]);
-          }
-        };
+      // The block's four chunks of 32 columns: loaded while the one before is summed, the accumulator
+      // released as soon as the last is in registers.
+      auto sum_block = [&](uint32_t b, auto add) {
         const uint32_t tb = tq + b * kBN;
         uint32_t va[32], vb[32];
         tmem_ld_32x32(tb, va);
@@ -525,9 +525,73 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
         __syncwarp();
         if (lane == 0) pair::arrive_remote_relaxed(leader_empty[b]);
         add(3, vb);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.sc_empty[slot]);
-        ++g;
+      };
+      if constexpr (K == Kind128::kWgrad) {
+#pragma unroll 1
+        for (int i = 0; i < tl.nk; ++i) {
+          const uint32_t b = g & 1;
+          const uint32_t slot = g % kScaleSlots;
+          if (!mbar_wait(&s.sc_full[slot], (g / kScaleSlots) & 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          const float *sc = scales + slot * kScaleSlotFloatsW;
+          const float *cs = sc + 128 + half * 128;
+          const float v = sc[r];
+          const float2 f = make_float2(v, v);
+          if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          // the block's MMAs are done: its operands' stage is free
+          if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
+          tc_fence_after();
+          auto add = [&](int c, const uint32_t(&d)[32]) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 x = make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+              acc[16 * c + j] = __ffma2_rn(x, __fmul2_rn(*reinterpret_cast<const float2 *>(cs + 32 * c + 2 * j), f), acc[16 * c + j]);
+            }
+          };
+          sum_block(b, add);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.sc_empty[slot]);
+          ++g;
+        }
+      } else {
+#pragma unroll 1
+        for (int i0 = 0; i0 < tl.nk && !stop; i0 += kScaleGroup, ++sg) {
+          const uint32_t slot = sg % kScaleSlots;
+          if (!mbar_wait(&s.sc_full[slot], (sg / kScaleSlots) & 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          const float4 f4 = reinterpret_cast<const float4 *>(scales + slot * kScaleSlotFloats)[half * 128 + r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.sc_empty[slot]);
+#pragma unroll
+          for (int u = 0; u < kScaleGroup; ++u) {
+            if (i0 + u >= tl.nk || stop) continue;
+            const uint32_t b = g & 1;
+            const float v = u == 0 ? f4.x : u == 1 ? f4.y : u == 2 ? f4.z : f4.w;
+            const float2 f = make_float2(v, v);
+            if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) {
+              stop = true;
+              continue;
+            }
+            if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
+            tc_fence_after();
+            auto add = [&](int c, const uint32_t(&d)[32]) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 x = make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+                acc[16 * c + j] = __ffma2_rn(x, f, acc[16 * c + j]);
+              }
+            };
+            sum_block(b, add);
+            ++g;
+          }
+        }
       }
       if (stop) break;
       // ---- the tile's sums out
