@@ -12,6 +12,12 @@
 
 namespace fme {
 
+// Programmatic serialization: a kernel launched with it may start once the one before it in the stream
+// lets it (or ends), and waits here for all of that one's writes; before this it touches no
+// global memory.  The row-wise quantizer lets its successor start at once.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void start_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Groups of up to 32 at a time: lane l of the calling warp holds group g0 + l.
 // Calls fn(g, first row, rows, first unit) for the lane's group, where a group of
 // n rows takes ceil(n / unit) units; returns the total units, or -1 if the offsets

@@ -480,10 +480,6 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
   }
 }
 
-// Launched with programmatic serialization: starts while the kernel before it ends, and waits
-// here for all of its writes.
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Sum over a CTA of 1024 threads, in every thread.
 __device__ __forceinline__ float block_sum(float v, float *part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

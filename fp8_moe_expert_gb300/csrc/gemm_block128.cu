@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
   const uint32_t pair_id = blockIdx.x >> 1;
   const uint32_t pairs = gridDim.x >> 1;
 
+  wait_for_previous_kernel();
   // ---- tables (both CTAs of a pair see the same offsets and take the same way out)
   if constexpr (K == Kind128::kWgrad) {
     if (warp == 0) {
@@ -802,18 +803,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  if (warp == 0) {
-    const int32_t total = scan_groups(p.offsets, p.num_experts, p.m, kFewTokens,
-                                      [&](int g, int32_t lo, int32_t, int32_t first) {
-                                        tab.off[g] = lo;
-                                        tab.aux[g] = first;
-                                      });
-    if (lane == 0) {
-      tab.off[p.num_experts] = static_cast<int32_t>(p.m);
-      tab.aux[p.num_experts] = total;
-      s.ok_flag = total >= 0;
-    }
-  } else if (warp == 1) {
+  if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem_base)),
                  "r"(kFewTmemCols)
                  : "memory");
@@ -837,6 +827,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const
     fence_proxy_async_shared();
     prefetch_tensormap(&p.map_a);
     prefetch_tensormap(&p.map_b);
+  }
+  wait_for_previous_kernel();
+  if (warp == 0) {
+    const int32_t total = scan_groups(p.offsets, p.num_experts, p.m, kFewTokens,
+                                      [&](int g, int32_t lo, int32_t, int32_t first) {
+                                        tab.off[g] = lo;
+                                        tab.aux[g] = first;
+                                      });
+    if (lane == 0) {
+      tab.off[p.num_experts] = static_cast<int32_t>(p.m);
+      tab.aux[p.num_experts] = total;
+      s.ok_flag = total >= 0;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1026,13 +1029,15 @@ cudaError_t launch128(const LaunchBlock128 &a) {
   cfg.blockDim = dim3(kThreads128, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -1042,9 +1047,17 @@ cudaError_t launch_few(const LaunchBlock128 &a) {
       cudaFuncSetAttribute(gemm_block128_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   const int64_t items = (a.m / kFewTokens + std::min<int64_t>(a.num_experts, a.m)) * ((a.n + kBM - 1) / kBM);
-  gemm_block128_few_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.num_sms, items)), kFewThreads, smem, a.stream>>>(
-      a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, items)), 1, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_block128_few_kernel, a);
 }
 
 }  // namespace

@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const uint16_t *__restric
                                                        int cols_per_cta, uint8_t *__restrict__ codes,
                                                        float *__restrict__ scale, const int32_t *__restrict__ gather,
                                                        int gather_div, int64_t gather_limit, int32_t *status) {
+  start_next_kernel();
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
