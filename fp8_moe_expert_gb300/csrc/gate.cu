@@ -96,12 +96,13 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // sigmoid(l) and 1 - sigmoid(l) = sigmoid(-l) from one exponential that cannot overflow,
-// t = e^-|l|: 1 / (1 + t) and t / (1 + t).
+// t = e^-|l|: 1 / (1 + t) and t / (1 + t).  A NaN stays one.
 __device__ __forceinline__ void sigmoids(float l, float &s, float &rest) {
   const float t = __expf(-fabsf(l));
   const float r = rcp_approx(1.0f + t);
-  s = l != l ? l : l >= 0.0f ? r : t * r;
-  rest = l != l ? l : l >= 0.0f ? t * r : r;
+  const float tr = t * r;
+  s = l >= 0.0f ? r : tr;
+  rest = l >= 0.0f ? tr : r;
 }
 __device__ __forceinline__ float sigmoid(float l) {
   float s, rest;
@@ -115,21 +116,24 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return static_cast<uint32_t>(b) ^ (static_cast<uint32_t>(b >> 31) | 0x80000000u);
 }
 
-// exp(l - max) of a row held V values a lane; a row without a finite maximum gets zeros (all
-// -inf: nothing is left of the row) or NaN (+inf or NaN among them).
+// The largest of a row held V values a lane, or 0 where nothing is above -inf: a finite offset for
+// exponentials, so that such a row's are 0 and only +inf and NaN give NaN.
 template <int V>
-__device__ __forceinline__ float exp_row(const float (&l)[V], float (&x)[V]) {
-  float m = -INFINITY, bad = 0.0f;
+__device__ __forceinline__ float row_offset(const float (&l)[V]) {
+  float m = l[0];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    m = fmaxf(m, l[j]);
-    bad += l[j] == l[j] ? 0.0f : l[j];
-  }
+  for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
   m = warp_max(m);
-  float sum = bad;
+  return m == -INFINITY ? 0.0f : m;
+}
+
+// x = exp(l - m) of the row (lanes past the experts hold -inf) and its sum.
+template <int V>
+__device__ __forceinline__ float exp_row(const float (&l)[V], float m, float (&x)[V]) {
+  float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    x[j] = m == -INFINITY ? 0.0f : __expf(l[j] - m);  // lanes past the experts hold -inf
+    x[j] = __expf(l[j] - m);
     sum += x[j];
   }
   return warp_sum(sum);
@@ -153,11 +157,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const T *__restri
   float denom = 1.0f, m_all = 0.0f;  // softmax over all experts, only where the weights need it
   if (softmax && !normalize) {
     float x[V];
-    denom = exp_row<V>(l, x);
-    m_all = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < V; ++j) m_all = fmaxf(m_all, l[j]);
-    m_all = warp_max(m_all);
+    m_all = row_offset<V>(l);
+    denom = exp_row<V>(l, m_all, x);
   }
   uint32_t key[V];
 #pragma unroll
@@ -231,8 +232,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const T *__restri
   const float my_l = mine ? to_float(row[my_id]) : -INFINITY;  // without the bias
   float s;
   if (softmax) {
-    const float ref = normalize ? warp_max(my_l) : m_all;
-    s = !mine ? 0.0f : my_l != my_l ? my_l : ref == -INFINITY ? 0.0f : __expf(my_l - ref);
+    float ref = normalize ? warp_max(my_l) : m_all;
+    if (ref == -INFINITY) ref = 0.0f;
+    s = mine ? __expf(my_l - ref) : 0.0f;
   } else {
     s = mine ? sigmoid(my_l) : 0.0f;
   }
@@ -262,11 +264,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_dense_kernel(
   const bool live = id >= 0;
   const float g = live ? scale * __ldg(d_weights + t * top_k + lane) : 0.0f;
   const float my_l = live ? to_float(row[id]) : -INFINITY;
-  const float denom = exp_row<V>(l, x);
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
-  m = warp_max(m);
+  const float m = row_offset<V>(l);
+  const float denom = exp_row<V>(l, m, x);
   const float inner = warp_sum(live && denom != 0.0f ? __expf(my_l - m) / denom * g : 0.0f);
   const float r = denom == 0.0f ? 0.0f : 1.0f / denom;
 #pragma unroll
@@ -325,7 +324,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_kernel(
     float ref = l;
 #pragma unroll
     for (int s = kWidth / 2; s; s >>= 1) ref = fmaxf(ref, __shfl_xor_sync(kAll, ref, s));
-    const float s = !live || ref == -INFINITY ? 0.0f : __expf(l - ref);
+    if (ref == -INFINITY) ref = 0.0f;
+    const float s = live ? __expf(l - ref) : 0.0f;
     const float total = group_sum(s);
     const float p = total == 0.0f ? 0.0f : s / total;
     d = p * (g - group_sum(p * g));
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_kernel(
 template <int V>
 __device__ __forceinline__ void probabilities(const float (&l)[V], bool softmax, float (&p)[V], float (&slope)[V]) {
   if (softmax) {
-    const float z = exp_row<V>(l, p);
+    const float z = exp_row<V>(l, row_offset<V>(l), p);
     const float r = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
     for (int j = 0; j < V; ++j) slope[j] = p[j] = p[j] * r;
@@ -396,6 +396,7 @@ template <typename T, int V, int VEC>
 __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(LaunchBalance a) {
   extern __shared__ float smem[];  // [kPartWarps / 2][experts] sums, then [experts] counts
   constexpr int kHalf = kPartWarps / 2;
+  start_next_kernel();
   const int experts = a.num_experts;
   int32_t *cnt = reinterpret_cast<int32_t *>(smem + kHalf * experts);
   __shared__ int32_t n_tokens;
@@ -506,10 +507,12 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
   const int e = static_cast<int>(blockIdx.x - s * groups) * 32 + lane;
   if (tid == 0) total_tokens = 0;
   // the sequence's pieces: slots first .. last
-  const int64_t lo = a.seq_offsets ? __ldg(a.seq_offsets + s) : 0;
-  const int64_t hi = a.seq_offsets ? __ldg(a.seq_offsets + s + 1) : a.tokens;
   wait_for_previous_kernel();
-  const bool none = a.tokens == 0 || hi <= lo || __ldcg(a.flags + 1) != 0;  // malformed sequences count no token
+  const bool bad = __ldcg(a.flags + 1) != 0;  // malformed sequences: no token counts
+  // (cut to the tokens, so that malformed ones stay inside the workspace until `bad` is known)
+  const int64_t lo = a.seq_offsets ? max(0, __ldg(a.seq_offsets + s)) : 0;
+  const int64_t hi = a.seq_offsets ? min(a.tokens, static_cast<int64_t>(__ldg(a.seq_offsets + s + 1))) : a.tokens;
+  const bool none = hi <= lo;
   const int64_t first = none ? 0 : lo / a.chunk + s;
   const int64_t last_slot = none ? -1 : (hi - 1) / a.chunk + s;
   float v = 0.0f;
@@ -521,12 +524,12 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
       c += a.part_count[i * experts + e];
     }
   }
-  sums[warp][lane] = v;
-  cnts[warp][lane] = c;
+  sums[warp][lane] = bad ? 0.0f : v;
+  cnts[warp][lane] = bad ? 0 : c;
   int32_t n = 0;
   for (int64_t i = first + tid; i <= last_slot; i += 1024) n += a.part_tokens[i];
   __syncthreads();
-  if (n) atomicAdd(&total_tokens, n);
+  if (n && !bad) atomicAdd(&total_tokens, n);
   __syncthreads();
   if (warp == 0) {
     v = 0.0f;
@@ -697,9 +700,8 @@ cudaError_t balance_partial(const LaunchBalance &a) {
 
 template <typename T>
 cudaError_t balance_backward(const LaunchBalance &a) {
-  // up to four tokens a warp, as long as that leaves about 32 warps an SM
-  const int64_t fit = a.tokens / 4864;
-  const int per_warp = static_cast<int>(fit < 1 ? 1 : fit > 4 ? 4 : fit);
+  // one wave: as many tokens a warp as 32 warps an SM leave (32768 x 256: 12.9 us; four a warp 13.7, two 15.8)
+  const int per_warp = static_cast<int>((a.tokens + 4863) / 4864);
   const int64_t warps = (a.tokens + per_warp - 1) / per_warp;
   const unsigned blocks = static_cast<unsigned>((warps + kGateWarps - 1) / kGateWarps);
   return by_width<T>(a.num_experts, [&](auto v, auto vec) {
