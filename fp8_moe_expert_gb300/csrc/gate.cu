@@ -419,8 +419,16 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
     }
   }
   const T *logits = static_cast<const T *>(a.logits);
-  float next[V];  // the next token's row, loaded while this one is summed
-  if (c0 + warp < c1) load_row<T, V, VEC>(logits + (c0 + warp) * experts, experts, lane, next);
+  // the next token's row, mask and choice, loaded while this one is summed
+  float next[V];
+  bool next_on = false;
+  int32_t next_id = 0;
+  auto prefetch = [&](int64_t t) {
+    load_row<T, V, VEC>(logits + t * experts, experts, lane, next);
+    next_on = !a.token_mask || __ldg(a.token_mask + t);
+    if (lane < a.top_k) next_id = __ldg(a.ids + t * a.top_k + lane);
+  };
+  if (c0 + warp < c1) prefetch(c0 + warp);
   for (int64_t t0 = c0; t0 < c1;) {
     int64_t seq = 0, t1 = c1;
     if (a.seq_offsets) {
@@ -428,7 +436,7 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
       t1 = min(c1, static_cast<int64_t>(__ldg(a.seq_offsets + seq + 1)));
       if (t1 <= t0) break;  // malformed: no sequence holds t0
     }
-    if (t0 > c0 && t0 + warp < t1) load_row<T, V, VEC>(logits + (t0 + warp) * experts, experts, lane, next);
+    if (t0 > c0 && t0 + warp < t1) prefetch(t0 + warp);
     for (int e = threadIdx.x; e < experts; e += blockDim.x) cnt[e] = 0;
     if (threadIdx.x == 0) n_tokens = 0;
     __syncthreads();
@@ -440,10 +448,11 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
       float l[V], p[V], slope[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) l[j] = next[j];
-      if (t + kPartWarps < t1) load_row<T, V, VEC>(logits + (t + kPartWarps) * experts, experts, lane, next);
-      if (a.token_mask && !__ldg(a.token_mask + t)) continue;
+      const bool on = next_on;
+      const int32_t e = next_id;
+      if (t + kPartWarps < t1) prefetch(t + kPartWarps);
+      if (!on) continue;
       if (lane < a.top_k) {
-        const int32_t e = __ldg(a.ids + t * a.top_k + lane);
         if (e >= 0 && e < experts)
           atomicAdd(&cnt[e], 1);
         else
@@ -573,6 +582,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) balance_backward_kernel(Launc
   const T *logits = static_cast<const T *>(a.logits);
   float l[V], w[V];
   load_row<T, V, VEC>(logits + t0 * experts, experts, lane, l);
+  bool next_on = !a.token_mask || __ldg(a.token_mask + t0);
   int live = 0;  // sequences with tokens
   for (int64_t s = lane; s < a.num_seqs; s += 32) live += __ldg(a.seq_tokens + s) > 0;
   live = __reduce_add_sync(kAll, live);
@@ -582,14 +592,15 @@ __global__ void __launch_bounds__(32 * kGateWarps) balance_backward_kernel(Launc
     next_start = seq + 1 < a.num_seqs ? __ldg(a.seq_offsets + seq + 1) : a.tokens;
   }
   const float up = __ldg(a.d_loss) * a.alpha / static_cast<float>(live);
-  int64_t loaded = -1;  // the sequence that w belongs to
+  int64_t loaded = -1;  // the sequence that w and n belong to
+  int32_t n = 0;
   for (int64_t t = t0; t < t1; ++t) {
     while (t >= next_start && seq + 1 < a.num_seqs) {
       ++seq;
       next_start = seq + 1 < a.num_seqs ? __ldg(a.seq_offsets + seq + 1) : a.tokens;
     }
-    const int32_t n = __ldg(a.seq_tokens + seq);
     if (seq != loaded) {
+      n = __ldg(a.seq_tokens + seq);
       const float tn = static_cast<float>(n);
       const float c = n > 0 ? up * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tn)) / tn : 0.0f;
 #pragma unroll
@@ -602,9 +613,13 @@ __global__ void __launch_bounds__(32 * kGateWarps) balance_backward_kernel(Launc
     float cur[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) cur[j] = l[j];
-    if (t + 1 < t1) load_row<T, V, VEC>(logits + (t + 1) * experts, experts, lane, l);
+    const bool on = next_on;
+    if (t + 1 < t1) {
+      load_row<T, V, VEC>(logits + (t + 1) * experts, experts, lane, l);
+      next_on = !a.token_mask || __ldg(a.token_mask + t + 1);
+    }
     T *out = static_cast<T *>(a.d_logits) + t * experts;
-    if ((a.token_mask && !__ldg(a.token_mask + t)) || n <= 0) {
+    if (!on || n <= 0) {
       if (!a.accumulate) {
 #pragma unroll
         for (int j = 0; j < V; ++j) cur[j] = 0.0f;
