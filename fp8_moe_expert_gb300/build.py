@@ -114,7 +114,9 @@ def build(output: str = LIBRARY, extra_flags: list[str] | None = None, verbose: 
             if pending:
                 pending.result()
         tmp_out = output + ".tmp"
-        cmd = [tool, *ARCH, "-shared", "-Xlinker", "-soname=libfme.so", "-o", tmp_out, *objs]
+        # a soname of its own: the binding, linked to the package's library, must not be given another build of it
+        # that the process loaded first
+        cmd = [tool, *ARCH, "-shared", "-Xlinker", f"-soname={os.path.basename(output)}", "-o", tmp_out, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True, env=env)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")

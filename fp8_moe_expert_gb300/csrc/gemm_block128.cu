@@ -7,12 +7,17 @@
 //
 // The tensor core sums the 128 products of a block in tensor memory (four K = 32
 // kind::f8f6f4 MMAs from zero); the scales are no powers of two, so each block's
-// partial sum is multiplied by its scale and added to fp32 sums in registers.  That
-// is 128 x 256 fused multiply-adds a block and CTA, 256 cycles of the FMA pipe against
-// about 600 of the tensor pipe (measured for a pair's M = 256, N = 256, K = 32 FP8 MMA:
-// 151 cycles), so with two accumulators in tensor memory (2 x 256 of its 512 columns;
-// there are no block scales to keep there) the two overlap.  wgrad's scale differs for
-// every output element: one multiply more each.
+// partial sum is multiplied by its scale and added to fp32 sums in registers, while the
+// next block's MMAs fill the other of two accumulators (2 x 256 of tensor memory's 512
+// columns; there are no block scales to keep there).  wgrad's scale differs for every
+// output element: one multiply more each.
+//
+// What bounds them.  A pair's M = 256, N = 256, K = 128 block takes 632 cycles of MMAs
+// alone: their operands are 80 KB a block and SM, 625 cycles at shared memory's 128 bytes
+// a cycle.  With the sums it takes about 850: the scales' reads and the barriers go
+// through the same shared memory and the accumulator is held while it is read out.
+// 65536 x 4096 x 7168: 1.35 ms, 2.85 PFLOP/s; dgrad 65536 x 7168 x 2048, 32 experts:
+// 0.70 ms, 2.74 PFLOP/s; wgrad of the same: 1.31 ms, 1.47 PFLOP/s.
 //
 // One set of weight codes serves both directions: blocks are 128 x 128, and dgrad reads
 // the same [n x k] codes as an MN-major operand (its contraction runs down the rows).
@@ -29,8 +34,7 @@
 //   warps 2-3   bring the blocks' scales into shared memory, in turn (loads by the epilogue
 //               threads themselves, a few blocks ahead in registers, kept them waiting on the loads:
 //               2.09 -> 1.48 ms for 65536 x 4096 x 7168).  Four blocks' together where a row's scale is one
-//               product a block: the MMAs' operands take nearly all of shared memory's bandwidth (80 KB a
-//               block and SM in 632 cycles), so every access of the epilogue waits (1.42 -> 1.36 ms);
+//               product a block, for fewer accesses (1.42 -> 1.36 ms);
 //   warps 4-11  epilogue: 32 rows x 128 columns each, sums in 128 registers a thread.
 #include <algorithm>
 
@@ -104,6 +108,13 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(e));
   return e != 0;
 }
+
+// Warps that work as one (epilogue, scales) give up as one, so that no lane is left waiting at a
+// warp-wide instruction: a lane whose wait ran out goes on with the others, every later wait of the CTA
+// ends at once, and the warp leaves at the next vote, before it writes the tile.  The vote is once for a
+// few blocks: one at every wait cost 2.5% (65536 x 4096 x 7168: 1.36 -> 1.40 ms).
+constexpr int kVoteBlocks = 8;
+__device__ __forceinline__ bool warp_any(bool stop) { return __any_sync(0xFFFFFFFFu, stop); }
 
 // Instruction descriptor: fp32 accumulator (bit 4), E4M3 operands (0), the operands'
 // major-ness (bits 15, 16: 1 = MN-major), N / 8 and M / 16.
@@ -433,10 +444,8 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
             const float *b = p.b_scale + ((tl.p0 >> 7) + i) * p.n + tl.col0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) cb[j] = tl.col0 + lane + 32 * j < p.n ? __ldg(b + lane + 32 * j) : 0.0f;
-            if (!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status)) {
-              stop = true;
-              break;
-            }
+            stop = warp_any(!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status));
+            if (stop) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = ra[j];
 #pragma unroll
@@ -468,10 +477,8 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
                 cb[h][u] = c < nb128 && i < tl.nk ? __ldg(p.b_scale + at) : 0.0f;
               }
             }
-            if (!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status)) {
-              stop = true;
-              break;
-            }
+            stop = warp_any(!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status));
+            if (stop) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -532,15 +539,13 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
         for (int i = 0; i < tl.nk; ++i) {
           const uint32_t b = g & 1;
           const uint32_t slot = g % kScaleSlots;
-          if (!mbar_wait(&s.sc_full[slot], (g / kScaleSlots) & 1, abort_flag, p.status)) {
-            stop = true;
-            break;
-          }
+          if (!mbar_wait(&s.sc_full[slot], (g / kScaleSlots) & 1, abort_flag, p.status)) stop = true;
           const float *sc = scales + slot * kScaleSlotFloatsW;
           const float *cs = sc + 128 + half * 128;
           const float v = sc[r];
           const float2 f = make_float2(v, v);
-          if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) {
+          if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) stop = true;
+          if (i % kVoteBlocks == kVoteBlocks - 1 && warp_any(stop)) {
             stop = true;
             break;
           }
@@ -561,25 +566,21 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
         }
       } else {
 #pragma unroll 1
-        for (int i0 = 0; i0 < tl.nk && !stop; i0 += kScaleGroup, ++sg) {
+        for (int i0 = 0; i0 < tl.nk; i0 += kScaleGroup, ++sg) {
           const uint32_t slot = sg % kScaleSlots;
-          if (!mbar_wait(&s.sc_full[slot], (sg / kScaleSlots) & 1, abort_flag, p.status)) {
-            stop = true;
-            break;
-          }
+          if (!mbar_wait(&s.sc_full[slot], (sg / kScaleSlots) & 1, abort_flag, p.status)) stop = true;
+          stop = warp_any(stop);
+          if (stop) break;
           const float4 f4 = reinterpret_cast<const float4 *>(scales + slot * kScaleSlotFloats)[half * 128 + r];
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.sc_empty[slot]);
 #pragma unroll
           for (int u = 0; u < kScaleGroup; ++u) {
-            if (i0 + u >= tl.nk || stop) continue;
+            if (i0 + u >= tl.nk) continue;
             const uint32_t b = g & 1;
             const float v = u == 0 ? f4.x : u == 1 ? f4.y : u == 2 ? f4.z : f4.w;
             const float2 f = make_float2(v, v);
-            if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) {
-              stop = true;
-              continue;
-            }
+            if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) stop = true;
             if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
             tc_fence_after();
             auto add = [&](int c, const uint32_t(&d)[32]) {
@@ -594,6 +595,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
           }
         }
       }
+      stop = warp_any(stop);
       if (stop) break;
       // ---- the tile's sums out
       const int warp_rows = tl.rows_valid - 32 * q;
@@ -940,10 +942,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const
         for (int u = 0; u < 2; ++u) {
           if (i0 + u >= nk) break;
           const uint32_t q = g + i0 + u, slot = q % kFewSlots;
-          if (!mbar_wait<true>(&s.sc_empty[slot], ((q / kFewSlots) & 1) ^ 1, abort_flag, p.status)) {
-            stop = true;
-            break;
-          }
+          stop = warp_any(!mbar_wait<true>(&s.sc_empty[slot], ((q / kFewSlots) & 1) ^ 1, abort_flag, p.status));
+          if (stop) break;
           s.scales[slot][lane] = v[u][0];
           s.scales[slot][lane + 32] = v[u][1];
           __syncwarp();
@@ -966,7 +966,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const
       for (int i = 0; i < nk; ++i, ++g) {
         const uint32_t b = g % kFewAccs, slot = g % kFewSlots;
         if (!mbar_wait(&s.sc_full[slot], (g / kFewSlots) & 1, abort_flag, p.status) ||
-            !mbar_wait(&s.acc_full[b], (g / kFewAccs) & 1, abort_flag, p.status)) {
+            !mbar_wait(&s.acc_full[b], (g / kFewAccs) & 1, abort_flag, p.status))
+          stop = true;
+        if (i % kVoteBlocks == kVoteBlocks - 1 && warp_any(stop)) {
           stop = true;
           break;
         }
@@ -996,6 +998,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const
           mbar_arrive(&s.sc_empty[slot]);
         }
       }
+      stop = warp_any(stop);
       if (stop) break;
       const int64_t col = it.n0 + q * 32 + lane;
       if (col < p.n) {
