@@ -17,7 +17,8 @@
 // a cycle.  With the sums it takes about 850: the scales' reads and the barriers go
 // through the same shared memory and the accumulator is held while it is read out.
 // 65536 x 4096 x 7168: 1.35 ms, 2.85 PFLOP/s; dgrad 65536 x 7168 x 2048, 32 experts:
-// 0.70 ms, 2.74 PFLOP/s; wgrad of the same: 1.31 ms, 1.47 PFLOP/s.
+// 0.70 ms, 2.74 PFLOP/s; wgrad of the same: 1.17 ms, 1.64 PFLOP/s (about 1290 cycles a block,
+// the epilogue's: without its sums and products 800).
 //
 // One set of weight codes serves both directions: blocks are 128 x 128, and dgrad reads
 // the same [n x k] codes as an MN-major operand (its contraction runs down the rows).
@@ -35,7 +36,10 @@
 //               threads themselves, a few blocks ahead in registers, kept them waiting on the loads:
 //               2.09 -> 1.48 ms for 65536 x 4096 x 7168).  Four blocks' together where a row's scale is one
 //               product a block, for fewer accesses (1.42 -> 1.36 ms);
-//   warps 4-11  epilogue: 32 rows x 128 columns each, sums in 128 registers a thread.
+//   warps 4-11  epilogue: 32 rows x 128 columns each, sums in 128 registers a thread.  Forward, dgrad: a
+//               thread has a row, so a block needs one scale.  wgrad: a thread has four rows and 32 columns,
+//               so 36 scales serve its 128 sums (one row: 129 scales, 256 reads of 16 bytes a block and SM:
+//               1.18 -> 1.02 ms for 65536 x 7168 x 2048).
 #include <algorithm>
 
 #include "block128.cuh"
@@ -55,7 +59,8 @@ constexpr int kScaleWarp0 = 2;                // and 3
 constexpr int kScaleSlots = 4;                // slots of blocks' scales in shared memory
 constexpr int kScaleGroup = 4;                // blocks of a slot (forward, dgrad); wgrad's holds one
 constexpr int kScaleSlotFloats = kScaleGroup * 2 * 128;  // forward, dgrad: [column half][row][block]
-constexpr int kScaleSlotFloatsW = 128 + kBN;             // wgrad: [row], [column]
+constexpr int kColSet = 36;                              // wgrad: a lane's 32 column scales, spread over the banks
+constexpr int kScaleSlotFloatsW = 128 + 2 * 4 * kColSet;  // wgrad: rows, then [column half][lane % 4][column]
 constexpr int kStageOut = 8 * kOutBlocks * kOutBlockBytes + kScaleSlots * kScaleSlotFloats * 4;
 
 enum class Kind128 { kFwd, kDgrad, kWgrad };
@@ -156,6 +161,23 @@ __device__ __forceinline__ void tmem_wait_ld_for(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
+__device__ __forceinline__ void tmem_wait_ld_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])::"memory");
+}
+
+// 16 lanes x 32 columns: of each 8 columns a thread gets those at 2 (lane % 4) and the next, of rows
+// lane / 4 and lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // Expert tables in shared memory: first row and first 256-row block of each expert (forward,
 // dgrad), or padded offsets and experts by decreasing work (wgrad).
 struct Tables {
@@ -222,30 +244,27 @@ __device__ __forceinline__ void store_block_cut(__nv_bfloat16 *dst, int64_t ld, 
   __syncwarp();
 }
 
-// The same for 16 fp32 columns, written or added (one unfused add an element).
-__device__ __forceinline__ void store_fp32_cut(float *dst, int64_t ld, int rows_valid, int cols_left, bool add,
-                                               uint8_t *stage, int lane, const float2 *v) {
-  uint8_t *row = stage + lane * 64;
-  const int x = (lane >> 1) & 3;
+// wgrad: a staged block (32 rows of 128 bytes, swizzled) to columns `col` on, by plain stores; with
+// p.accumulate added to dW (one unfused add an element).  Past the output's edge nothing is written.
+__device__ __forceinline__ void store_staged(const LaunchBlock128 &p, bool fp32, int64_t out_row, int64_t col,
+                                             int rows_valid, const uint8_t *blk, int lane) {
+  const int j = lane & 7;
+  col += (fp32 ? 4 : 8) * j;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<float4 *>(row + 16 * (j ^ x)) = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
-  __syncwarp();
-  const int j = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    float4 o = *reinterpret_cast<const float4 *>(stage + r * 64 + 16 * (j ^ ((r >> 1) & 3)));
-    if (r < rows_valid && 4 * j < cols_left) {
-      float4 *at = reinterpret_cast<float4 *>(dst + r * ld + 4 * j);
-      if (add) {
-        const float4 b = *at;
-        o = make_float4(__fadd_rn(b.x, o.x), __fadd_rn(b.y, o.y), __fadd_rn(b.z, o.z), __fadd_rn(b.w, o.w));
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    float4 v = *reinterpret_cast<const float4 *>(blk + r * 128 + 16 * (j ^ (r & 7)));
+    if (r < rows_valid && col < p.n) {
+      const int64_t at = (out_row + r) * p.n + col;
+      float4 *to = fp32 ? reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at)
+                        : reinterpret_cast<float4 *>(static_cast<__nv_bfloat16 *>(p.y) + at);
+      if (fp32 && p.accumulate) {
+        const float4 b = *to;
+        v = make_float4(__fadd_rn(b.x, v.x), __fadd_rn(b.y, v.y), __fadd_rn(b.z, v.z), __fadd_rn(b.w, v.w));
       }
-      *at = o;
+      *to = v;
     }
   }
-  __syncwarp();
 }
 
 template <Kind128 K>
@@ -447,9 +466,10 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
             stop = warp_any(!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status));
             if (stop) break;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dst[lane + 32 * j] = ra[j];
+            for (int j = 0; j < 4; ++j) dst[32 * j + 4 * (lane & 7) + (lane >> 3)] = ra[j];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[128 + lane + 32 * j] = cb[j];
+            for (int j = 0; j < 8; ++j)  // column lane + 32 (j % 4) of half j / 4
+              dst[128 + ((j >> 2) * 4 + ((lane >> 1) & 3)) * kColSet + 8 * (j & 3) + 2 * (lane >> 3) + (lane & 1)] = cb[j];
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.sc_full[slot]);
           }
@@ -513,7 +533,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      // The block's four chunks of 32 columns: loaded while the one before is summed, the accumulator
+      // Forward, dgrad: the block's four chunks of 32 columns, loaded while the one before is summed, the accumulator
       // released as soon as the last is in registers.
       auto sum_block = [&](uint32_t b, auto add) {
         const uint32_t tb = tq + b * kBN;
@@ -541,9 +561,10 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
           const uint32_t slot = g % kScaleSlots;
           if (!mbar_wait(&s.sc_full[slot], (g / kScaleSlots) & 1, abort_flag, p.status)) stop = true;
           const float *sc = scales + slot * kScaleSlotFloatsW;
-          const float *cs = sc + 128 + half * 128;
-          const float v = sc[r];
-          const float2 f = make_float2(v, v);
+          const float4 rs = *reinterpret_cast<const float4 *>(sc + 32 * q + 4 * (lane >> 2));
+          const float2 rf[4] = {make_float2(rs.x, rs.x), make_float2(rs.y, rs.y), make_float2(rs.z, rs.z),
+                                make_float2(rs.w, rs.w)};
+          const float4 *cs = reinterpret_cast<const float4 *>(sc + 128 + (half * 4 + (lane & 3)) * kColSet);
           if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) stop = true;
           if (i % kVoteBlocks == kVoteBlocks - 1 && warp_any(stop)) {
             stop = true;
@@ -552,14 +573,45 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
           // the block's MMAs are done: its operands' stage is free
           if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
           tc_fence_after();
-          auto add = [&](int c, const uint32_t(&d)[32]) {
+          // Chunks of 16 rows x 32 columns, the two row halves of the columns in turn.
+          float4 cv[2];
+          const uint32_t tb = tq + b * kBN;
+          auto at = [&](int c) { return tb + (static_cast<uint32_t>((c & 1) * 16) << 16) + (c >> 1) * 32; };
+          auto add = [&](int c, const uint32_t(&d)[16]) {
+            if ((c & 1) == 0) cv[0] = cs[c], cv[1] = cs[c + 1];
+            float2 f[2][4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 x = make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
-              acc[16 * c + j] = __ffma2_rn(x, __fmul2_rn(*reinterpret_cast<const float2 *>(cs + 32 * c + 2 * j), f), acc[16 * c + j]);
-            }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                f[u][j] = __fmul2_rn(j & 1 ? make_float2(cv[j / 2].z, cv[j / 2].w) : make_float2(cv[j / 2].x, cv[j / 2].y),
+                                     rf[2 * (c & 1) + u]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float2 &to = acc[32 * (c & 1) + 16 * u + (c >> 1) * 4 + j];
+                to = __ffma2_rn(f[u][j], make_float2(__uint_as_float(d[4 * j + 2 * u]), __uint_as_float(d[4 * j + 2 * u + 1])), to);
+              }
           };
-          sum_block(b, add);
+          uint32_t va[16], vb[16];
+          tmem_ld_16x256b(at(0), va);
+          tmem_wait_ld_for(va);
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {
+            tmem_ld_16x256b(at(c + 1), vb);
+            add(c, va);
+            tmem_wait_ld_for(vb);
+            if (c < 6) {
+              tmem_ld_16x256b(at(c + 2), va);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) pair::arrive_remote_relaxed(leader_empty[b]);
+            }
+            add(c + 1, vb);
+            if (c < 6) tmem_wait_ld_for(va);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.sc_empty[slot]);
           ++g;
@@ -610,15 +662,45 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
       };
-      const bool fp32 = K == Kind128::kWgrad && p.out_fp32;
-      if (fp32 && tl.nk == 0 && p.accumulate) continue;
+      if constexpr (K == Kind128::kWgrad) {
+        const bool fp32 = p.out_fp32;
+        if (fp32 && tl.nk == 0 && p.accumulate) continue;
+        const int fr = lane >> 2, fc = lane & 3;  // rows fr + 8 i, columns 2 fc and the next of each 8
 #pragma unroll
-      for (int half_tile = 0; half_tile < (K == Kind128::kWgrad ? 2 : 1); ++half_tile) {
-        if (!fp32 && half_tile == 1) break;
-        const int wide = fp32 ? 32 : 64;  // columns of a block
-        const int base = c0 + half_tile * 64;
-        if (base >= p.n) break;
-        const int whole = (fp32 && p.accumulate) || warp_rows < 32 ? 0 : min(2, (static_cast<int>(p.n) - base) / wide);
+        for (int half_tile = 0; half_tile < 2; ++half_tile) {
+          if (!fp32 && half_tile == 1) break;
+          const int wide = fp32 ? 32 : 64;
+          const int base = c0 + half_tile * 64;
+          if (base >= p.n) break;
+          const int whole = (fp32 && p.accumulate) || warp_rows < 32 ? 0 : min(2, (static_cast<int>(p.n) - base) / wide);
+          await_staging();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint8_t *row = stage_blks + (fr + 8 * i) * 128;
+            if (fp32) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float2 *>(row + (j >> 2) * kOutBlockBytes + 16 * ((2 * (j & 3) + (fc >> 1)) ^ fr) +
+                                            8 * (fc & 1)) = acc[16 * i + 8 * half_tile + j];
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                *reinterpret_cast<__nv_bfloat162 *>(row + (j >> 3) * kOutBlockBytes + 16 * ((j & 7) ^ fr) + 4 * fc) =
+                    __floats2bfloat162_rn(acc[16 * i + j].x, acc[16 * i + j].y);
+            }
+          }
+          if (whole > 0) fence_proxy_async_shared();
+          __syncwarp();
+          if (whole > 0 && lane == 0) {
+            for (int c = 0; c < whole; ++c)
+              tma_store_2d(&p.map_y, base + wide * c, static_cast<int32_t>(out_row), stage_blks + c * kOutBlockBytes);
+            bulk_commit();
+          }
+          for (int c = whole; c < 2; ++c)
+            store_staged(p, fp32, out_row, base + wide * c, warp_rows, stage_blks + c * kOutBlockBytes, lane);
+        }
+      } else {
+        const int whole = warp_rows < 32 ? 0 : min(2, (static_cast<int>(p.n) - c0) / 64);
         await_staging();
         if (whole > 0) {
 #pragma unroll
@@ -626,55 +708,38 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
             uint4 *row = reinterpret_cast<uint4 *>(stage_blks + c * kOutBlockBytes + lane * 128);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              uint4 v;
-              if (fp32) {
-                const float2 lo = acc[32 * half_tile + 16 * c + 2 * j], hi = acc[32 * half_tile + 16 * c + 2 * j + 1];
-                v = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
-              } else {
-                uint32_t w[4];
+              uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(acc[32 * c + 4 * j + i].x, acc[32 * c + 4 * j + i].y);
-                  w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                v = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[32 * c + 4 * j + i].x, acc[32 * c + 4 * j + i].y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
               }
-              row[j ^ xs] = v;
+              row[j ^ xs] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
             for (int c = 0; c < whole; ++c)
-              tma_store_2d(&p.map_y, base + wide * c, static_cast<int32_t>(out_row), stage_blks + c * kOutBlockBytes);
+              tma_store_2d(&p.map_y, c0 + 64 * c, static_cast<int32_t>(out_row), stage_blks + c * kOutBlockBytes);
             bulk_commit();
           }
         }
-        if (whole < 2 && base + wide * whole < p.n) {
+        if (whole < 2 && c0 + 64 * whole < p.n) {
           await_staging();
-          const int done = base + wide * whole;  // columns before it are stored
-          if (fp32) {
+          const int done = c0 + 64 * whole;  // columns before it are stored
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int col = base + 16 * c;
-              if (col >= done && col < p.n)
-                store_fp32_cut(static_cast<float *>(p.y) + out_row * p.n + col, p.n, warp_rows, 16, p.accumulate,
-                               stage_blks, lane, acc + 32 * half_tile + 8 * c);
+          for (int c = 0; c < 4; ++c) {
+            const int col = c0 + 32 * c;
+            if (col < done || col >= p.n) continue;
+            uint32_t packed[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * c + j].x, acc[16 * c + j].y);
+              packed[j] = *reinterpret_cast<const uint32_t *>(&h);
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int col = base + 32 * c;
-              if (col < done || col >= p.n) continue;
-              uint32_t packed[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[16 * c + j].x, acc[16 * c + j].y);
-                packed[j] = *reinterpret_cast<const uint32_t *>(&h);
-              }
-              store_block_cut(static_cast<__nv_bfloat16 *>(p.y) + out_row * p.n + col, p.n, warp_rows,
-                              static_cast<int>(p.n) - col, stage_blks, lane, packed);
-            }
+            store_block_cut(static_cast<__nv_bfloat16 *>(p.y) + out_row * p.n + col, p.n, warp_rows,
+                            static_cast<int>(p.n) - col, stage_blks, lane, packed);
           }
         }
       }
@@ -768,13 +833,6 @@ __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16])
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld_for(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15])::"memory");
-}
-
 struct ItemFew {
   int32_t e;
   int32_t row0;    // first token row
