@@ -110,10 +110,13 @@ __device__ __forceinline__ float sigmoid(float l) {
   return s;
 }
 
-// Order of keys as unsigned integers: larger float, larger integer, none 0; -0 as +0, a NaN as -inf.
+// Order of floats (no NaN) as unsigned integers: larger float, larger integer, none 0; -0 as +0.
 __device__ __forceinline__ uint32_t order_key(float f) {
-  const int32_t b = __float_as_int(fmaxf(f, -INFINITY) + 0.0f);
+  const int32_t b = __float_as_int(f + 0.0f);
   return static_cast<uint32_t>(b) ^ (static_cast<uint32_t>(b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_order(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 // The largest of a row held V values a lane, or 0 where nothing is above -inf: a finite offset for
@@ -145,8 +148,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const T *__restri
                                                                float scale, const float *__restrict__ bias,
                                                                int32_t *__restrict__ ids,
                                                                float *__restrict__ weights) {
-  // candidates: key, then the lower expert first
-  __shared__ uint64_t cand[kGateWarps][32];
+  // candidates' keys and experts
+  __shared__ alignas(16) float cand[kGateWarps][32];
+  __shared__ int cand_id[kGateWarps][32];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
@@ -160,76 +164,94 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const T *__restri
     m_all = row_offset<V>(l);
     denom = exp_row<V>(l, m_all, x);
   }
-  uint32_t key[V];
+  // Keys, a NaN as -inf; `live`: not past the experts (whole packs are or are not).
+  float key[V];
+  bool live[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = expert_of<VEC>(j, lane);
-    if (bias && e < experts) l[j] += __ldg(bias + e);
-    key[j] = e < experts ? order_key(l[j]) : 0u;
-  }
-  // A lower bound of the top_k-th key: the top_k-th largest of the lanes' largest keys (equal ones
-  // taken together, which only lowers it).
-  uint32_t bound = 1;
-  if constexpr (V > 1) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) m = max(m, key[j]);
-    for (int i = 0; i < top_k; ++i) {
-      bound = __reduce_max_sync(kAll, m);
-      if (m == bound) m = 0;
-    }
-    bound = max(bound, 1u);
-  }
-  // The keys at or above it, in any order: how many in the lanes before this one, by the bits of
-  // the lanes' counts.
-  int mine_n = 0;
-#pragma unroll
-  for (int j = 0; j < V; ++j) mine_n += key[j] >= bound ? 1 : 0;
-  int at = 0, n = 0;
-#pragma unroll
-  for (int b = 1; b <= V; b <<= 1) {
-    const uint32_t has = __ballot_sync(kAll, mine_n & b);
-    at += __popc(has & ((1u << lane) - 1)) * b;
-    n += __popc(has) * b;
-  }
-  int pos = top_k, my_id = 0;  // this lane's choice: number and expert; none if pos >= top_k
-  if (n <= 32) {
+  for (int j = 0; j < V; ++j) live[j] = expert_of<VEC>(j - j % VEC, lane) < experts;
+  if (bias) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (key[j] >= bound)
-        cand[warp][at++] = (static_cast<uint64_t>(key[j]) << 32) | static_cast<uint32_t>(~expert_of<VEC>(j, lane));
-    __syncwarp();
-    // every candidate counts those before it
-    if (lane < n) {
-      const uint64_t me = cand[warp][lane];
-      pos = 0;
-#pragma unroll 4
-      for (int q = 0; q < n; ++q) pos += cand[warp][q] > me ? 1 : 0;
-      my_id = static_cast<int>(~static_cast<uint32_t>(me));
+      if (live[j]) l[j] += __ldg(bias + expert_of<VEC>(j, lane));
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) key[j] = fmaxf(l[j], -INFINITY);
+  // A lower bound of the top_k-th key: the top_k-th largest of the lanes' largest keys (equal ones
+  // taken together, which only lowers it).
+  float bound = -INFINITY;
+  if constexpr (V > 1) {
+    float largest = key[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) largest = fmaxf(largest, key[j]);
+    uint32_t m = order_key(largest), at_most = 0;
+    for (int i = 0; i < top_k; ++i) {
+      at_most = __reduce_max_sync(kAll, m);
+      if (m == at_most) m = 0;
     }
+    if (at_most) bound = from_order(at_most);
+  }
+  // The keys at or above it are the candidates, in any order: every lane hands in one at a time.
+  uint32_t mine_set = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (key[j] >= bound && live[j]) mine_set |= 1u << j;
+  int *ci = cand_id[warp];
+  int n = 0;
+  while (const uint32_t has = __ballot_sync(kAll, mine_set != 0)) {
+    const int at = n + __popc(has & ((1u << lane) - 1));
+    if (mine_set && at < 32) ci[at] = expert_of<VEC>(__ffs(mine_set) - 1, lane);
+    mine_set &= mine_set - 1;
+    n += __popc(has);
+  }
+  int pos = top_k, my_id = 0;  // this lane's choice: number and expert; none if pos >= top_k
+  float my_l = -INFINITY;      // without the bias
+  if (n <= 32) {
+    float *ck = cand[warp];
+    __syncwarp();
+    if (lane < n) {
+      my_id = ci[lane];
+      my_l = to_float(row[my_id]);
+    }
+    const float me = fmaxf(bias && lane < n ? my_l + __ldg(bias + my_id) : my_l, -INFINITY);
+    ck[lane] = me;
+    __syncwarp();
+    // every candidate counts the larger keys
+    int before = 0;
+    for (int q = 0; q < n; q += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(ck + q);
+      before += (k.x > me ? 1 : 0) + (k.y > me ? 1 : 0) + (k.z > me ? 1 : 0) + (k.w > me ? 1 : 0);
+    }
+    // Of two different keys one counts the other: fewer counts than pairs, and some are equal.
+    if (__reduce_add_sync(kAll, lane < n ? before : 0) != n * (n - 1) / 2)
+      for (int q = 0; q < n; ++q) before += ck[q] == me && ci[q] < my_id ? 1 : 0;
+    if (lane < n) pos = before;
   } else {
     // many equal keys: one choice after the other
+    uint32_t left[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) left[j] = live[j] ? order_key(key[j]) : 0u;
     for (int i = 0; i < top_k; ++i) {
       uint32_t best = 0;
 #pragma unroll
-      for (int j = 0; j < V; ++j) best = max(best, key[j]);
+      for (int j = 0; j < V; ++j) best = max(best, left[j]);
       best = __reduce_max_sync(kAll, best);
       int e = INT32_MAX;
 #pragma unroll
       for (int j = V - 1; j >= 0; --j)
-        if (key[j] == best) e = expert_of<VEC>(j, lane);
+        if (left[j] == best) e = expert_of<VEC>(j, lane);
       e = __reduce_min_sync(kAll, e);
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (e == expert_of<VEC>(j, lane)) key[j] = 0;
+        if (e == expert_of<VEC>(j, lane)) left[j] = 0;
       if (lane == i) {
         pos = i;
         my_id = e;
+        my_l = to_float(row[e]);
       }
     }
   }
   const bool mine = pos < top_k;
-  const float my_l = mine ? to_float(row[my_id]) : -INFINITY;  // without the bias
+  if (!mine) my_l = -INFINITY;
   float s;
   if (softmax) {
     float ref = normalize ? warp_max(my_l) : m_all;
