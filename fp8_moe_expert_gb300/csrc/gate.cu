@@ -512,23 +512,20 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
   }
 }
 
-// Sum over a CTA of 1024 threads, in every thread.
-__device__ __forceinline__ float block_sum(float v, float *part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = warp_sum(v);
-  __syncthreads();
-  if (lane == 0) part[warp] = v;
-  __syncthreads();
-  return warp_sum(part[lane]);
+// Adds one and returns what was there; orders the thread's writes before it, and later reads after it.
+__device__ __forceinline__ int32_t take_ticket(int32_t *counter) {
+  int32_t old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
 }
 
 // One CTA for 32 experts of a sequence: lane = expert, each warp adds every 32nd piece, the warps'
 // sums are added in order; then the experts' part of the sequence's term.  The last CTA to finish adds
-// all parts in order.
+// all parts in order; an only CTA has nothing to add (1023 tokens x 32 experts: the loss 8.5 -> 6.1 us).
 __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
   __shared__ float sums[32][33];
   __shared__ int32_t cnts[32][33];
-  __shared__ float red[32];
+  __shared__ float2 red[32];
   __shared__ int last;
   __shared__ int32_t total_tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -576,26 +573,37 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(LaunchBalance a) {
       const int32_t t = total_tokens;
       const float tf = static_cast<float>(t);
       if (e < 32) a.seq_tokens[s] = t;
-      a.term[blockIdx.x] = t > 0 ? term / tf * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tf)) : 0.0f;
-      __threadfence();
-      last = atomicAdd(a.flags, 1) == static_cast<int>(gridDim.x) - 1;
+      const float all = t > 0 ? term / tf * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tf)) : 0.0f;
+      if (gridDim.x == 1) {  // the only part
+        a.loss[0] = a.alpha * all;
+        last = 0;
+      } else {
+        a.term[blockIdx.x] = all;
+        last = take_ticket(a.flags) == static_cast<int32_t>(gridDim.x) - 1;
+      }
     }
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
   float all = 0.0f, live = 0.0f;
   for (int64_t i = tid; i < gridDim.x; i += 1024) all += __ldcg(a.term + i);
   for (int64_t i = tid; i < a.num_seqs; i += 1024) live += __ldcg(a.seq_tokens + i) > 0 ? 1.0f : 0.0f;
-  all = block_sum(all, red);
-  live = block_sum(live, red);
-  if (tid == 0) a.loss[0] = live > 0.0f ? a.alpha * all / live : 0.0f;
+  all = warp_sum(all);
+  live = warp_sum(live);
+  if (lane == 0) red[warp] = make_float2(all, live);
+  __syncthreads();
+  if (warp == 0) {
+    all = warp_sum(red[lane].x);
+    live = warp_sum(red[lane].y);
+    if (lane == 0) a.loss[0] = live > 0.0f ? a.alpha * all / live : 0.0f;
+  }
 }
 
 // A warp takes `per_warp` consecutive tokens; the sequence's coefficients stay in registers from
-// one token to the next.
+// one token to the next.  Four CTAs fit an SM, as the launch assumes (fp32, 8 values a lane: three
+// without the bound, 13.8 -> 11.5 us for 32768 x 256).
 template <typename T, int V, int VEC>
-__global__ void __launch_bounds__(32 * kGateWarps) balance_backward_kernel(LaunchBalance a, int per_warp) {
+__global__ void __launch_bounds__(32 * kGateWarps, V <= 8 ? 4 : 1) balance_backward_kernel(LaunchBalance a, int per_warp) {
   const int lane = threadIdx.x & 31;
   const int experts = a.num_experts;
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5)) * per_warp;
