@@ -22,7 +22,9 @@
 //
 // One warp a token, V experts a lane, VEC of them neighbours (one load of up to 16 bytes); all
 // sums fp32.  Reads the logits once.  Few tokens: launch-bound.  Many: the instructions of the
-// selection and of the exponentials, a few hundred a token, take longer than its bytes.
+// selection (388 a token of 256 experts, top 8) and of the probabilities (203 in the loss, 250 in its
+// gradient), at 70 to 86% of the issue rate, take longer than its bytes.  32768 x 256, us: gate 13.6,
+// gradient 7.6; balance loss (bf16, sigmoid) 17.4, gradient 13.5.
 #include "block128.cuh"
 
 namespace fme {
