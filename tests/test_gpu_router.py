@@ -130,6 +130,18 @@ def test_gate_ties_go_to_the_lower_expert():
     assert bool((w[0] == 0.25).all())
 
 
+@pytest.mark.parametrize("experts", [24, 64, 100, 256, 1000])
+@pytest.mark.parametrize("step", [0.125, 1.0, 4.0])
+def test_gate_rows_with_equal_keys(experts, step):
+    """Coarse logits: a few, some, or most of a row's largest keys are equal."""
+    l = torch.round(logits_of(500, experts, torch.float32, experts, 3.0) / step) * step
+    bias = torch.round(torch.randn((experts,), generator=gen(1), device=DEV)) * step
+    for b in (None, bias):
+        for k in (1, 5, 8):
+            ids, _ = fme.moe_gate(l, k, bias=b)
+            assert torch.equal(ids.long(), choice(l, b, k))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_gate_masked_logits(dtype):
     low = torch.finfo(dtype).min
