@@ -14,7 +14,9 @@ namespace fme {
 
 // Programmatic serialization: a kernel launched with it may start once the one before it in the stream
 // lets it (or ends), and waits here for all of that one's writes; before this it touches no
-// global memory.  The row-wise quantizer lets its successor start at once.
+// global memory.  The row-wise quantizer and the products let their successors start at once: a
+// product sets up its barriers and tensor memory while the last CTAs of the kernel before it end (about
+// 1 us of 11 and of 20 for the gradients of 1999 rows).
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void start_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
