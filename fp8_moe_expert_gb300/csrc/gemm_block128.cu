@@ -116,8 +116,10 @@ __device__ __forceinline__ bool elect_one() {
 
 // Warps that work as one (epilogue, scales) give up as one, so that no lane is left waiting at a
 // warp-wide instruction: a lane whose wait ran out goes on with the others, every later wait of the CTA
-// ends at once, and the warp leaves at the next vote, before it writes the tile.  The vote is once for a
-// few blocks: one at every wait cost 2.5% (65536 x 4096 x 7168: 1.36 -> 1.40 ms).
+// ends at once, and the warp leaves at the next vote, before it writes the tile.  What it adds until then
+// is garbage, and so may be what the pair's other warps add; but it frees no stage any more, so the producers'
+// fills stay within a ring of those consumed, as the drain at the end assumes.  The vote is once for a few
+// blocks: one at every wait cost 2.5% (65536 x 4096 x 7168: 1.36 -> 1.40 ms).
 constexpr int kVoteBlocks = 8;
 __device__ __forceinline__ bool warp_any(bool stop) { return __any_sync(0xFFFFFFFFu, stop); }
 
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
             break;
           }
           // the block's MMAs are done: its operands' stage is free
-          if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
+          if (ew == 0 && lane == 0 && !stop) mbar_arrive(&s.freed[g % S]);
           tc_fence_after();
           // Chunks of 16 rows x 32 columns, the two row halves of the columns in turn.
           float4 cv[2];
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
             const float v = u == 0 ? f4.x : u == 1 ? f4.y : u == 2 ? f4.z : f4.w;
             const float2 f = make_float2(v, v);
             if (!mbar_wait(&s.acc_full[b], (g >> 1) & 1, abort_flag, p.status)) stop = true;
-            if (ew == 0 && lane == 0) mbar_arrive(&s.freed[g % S]);
+            if (ew == 0 && lane == 0 && !stop) mbar_arrive(&s.freed[g % S]);
             tc_fence_after();
             auto add = [&](int c, const uint32_t(&d)[32]) {
 #pragma unroll
@@ -1038,7 +1040,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const
           stop = true;
           break;
         }
-        if (warp == kEpiWarp0 && lane == 0) mbar_arrive(&s.freed[g % S]);  // the block's MMAs are done
+        if (warp == kEpiWarp0 && lane == 0 && !stop) mbar_arrive(&s.freed[g % S]);  // the block's MMAs are done
         tc_fence_after();
         const float4 *f = reinterpret_cast<const float4 *>(s.scales[slot]);
 #pragma unroll
