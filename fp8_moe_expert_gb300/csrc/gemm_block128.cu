@@ -17,7 +17,7 @@
 // a cycle.  With the sums it takes about 850: the scales' reads and the barriers go
 // through the same shared memory and the accumulator is held while it is read out.
 // 65536 x 4096 x 7168: 1.35 ms, 2.85 PFLOP/s; dgrad 65536 x 7168 x 2048, 32 experts:
-// 0.70 ms, 2.74 PFLOP/s; wgrad of the same: 1.17 ms, 1.64 PFLOP/s (about 1290 cycles a block,
+// 0.70 ms, 2.74 PFLOP/s; wgrad of the same: 1.18 ms, 1.63 PFLOP/s (about 1290 cycles a block,
 // the epilogue's: without its sums and products 800).
 //
 // One set of weight codes serves both directions: blocks are 128 x 128, and dgrad reads
