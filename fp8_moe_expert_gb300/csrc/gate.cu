@@ -106,11 +106,12 @@ __device__ __forceinline__ void sigmoids(float l, float &s, float &rest) {
   s = l >= 0.0f ? r : tr;
   rest = l >= 0.0f ? tr : r;
 }
-__device__ __forceinline__ float sigmoid(float l) {
-  float s, rest;
-  sigmoids(l, s, rest);
-  return s;
-}
+
+// Ratios of sigmoids, s_i / sum of s, of rows far below zero.  Sigmoids are subnormal from -87 and zero from -104 down,
+// their ratios are not.  Where the sum is below this, every logit is negative, and e^(l - max) (1 - s), which is
+// s e^-max, takes the place of s: the factor cancels.  2^-8: what the sigmoids themselves then lose is a ratio
+// below 2^-118, next to fp32's own 2^-126.  Other rows keep their one exponential.
+constexpr float kSmallSum = 0x1p-8f;
 
 // Order of floats (no NaN) as unsigned integers: larger float, larger integer, none 0; -0 as +0.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -260,7 +261,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const T *__restri
     if (ref == -INFINITY) ref = 0.0f;
     s = mine ? __expf(my_l - ref) : 0.0f;
   } else {
-    s = mine ? sigmoid(my_l) : 0.0f;
+    float rest;
+    sigmoids(my_l, s, rest);  // 0 at -inf: not a choice
+    if (normalize && warp_sum(s) < kSmallSum) {
+      const float top = warp_max(my_l);
+      s = __expf(my_l - (top == -INFINITY ? 0.0f : top)) * rest;
+    }
   }
   if (normalize) denom = warp_sum(s);
   if (mine) {
@@ -357,9 +363,17 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_kernel(
     float s = 0.0f, rest = 0.0f;
     if (live) sigmoids(l, s, rest);
     if (normalize) {
-      const float total = group_sum(s);
-      const float sum = group_sum(s * g);
-      d = total == 0.0f ? 0.0f : (g - sum / total) / total * s * rest;
+      float total = group_sum(s);
+      if (__any_sync(kAll, total < kSmallSum)) {
+        float top = l;
+#pragma unroll
+        for (int o = kWidth / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        const float near = __expf(l - (top == -INFINITY ? 0.0f : top)) * rest;
+        if (total < kSmallSum) s = near;
+        total = group_sum(s);
+      }
+      const float p = total == 0.0f ? 0.0f : s / total;
+      d = p * (g - group_sum(p * g)) * rest;
     } else {
       d = g * s * rest;
     }
@@ -385,6 +399,16 @@ __device__ __forceinline__ void probabilities(const float (&l)[V], bool softmax,
       z += p[j];
     }
     z = warp_sum(z);
+    if (z < kSmallSum) {  // slope holds 1 - s
+      const float top = row_offset<V>(l);
+      z = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        p[j] = __expf(l[j] - top) * slope[j];
+        z += p[j];
+      }
+      z = warp_sum(z);
+    }
     const float r = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
