@@ -80,27 +80,43 @@ fme_status get_encoder(EncodeTiledFn *fn) {
   return FME_OK;
 }
 
-// 2-D uint8 tensor [rows x inner] (row stride `stride` bytes), box {128 bytes, box_rows},
-// 128-byte swizzle, zero fill out of bounds.
-fme_status encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint64_t stride,
-                        uint32_t box_rows) {
+// Encodes a map.  The encoder is a driver call and wants a current context, which a host thread that has made no
+// runtime call yet does not have: the runtime binds the device's own, and the map is encoded again.
+fme_status encode_map(const char *what, CUtensorMap *map, CUtensorMapDataType type, cuuint32_t rank, void *base,
+                      const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                      CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
   EncodeTiledFn fn;
-  fme_status st = get_encoder(&fn);
+  const fme_status st = get_encoder(&fn);
   if (st != FME_OK) return st;
-  cuuint64_t dims[2] = {inner, rows};
-  cuuint64_t strides[1] = {stride};
-  cuuint32_t box[2] = {128, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = CUDA_SUCCESS;
+  for (int tries = 0; tries < 2; ++tries) {
+    r = fn(map, type, rank, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_ERROR_INVALID_CONTEXT || tries > 0) break;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaSetDevice(dev);
+    if (err != cudaSuccess) return cuda_fail(err, "cudaSetDevice");
+  }
   if (r != CUDA_SUCCESS) {
     char buf[96];
-    std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled%s failed (CUresult %d)", what, static_cast<int>(r));
     g_last_cuda_error = buf;
     return FME_ERR_CUDA;
   }
   return FME_OK;
+}
+
+// 2-D uint8 tensor [rows x inner] (row stride `stride` bytes), box {128 bytes, box_rows},
+// 128-byte swizzle, zero fill out of bounds.
+fme_status encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint64_t stride,
+                        uint32_t box_rows) {
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {stride};
+  cuuint32_t box[2] = {128, box_rows};
+  return encode_map("", map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // bf16 matrix [rows x cols] (row stride cols * 2 bytes) for bulk tensor stores of
@@ -108,24 +124,13 @@ fme_status encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint
 // 128-byte swizzle, bf16 or fp32.
 enum class OutBox { kBf16, kWideBf16, kWideFp32 };
 fme_status encode_bf16_out(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, OutBox kind = OutBox::kBf16) {
-  EncodeTiledFn fn;
-  fme_status st = get_encoder(&fn);
-  if (st != FME_OK) return st;
   const bool fp32 = kind == OutBox::kWideFp32, wide = kind != OutBox::kBf16;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * (fp32 ? 4 : 2)};
   cuuint32_t box[2] = {kind == OutBox::kWideBf16 ? 64u : 32u, 32};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    char buf[96];
-    std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled (output) failed (CUresult %d)", static_cast<int>(r));
-    g_last_cuda_error = buf;
-    return FME_ERR_CUDA;
-  }
-  return FME_OK;
+  return encode_map(" (output)", map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                    base, dims, strides, box, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 // Tiled scales of a tensor as a 2-D map of 8-byte words: one row per 128-row
@@ -133,23 +138,11 @@ fme_status encode_bf16_out(CUtensorMap *map, void *base, uint64_t cols, uint64_t
 // blocks, no swizzle, zero fill out of bounds.
 fme_status encode_scales_2d(CUtensorMap *map, const void *base, uint64_t row_blocks, uint64_t row_bytes,
                             uint32_t box_tiles, uint32_t box_rows) {
-  EncodeTiledFn fn;
-  fme_status st = get_encoder(&fn);
-  if (st != FME_OK) return st;
   cuuint64_t dims[2] = {row_bytes / 8, row_blocks};
   cuuint64_t strides[1] = {row_bytes};
   cuuint32_t box[2] = {64 * box_tiles, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    char buf[96];
-    std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled (scales) failed (CUresult %d)", static_cast<int>(r));
-    g_last_cuda_error = buf;
-    return FME_ERR_CUDA;
-  }
-  return FME_OK;
+  return encode_map(" (scales)", map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void *>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 int64_t padded_rows_bound(int64_t rows, int32_t groups) {
@@ -685,23 +678,11 @@ bool block128_cols(int64_t c) { return c >= 16 && c <= 65536 && c % 16 == 0; }
 // 3-D uint8 weights [experts][n][k], box {128, 128, 1}, 128-byte swizzle, zero fill past each
 // expert's n and k.
 fme_status encode_u8_weights(CUtensorMap *map, const void *base, uint64_t experts, uint64_t n, uint64_t k) {
-  EncodeTiledFn fn;
-  fme_status st = get_encoder(&fn);
-  if (st != FME_OK) return st;
   cuuint64_t dims[3] = {k, n, experts};
   cuuint64_t strides[2] = {k, n * k};
   cuuint32_t box[3] = {128, 128, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    char buf[96];
-    std::snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled (weights) failed (CUresult %d)", static_cast<int>(r));
-    g_last_cuda_error = buf;
-    return FME_ERR_CUDA;
-  }
-  return FME_OK;
+  return encode_map(" (weights)", map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // 128 x 128 tiles of a [rows x cols] tensor fit one launch.
