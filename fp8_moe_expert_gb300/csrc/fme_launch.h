@@ -6,7 +6,30 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fme {
+
+// Lets a kernel have as much dynamic shared memory as a block can get on the current device; `done` is the
+// kernel's own (of internal linkage: a process may hold two builds), a bit for each device.  Once and never lowered:
+// the limit belongs to the function, and set to each launch's own size it could be lowered by another host
+// thread's call before the launch that needed it.
+inline cudaError_t allow_shared(const void *kernel, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (dev & 63);  // current_device() admits 64
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  int most = 0;
+  cudaFuncAttributes f{};
+  if ((err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
+      (err = cudaFuncGetAttributes(&f, kernel)) != cudaSuccess ||
+      (err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  most - static_cast<int>(f.sharedSizeBytes))) != cudaSuccess)
+    return err;
+  done.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
 
 struct LaunchNvfp4 {
   const void *x;

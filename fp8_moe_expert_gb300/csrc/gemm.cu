@@ -293,7 +293,8 @@ static cudaError_t launch_mx(const LaunchGemm &in) {
   a.stages = C::kStages;
   while (a.stages > 2 && gemm_smem_bytes(a.stages, C::kStageBytes, a.num_experts) > kGemmSmemLimit) --a.stages;
   const int smem_bytes = static_cast<int>(gemm_smem_bytes(a.stages, C::kStageBytes, a.num_experts));
-  return launch_pairs(grouped_gemm_mx_kernel<K>, a, kThreads, smem_bytes, gemm_tile_bound(a));
+  static std::atomic<uint64_t> allowed{0};
+  return launch_pairs(grouped_gemm_mx_kernel<K>, allowed, a, kThreads, smem_bytes, gemm_tile_bound(a));
 }
 
 cudaError_t launch_grouped_gemm(const LaunchGemm &a) {

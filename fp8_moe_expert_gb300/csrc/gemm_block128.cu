@@ -1088,7 +1088,8 @@ template <Kind128 K>
 cudaError_t launch128(const LaunchBlock128 &a) {
   const int smem = 1024 + kStages128 * kStageBytes128 + kStageOut + 8 * (a.num_experts + 1);
   auto kernel = gemm_block128_kernel<K>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
   if (err != cudaSuccess) return err;
   const int64_t nb = (a.n + kBN - 1) / kBN;
   const int64_t bound = K == Kind128::kWgrad ? a.num_experts * ((a.m + kPairM - 1) / kPairM) * nb
@@ -1114,8 +1115,8 @@ cudaError_t launch128(const LaunchBlock128 &a) {
 
 cudaError_t launch_few(const LaunchBlock128 &a) {
   const int smem = 1024 + kFewStages * kFewStageBytes + 8 * (a.num_experts + 1);
-  cudaError_t err =
-      cudaFuncSetAttribute(gemm_block128_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_shared(reinterpret_cast<const void *>(gemm_block128_few_kernel), allowed);
   if (err != cudaSuccess) return err;
   const int64_t items = (a.m / kFewTokens + std::min<int64_t>(a.num_experts, a.m)) * ((a.n + kBM - 1) / kBM);
   cudaLaunchConfig_t cfg = {};

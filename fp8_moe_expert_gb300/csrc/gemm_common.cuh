@@ -493,8 +493,9 @@ __device__ __forceinline__ void epilogue_warp(const LaunchGemm &p, const Groups 
 
 // A pair-cluster launch of `kernel` on as many pairs as the work and the SMs allow.
 template <typename Kernel>
-cudaError_t launch_pairs(Kernel kernel, const LaunchGemm &a, int threads, int smem_bytes, int64_t tile_bound) {
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+cudaError_t launch_pairs(Kernel kernel, std::atomic<uint64_t> &allowed, const LaunchGemm &a, int threads, int smem_bytes,
+                         int64_t tile_bound) {
+  cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
   if (err != cudaSuccess) return err;
   int pairs = a.num_sms / 2;
   if (tile_bound < pairs) pairs = static_cast<int>(tile_bound > 0 ? tile_bound : 1);

@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_nvfp4_kernel(const _
 }  // namespace
 
 template <GemmKind K>
-cudaError_t launch_gemm_nvfp4_kind(const LaunchGemm &in) {
+static cudaError_t launch_gemm_nvfp4_kind(const LaunchGemm &in) {
   LaunchGemm a = in;
   a.stages = kStages;
   while (a.stages > 2 && gemm_smem_bytes(a.stages, kStageBytes, a.num_experts) > kGemmSmemLimit) --a.stages;
@@ -360,7 +360,8 @@ cudaError_t launch_gemm_nvfp4_kind(const LaunchGemm &in) {
   cudaError_t err = cudaFuncGetAttributes(&fa, grouped_gemm_nvfp4_kernel<K>);
   if (err != cudaSuccess) return err;
   if (fa.numRegs != 65536 / kThreads) return cudaErrorInvalidConfiguration;
-  return launch_pairs(grouped_gemm_nvfp4_kernel<K>, a, kThreads, smem_bytes, gemm_tile_bound(a));
+  static std::atomic<uint64_t> allowed{0};
+  return launch_pairs(grouped_gemm_nvfp4_kernel<K>, allowed, a, kThreads, smem_bytes, gemm_tile_bound(a));
 }
 
 cudaError_t launch_grouped_gemm_nvfp4(const LaunchGemm &in) {

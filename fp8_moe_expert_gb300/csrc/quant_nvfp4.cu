@@ -414,7 +414,8 @@ static cudaError_t launch_nvfp4(const LaunchNvfp4 &a) {
   stages = stages < 3 ? 3 : (stages > 16 ? 16 : stages);
   const size_t smem = nv_smem_bytes(static_cast<int>(stages), row_bytes, a.num_groups);
   auto kernel = nvfp4_pertoken_kernel<R, kSwiGLU, kGather>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
   if (err != cudaSuccess) return err;
   const int64_t cap = static_cast<int64_t>(a.num_sms) * per_sm;
   const int blocks = static_cast<int>(a.rows < cap ? (a.rows > 0 ? a.rows : 1) : cap);
