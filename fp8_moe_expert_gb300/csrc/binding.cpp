@@ -44,40 +44,62 @@ const char *name_of(at::ScalarType t) {
   }
 }
 
-const at::Tensor &tensor(const char *where, const char *name, PyObject *o) {
-  if (!THPVariable_Check(o)) throw Refused(std::string(where) + ": " + name + " must be a tensor");
+// A call: its name, and the device that all its tensors must share.
+struct Call {
+  const char *where;
+  const char *first = nullptr;  // the argument whose device it is
+  int device = -1;
+};
+
+const at::Tensor &tensor(const Call &c, const char *name, PyObject *o) {
+  if (!THPVariable_Check(o)) throw Refused(std::string(c.where) + ": " + name + " must be a tensor");
   return THPVariable_Unpack(o);
 }
 
-void need(const char *where, const char *name, const at::Tensor &t, at::ScalarType type, Shape shape) {
-  if (t.scalar_type() == type && t.sizes() == shape && t.is_cuda() && t.is_contiguous()) return;
+// The kernels get plain addresses, so one of another GPU's would be an illegal access there.
+void on_one_device(Call &c, const char *name, const at::Tensor &t) {
+  const int device = t.device().index();
+  if (!c.first) {
+    c.first = name;
+    c.device = device;
+  } else if (device != c.device) {
+    std::ostringstream s;
+    s << c.where << ": " << name << " is on " << t.device() << ", " << c.first << " on cuda:" << c.device;
+    throw Refused(s.str());
+  }
+}
+
+void need(Call &c, const char *name, const at::Tensor &t, at::ScalarType type, Shape shape) {
+  if (t.scalar_type() == type && t.sizes() == shape && t.is_cuda() && t.is_contiguous()) {
+    on_one_device(c, name, t);
+    return;
+  }
   std::ostringstream s;
-  s << where << ": " << name << " must be a contiguous CUDA tensor of " << name_of(type) << " " << describe(shape)
+  s << c.where << ": " << name << " must be a contiguous CUDA tensor of " << name_of(type) << " " << describe(shape)
     << ", got " << name_of(t.scalar_type()) << " " << describe(t.sizes()) << " on " << t.device()
     << (t.is_contiguous() ? "" : " (not contiguous)");
   throw Refused(s.str());
 }
 
-const at::Tensor &input(const char *where, const char *name, PyObject *o, at::ScalarType type, Shape shape) {
-  const at::Tensor &t = tensor(where, name, o);
-  need(where, name, t, type, shape);
+const at::Tensor &input(Call &c, const char *name, PyObject *o, at::ScalarType type, Shape shape) {
+  const at::Tensor &t = tensor(c, name, o);
+  need(c, name, t, type, shape);
   return t;
 }
 
 // Dimensions of an argument that the others' shapes follow from.
-Shape dims(const char *where, const char *name, PyObject *o, size_t n) {
-  const at::Tensor &t = tensor(where, name, o);
+Shape dims(const Call &c, const char *name, PyObject *o, size_t n) {
+  const at::Tensor &t = tensor(c, name, o);
   if (t.dim() != static_cast<int64_t>(n))
-    throw Refused(std::string(where) + ": " + name + " must have " + std::to_string(n) + " dimensions, got " +
+    throw Refused(std::string(c.where) + ": " + name + " must have " + std::to_string(n) + " dimensions, got " +
                   describe(t.sizes()));
   return t.sizes();
 }
 
 // The caller's output tensor, checked, or a new one.
-at::Tensor output(const char *where, const char *name, PyObject *o, at::ScalarType type, Shape shape,
-                  const at::Tensor &like) {
+at::Tensor output(Call &c, const char *name, PyObject *o, at::ScalarType type, Shape shape, const at::Tensor &like) {
   if (o == Py_None) return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
-  return input(where, name, o, type, shape);
+  return input(c, name, o, type, shape);
 }
 
 template <typename T = void>
@@ -85,11 +107,12 @@ T *ptr(const at::Tensor &t) {
   return static_cast<T *>(t.data_ptr());
 }
 
-int32_t *status_ptr(const char *where, PyObject *o) {
+int32_t *status_ptr(Call &c, PyObject *o) {
   if (o == Py_None) return nullptr;
-  const at::Tensor &t = tensor(where, "status", o);
+  const at::Tensor &t = tensor(c, "status", o);
   if (t.scalar_type() != at::kInt || !t.is_cuda() || t.numel() < 1)
-    throw Refused(std::string(where) + ": status must be a CUDA tensor of torch.int32");
+    throw Refused(std::string(c.where) + ": status must be a CUDA tensor of torch.int32");
+  on_one_device(c, "status", t);
   return ptr<int32_t>(t);
 }
 
@@ -114,6 +137,15 @@ bool truth(PyObject *o) {
   return v != 0;
 }
 
+// The tensors' device must be the current one: its streams, properties and launches are the call's.
+void on_current_device(const Call &c) {
+  const int current = c10::cuda::current_device();
+  if (c.device == current) return;
+  std::ostringstream s;
+  s << c.where << ": " << c.first << " is on cuda:" << c.device << ", the current device is cuda:" << current;
+  throw Refused(s.str());
+}
+
 // A raw stream, or None for the current one of the current device.
 void *stream_of(PyObject *o) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
@@ -123,11 +155,11 @@ void *stream_of(PyObject *o) {
 }
 
 template <typename F>
-void call(const char *where, F f) {
+void call(const Call &c, F f) {
   fme_status st;
   Py_BEGIN_ALLOW_THREADS st = f();
   Py_END_ALLOW_THREADS if (st == FME_OK) return;
-  PyObject *e = PyObject_CallFunction(g_fme_error, "iss", st, where, st == FME_ERR_CUDA ? fme_last_cuda_error() : "");
+  PyObject *e = PyObject_CallFunction(g_fme_error, "iss", st, c.where, st == FME_ERR_CUDA ? fme_last_cuda_error() : "");
   if (e) {
     PyErr_SetObject(g_fme_error, e);
     Py_DECREF(e);
@@ -186,7 +218,7 @@ constexpr auto kU8 = at::kByte;
 // ------------------------------------------------------------------ quantizers --
 // x, src_row, top_k, codes, scale, status, stream
 PyObject *quantize_rows(PyObject *const *a) {
-  const char *w = "quantize_fp8_block128";
+  Call w{"quantize_fp8_block128"};
   const Shape s = dims(w, "x", a[0], 2);
   const int64_t rows = s[0], cols = s[1];
   const at::Tensor &x = input(w, "x", a[0], kBf16, {rows, cols});
@@ -194,9 +226,10 @@ PyObject *quantize_rows(PyObject *const *a) {
   const bool gather = a[1] != Py_None;
   const int64_t out = gather ? rows * top_k : rows;
   const int32_t *src = gather ? ptr<int32_t>(input(w, "src_row", a[1], kI32, {out})) : nullptr;
+  int32_t *st = status_ptr(w, a[5]);
+  on_current_device(w);
   const at::Tensor codes = output(w, "codes", a[3], kU8, {out, cols}, x);
   const at::Tensor scale = output(w, "scale", a[4], kF32, {(cols + 127) / 128, out}, x);
-  int32_t *st = status_ptr(w, a[5]);
   void *stream = stream_of(a[6]);
   call(w, [&] {
     return gather ? permute_quantize_fp8_block128(ptr(x), rows, cols, src, top_k, ptr<uint8_t>(codes), ptr<float>(scale),
@@ -208,7 +241,7 @@ PyObject *quantize_rows(PyObject *const *a) {
 }
 
 // The groups of a column-wise call: offsets (or None) and their number (or None).
-int32_t groups_of(const char *w, PyObject *offsets, PyObject *num_groups, const int32_t **out) {
+int32_t groups_of(Call &w, PyObject *offsets, PyObject *num_groups, const int32_t **out) {
   *out = nullptr;
   if (offsets == Py_None) return num_groups == Py_None ? 1 : integer32(num_groups);
   const int64_t n = num_groups == Py_None ? dims(w, "offsets", offsets, 1)[0] - 1 : integer(num_groups);
@@ -218,17 +251,18 @@ int32_t groups_of(const char *w, PyObject *offsets, PyObject *num_groups, const 
 
 // x, offsets, num_groups, codes, scale, padded_offsets, status, stream
 PyObject *quantize_cols(PyObject *const *a) {
-  const char *w = "quantize_fp8_block128";
+  Call w{"quantize_fp8_block128"};
   const Shape s = dims(w, "x", a[0], 2);
   const int64_t rows = s[0], cols = s[1];
   const at::Tensor &x = input(w, "x", a[0], kBf16, {rows, cols});
   const int32_t *off;
   const int32_t g = groups_of(w, a[1], a[2], &off);
   const int64_t ld = fme_colwise_ld(rows, g);
+  int32_t *st = status_ptr(w, a[6]);
+  on_current_device(w);
   const at::Tensor codes = output(w, "codes", a[3], kU8, {ld, cols}, x);
   const at::Tensor scale = output(w, "scale", a[4], kF32, {ld / 128, cols}, x);
   const at::Tensor po = output(w, "padded_offsets", a[5], kI32, {g < 0 ? 0 : int64_t(g) + 1}, x);
-  int32_t *st = status_ptr(w, a[6]);
   void *stream = stream_of(a[7]);
   call(w, [&] {
     return quantize_fp8_block128(ptr(x), rows, cols, FME_COLWISE, off, g, ptr<uint8_t>(codes), ptr<float>(scale),
@@ -239,19 +273,20 @@ PyObject *quantize_cols(PyObject *const *a) {
 
 // x, offsets, num_groups, row_codes, row_scale, col_codes, col_scale, padded_offsets, status, stream
 PyObject *quantize_rowcol(PyObject *const *a) {
-  const char *w = "quantize_fp8_block128_rowcol";
+  Call w{"quantize_fp8_block128_rowcol"};
   const Shape s = dims(w, "x", a[0], 2);
   const int64_t rows = s[0], cols = s[1];
   const at::Tensor &x = input(w, "x", a[0], kBf16, {rows, cols});
   const int32_t *off;
   const int32_t g = groups_of(w, a[1], a[2], &off);
   const int64_t ld = fme_colwise_ld(rows, g);
+  int32_t *st = status_ptr(w, a[8]);
+  on_current_device(w);
   const at::Tensor rc = output(w, "row_codes", a[3], kU8, {rows, cols}, x);
   const at::Tensor rs = output(w, "row_scale", a[4], kF32, {(cols + 127) / 128, rows}, x);
   const at::Tensor cc = output(w, "col_codes", a[5], kU8, {ld, cols}, x);
   const at::Tensor cs = output(w, "col_scale", a[6], kF32, {ld / 128, cols}, x);
   const at::Tensor po = output(w, "padded_offsets", a[7], kI32, {g < 0 ? 0 : int64_t(g) + 1}, x);
-  int32_t *st = status_ptr(w, a[8]);
   void *stream = stream_of(a[9]);
   call(w, [&] {
     return quantize_fp8_block128_rowcol(ptr(x), rows, cols, off, g, ptr<uint8_t>(rc), ptr<float>(rs), ptr<uint8_t>(cc),
@@ -262,10 +297,11 @@ PyObject *quantize_rowcol(PyObject *const *a) {
 
 // w, codes, scale, stream
 PyObject *quantize_weights(PyObject *const *a) {
-  const char *w = "quantize_fp8_block128_weights";
+  Call w{"quantize_fp8_block128_weights"};
   const Shape s = dims(w, "w", a[0], 3);
   const int64_t e = s[0], n = s[1], k = s[2];
   const at::Tensor &x = input(w, "w", a[0], kBf16, {e, n, k});
+  on_current_device(w);
   const at::Tensor codes = output(w, "codes", a[1], kU8, {e, n, k}, x);
   const at::Tensor scale = output(w, "scale", a[2], kF32, {e, (n + 127) / 128, (k + 127) / 128}, x);
   void *stream = stream_of(a[3]);
@@ -280,18 +316,20 @@ PyObject *quantize_weights(PyObject *const *a) {
 // a_codes, a_scale, w_codes, w_scale, offsets, y, status, stream
 template <bool kDgrad>
 PyObject *rows_gemm(PyObject *const *a) {
-  const char *w = kDgrad ? "grouped_gemm_dgrad_fp8_block128" : "grouped_gemm_fwd_fp8_block128";
+  Call w{kDgrad ? "grouped_gemm_dgrad_fp8_block128" : "grouped_gemm_fwd_fp8_block128"};
   const Shape ws = dims(w, "w_codes", a[2], 3);
   const int64_t e = ws[0], n = ws[1], k = ws[2];
-  const int64_t m = dims(w, "a_codes", a[0], 2)[0];
+  const char *codes = kDgrad ? "dy_codes" : "a_codes";
+  const int64_t m = dims(w, codes, a[0], 2)[0];
   const int64_t inner = kDgrad ? n : k, cols = kDgrad ? k : n;
-  const at::Tensor &ac = input(w, "a_codes", a[0], kU8, {m, inner});
-  const at::Tensor &as = input(w, "a_scale", a[1], kF32, {(inner + 127) / 128, m});
+  const at::Tensor &ac = input(w, codes, a[0], kU8, {m, inner});
+  const at::Tensor &as = input(w, kDgrad ? "dy_scale" : "a_scale", a[1], kF32, {(inner + 127) / 128, m});
   const at::Tensor &wc = input(w, "w_codes", a[2], kU8, {e, n, k});
   const at::Tensor &wsc = input(w, "w_scale", a[3], kF32, {e, (n + 127) / 128, (k + 127) / 128});
   const at::Tensor &off = input(w, "offsets", a[4], kI32, {e + 1});
-  const at::Tensor y = output(w, kDgrad ? "dx" : "y", a[5], kBf16, {m, cols}, ac);
   int32_t *st = status_ptr(w, a[6]);
+  on_current_device(w);
+  const at::Tensor y = output(w, kDgrad ? "dx" : "y", a[5], kBf16, {m, cols}, ac);
   void *stream = stream_of(a[7]);
   const int32_t experts = static_cast<int32_t>(e);
   call(w, [&] {
@@ -304,7 +342,7 @@ PyObject *rows_gemm(PyObject *const *a) {
 
 // dy_codes, dy_scale, x_codes, x_scale, padded_offsets, dw, mode (FME_DW_*), status, stream
 PyObject *wgrad(PyObject *const *a) {
-  const char *w = "grouped_gemm_wgrad_fp8_block128";
+  Call w{"grouped_gemm_wgrad_fp8_block128"};
   const Shape ds = dims(w, "dy_codes", a[0], 2);
   const int64_t ld = ds[0], n = ds[1], k = dims(w, "x_codes", a[2], 2)[1];
   const int64_t e = dims(w, "padded_offsets", a[4], 1)[0] - 1;
@@ -314,9 +352,10 @@ PyObject *wgrad(PyObject *const *a) {
   const at::Tensor &xs = input(w, "x_scale", a[3], kF32, {ld / 128, k});
   const at::Tensor &po = input(w, "padded_offsets", a[4], kI32, {e + 1});
   const int32_t mode = integer32(a[6]);
-  if (e < 1) throw Refused(std::string(w) + ": padded_offsets must have at least 2 elements");
-  const at::Tensor dw = output(w, "dw", a[5], mode == FME_DW_BF16 ? kBf16 : kF32, {e, n, k}, dc);
+  if (e < 1) throw Refused(std::string(w.where) + ": padded_offsets must have at least 2 elements");
   int32_t *st = status_ptr(w, a[7]);
+  on_current_device(w);
+  const at::Tensor dw = output(w, "dw", a[5], mode == FME_DW_BF16 ? kBf16 : kF32, {e, n, k}, dc);
   void *stream = stream_of(a[8]);
   call(w, [&] {
     return grouped_gemm_wgrad_fp8_block128(ptr<uint8_t>(dc), ptr<float>(dsc), ptr<uint8_t>(xc), ptr<float>(xs), ld,
@@ -331,30 +370,31 @@ struct Logits {
   int64_t tokens, experts;
   int32_t experts32, dtype;
 };
-Logits logits_of(const char *w, PyObject *o) {
+Logits logits_of(Call &w, PyObject *o) {
   const Shape s = dims(w, "logits", o, 2);
   const at::Tensor &t = THPVariable_Unpack(o);
   const auto type = t.scalar_type();
   if (type != kBf16 && type != kF32)
-    throw Refused(std::string(w) + ": logits must be bfloat16 or float32, got " + name_of(type));
+    throw Refused(std::string(w.where) + ": logits must be bfloat16 or float32, got " + name_of(type));
   need(w, "logits", t, type, s);
   return {t, s[0], s[1], s[1] > INT32_MAX ? INT32_MAX : static_cast<int32_t>(s[1]), type == kBf16 ? FME_BF16 : FME_FP32};
 }
-int32_t score_of(const char *w, PyObject *o) {
+int32_t score_of(const Call &w, PyObject *o) {
   const char *s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
   if (s && std::string(s) == "softmax") return FME_SCORE_SOFTMAX;
   if (s && std::string(s) == "sigmoid") return FME_SCORE_SIGMOID;
   PyErr_Clear();
-  throw Refused(std::string(w) + ": score must be 'softmax' or 'sigmoid'");
+  throw Refused(std::string(w.where) + ": score must be 'softmax' or 'sigmoid'");
 }
 
 // logits, top_k, score, bias, normalize, scale, ids, weights, stream
 PyObject *gate(PyObject *const *a) {
-  const char *w = "moe_gate";
+  Call w{"moe_gate"};
   const Logits l = logits_of(w, a[0]);
   const int32_t top_k = integer32(a[1]), score = score_of(w, a[2]);
   const float *bias = a[3] == Py_None ? nullptr : ptr<float>(input(w, "bias", a[3], kF32, {l.experts}));
-  if (top_k < 0) throw Refused(std::string(w) + ": top_k must not be negative");
+  if (top_k < 0) throw Refused(std::string(w.where) + ": top_k must not be negative");
+  on_current_device(w);
   const at::Tensor ids = output(w, "ids", a[6], kI32, {l.tokens, top_k}, l.t);
   const at::Tensor weights = output(w, "weights", a[7], kF32, {l.tokens, top_k}, l.t);
   const int32_t normalize = truth(a[4]);
@@ -369,15 +409,16 @@ PyObject *gate(PyObject *const *a) {
 
 // logits, ids, d_weights, score, normalize, scale, d_logits, status, stream
 PyObject *gate_backward(PyObject *const *a) {
-  const char *w = "moe_gate_backward";
+  Call w{"moe_gate_backward"};
   const Logits l = logits_of(w, a[0]);
   const int64_t top_k = dims(w, "ids", a[1], 2)[1];
   const at::Tensor &ids = input(w, "ids", a[1], kI32, {l.tokens, top_k});
   const at::Tensor &d = input(w, "d_weights", a[2], kF32, {l.tokens, top_k});
   const int32_t score = score_of(w, a[3]), normalize = truth(a[4]);
   const float scale = real(a[5]);
-  const at::Tensor out = output(w, "d_logits", a[6], l.t.scalar_type(), {l.tokens, l.experts}, l.t);
   int32_t *st = status_ptr(w, a[7]);
+  on_current_device(w);
+  const at::Tensor out = output(w, "d_logits", a[6], l.t.scalar_type(), {l.tokens, l.experts}, l.t);
   void *stream = stream_of(a[8]);
   const int32_t k = top_k > INT32_MAX ? INT32_MAX : static_cast<int32_t>(top_k);
   call(w, [&] {
@@ -392,7 +433,7 @@ struct Sequences {
   int64_t count;
   const uint8_t *mask;
 };
-Sequences sequences_of(const char *w, PyObject *offsets, PyObject *mask, int64_t tokens) {
+Sequences sequences_of(Call &w, PyObject *offsets, PyObject *mask, int64_t tokens) {
   Sequences s{nullptr, 1, nullptr};
   if (offsets != Py_None) {
     const int64_t n = dims(w, "seq_offsets", offsets, 1)[0];
@@ -402,7 +443,7 @@ Sequences sequences_of(const char *w, PyObject *offsets, PyObject *mask, int64_t
   if (mask != Py_None) {
     const at::Tensor &t = tensor(w, "token_mask", mask);
     if (t.scalar_type() != at::kBool && t.scalar_type() != kU8)
-      throw Refused(std::string(w) + ": token_mask must be bool or uint8, got " + name_of(t.scalar_type()));
+      throw Refused(std::string(w.where) + ": token_mask must be bool or uint8, got " + name_of(t.scalar_type()));
     need(w, "token_mask", t, t.scalar_type(), {tokens});
     s.mask = ptr<uint8_t>(t);
   }
@@ -411,14 +452,16 @@ Sequences sequences_of(const char *w, PyObject *offsets, PyObject *mask, int64_t
 
 // logits, ids, score, alpha, seq_offsets, token_mask, loss, counts, seq_tokens, workspace, status, stream
 PyObject *balance_loss(PyObject *const *a) {
-  const char *w = "moe_balance_loss";
+  Call w{"moe_balance_loss"};
   const Logits l = logits_of(w, a[0]);
   const int64_t top_k = dims(w, "ids", a[1], 2)[1];
   const at::Tensor &ids = input(w, "ids", a[1], kI32, {l.tokens, top_k});
   const int32_t score = score_of(w, a[2]);
   const float alpha = real(a[3]);
   const Sequences s = sequences_of(w, a[4], a[5], l.tokens);
-  if (s.count < 1) throw Refused(std::string(w) + ": seq_offsets must have at least 2 elements");
+  if (s.count < 1) throw Refused(std::string(w.where) + ": seq_offsets must have at least 2 elements");
+  int32_t *st = status_ptr(w, a[10]);
+  on_current_device(w);
   const at::Tensor loss = output(w, "loss", a[6], kF32, {1}, l.t);
   const at::Tensor counts = output(w, "counts", a[7], kI32, {s.count, l.experts}, l.t);
   const at::Tensor n = output(w, "seq_tokens", a[8], kI32, {s.count}, l.t);
@@ -428,8 +471,8 @@ PyObject *balance_loss(PyObject *const *a) {
                                 std::nullopt);
   else
     ws = tensor(w, "workspace", a[9]);
-  if (!ws.is_cuda() || !ws.is_contiguous()) throw Refused(std::string(w) + ": workspace must be a contiguous CUDA tensor");
-  int32_t *st = status_ptr(w, a[10]);
+  if (!ws.is_cuda() || !ws.is_contiguous()) throw Refused(std::string(w.where) + ": workspace must be a contiguous CUDA tensor");
+  on_one_device(w, "workspace", ws);
   void *stream = stream_of(a[11]);
   const int32_t k = top_k > INT32_MAX ? INT32_MAX : static_cast<int32_t>(top_k);
   call(w, [&] {
@@ -442,7 +485,7 @@ PyObject *balance_loss(PyObject *const *a) {
 
 // logits, counts, seq_tokens, d_loss, top_k, score, alpha, seq_offsets, token_mask, d_logits, accumulate, stream
 PyObject *balance_loss_backward(PyObject *const *a) {
-  const char *w = "moe_balance_loss_backward";
+  Call w{"moe_balance_loss_backward"};
   const Logits l = logits_of(w, a[0]);
   const Sequences s = sequences_of(w, a[7], a[8], l.tokens);
   const at::Tensor &counts = input(w, "counts", a[1], kI32, {s.count, l.experts});
@@ -451,7 +494,8 @@ PyObject *balance_loss_backward(PyObject *const *a) {
   const int32_t top_k = integer32(a[4]), score = score_of(w, a[5]);
   const float alpha = real(a[6]);
   const bool accumulate = truth(a[10]);
-  if (accumulate && a[9] == Py_None) throw Refused(std::string(w) + ": accumulate needs the d_logits to add to");
+  if (accumulate && a[9] == Py_None) throw Refused(std::string(w.where) + ": accumulate needs the d_logits to add to");
+  on_current_device(w);
   const at::Tensor out = output(w, "d_logits", a[9], l.t.scalar_type(), {l.tokens, l.experts}, l.t);
   void *stream = stream_of(a[11]);
   call(w, [&] {
@@ -464,16 +508,17 @@ PyObject *balance_loss_backward(PyObject *const *a) {
 
 // d_out, y, row_of, weights, d_y, d_weights, status, stream
 PyObject *combine_backward(PyObject *const *a) {
-  const char *w = "moe_combine_backward";
+  Call w{"moe_combine_backward"};
   const Shape ys = dims(w, "y", a[1], 2), rs = dims(w, "row_of", a[2], 2);
   const int64_t rows = ys[0], n = ys[1], tokens = rs[0], top_k = rs[1];
   const at::Tensor &d = input(w, "d_out", a[0], kBf16, {tokens, n});
   const at::Tensor &y = input(w, "y", a[1], kBf16, {rows, n});
   const at::Tensor &row_of = input(w, "row_of", a[2], kI32, {tokens, top_k});
   const at::Tensor &weights = input(w, "weights", a[3], kF32, {tokens, top_k});
+  int32_t *st = status_ptr(w, a[6]);
+  on_current_device(w);
   const at::Tensor dy = output(w, "d_y", a[4], kBf16, {rows, n}, y);
   const at::Tensor dw = output(w, "d_weights", a[5], kF32, {tokens, top_k}, y);
-  int32_t *st = status_ptr(w, a[6]);
   void *stream = stream_of(a[7]);
   const int32_t k = top_k > INT32_MAX ? INT32_MAX : static_cast<int32_t>(top_k);
   call(w, [&] {
