@@ -7,6 +7,10 @@ kernels; the binding only turns torch tensors into pointers, allocates outputs
 with torch when the caller does not pass them, and turns status codes into
 exceptions.  There is no fallback: if the library is missing or the device is not
 a GB300, calls raise.
+
+With `stream` a call runs there and not on the current stream: its inputs must be ready on it and must live
+until it is done with them.  What the FP8 block-128 and router calls allocate then comes from that stream's memory; the
+outputs may be used on the current stream once that waits for it, and freed at any time.
 """
 from __future__ import annotations
 
@@ -647,13 +651,6 @@ def moe_balance_loss(logits, ids, *, score="softmax", alpha=1.0, seq_offsets=Non
 
     seq_offsets: int32 [S+1], rising from 0 to tokens (None: one sequence); token_mask: bool or
     uint8 [tokens], the tokens that count (None: all)."""
-    if stream is not None and workspace is None:
-        seqs = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-        import torch
-
-        workspace = _empty((balance_workspace_bytes(logits.shape[0], seqs, logits.shape[1]),), torch.uint8,
-                           logits.device)
-        workspace.record_stream(stream)  # it is released when this call returns
     return _bind().balance_loss(logits, ids, score, alpha, seq_offsets, token_mask, loss, counts, seq_tokens, workspace,
                                 status, _raw(stream))
 

@@ -1,10 +1,11 @@
 // binding.cpp -- the Python side of the FP8 block-128, router and combine-gradient calls: checks
-// torch tensors, allocates the outputs that the caller does not bring, takes the current stream
+// torch tensors, allocates the outputs that the caller does not bring, takes the current stream or the given one
 // and calls the C ABI (include/fme.h).
 //
 // These calls take a few microseconds on the GPU in a decode step, less than their Python checks
 // and allocations took on a Grace core (moe_gate of 16 tokens: 11 us a call through ctypes).
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -96,12 +97,6 @@ Shape dims(const Call &c, const char *name, PyObject *o, size_t n) {
   return t.sizes();
 }
 
-// The caller's output tensor, checked, or a new one.
-at::Tensor output(Call &c, const char *name, PyObject *o, at::ScalarType type, Shape shape, const at::Tensor &like) {
-  if (o == Py_None) return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
-  return input(c, name, o, type, shape);
-}
-
 template <typename T = void>
 T *ptr(const at::Tensor &t) {
   return static_cast<T *>(t.data_ptr());
@@ -137,21 +132,48 @@ bool truth(PyObject *o) {
   return v != 0;
 }
 
-// The tensors' device must be the current one: its streams, properties and launches are the call's.
-void on_current_device(const Call &c) {
-  const int current = c10::cuda::current_device();
-  if (c.device == current) return;
-  std::ostringstream s;
-  s << c.where << ": " << c.first << " is on cuda:" << c.device << ", the current device is cuda:" << current;
-  throw Refused(s.str());
-}
+// The stream of a call: a raw one, or None for the current one.  The tensors' device must be the current one: its
+// streams, properties and launches are the call's.  What the call allocates while this lives comes from the pool
+// of its own stream: a block of another's, just freed, may still be used by work queued there.
+class OnStream {
+ public:
+  OnStream(const Call &c, PyObject *o) : outer_(c10::cuda::getCurrentCUDAStream()), own_(outer_) {
+    if (c.device != outer_.device_index()) {
+      std::ostringstream s;
+      s << c.where << ": " << c.first << " is on cuda:" << c.device << ", the current device is cuda:"
+        << static_cast<int>(outer_.device_index());
+      throw Refused(s.str());
+    }
+    if (o == Py_None) return;
+    void *raw = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw PythonError{};
+    own_ = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), outer_.device_index());
+    if (raw == outer_.stream()) return;
+    other_ = true;
+    c10::cuda::setCurrentCUDAStream(own_);
+  }
+  ~OnStream() {
+    if (other_) c10::cuda::setCurrentCUDAStream(outer_);
+  }
+  OnStream(const OnStream &) = delete;
+  OnStream &operator=(const OnStream &) = delete;
+  void *raw() const { return own_.stream(); }
+  // The caller goes on with an output on its own stream: freed, its memory waits for that one as well.
+  at::Tensor shared(at::Tensor t) const {
+    if (other_) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), outer_);
+    return t;
+  }
 
-// A raw stream, or None for the current one of the current device.
-void *stream_of(PyObject *o) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-  void *s = PyLong_AsVoidPtr(o);
-  if (PyErr_Occurred()) throw PythonError{};
-  return s;
+ private:
+  c10::cuda::CUDAStream outer_, own_;
+  bool other_ = false;
+};
+
+// The caller's output tensor, checked, or a new one.
+at::Tensor output(Call &c, const OnStream &on, const char *name, PyObject *o, at::ScalarType type, Shape shape,
+                  const at::Tensor &like) {
+  if (o == Py_None) return on.shared(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+  return input(c, name, o, type, shape);
 }
 
 template <typename F>
@@ -227,15 +249,14 @@ PyObject *quantize_rows(PyObject *const *a) {
   const int64_t out = gather ? rows * top_k : rows;
   const int32_t *src = gather ? ptr<int32_t>(input(w, "src_row", a[1], kI32, {out})) : nullptr;
   int32_t *st = status_ptr(w, a[5]);
-  on_current_device(w);
-  const at::Tensor codes = output(w, "codes", a[3], kU8, {out, cols}, x);
-  const at::Tensor scale = output(w, "scale", a[4], kF32, {(cols + 127) / 128, out}, x);
-  void *stream = stream_of(a[6]);
+  const OnStream on(w, a[6]);
+  const at::Tensor codes = output(w, on, "codes", a[3], kU8, {out, cols}, x);
+  const at::Tensor scale = output(w, on, "scale", a[4], kF32, {(cols + 127) / 128, out}, x);
   call(w, [&] {
     return gather ? permute_quantize_fp8_block128(ptr(x), rows, cols, src, top_k, ptr<uint8_t>(codes), ptr<float>(scale),
-                                                  st, stream)
+                                                  st, on.raw())
                   : quantize_fp8_block128(ptr(x), rows, cols, FME_ROWWISE, nullptr, 1, ptr<uint8_t>(codes),
-                                          ptr<float>(scale), nullptr, st, stream);
+                                          ptr<float>(scale), nullptr, st, on.raw());
   });
   return tuple({{a[3], codes}, {a[4], scale}});
 }
@@ -259,14 +280,13 @@ PyObject *quantize_cols(PyObject *const *a) {
   const int32_t g = groups_of(w, a[1], a[2], &off);
   const int64_t ld = fme_colwise_ld(rows, g);
   int32_t *st = status_ptr(w, a[6]);
-  on_current_device(w);
-  const at::Tensor codes = output(w, "codes", a[3], kU8, {ld, cols}, x);
-  const at::Tensor scale = output(w, "scale", a[4], kF32, {ld / 128, cols}, x);
-  const at::Tensor po = output(w, "padded_offsets", a[5], kI32, {g < 0 ? 0 : int64_t(g) + 1}, x);
-  void *stream = stream_of(a[7]);
+  const OnStream on(w, a[7]);
+  const at::Tensor codes = output(w, on, "codes", a[3], kU8, {ld, cols}, x);
+  const at::Tensor scale = output(w, on, "scale", a[4], kF32, {ld / 128, cols}, x);
+  const at::Tensor po = output(w, on, "padded_offsets", a[5], kI32, {g < 0 ? 0 : int64_t(g) + 1}, x);
   call(w, [&] {
     return quantize_fp8_block128(ptr(x), rows, cols, FME_COLWISE, off, g, ptr<uint8_t>(codes), ptr<float>(scale),
-                                 ptr<int32_t>(po), st, stream);
+                                 ptr<int32_t>(po), st, on.raw());
   });
   return tuple({{a[3], codes}, {a[4], scale}, {a[5], po}});
 }
@@ -281,16 +301,15 @@ PyObject *quantize_rowcol(PyObject *const *a) {
   const int32_t g = groups_of(w, a[1], a[2], &off);
   const int64_t ld = fme_colwise_ld(rows, g);
   int32_t *st = status_ptr(w, a[8]);
-  on_current_device(w);
-  const at::Tensor rc = output(w, "row_codes", a[3], kU8, {rows, cols}, x);
-  const at::Tensor rs = output(w, "row_scale", a[4], kF32, {(cols + 127) / 128, rows}, x);
-  const at::Tensor cc = output(w, "col_codes", a[5], kU8, {ld, cols}, x);
-  const at::Tensor cs = output(w, "col_scale", a[6], kF32, {ld / 128, cols}, x);
-  const at::Tensor po = output(w, "padded_offsets", a[7], kI32, {g < 0 ? 0 : int64_t(g) + 1}, x);
-  void *stream = stream_of(a[9]);
+  const OnStream on(w, a[9]);
+  const at::Tensor rc = output(w, on, "row_codes", a[3], kU8, {rows, cols}, x);
+  const at::Tensor rs = output(w, on, "row_scale", a[4], kF32, {(cols + 127) / 128, rows}, x);
+  const at::Tensor cc = output(w, on, "col_codes", a[5], kU8, {ld, cols}, x);
+  const at::Tensor cs = output(w, on, "col_scale", a[6], kF32, {ld / 128, cols}, x);
+  const at::Tensor po = output(w, on, "padded_offsets", a[7], kI32, {g < 0 ? 0 : int64_t(g) + 1}, x);
   call(w, [&] {
     return quantize_fp8_block128_rowcol(ptr(x), rows, cols, off, g, ptr<uint8_t>(rc), ptr<float>(rs), ptr<uint8_t>(cc),
-                                        ptr<float>(cs), ptr<int32_t>(po), st, stream);
+                                        ptr<float>(cs), ptr<int32_t>(po), st, on.raw());
   });
   return tuple({{a[3], rc}, {a[4], rs}, {a[5], cc}, {a[6], cs}, {a[7], po}});
 }
@@ -301,13 +320,12 @@ PyObject *quantize_weights(PyObject *const *a) {
   const Shape s = dims(w, "w", a[0], 3);
   const int64_t e = s[0], n = s[1], k = s[2];
   const at::Tensor &x = input(w, "w", a[0], kBf16, {e, n, k});
-  on_current_device(w);
-  const at::Tensor codes = output(w, "codes", a[1], kU8, {e, n, k}, x);
-  const at::Tensor scale = output(w, "scale", a[2], kF32, {e, (n + 127) / 128, (k + 127) / 128}, x);
-  void *stream = stream_of(a[3]);
+  const OnStream on(w, a[3]);
+  const at::Tensor codes = output(w, on, "codes", a[1], kU8, {e, n, k}, x);
+  const at::Tensor scale = output(w, on, "scale", a[2], kF32, {e, (n + 127) / 128, (k + 127) / 128}, x);
   const int32_t experts = e > INT32_MAX ? INT32_MAX : static_cast<int32_t>(e);
   call(w, [&] {
-    return quantize_fp8_block128_weights(ptr(x), experts, n, k, ptr<uint8_t>(codes), ptr<float>(scale), stream);
+    return quantize_fp8_block128_weights(ptr(x), experts, n, k, ptr<uint8_t>(codes), ptr<float>(scale), on.raw());
   });
   return tuple({{a[1], codes}, {a[2], scale}});
 }
@@ -328,14 +346,13 @@ PyObject *rows_gemm(PyObject *const *a) {
   const at::Tensor &wsc = input(w, "w_scale", a[3], kF32, {e, (n + 127) / 128, (k + 127) / 128});
   const at::Tensor &off = input(w, "offsets", a[4], kI32, {e + 1});
   int32_t *st = status_ptr(w, a[6]);
-  on_current_device(w);
-  const at::Tensor y = output(w, kDgrad ? "dx" : "y", a[5], kBf16, {m, cols}, ac);
-  void *stream = stream_of(a[7]);
+  const OnStream on(w, a[7]);
+  const at::Tensor y = output(w, on, kDgrad ? "dx" : "y", a[5], kBf16, {m, cols}, ac);
   const int32_t experts = static_cast<int32_t>(e);
   call(w, [&] {
     return (kDgrad ? grouped_gemm_dgrad_fp8_block128 : grouped_gemm_fwd_fp8_block128)(
         ptr<uint8_t>(ac), ptr<float>(as), ptr<uint8_t>(wc), ptr<float>(wsc), ptr<int32_t>(off), experts, m, n, k, ptr(y),
-        st, stream);
+        st, on.raw());
   });
   return one(a[5], y);
 }
@@ -354,12 +371,12 @@ PyObject *wgrad(PyObject *const *a) {
   const int32_t mode = integer32(a[6]);
   if (e < 1) throw Refused(std::string(w.where) + ": padded_offsets must have at least 2 elements");
   int32_t *st = status_ptr(w, a[7]);
-  on_current_device(w);
-  const at::Tensor dw = output(w, "dw", a[5], mode == FME_DW_BF16 ? kBf16 : kF32, {e, n, k}, dc);
-  void *stream = stream_of(a[8]);
+  const OnStream on(w, a[8]);
+  const at::Tensor dw = output(w, on, "dw", a[5], mode == FME_DW_BF16 ? kBf16 : kF32, {e, n, k}, dc);
   call(w, [&] {
     return grouped_gemm_wgrad_fp8_block128(ptr<uint8_t>(dc), ptr<float>(dsc), ptr<uint8_t>(xc), ptr<float>(xs), ld,
-                                           ptr<int32_t>(po), static_cast<int32_t>(e), n, k, ptr(dw), mode, st, stream);
+                                           ptr<int32_t>(po), static_cast<int32_t>(e), n, k, ptr(dw), mode, st,
+                                           on.raw());
   });
   return one(a[5], dw);
 }
@@ -394,15 +411,14 @@ PyObject *gate(PyObject *const *a) {
   const int32_t top_k = integer32(a[1]), score = score_of(w, a[2]);
   const float *bias = a[3] == Py_None ? nullptr : ptr<float>(input(w, "bias", a[3], kF32, {l.experts}));
   if (top_k < 0) throw Refused(std::string(w.where) + ": top_k must not be negative");
-  on_current_device(w);
-  const at::Tensor ids = output(w, "ids", a[6], kI32, {l.tokens, top_k}, l.t);
-  const at::Tensor weights = output(w, "weights", a[7], kF32, {l.tokens, top_k}, l.t);
+  const OnStream on(w, a[8]);
+  const at::Tensor ids = output(w, on, "ids", a[6], kI32, {l.tokens, top_k}, l.t);
+  const at::Tensor weights = output(w, on, "weights", a[7], kF32, {l.tokens, top_k}, l.t);
   const int32_t normalize = truth(a[4]);
   const float scale = real(a[5]);
-  void *stream = stream_of(a[8]);
   call(w, [&] {
     return moe_gate(ptr(l.t), l.dtype, l.tokens, l.experts32, top_k, score, normalize, scale, bias, ptr<int32_t>(ids),
-                    ptr<float>(weights), stream);
+                    ptr<float>(weights), on.raw());
   });
   return tuple({{a[6], ids}, {a[7], weights}});
 }
@@ -417,13 +433,12 @@ PyObject *gate_backward(PyObject *const *a) {
   const int32_t score = score_of(w, a[3]), normalize = truth(a[4]);
   const float scale = real(a[5]);
   int32_t *st = status_ptr(w, a[7]);
-  on_current_device(w);
-  const at::Tensor out = output(w, "d_logits", a[6], l.t.scalar_type(), {l.tokens, l.experts}, l.t);
-  void *stream = stream_of(a[8]);
+  const OnStream on(w, a[8]);
+  const at::Tensor out = output(w, on, "d_logits", a[6], l.t.scalar_type(), {l.tokens, l.experts}, l.t);
   const int32_t k = top_k > INT32_MAX ? INT32_MAX : static_cast<int32_t>(top_k);
   call(w, [&] {
     return moe_gate_backward(ptr(l.t), l.dtype, ptr<int32_t>(ids), ptr<float>(d), l.tokens, l.experts32, k, score,
-                             normalize, scale, ptr(out), st, stream);
+                             normalize, scale, ptr(out), st, on.raw());
   });
   return one(a[6], out);
 }
@@ -461,10 +476,10 @@ PyObject *balance_loss(PyObject *const *a) {
   const Sequences s = sequences_of(w, a[4], a[5], l.tokens);
   if (s.count < 1) throw Refused(std::string(w.where) + ": seq_offsets must have at least 2 elements");
   int32_t *st = status_ptr(w, a[10]);
-  on_current_device(w);
-  const at::Tensor loss = output(w, "loss", a[6], kF32, {1}, l.t);
-  const at::Tensor counts = output(w, "counts", a[7], kI32, {s.count, l.experts}, l.t);
-  const at::Tensor n = output(w, "seq_tokens", a[8], kI32, {s.count}, l.t);
+  const OnStream on(w, a[11]);
+  const at::Tensor loss = output(w, on, "loss", a[6], kF32, {1}, l.t);
+  const at::Tensor counts = output(w, on, "counts", a[7], kI32, {s.count, l.experts}, l.t);
+  const at::Tensor n = output(w, on, "seq_tokens", a[8], kI32, {s.count}, l.t);
   at::Tensor ws;
   if (a[9] == Py_None)
     ws = at::detail::empty_cuda({fme_balance_workspace_bytes(l.tokens, s.count, l.experts32)}, kU8, l.t.device(),
@@ -473,12 +488,11 @@ PyObject *balance_loss(PyObject *const *a) {
     ws = tensor(w, "workspace", a[9]);
   if (!ws.is_cuda() || !ws.is_contiguous()) throw Refused(std::string(w.where) + ": workspace must be a contiguous CUDA tensor");
   on_one_device(w, "workspace", ws);
-  void *stream = stream_of(a[11]);
   const int32_t k = top_k > INT32_MAX ? INT32_MAX : static_cast<int32_t>(top_k);
   call(w, [&] {
     return moe_balance_loss(ptr(l.t), l.dtype, ptr<int32_t>(ids), l.tokens, l.experts32, k, score, alpha, s.offsets,
                             s.count, s.mask, ptr<float>(loss), ptr<int32_t>(counts), ptr<int32_t>(n), ptr(ws),
-                            static_cast<int64_t>(ws.nbytes()), st, stream);
+                            static_cast<int64_t>(ws.nbytes()), st, on.raw());
   });
   return tuple({{a[6], loss}, {a[7], counts}, {a[8], n}});
 }
@@ -495,13 +509,12 @@ PyObject *balance_loss_backward(PyObject *const *a) {
   const float alpha = real(a[6]);
   const bool accumulate = truth(a[10]);
   if (accumulate && a[9] == Py_None) throw Refused(std::string(w.where) + ": accumulate needs the d_logits to add to");
-  on_current_device(w);
-  const at::Tensor out = output(w, "d_logits", a[9], l.t.scalar_type(), {l.tokens, l.experts}, l.t);
-  void *stream = stream_of(a[11]);
+  const OnStream on(w, a[11]);
+  const at::Tensor out = output(w, on, "d_logits", a[9], l.t.scalar_type(), {l.tokens, l.experts}, l.t);
   call(w, [&] {
     return moe_balance_loss_backward(ptr(l.t), l.dtype, ptr<int32_t>(counts), ptr<int32_t>(n), ptr<float>(d), l.tokens,
                                      l.experts32, top_k, score, alpha, s.offsets, s.count, s.mask, ptr(out), accumulate,
-                                     stream);
+                                     on.raw());
   });
   return one(a[9], out);
 }
@@ -516,14 +529,13 @@ PyObject *combine_backward(PyObject *const *a) {
   const at::Tensor &row_of = input(w, "row_of", a[2], kI32, {tokens, top_k});
   const at::Tensor &weights = input(w, "weights", a[3], kF32, {tokens, top_k});
   int32_t *st = status_ptr(w, a[6]);
-  on_current_device(w);
-  const at::Tensor dy = output(w, "d_y", a[4], kBf16, {rows, n}, y);
-  const at::Tensor dw = output(w, "d_weights", a[5], kF32, {tokens, top_k}, y);
-  void *stream = stream_of(a[7]);
+  const OnStream on(w, a[7]);
+  const at::Tensor dy = output(w, on, "d_y", a[4], kBf16, {rows, n}, y);
+  const at::Tensor dw = output(w, on, "d_weights", a[5], kF32, {tokens, top_k}, y);
   const int32_t k = top_k > INT32_MAX ? INT32_MAX : static_cast<int32_t>(top_k);
   call(w, [&] {
     return moe_combine_backward(ptr(d), ptr(y), rows, ptr<int32_t>(row_of), ptr<float>(weights), tokens, k, n, ptr(dy),
-                                ptr<float>(dw), st, stream);
+                                ptr<float>(dw), st, on.raw());
   });
   return tuple({{a[4], dy}, {a[5], dw}});
 }
