@@ -9,8 +9,8 @@ exceptions.  There is no fallback: if the library is missing or the device is no
 a GB300, calls raise.
 
 With `stream` a call runs there and not on the current stream: its inputs must be ready on it and must live
-until it is done with them.  What the FP8 block-128 and router calls allocate then comes from that stream's memory; the
-outputs may be used on the current stream once that waits for it, and freed at any time.
+until it is done with them.  What the call allocates then comes from that stream's memory; the outputs may be used
+on the current stream once that waits for it, and freed at any time.
 """
 from __future__ import annotations
 
@@ -185,10 +185,19 @@ def _groups(offsets, num_groups):
     return offsets, n
 
 
-def _empty(shape, dtype, device):
+def _empty(shape, dtype, device, stream=None):
+    """A new tensor for a call on `stream` (None: the current one), from that stream's memory: a block of the current
+    stream's, just freed, may still be used by work queued there.  The caller goes on with it on the current stream, so
+    its memory waits for that one as well when it is freed."""
     import torch
 
-    return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    outer = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(outer)
+    return t
 
 
 # --------------------------------------------------------------- the five calls --
@@ -202,11 +211,11 @@ def quantize_nvfp4_pertoken(x, offsets=None, num_groups=None, *, codes=None, sf=
     offsets, g = _groups(offsets, num_groups)
     dev = x.device
     if codes is None:
-        codes = _empty((rows, k // 2), torch.uint8, dev)
+        codes = _empty((rows, k // 2), torch.uint8, dev, stream)
     if sf is None:
-        sf = _empty((max(sf_bytes(rows, k, 16, g), 16),), torch.uint8, dev)
+        sf = _empty((max(sf_bytes(rows, k, 16, g), 16),), torch.uint8, dev, stream)
     if row_scale is None:
-        row_scale = _empty((rows,), torch.float32, dev)
+        row_scale = _empty((rows,), torch.float32, dev, stream)
     st = lib().quantize_nvfp4_pertoken(_ptr(x), rows, k, _ptr(offsets), g, _ptr(codes), _ptr(sf), _ptr(row_scale),
                                        _ptr(status), _stream(stream))
     _check(st, "quantize_nvfp4_pertoken")
@@ -223,13 +232,13 @@ def quantize_nvfp4_pertensor(x, offsets=None, num_groups=None, *, codes=None, sf
     offsets, g = _groups(offsets, num_groups)
     dev = x.device
     if codes is None:
-        codes = _empty((rows, k // 2), torch.uint8, dev)
+        codes = _empty((rows, k // 2), torch.uint8, dev, stream)
     if sf is None:
-        sf = _empty((max(sf_bytes(rows, k, 16, g), 16),), torch.uint8, dev)
+        sf = _empty((max(sf_bytes(rows, k, 16, g), 16),), torch.uint8, dev, stream)
     if row_scale is None:
-        row_scale = _empty((max(rows, 1),), torch.float32, dev)
+        row_scale = _empty((max(rows, 1),), torch.float32, dev, stream)
     if tensor_amax is None:
-        tensor_amax = _empty((4,), torch.float32, dev)
+        tensor_amax = _empty((4,), torch.float32, dev, stream)
     st = lib().quantize_nvfp4_pertensor(_ptr(x), rows, k, _ptr(offsets), g, _ptr(codes), _ptr(sf),
                                         _ptr(row_scale), _ptr(tensor_amax), _ptr(status), _stream(stream))
     _check(st, "quantize_nvfp4_pertensor")
@@ -247,13 +256,13 @@ def swiglu_quantize_nvfp4(gate_up, offsets=None, num_groups=None, *, codes=None,
     offsets, g = _groups(offsets, num_groups)
     dev = gate_up.device
     if codes is None:
-        codes = _empty((rows, inter // 2), torch.uint8, dev)
+        codes = _empty((rows, inter // 2), torch.uint8, dev, stream)
     if sf is None:
-        sf = _empty((max(sf_bytes(rows, inter, 16, g), 16),), torch.uint8, dev)
+        sf = _empty((max(sf_bytes(rows, inter, 16, g), 16),), torch.uint8, dev, stream)
     if row_scale is None:
-        row_scale = _empty((rows,), torch.float32, dev)
+        row_scale = _empty((rows,), torch.float32, dev, stream)
     if h is None and want_h:
-        h = _empty((rows, inter), torch.bfloat16, dev)
+        h = _empty((rows, inter), torch.bfloat16, dev, stream)
     st = lib().swiglu_quantize_nvfp4(_ptr(gate_up), rows, inter, _ptr(offsets), g, _ptr(codes), _ptr(sf),
                                      _ptr(row_scale), _ptr(h), _ptr(status), _stream(stream))
     _check(st, "swiglu_quantize_nvfp4")
@@ -273,20 +282,20 @@ def quantize_mxfp8(x, axis=ROWWISE, offsets=None, num_groups=None, *, codes=None
     dev = x.device
     if (axis & ~MX_SCALE_CEIL) == ROWWISE:
         if codes is None:
-            codes = _empty((rows, cols), torch.uint8, dev)
+            codes = _empty((rows, cols), torch.uint8, dev, stream)
         if sf is None:
-            sf = _empty((max(sf_bytes(rows, cols, 32, g), 16),), torch.uint8, dev)
+            sf = _empty((max(sf_bytes(rows, cols, 32, g), 16),), torch.uint8, dev, stream)
         st = lib().quantize_mxfp8(_ptr(x), rows, cols, axis, _ptr(offsets), g, _ptr(codes), _ptr(sf), None,
                                   _ptr(status), _stream(stream))
         _check(st, "quantize_mxfp8")
         return codes, sf
     ld = colwise_ld(rows, g)
     if codes is None:
-        codes = _empty((cols, ld), torch.uint8, dev)
+        codes = _empty((cols, ld), torch.uint8, dev, stream)
     if sf is None:
-        sf = _empty((max(sf_bytes(cols, ld, 32, 1), 16),), torch.uint8, dev)
+        sf = _empty((max(sf_bytes(cols, ld, 32, 1), 16),), torch.uint8, dev, stream)
     if padded_offsets is None:
-        padded_offsets = _empty((g + 1,), torch.int32, dev)
+        padded_offsets = _empty((g + 1,), torch.int32, dev, stream)
     st = lib().quantize_mxfp8(_ptr(x), rows, cols, axis, _ptr(offsets), g, _ptr(codes), _ptr(sf),
                               _ptr(padded_offsets), _ptr(status), _stream(stream))
     _check(st, "quantize_mxfp8")
@@ -304,15 +313,15 @@ def quantize_mxfp8_rowcol(x, offsets=None, num_groups=None, *, row_codes=None, r
     dev = x.device
     ld = colwise_ld(rows, g)
     if row_codes is None:
-        row_codes = _empty((rows, cols), torch.uint8, dev)
+        row_codes = _empty((rows, cols), torch.uint8, dev, stream)
     if row_sf is None:
-        row_sf = _empty((max(sf_bytes(rows, cols, 32, g), 16),), torch.uint8, dev)
+        row_sf = _empty((max(sf_bytes(rows, cols, 32, g), 16),), torch.uint8, dev, stream)
     if col_codes is None:
-        col_codes = _empty((cols, ld), torch.uint8, dev)
+        col_codes = _empty((cols, ld), torch.uint8, dev, stream)
     if col_sf is None:
-        col_sf = _empty((max(sf_bytes(cols, ld, 32, 1), 16),), torch.uint8, dev)
+        col_sf = _empty((max(sf_bytes(cols, ld, 32, 1), 16),), torch.uint8, dev, stream)
     if padded_offsets is None:
-        padded_offsets = _empty((g + 1,), torch.int32, dev)
+        padded_offsets = _empty((g + 1,), torch.int32, dev, stream)
     st = lib().quantize_mxfp8_rowcol(_ptr(x), rows, cols, _ptr(offsets), g, _ptr(row_codes), _ptr(row_sf),
                                      _ptr(col_codes), _ptr(col_sf), _ptr(padded_offsets), _ptr(status),
                                      _stream(stream))
@@ -334,17 +343,17 @@ def swiglu_backward_quantize_mxfp8(gate_up, dh, offsets=None, num_groups=None, *
     dev = gate_up.device
     ld = colwise_ld(rows, g)
     if row_codes is None:
-        row_codes = _empty((rows, two_inter), torch.uint8, dev)
+        row_codes = _empty((rows, two_inter), torch.uint8, dev, stream)
     if row_sf is None:
-        row_sf = _empty((max(sf_bytes(rows, two_inter, 32, g), 16),), torch.uint8, dev)
+        row_sf = _empty((max(sf_bytes(rows, two_inter, 32, g), 16),), torch.uint8, dev, stream)
     if col_codes is None:
-        col_codes = _empty((two_inter, ld), torch.uint8, dev)
+        col_codes = _empty((two_inter, ld), torch.uint8, dev, stream)
     if col_sf is None:
-        col_sf = _empty((max(sf_bytes(two_inter, ld, 32, 1), 16),), torch.uint8, dev)
+        col_sf = _empty((max(sf_bytes(two_inter, ld, 32, 1), 16),), torch.uint8, dev, stream)
     if padded_offsets is None:
-        padded_offsets = _empty((g + 1,), torch.int32, dev)
+        padded_offsets = _empty((g + 1,), torch.int32, dev, stream)
     if d_gate_up is None and want_d:
-        d_gate_up = _empty((rows, two_inter), torch.bfloat16, dev)
+        d_gate_up = _empty((rows, two_inter), torch.bfloat16, dev, stream)
     st = lib().swiglu_backward_quantize_mxfp8(_ptr(gate_up), _ptr(dh), rows, inter, _ptr(offsets), g,
                                               _ptr(row_codes), _ptr(row_sf), _ptr(col_codes), _ptr(col_sf),
                                               _ptr(padded_offsets), _ptr(d_gate_up), _ptr(status), _stream(stream))
@@ -359,7 +368,7 @@ def grouped_gemm_fwd_nvfp4(a_codes, a_sf, a_scale, b_codes, b_sf, b_scale, offse
     m = a_codes.shape[0]
     e = offsets.numel() - 1
     if y is None:
-        y = _empty((m, n), torch.bfloat16, a_codes.device)
+        y = _empty((m, n), torch.bfloat16, a_codes.device, stream)
     st = lib().grouped_gemm_fwd_nvfp4(_ptr(a_codes), _ptr(a_sf), _ptr(a_scale), _ptr(b_codes), _ptr(b_sf),
                                       _ptr(b_scale), _ptr(offsets), e, m, n, k, _ptr(y), _ptr(status),
                                       _stream(stream))
@@ -377,7 +386,7 @@ def grouped_gemm_fwd_nvfp4_swiglu(a_codes, a_sf, a_scale, b_codes, b_sf, b_scale
     m = a_codes.shape[0]
     e = offsets.numel() - 1
     if h is None:
-        h = _empty((m, n // 2), torch.bfloat16, a_codes.device)
+        h = _empty((m, n // 2), torch.bfloat16, a_codes.device, stream)
     st = lib().grouped_gemm_fwd_nvfp4_swiglu(_ptr(a_codes), _ptr(a_sf), _ptr(a_scale), _ptr(b_codes), _ptr(b_sf),
                                              _ptr(b_scale), _ptr(offsets), e, m, n, k, _ptr(h), _ptr(status),
                                              _stream(stream))
@@ -393,7 +402,7 @@ def grouped_gemm_fwd_mxfp8(a_codes, a_sf, b_codes, b_sf, offsets, n, k, *, y=Non
     m = a_codes.shape[0]
     e = offsets.numel() - 1
     if y is None:
-        y = _empty((m, n), torch.bfloat16, a_codes.device)
+        y = _empty((m, n), torch.bfloat16, a_codes.device, stream)
     st = lib().grouped_gemm_fwd_mxfp8(_ptr(a_codes), _ptr(a_sf), _ptr(b_codes), _ptr(b_sf), _ptr(offsets), e, m, n, k,
                                       _ptr(y), _ptr(status), _stream(stream))
     _check(st, "grouped_gemm_fwd_mxfp8")
@@ -407,7 +416,7 @@ def grouped_gemm_dgrad_mxfp8(a_codes, a_sf, b_codes, b_sf, ldb, offsets, n, k, *
     m = a_codes.shape[0]
     e = offsets.numel() - 1
     if y is None:
-        y = _empty((m, n), torch.bfloat16, a_codes.device)
+        y = _empty((m, n), torch.bfloat16, a_codes.device, stream)
     st = lib().grouped_gemm_dgrad_mxfp8(_ptr(a_codes), _ptr(a_sf), _ptr(b_codes), _ptr(b_sf), ldb, _ptr(offsets),
                                         e, m, n, k, _ptr(y), _ptr(status), _stream(stream))
     _check(st, "grouped_gemm_dgrad_mxfp8")
@@ -420,7 +429,7 @@ def grouped_gemm_wgrad_mxfp8(a_codes, a_sf, lda, b_codes, b_sf, ldb, padded_offs
 
     e = padded_offsets.numel() - 1
     if y is None:
-        y = _empty((e, m, n), torch.bfloat16, padded_offsets.device)
+        y = _empty((e, m, n), torch.bfloat16, padded_offsets.device, stream)
     st = lib().grouped_gemm_wgrad_mxfp8(_ptr(a_codes), _ptr(a_sf), lda, _ptr(b_codes), _ptr(b_sf), ldb,
                                         _ptr(padded_offsets), e, m, n, _ptr(y), _ptr(status), _stream(stream))
     _check(st, "grouped_gemm_wgrad_mxfp8")
@@ -438,14 +447,14 @@ def moe_route(topk_ids, num_experts, *, offsets=None, row_of=None, src_row=None,
     tokens, top_k = topk_ids.shape
     dev = topk_ids.device
     if offsets is None:
-        offsets = _empty((num_experts + 1,), torch.int32, dev)
+        offsets = _empty((num_experts + 1,), torch.int32, dev, stream)
     if row_of is None:
-        row_of = _empty((tokens, top_k), torch.int32, dev)
+        row_of = _empty((tokens, top_k), torch.int32, dev, stream)
     if src_row is None:
-        src_row = _empty((tokens * top_k,), torch.int32, dev)
+        src_row = _empty((tokens * top_k,), torch.int32, dev, stream)
     need = route_workspace_bytes(tokens, top_k, num_experts)
     if workspace is None:
-        workspace = _empty((need,), torch.uint8, dev)
+        workspace = _empty((need,), torch.uint8, dev, stream)
     st = lib().moe_route(_ptr(topk_ids), tokens, top_k, num_experts, _ptr(offsets), _ptr(row_of), _ptr(src_row),
                          _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
                          _stream(stream))
@@ -482,11 +491,11 @@ def permute_quantize_nvfp4(x, src_row, top_k, offsets, *, codes=None, sf=None, r
     g = offsets.numel() - 1
     dev = x.device
     if codes is None:
-        codes = _empty((rows, k // 2), torch.uint8, dev)
+        codes = _empty((rows, k // 2), torch.uint8, dev, stream)
     if sf is None:
-        sf = _empty((max(sf_bytes(rows, k, 16, g), 16),), torch.uint8, dev)
+        sf = _empty((max(sf_bytes(rows, k, 16, g), 16),), torch.uint8, dev, stream)
     if row_scale is None:
-        row_scale = _empty((rows,), torch.float32, dev)
+        row_scale = _empty((rows,), torch.float32, dev, stream)
     st = lib().permute_quantize_nvfp4(_ptr(x), tokens, k, _ptr(src_row), top_k, _ptr(offsets), g, _ptr(codes),
                                       _ptr(sf), _ptr(row_scale), _ptr(status), _stream(stream))
     _check(st, "permute_quantize_nvfp4")
@@ -503,9 +512,9 @@ def permute_quantize_mxfp8(x, src_row, top_k, offsets, *, codes=None, sf=None, s
     g = offsets.numel() - 1
     dev = x.device
     if codes is None:
-        codes = _empty((rows, k), torch.uint8, dev)
+        codes = _empty((rows, k), torch.uint8, dev, stream)
     if sf is None:
-        sf = _empty((max(sf_bytes(rows, k, 32, g), 16),), torch.uint8, dev)
+        sf = _empty((max(sf_bytes(rows, k, 32, g), 16),), torch.uint8, dev, stream)
     st = lib().permute_quantize_mxfp8(_ptr(x), tokens, k, _ptr(src_row), top_k, _ptr(offsets), g, _ptr(codes),
                                       _ptr(sf), _ptr(status), _stream(stream))
     _check(st, "permute_quantize_mxfp8")
@@ -520,7 +529,7 @@ def moe_combine(y, row_of, weights, *, out=None, status=None, stream=None):
     rows_y, n = y.shape
     tokens, top_k = row_of.shape
     if out is None:
-        out = _empty((tokens, n), torch.bfloat16, y.device)
+        out = _empty((tokens, n), torch.bfloat16, y.device, stream)
     st = lib().moe_combine(_ptr(y), rows_y, _ptr(row_of), _ptr(weights), tokens, top_k, n, _ptr(out), _ptr(status),
                            _stream(stream))
     _check(st, "moe_combine")
