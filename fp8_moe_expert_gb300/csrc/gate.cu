@@ -659,10 +659,13 @@ __global__ void __launch_bounds__(32 * kGateWarps, V <= 8 ? 4 : 1) balance_backw
       n = __ldg(a.seq_tokens + seq);
       const float tn = static_cast<float>(n);
       const float c = n > 0 ? up * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tn)) / tn : 0.0f;
+      // Counts above their mean: the same for all experts falls out of a_e - sum p a, and where every expert is chosen
+      // (top_k = experts) nothing is left, not rounding noise.
+      const int32_t mean = static_cast<int32_t>(static_cast<int64_t>(n) * a.top_k / experts);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int e = expert_of<VEC>(j, lane);
-        w[j] = e < experts ? c * static_cast<float>(__ldg(a.counts + seq * experts + e)) : 0.0f;
+        w[j] = e < experts ? c * static_cast<float>(__ldg(a.counts + seq * experts + e) - mean) : 0.0f;
       }
       loaded = seq;
     }
