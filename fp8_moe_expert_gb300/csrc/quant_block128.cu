@@ -37,9 +37,9 @@ struct BlockScale {
 // Both quotients correctly rounded, by one step of P. Markstein's fused-multiply-add refinement (IBM J.
 // Res. Dev. 34(1), 1990): q + (n - d q) / d with the reciprocal in place of the last division.  A is
 // taken times 2^-14 in the second, so that neither it nor its reciprocal leaves the normal range.
-// Equal to IEEE division for every bf16 A from the floor up, and for reciprocals up to two ulps off
+// Equal to IEEE division for every finite bf16 A from the floor up, and for reciprocals up to two ulps off
 // (checked with exact rational arithmetic); two IEEE divisions a block were a fifth of the row-wise
-// kernel's instructions.
+// kernel's instructions.  An infinite A, for which the corrections are NaN, has its quotients set: inf and 0.
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
   const float a = fmaxf(bf16_bits_to_float(amax_bits), kAmaxFloor);
   constexpr float kInv = 1.0f / 448.0f;
@@ -49,7 +49,7 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
   const float t = rcp_approx(d);
   const float u = __fmul_rn(448.0f * 0x1p-14f, t);
   const float r = __fmaf_rn(__fmaf_rn(-d, u, 448.0f * 0x1p-14f), t, u);
-  return {s, r};
+  return a == INFINITY ? BlockScale{a, 0.0f} : BlockScale{s, r};
 }
 
 // The four bf16 of words a, b times (r0, r1, r2, r3) -> four E4M3 codes in order.
