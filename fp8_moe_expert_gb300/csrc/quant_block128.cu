@@ -28,8 +28,12 @@ __device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Largest magnitude of a word's two bf16, as bf16 bits.
-__device__ __forceinline__ uint32_t absmax_halves(uint32_t m) { return max(m & 0x7FFFu, (m >> 16) & 0x7FFFu); }
+// Largest magnitude of a word's two bf16, as bf16 bits; a half that has seen only NaN (which as an integer would
+// be the largest) counts as 0.
+__device__ __forceinline__ uint32_t absmax_halves(uint32_t m) {
+  m = absmax2(m, 0u);
+  return max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
+}
 
 struct BlockScale {
   float s, r;

@@ -80,3 +80,17 @@ def check_every_layout(x):
 @pytest.mark.parametrize("rows,cols", [(160, 272), (300, 512)])
 def test_infinities(rows, cols):
     check_every_layout(with_inf(rows, cols))
+
+
+def with_nan(rows, cols):
+    """NaN at every even, every odd, all, or single positions of rows, and down the columns."""
+    x = ref.normal((rows, cols), 1.0, 2)
+    x[2, 0::2], x[4, 1::2], x[6], x[8, 17], x[10, 130:140] = NAN, NAN, NAN, NAN, NAN
+    x[:, 40], x[0::2, 41], x[1::2, 42], x[20:30, 150:160] = NAN, NAN, NAN, NAN
+    x[128:136, 144:152] = NAN  # a thread's whole share of a tile
+    return x
+
+
+@pytest.mark.parametrize("rows,cols", [(160, 272), (300, 512)])
+def test_nan(rows, cols):
+    check_every_layout(with_nan(rows, cols))
