@@ -361,7 +361,7 @@ fme_status permute_quantize_mxfp8(const void *x, int64_t tokens, int64_t k, cons
 fme_status moe_combine(const void *y, int64_t rows_y, const int32_t *row_of, const float *weights, int64_t tokens,
                        int32_t top_k, int64_t n, void *out, int32_t *dev_status, void *stream) {
   if (tokens < 0 || rows_y < 0 || top_k < 1 || top_k > 64 || n < 0) return FME_ERR_INVALID_ARGUMENT;
-  if (n % 8 != 0 || n == 0) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (n % 8 != 0 || n == 0 || n > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
   if (tokens * top_k > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
   if (tokens == 0) return FME_OK;
   if (!row_of || !weights || !out || (rows_y > 0 && !y)) return FME_ERR_INVALID_ARGUMENT;

@@ -183,12 +183,13 @@ cudaError_t launch_route(const LaunchRoute &r) {
 // each product and sum rounded separately; assignments with row_of < 0 are
 // skipped.  One warp per token row, 8 columns per lane per step; the rows of
 // kCombineBatch assignments are loaded before they are summed (in order), so a
-// lane keeps that many 16-byte loads in flight.
+// lane keeps that many 16-byte loads in flight.  Columns (below 2^31) are counted unsigned: the step past the
+// last would leave a signed counter's range.
 constexpr int kCombineBatch = 4;
 
 __global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t *__restrict__ y, const int32_t *__restrict__ row_of,
                                                           const float *__restrict__ weights, int64_t tokens,
-                                                          int top_k, int n, int64_t rows_y, uint16_t *__restrict__ out,
+                                                          int top_k, uint32_t n, int64_t rows_y, uint16_t *__restrict__ out,
                                                           int32_t *status) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const uint16_t *__rest
     const int32_t *rt = row_of + t * top_k;
     const float *wt = weights + t * top_k;
     bool bad = false;
-    for (int c0 = lane * 8; c0 < n; c0 += 256) {
+    for (uint32_t c0 = lane * 8; c0 < n; c0 += 256) {
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int k0 = 0; k0 < top_k; k0 += kCombineBatch) {
         uint4 v[kCombineBatch];
@@ -241,7 +242,7 @@ cudaError_t launch_combine(const LaunchCombine &c) {
   const int64_t cap = static_cast<int64_t>(c.num_sms) * 8;
   const int blocks = static_cast<int>(need < cap ? (need > 0 ? need : 1) : cap);
   moe_combine_kernel<<<blocks, 256, 0, c.stream>>>(static_cast<const uint16_t *>(c.y), c.row_of, c.weights, c.tokens,
-                                                   c.top_k, static_cast<int>(c.n), c.rows_y,
+                                                   c.top_k, static_cast<uint32_t>(c.n), c.rows_y,
                                                    static_cast<uint16_t *>(c.out), c.status);
   return cudaGetLastError();
 }
@@ -259,7 +260,7 @@ constexpr int kCombineBwdThreads = 256;
 template <int kGroup, int kRows>
 __global__ void __launch_bounds__(kCombineBwdThreads) moe_combine_backward_kernel(
     const uint16_t *__restrict__ d_out, const uint16_t *__restrict__ y, const int32_t *__restrict__ row_of,
-    const float *__restrict__ weights, int64_t tokens, int top_k, int n, int64_t rows_y, uint16_t *__restrict__ d_y,
+    const float *__restrict__ weights, int64_t tokens, int top_k, uint32_t n, int64_t rows_y, uint16_t *__restrict__ d_y,
     float *__restrict__ d_weights, int32_t *status) {
   constexpr int kWarps = kGroup / 32;  // of a token
   __shared__ float part[kCombineBwdThreads / 32][kRows];
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kCombineBwdThreads) moe_combine_backward_kerne
       acc[b] = 0.0f;
     }
     if (live) {
-      for (int c = me * 8; c < n; c += kGroup * 8) {
+      for (uint32_t c = me * 8; c < n; c += kGroup * 8) {
         const uint4 g = __ldg(reinterpret_cast<const uint4 *>(d_out + t * n + c));
         const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
         uint4 v[kRows];
@@ -340,7 +341,7 @@ static cudaError_t launch_combine_bwd(const LaunchCombineBackward &c) {
   moe_combine_backward_kernel<kGroup, kRows>
       <<<static_cast<unsigned>((c.tokens + kTokens - 1) / kTokens), kCombineBwdThreads, 0, c.stream>>>(
           static_cast<const uint16_t *>(c.d_out), static_cast<const uint16_t *>(c.y), c.row_of, c.weights, c.tokens,
-          c.top_k, static_cast<int>(c.n), c.rows_y, static_cast<uint16_t *>(c.d_y), c.d_weights, c.status);
+          c.top_k, static_cast<uint32_t>(c.n), c.rows_y, static_cast<uint16_t *>(c.d_y), c.d_weights, c.status);
   return cudaGetLastError();
 }
 

@@ -260,7 +260,7 @@ fme_status permute_quantize_mxfp8(const void *x, int64_t tokens, int64_t k, cons
  * even (no fused multiply-add); assignments with row_of < 0 contribute nothing.
  *   y          device bf16 [rows_y x n], the grouped expert outputs
  *   row_of     from moe_route; weights device float [tokens x top_k]
- *   n          a multiple of 8
+ *   n          a multiple of 8, below 2^31
  *   out        device bf16 [tokens x n]
  */
 fme_status moe_combine(const void *y, int64_t rows_y, const int32_t *row_of, const float *weights, int64_t tokens,
