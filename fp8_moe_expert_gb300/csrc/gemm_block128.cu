@@ -323,8 +323,8 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
     if (warp == 0) {
       bool ok = true;
       for (int e = lane; e <= p.num_experts; e += 32) {
-        const int32_t v = __ldg(p.offsets + e);
-        const int32_t before = e ? __ldg(p.offsets + e - 1) : 0;
+        const int32_t v = p.offsets[e];
+        const int32_t before = e ? p.offsets[e - 1] : 0;
         if ((e == 0 && v != 0) || v < before || (v & 127) != 0 || v > p.positions) ok = false;
         tab.off[e] = v;
       }
@@ -467,11 +467,11 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int r = lane + 32 * j;
-              ra[j] = r < tl.rows_valid ? __ldg(a + i * p.m + r) : 0.0f;
+              ra[j] = r < tl.rows_valid ? a[i * p.m + r] : 0.0f;
             }
             const float *b = p.b_scale + ((tl.p0 >> 7) + i) * p.n + tl.col0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) cb[j] = tl.col0 + lane + 32 * j < p.n ? __ldg(b + lane + 32 * j) : 0.0f;
+            for (int j = 0; j < 8; ++j) cb[j] = tl.col0 + lane + 32 * j < p.n ? b[lane + 32 * j] : 0.0f;
             stop = warp_any(!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status));
             if (stop) break;
 #pragma unroll
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
               const int r = lane + 32 * j;
 #pragma unroll
               for (int u = 0; u < kScaleGroup; ++u)
-                ra[j][u] = r < tl.rows_valid && i0 + u < tl.nk ? __ldg(a + (i0 + u) * p.m + r) : 0.0f;
+                ra[j][u] = r < tl.rows_valid && i0 + u < tl.nk ? a[(i0 + u) * p.m + r] : 0.0f;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kThreads128, 1) gemm_block128_kernel(const __g
               for (int u = 0; u < kScaleGroup; ++u) {
                 const int64_t i = i0 + u;
                 const int64_t at = K == Kind128::kFwd ? (tl.e * nb128 + c) * kb_count + i : (tl.e * kb_count + i) * nb128 + c;
-                cb[h][u] = c < nb128 && i < tl.nk ? __ldg(p.b_scale + at) : 0.0f;
+                cb[h][u] = c < nb128 && i < tl.nk ? p.b_scale[at] : 0.0f;
               }
             }
             stop = warp_any(!mbar_wait<true>(&s.sc_empty[slot], ((g / kScaleSlots) & 1) ^ 1, abort_flag, p.status));
@@ -999,11 +999,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_block128_few_kernel(const
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int i = i0 + u;
-          const float w = i < nk ? __ldg(b + i) : 0.0f;
+          const float w = i < nk ? b[i] : 0.0f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int tok = lane + 32 * h;
-            v[u][h] = i < nk && tok < it.tokens ? __ldg(a + i * p.m + tok) * w : 0.0f;
+            v[u][h] = i < nk && tok < it.tokens ? a[i * p.m + tok] * w : 0.0f;
           }
         }
 #pragma unroll
