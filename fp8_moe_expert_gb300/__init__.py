@@ -58,12 +58,10 @@ class FmeError(RuntimeError):
 
 
 def ensure_built() -> str:
-    """Build libfme.so if it is missing or older than its sources."""
+    """Build libfme.so and the binding if they are missing or older than their sources."""
     from . import build as _build
 
-    if _build.stale():
-        _build.build()
-    return LIBRARY
+    return _build.refresh()
 
 
 def lib() -> ctypes.CDLL:
@@ -559,11 +557,16 @@ def _bind():
         lib()
         import torch  # noqa: F401  (the module's symbols come from torch's libraries)
 
+        from .build import binding_target
+
         try:
             from . import _binding
         except ImportError as e:
             raise RuntimeError("the binding is missing or was built for another torch: build it with "
                                "`python -m fp8_moe_expert_gb300.build`") from e
+        if _binding.built_for != binding_target():
+            raise RuntimeError(f"the binding was built for {_binding.built_for}, this is {binding_target()}: build it "
+                               "with `python -m fp8_moe_expert_gb300.build`")
         _binding.set_error(FmeError)
         _native = _binding
     return _native

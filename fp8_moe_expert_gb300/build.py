@@ -14,6 +14,7 @@ import subprocess
 import sys
 import sysconfig
 import tempfile
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -54,8 +55,26 @@ def _binding_inputs() -> list[str]:
     return [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "fme.h")]
 
 
+def binding_target() -> str:
+    """What a binding is built for: it is compiled against torch's headers and Python's."""
+    import torch
+
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _binding_stale() -> bool:
+    if _older(BINDING, _binding_inputs()):
+        return True
+    try:
+        target = binding_target()
+    except ImportError:  # no torch: there is nothing to bind for
+        return False
+    with open(BINDING, "rb") as f:  # a constant of the module (built_for)
+        return target.encode() not in f.read()
+
+
 def stale(output: str = LIBRARY) -> bool:
-    return _older(output, _inputs()) or (output == LIBRARY and _older(BINDING, _binding_inputs()))
+    return _older(output, _inputs()) or (output == LIBRARY and _binding_stale())
 
 
 def _torch_dir() -> str:
@@ -69,7 +88,8 @@ def _build_binding_object(obj: str, env: dict) -> None:
     include = [os.path.join(_torch_dir(), "include"), sysconfig.get_paths()["include"],
                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-DNDEBUG",
-           *(f"-I{p}" for p in include), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+           f'-DFME_BUILT_FOR="{binding_target()}"', *(f"-I{p}" for p in include), "-c",
+           os.path.join(CSRC, "binding.cpp"), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True, env=env)
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
@@ -86,9 +106,41 @@ def _link_binding(obj: str, env: dict) -> None:
     os.replace(tmp_out, BINDING)
 
 
+def _without_binding(error: Exception) -> None:
+    """The library serves the C ABI and the ctypes calls without the binding, which needs a host compiler and the
+    headers of Python and torch; its own calls raise until it is built, so an outdated one is taken away."""
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
+    warnings.warn(f"the compiled binding was not built, the FP8 block-128 and router calls will raise: {error}",
+                  RuntimeWarning, stacklevel=3)
+
+
+def build_binding() -> None:
+    """Compile and link the binding to the package's library."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with tempfile.TemporaryDirectory(prefix=f"{os.getpid()}_", dir=BUILD_DIR) as tmp:
+        env = dict(os.environ, TMPDIR=tmp)
+        obj = os.path.join(tmp, "binding.o")
+        _build_binding_object(obj, env)
+        _link_binding(obj, env)
+
+
+def refresh() -> str:
+    """Build what is missing or out of date of the library and the binding; returns the library's path."""
+    if _older(LIBRARY, _inputs()):
+        return build()
+    if _binding_stale():
+        try:
+            build_binding()
+        except (ImportError, OSError, RuntimeError) as e:
+            _without_binding(e)
+    return LIBRARY
+
+
 def build(output: str = LIBRARY, extra_flags: list[str] | None = None, verbose: bool = False) -> str:
-    """Compile and link the library (and, for the package's own, the binding); returns its path."""
-    binding = output == LIBRARY and _older(BINDING, _binding_inputs())
+    """Compile and link the library (and, for the package's own, the binding); returns its path.  A binding that cannot
+    be built is warned of: the library is in place then."""
+    binding = output == LIBRARY and _binding_stale()
     flags = NVCC_FLAGS + (extra_flags or [])
     tool = nvcc()
     # objects and nvcc's own intermediates stay inside the package tree (git-ignored)
@@ -111,8 +163,7 @@ def build(output: str = LIBRARY, extra_flags: list[str] | None = None, verbose: 
         with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
             pending = pool.submit(_build_binding_object, binding_obj, env) if binding else None
             objs = list(pool.map(compile_one, SOURCES))
-            if pending:
-                pending.result()
+            failed = pending.exception() if pending else None
         tmp_out = output + ".tmp"
         # a soname of its own: the binding, linked to the package's library, must not be given another build of it
         # that the process loaded first
@@ -122,7 +173,12 @@ def build(output: str = LIBRARY, extra_flags: list[str] | None = None, verbose: 
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp_out, output)
         if binding:
-            _link_binding(binding_obj, env)
+            try:
+                if failed:
+                    raise failed
+                _link_binding(binding_obj, env)
+            except (ImportError, OSError, RuntimeError) as e:
+                _without_binding(e)
     return output
 
 

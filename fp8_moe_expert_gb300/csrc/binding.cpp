@@ -574,4 +574,11 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_method
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject *PyInit__binding(void) { return PyModule_Create(&g_module); }
+extern "C" __attribute__((visibility("default"))) PyObject *PyInit__binding(void) {
+  PyObject *m = PyModule_Create(&g_module);
+  if (m && PyModule_AddStringConstant(m, "built_for", FME_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
