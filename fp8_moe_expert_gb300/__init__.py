@@ -162,12 +162,11 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
+    if stream is None:
+        import torch
 
-    # the current device's current stream, without a Stream object (3 us a call on a Grace core)
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream
 
 
 def _check(status: int, where: str):
