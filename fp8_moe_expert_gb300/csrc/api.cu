@@ -1036,6 +1036,7 @@ fme_status moe_balance_loss(const void *logits, int32_t dtype, const int32_t *id
   a.term = reinterpret_cast<float *>(base + w.term);
   a.flags = reinterpret_cast<int32_t *>(base + w.flags);
   a.status = dev_status;
+  a.num_sms = sms;
   a.stream = static_cast<cudaStream_t>(stream);
   cudaError_t err = fme::launch_balance_loss(a);
   return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_balance_loss launch");
@@ -1072,6 +1073,7 @@ fme_status moe_balance_loss_backward(const void *logits, int32_t dtype, const in
   a.d_loss = d_loss;
   a.d_logits = d_logits;
   a.accumulate = accumulate != 0;
+  a.num_sms = sms;
   a.stream = static_cast<cudaStream_t>(stream);
   cudaError_t err = fme::launch_balance_backward(a);
   return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_balance_loss_backward launch");

@@ -209,6 +209,7 @@ struct LaunchBalance {
   void *d_logits;
   bool accumulate;
   int32_t *status;
+  int num_sms;
   cudaStream_t stream;
 };
 cudaError_t launch_gate(const LaunchGate &a);

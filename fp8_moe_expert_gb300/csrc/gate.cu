@@ -775,7 +775,8 @@ cudaError_t balance_partial(const LaunchBalance &a) {
 template <typename T>
 cudaError_t balance_backward(const LaunchBalance &a) {
   // one wave: as many tokens a warp as 32 warps an SM leave (32768 x 256: 12.9 us; four a warp 13.7, two 15.8)
-  const int per_warp = static_cast<int>((a.tokens + 4863) / 4864);
+  const int64_t wave = 32 * static_cast<int64_t>(a.num_sms);
+  const int per_warp = static_cast<int>((a.tokens + wave - 1) / wave);
   const int64_t warps = (a.tokens + per_warp - 1) / per_warp;
   const unsigned blocks = static_cast<unsigned>((warps + kGateWarps - 1) / kGateWarps);
   return by_width<T>(a.num_experts, [&](auto v, auto vec) {
