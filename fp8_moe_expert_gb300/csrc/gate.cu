@@ -106,6 +106,11 @@ __device__ __forceinline__ void sigmoids(float l, float &s, float &rest) {
   s = l >= 0.0f ? r : tr;
   rest = l >= 0.0f ? tr : r;
 }
+__device__ __forceinline__ float sigmoid(float l) {
+  float s, rest;
+  sigmoids(l, s, rest);
+  return s;
+}
 
 // Ratios of sigmoids, s_i / sum of s, of rows far below zero.  Sigmoids are subnormal from -87 and zero from -104 down,
 // their ratios are not.  Where the sum is below this, every logit is negative, and e^(l - max) (1 - s), which is
@@ -261,14 +266,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const T *__restri
     if (ref == -INFINITY) ref = 0.0f;
     s = mine ? __expf(my_l - ref) : 0.0f;
   } else {
-    float rest;
-    sigmoids(my_l, s, rest);  // 0 at -inf: not a choice
-    if (normalize && warp_sum(s) < kSmallSum) {
+    s = mine ? sigmoid(my_l) : 0.0f;
+  }
+  if (normalize) {
+    denom = warp_sum(s);
+    if (!softmax && denom < kSmallSum) {
       const float top = warp_max(my_l);
-      s = __expf(my_l - (top == -INFINITY ? 0.0f : top)) * rest;
+      s = __expf(my_l - (top == -INFINITY ? 0.0f : top)) * (1.0f - s);
+      denom = warp_sum(s);
     }
   }
-  if (normalize) denom = warp_sum(s);
   if (mine) {
     ids[t * top_k + pos] = my_id;
     weights[t * top_k + pos] = denom == 0.0f ? 0.0f : scale * s / denom;
@@ -383,9 +390,11 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_backward_kernel(
 }
 
 // ------------------------------------------------------------- balance loss --
-// Probabilities of one token's row, V a lane; also s and 1 - s scaled for the gradient.
-template <int V>
-__device__ __forceinline__ void probabilities(const float (&l)[V], bool softmax, float (&p)[V], float (&slope)[V]) {
+// Probabilities of one token's row, V a lane; also s and 1 - s scaled for the gradient.  A row far below zero is
+// read again (kept for that, its logits would cost the other rows registers).
+template <typename T, int V, int VEC>
+__device__ __forceinline__ void probabilities(const float (&l)[V], const T *row, int experts, int lane, bool softmax,
+                                              float (&p)[V], float (&slope)[V]) {
   if (softmax) {
     const float z = exp_row<V>(l, row_offset<V>(l), p);
     const float r = z == 0.0f ? 0.0f : 1.0f / z;
@@ -399,12 +408,15 @@ __device__ __forceinline__ void probabilities(const float (&l)[V], bool softmax,
       z += p[j];
     }
     z = warp_sum(z);
-    if (z < kSmallSum) {  // slope holds 1 - s
-      const float top = row_offset<V>(l);
+    if (z < kSmallSum) {  // slope: 1 - s
+      load_row<T, V, VEC>(row, experts, lane, p);
+      const float top = row_offset<V>(p);
       z = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        p[j] = __expf(l[j] - top) * slope[j];
+        float s;
+        sigmoids(p[j], s, slope[j]);
+        p[j] = __expf(p[j] - top) * slope[j];
         z += p[j];
       }
       z = warp_sum(z);
@@ -506,7 +518,7 @@ __global__ void __launch_bounds__(32 * kPartWarps) balance_partial_kernel(Launch
         else
           report(a.status, kDevBadIndex);
       }
-      probabilities<V>(l, a.softmax, p, slope);
+      probabilities<T, V, VEC>(l, logits + t * experts, experts, lane, a.softmax, p, slope);
 #pragma unroll
       for (int j = 0; j < V; ++j) sum[j] += p[j];
       ++mine;
@@ -661,7 +673,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, V <= 8 ? 4 : 1) balance_backw
       const float c = n > 0 ? up * (static_cast<float>(experts) / (static_cast<float>(a.top_k) * tn)) / tn : 0.0f;
       // Counts above their mean: the same for all experts falls out of a_e - sum p a, and where every expert is chosen
       // (top_k = experts) nothing is left, not rounding noise.
-      const int32_t mean = static_cast<int32_t>(static_cast<int64_t>(n) * a.top_k / experts);
+      const int32_t mean = n / experts * a.top_k + n % experts * a.top_k / experts;  // of n top_k choices, in 32 bits
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int e = expert_of<VEC>(j, lane);
@@ -687,7 +699,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, V <= 8 ? 4 : 1) balance_backw
       continue;
     }
     float p[V], slope[V];
-    probabilities<V>(cur, a.softmax, p, slope);
+    probabilities<T, V, VEC>(cur, logits + t * experts, experts, lane, a.softmax, p, slope);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) dot += p[j] * w[j];
