@@ -10,7 +10,7 @@
 // Gradient, g_i = dL/dw_i, sums over the choices:
 //   softmax, normalised   dl_i = w_i (g_i - sum_j w_j g_j / c)
 //   softmax               dl_e = p_e (c g_e [e chosen] - sum_j c p_j g_j)
-//   sigmoid, normalised   dl_i = (c g_i - sum_j (s_j / S) c g_j) / S  s_i (1 - s_i),  S = sum_j s_j
+//   sigmoid, normalised   dl_i = p_i (1 - s_i) (c g_i - sum_j p_j c g_j),  p_i = s_i / sum_j s_j
 //   sigmoid               dl_i = c g_i s_i (1 - s_i)
 //
 // Balance loss.  p = softmax(l) or sigmoid(l) / Z.  Over the T_q counted tokens of each
@@ -22,9 +22,10 @@
 //
 // One warp a token, V experts a lane, VEC of them neighbours (one load of up to 16 bytes); all
 // sums fp32.  Reads the logits once.  Few tokens: launch-bound.  Many: the instructions of the
-// selection (388 a token of 256 experts, top 8) and of the probabilities (203 in the loss, 250 in its
-// gradient), at 70 to 86% of the issue rate, take longer than its bytes.  32768 x 256, us: gate 13.6,
-// gradient 7.6; balance loss (bf16, sigmoid) 17.4, gradient 13.5.
+// selection (393 a token of 256 experts, top 8) and of the probabilities (208 in the loss, 254 in its
+// gradient), at 68 to 86% of the issue rate, take longer than its bytes.  32768 x 256, us, launched from a graph:
+// gate (fp32, softmax) 13.1, gradient 7.0, without normalize 15.6; balance loss (bf16, sigmoid, 13 sequences)
+// 17.5, gradient 13.2, added onto another 14.4.
 #include "block128.cuh"
 
 namespace fme {

@@ -16,9 +16,10 @@
 // alone: their operands are 80 KB a block and SM, 625 cycles at shared memory's 128 bytes
 // a cycle.  With the sums it takes about 850: the scales' reads and the barriers go
 // through the same shared memory and the accumulator is held while it is read out.
-// 65536 x 4096 x 7168: 1.35 ms, 2.85 PFLOP/s; dgrad 65536 x 7168 x 2048, 32 experts:
-// 0.70 ms, 2.74 PFLOP/s; wgrad of the same: 1.18 ms, 1.63 PFLOP/s (about 1290 cycles a block,
-// the epilogue's: without its sums and products 800).
+// 65536 x 4096 x 7168, one expert: 1.34 ms, 2.88 PFLOP/s; dgrad 65536 x 7168 x 2048, 32 experts of
+// 2048 rows: 0.74 ms, 2.59 PFLOP/s; wgrad of the same: 1.17 ms, 1.64 PFLOP/s (about 1290 cycles a block,
+// the epilogue's: without its sums and products 800), to fp32 1.28 ms, added into fp32 3.14 ms (the epilogue's
+// reads of dW follow one another; one expert 1.04 and 1.09 ms).
 //
 // One set of weight codes serves both directions: blocks are 128 x 128, and dgrad reads
 // the same [n x k] codes as an MN-major operand (its contraction runs down the rows).

@@ -486,7 +486,9 @@ fme_status grouped_gemm_wgrad_mxfp8_accumulate(const uint8_t *a_codes, const uin
  *
  * For a block with largest magnitude a: A = max(a, 2^-100), scale = fl32(A / 448),
  * r = fl32(448 / A) (both IEEE divisions), code = E4M3(fl32(x r)), round to nearest
- * even, saturating.  Dequantized value = code * scale.
+ * even, saturating.  Dequantized value = code * scale.  a is taken over the values that are
+ * not NaN; a NaN gets a NaN code.  In a block with an infinity the quotients are inf and 0: finite
+ * values get codes 0, infinities NaN.
  * ("Scaling and Optimizing Frontier Model Training": DeepSeek-V3-class experts, which
  * are stored and trained in this format; the floor 2^-100 is this library's choice.)
  *
@@ -572,7 +574,11 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
  * ("Composer 2 Technical Report", section 6.2).  With s = softmax over the token's
  * experts or sigmoid, of the logits without bias:
  *   weights[t, i] = scale s_i / sum of s over the choices (normalize), or scale s_i.
- * All arithmetic in fp32.  A token whose chosen logits (without normalize: all its logits)
+ * The bias is added to the logit.  A correction bias that was trained on the score (sigmoid(l) + b, as in
+ * DeepSeek-V3's loss-free balancing) orders the experts differently: it does not belong here, nor is
+ * there a choice limited to groups of experts.
+ * All arithmetic in fp32; the ratio of normalized sigmoids also where the sigmoids themselves would
+ * vanish.  A token whose chosen logits (without normalize: all its logits)
  * are -inf gets weights 0; +inf under softmax, or a NaN, gives weights NaN.
  *
  *   logits     device bf16 (FME_BF16) or float (FME_FP32) [tokens x num_experts]
