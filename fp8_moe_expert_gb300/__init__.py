@@ -111,6 +111,9 @@ SYMBOLS = {
     "grouped_gemm_dgrad_fp8_block128": ("i32", ["p", "p", "p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
     "grouped_gemm_wgrad_fp8_block128": ("i32", ["p", "p", "p", "p", "i64", "p", "i32", "i64", "i64", "p", "i32", "p",
                                                 "p"]),
+    "grouped_gemm_fwd_bf16": ("i32", ["p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
+    "grouped_gemm_dgrad_bf16": ("i32", ["p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
+    "grouped_gemm_wgrad_bf16": ("i32", ["p", "p", "i64", "p", "i32", "i64", "i64", "p", "i32", "p", "p"]),
     "moe_gate": ("i32", ["p", "i32", "i64", "i32", "i32", "i32", "i32", "f32", "p", "p", "p", "p"]),
     "moe_gate_backward": ("i32", ["p", "i32", "p", "p", "i64", "i32", "i32", "i32", "i32", "f32", "p", "p", "p"]),
     "moe_balance_loss": ("i32", ["p", "i32", "p", "i64", "i32", "i32", "i32", "f32", "p", "i64", "p", "p", "p", "p",
@@ -625,15 +628,37 @@ def grouped_gemm_wgrad_fp8_block128(dy_codes, dy_scale, x_codes, x_scale, padded
     """dW [E, n, k] = dY_e^T X_e per expert, from quantize_fp8_block128(COLWISE) of dY [rows, n]
     and X [rows, k] with the same offsets.  dtype bfloat16 (default) or float32; with accumulate
     the result is added into dw (float32)."""
+    mode = _dw_mode("grouped_gemm_wgrad_fp8_block128", dw, dtype, accumulate)
+    return _bind().wgrad(dy_codes, dy_scale, x_codes, x_scale, padded_offsets, dw, mode, status, _raw(stream))
+
+
+def _dw_mode(where, dw, dtype, accumulate):
     import torch
 
     if dtype is None:
         dtype = torch.bfloat16 if dw is None else dw.dtype
     if dtype not in (torch.bfloat16, torch.float32) or (accumulate and (dw is None or dtype != torch.float32)):
-        raise ValueError("grouped_gemm_wgrad_fp8_block128: dw is bfloat16 or float32, and a given float32 tensor to "
-                         "accumulate into")
-    mode = DW_BF16 if dtype == torch.bfloat16 else DW_FP32_ADD if accumulate else DW_FP32
-    return _bind().wgrad(dy_codes, dy_scale, x_codes, x_scale, padded_offsets, dw, mode, status, _raw(stream))
+        raise ValueError(f"{where}: dw is bfloat16 or float32, and a given float32 tensor to accumulate into")
+    return DW_BF16 if dtype == torch.bfloat16 else DW_FP32_ADD if accumulate else DW_FP32
+
+
+# ------------------------------------------------------------ bf16 products --
+def grouped_gemm_fwd_bf16(x, w, offsets, *, y=None, status=None, stream=None):
+    """Y [m, n] (bf16) = X_e W_e^T per expert, from bf16 rows x [m, k] grouped by expert (moe_permute) and weights
+    w [E, n, k]; offsets int32 [E+1].  n and k are multiples of 8."""
+    return _bind().fwd_bf16(x, w, offsets, y, status, _raw(stream))
+
+
+def grouped_gemm_dgrad_bf16(dy, w, offsets, *, dx=None, status=None, stream=None):
+    """dX [m, k] (bf16) = dY_e W_e per expert, from dy [m, n] and the forward's weights."""
+    return _bind().dgrad_bf16(dy, w, offsets, dx, status, _raw(stream))
+
+
+def grouped_gemm_wgrad_bf16(dy, x, offsets, *, dw=None, dtype=None, accumulate=False, status=None, stream=None):
+    """dW [E, n, k] = dY_e^T X_e per expert, from dy [m, n] and x [m, k] grouped with the same offsets.  dtype bfloat16
+    (default) or float32; with accumulate the result is added into dw (float32)."""
+    mode = _dw_mode("grouped_gemm_wgrad_bf16", dw, dtype, accumulate)
+    return _bind().wgrad_bf16(dy, x, offsets, dw, mode, status, _raw(stream))
 
 
 # ------------------------------------------------------------------- router --

@@ -896,6 +896,120 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
   return err == cudaSuccess ? FME_OK : cuda_fail(err, "grouped_gemm_wgrad_fp8_block128 launch");
 }
 
+// -------------------------------------------------------------- bf16 products --
+namespace {
+
+// Columns of a bf16 operand: its rows are a multiple of 16 bytes.
+bool bf16_cols(int64_t c) { return c >= 8 && c <= 65536 && c % 8 == 0; }
+
+// 2-D bf16 matrix [rows x cols], boxes of 128 bytes x box_rows, 128-byte swizzle, zero fill out of bounds.
+fme_status encode_bf16_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  return encode_map(" (rows)", map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// 3-D bf16 weights [experts][n][k], the same boxes, zero fill past each expert's n and k.
+fme_status encode_bf16_weights(CUtensorMap *map, const void *base, uint64_t experts, uint64_t n, uint64_t k,
+                               uint32_t box_rows) {
+  cuuint64_t dims[3] = {k, n, experts};
+  cuuint64_t strides[2] = {k * 2, n * k * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  return encode_map(" (weights)", map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// The forward (out = n columns, contraction k) and dgrad (out = k columns, contraction n).
+fme_status bf16_rows_gemm(bool dgrad, const void *a_rows, const void *w, const int32_t *offsets, int32_t num_experts,
+                          int64_t m, int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream,
+                          const char *what) {
+  if (m < 0 || n < 0 || k < 0 || check_groups(num_experts) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (!bf16_cols(n) || !bf16_cols(k)) return FME_ERR_UNSUPPORTED_SHAPE;
+  // row coordinates of the last, partly empty tiles and the number of tiles stay in 32 bits
+  if (m > (int64_t(1) << 31) - 1 - 256) return FME_ERR_UNSUPPORTED_SHAPE;
+  if ((m / 64 + num_experts) * (((dgrad ? k : n) + 127) / 128) > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets) return FME_ERR_INVALID_ARGUMENT;
+  if (m == 0) return FME_OK;
+  if (!a_rows || !w || !y) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(a_rows) || !aligned16(w) || !aligned16(y) || !aligned16(offsets)) return FME_ERR_MISALIGNED;
+  fme::LaunchBf16 a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  a.k = dgrad ? n : k;
+  a.n = dgrad ? k : n;
+  const bool few = !dgrad && fme::bf16_few_rows(m, num_experts);
+  CUtensorMap &rows_map = few ? a.map_b : a.map_a, &w_map = few ? a.map_a : a.map_b;
+  if ((st = encode_bf16_2d(&rows_map, a_rows, m, a.k, few ? 16 : 128)) != FME_OK) return st;
+  if ((st = encode_bf16_weights(&w_map, w, num_experts, n, k, dgrad ? 64 : 128)) != FME_OK) return st;
+  if ((st = encode_bf16_out(&a.map_y, y, a.n, m, OutBox::kWideBf16)) != FME_OK) return st;
+  a.offsets = offsets;
+  a.num_experts = num_experts;
+  a.rows = m;
+  a.m = m;
+  a.y = y;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = dgrad ? fme::launch_bf16_dgrad(a) : fme::launch_bf16_fwd(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, what);
+}
+
+}  // namespace
+
+fme_status grouped_gemm_fwd_bf16(const void *x, const void *w, const int32_t *offsets, int32_t num_experts, int64_t m,
+                                 int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream) {
+  return bf16_rows_gemm(false, x, w, offsets, num_experts, m, n, k, y, dev_status, stream,
+                        "grouped_gemm_fwd_bf16 launch");
+}
+
+fme_status grouped_gemm_dgrad_bf16(const void *dy, const void *w, const int32_t *offsets, int32_t num_experts, int64_t m,
+                                   int64_t n, int64_t k, void *dx, int32_t *dev_status, void *stream) {
+  return bf16_rows_gemm(true, dy, w, offsets, num_experts, m, n, k, dx, dev_status, stream,
+                        "grouped_gemm_dgrad_bf16 launch");
+}
+
+fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, const int32_t *offsets, int32_t num_experts,
+                                   int64_t n, int64_t k, void *dw, int32_t dw_mode, int32_t *dev_status, void *stream) {
+  if (n < 0 || k < 0 || m < 0 || check_groups(num_experts) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (dw_mode != FME_DW_BF16 && dw_mode != FME_DW_FP32 && dw_mode != FME_DW_FP32_ADD) return FME_ERR_INVALID_ARGUMENT;
+  if (!bf16_cols(n) || !bf16_cols(k) || m > (int64_t(1) << 31) - 1 - 256) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (num_experts * ((n + 255) / 256) * ((k + 255) / 256) > (int64_t(1) << 31) - 1 ||
+      num_experts * n > (int64_t(1) << 31) - 1 - 256)
+    return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets || !dw) return FME_ERR_INVALID_ARGUMENT;
+  if (m > 0 && (!dy || !x)) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(dw) || !aligned16(offsets)) return FME_ERR_MISALIGNED;
+  fme::LaunchBf16 a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  // without rows every expert is empty and the operands' maps are never used
+  const void *abase = m ? dy : dw, *bbase = m ? x : dw;
+  const int64_t extent = m ? m : 1;
+  if ((st = encode_bf16_2d(&a.map_a, abase, extent, n, 64)) != FME_OK ||
+      (st = encode_bf16_2d(&a.map_a8, abase, extent, n, 8)) != FME_OK ||
+      (st = encode_bf16_2d(&a.map_a1, abase, extent, n, 1)) != FME_OK ||
+      (st = encode_bf16_2d(&a.map_b, bbase, extent, k, 64)) != FME_OK ||
+      (st = encode_bf16_2d(&a.map_b8, bbase, extent, k, 8)) != FME_OK ||
+      (st = encode_bf16_2d(&a.map_b1, bbase, extent, k, 1)) != FME_OK)
+    return st;
+  if ((st = encode_bf16_out(&a.map_y, dw, k, static_cast<uint64_t>(num_experts) * n,
+                            dw_mode == FME_DW_BF16 ? OutBox::kWideBf16 : OutBox::kWideFp32)) != FME_OK)
+    return st;
+  a.offsets = offsets;
+  a.num_experts = num_experts;
+  a.rows = m;
+  a.m = n;
+  a.n = k;
+  a.y = dw;
+  a.out_fp32 = dw_mode != FME_DW_BF16;
+  a.accumulate = dw_mode == FME_DW_FP32_ADD;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_bf16_wgrad(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "grouped_gemm_wgrad_bf16 launch");
+}
+
 // ------------------------------------------------------------------ router --
 namespace {
 

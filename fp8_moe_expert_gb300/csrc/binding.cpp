@@ -381,6 +381,50 @@ PyObject *wgrad(PyObject *const *a) {
   return one(a[5], dw);
 }
 
+// --------------------------------------------------------------- bf16 products --
+// x or dy, w, offsets, y or dx, status, stream
+template <bool kDgrad>
+PyObject *rows_gemm_bf16(PyObject *const *a) {
+  Call c{kDgrad ? "grouped_gemm_dgrad_bf16" : "grouped_gemm_fwd_bf16"};
+  const Shape ws = dims(c, "w", a[1], 3);
+  const int64_t e = ws[0], n = ws[1], k = ws[2];
+  const char *rows = kDgrad ? "dy" : "x";
+  const int64_t m = dims(c, rows, a[0], 2)[0];
+  const at::Tensor &x = input(c, rows, a[0], kBf16, {m, kDgrad ? n : k});
+  const at::Tensor &w = input(c, "w", a[1], kBf16, {e, n, k});
+  const at::Tensor &off = input(c, "offsets", a[2], kI32, {e + 1});
+  int32_t *st = status_ptr(c, a[4]);
+  const OnStream on(c, a[5]);
+  const at::Tensor y = output(c, on, kDgrad ? "dx" : "y", a[3], kBf16, {m, kDgrad ? k : n}, x);
+  const int32_t experts = e > INT32_MAX ? INT32_MAX : static_cast<int32_t>(e);
+  call(c, [&] {
+    return (kDgrad ? grouped_gemm_dgrad_bf16 : grouped_gemm_fwd_bf16)(ptr(x), ptr(w), ptr<int32_t>(off), experts, m, n, k,
+                                                                      ptr(y), st, on.raw());
+  });
+  return one(a[3], y);
+}
+
+// dy, x, offsets, dw, mode (FME_DW_*), status, stream
+PyObject *wgrad_bf16(PyObject *const *a) {
+  Call c{"grouped_gemm_wgrad_bf16"};
+  const Shape ds = dims(c, "dy", a[0], 2);
+  const int64_t m = ds[0], n = ds[1], k = dims(c, "x", a[1], 2)[1];
+  const int64_t e = dims(c, "offsets", a[2], 1)[0] - 1;
+  const at::Tensor &dy = input(c, "dy", a[0], kBf16, {m, n});
+  const at::Tensor &x = input(c, "x", a[1], kBf16, {m, k});
+  const at::Tensor &off = input(c, "offsets", a[2], kI32, {e + 1});
+  const int32_t mode = integer32(a[4]);
+  if (e < 1) throw Refused(std::string(c.where) + ": offsets must have at least 2 elements");
+  int32_t *st = status_ptr(c, a[5]);
+  const OnStream on(c, a[6]);
+  const at::Tensor dw = output(c, on, "dw", a[3], mode == FME_DW_BF16 ? kBf16 : kF32, {e, n, k}, dy);
+  const int32_t experts = e > INT32_MAX ? INT32_MAX : static_cast<int32_t>(e);
+  call(c, [&] {
+    return grouped_gemm_wgrad_bf16(ptr(dy), ptr(x), m, ptr<int32_t>(off), experts, n, k, ptr(dw), mode, st, on.raw());
+  });
+  return one(a[3], dw);
+}
+
 // ---------------------------------------------------------------------- router --
 struct Logits {
   const at::Tensor &t;
@@ -561,6 +605,9 @@ PyMethodDef g_methods[] = {
     method<8, rows_gemm<false>>("fwd"),
     method<8, rows_gemm<true>>("dgrad"),
     method<9, wgrad>("wgrad"),
+    method<6, rows_gemm_bf16<false>>("fwd_bf16"),
+    method<6, rows_gemm_bf16<true>>("dgrad_bf16"),
+    method<7, wgrad_bf16>("wgrad_bf16"),
     method<9, gate>("gate"),
     method<9, gate_backward>("gate_backward"),
     method<12, balance_loss>("balance_loss"),

@@ -171,6 +171,31 @@ cudaError_t launch_block128_fwd(const LaunchBlock128 &a);
 cudaError_t launch_block128_dgrad(const LaunchBlock128 &a);
 cudaError_t launch_block128_wgrad(const LaunchBlock128 &a);
 
+// bf16 grouped GEMMs (gemm_bf16.cu).
+struct LaunchBf16 {
+  CUtensorMap map_a, map_b;                      // operands, 128-byte swizzle
+  CUtensorMap map_a8, map_a1, map_b8, map_b1;    // wgrad: the same in boxes of 8 rows and of one
+  CUtensorMap map_y;                             // output, boxes of 32 rows x 128 bytes, 128-byte swizzle
+  const int32_t *offsets;  // rows of each expert
+  int32_t num_experts;
+  int64_t rows;     // rows of all experts
+  int64_t m, n, k;  // output rows (wgrad: of one expert) and columns; contraction (not wgrad)
+  void *y;
+  bool out_fp32, accumulate;  // wgrad
+  int32_t *status;
+  int num_sms;
+  int stages;  // operand ring depth, set by the launcher
+  cudaStream_t stream;
+};
+// The forward takes its few-rows form (map_a = weights in 128-row boxes, map_b = tokens in 16-row
+// boxes) up to this many rows.
+inline bool bf16_few_rows(int64_t m, int32_t num_experts) {
+  return m <= 256 + 32 * static_cast<int64_t>(num_experts);
+}
+cudaError_t launch_bf16_fwd(const LaunchBf16 &a);
+cudaError_t launch_bf16_dgrad(const LaunchBf16 &a);
+cudaError_t launch_bf16_wgrad(const LaunchBf16 &a);
+
 // The router (gate.cu).
 struct LaunchGate {
   const void *logits;  // [tokens x num_experts], bf16 or fp32

@@ -1,0 +1,724 @@
+// gemm_bf16.cu -- grouped GEMMs on bf16 operands (forward, dgrad, wgrad), on tcgen05, CTA pairs.
+//
+//   forward  Y[t,n]    = sum_k X[t,k]  W[e,n,k]      (t a row of expert e)
+//   dgrad    dX[t,k]   = sum_n dY[t,n] W[e,n,k]
+//   wgrad    dW[e,n,k] = sum_{t of e} dY[t,n] X[t,k]
+//
+// The layers that stay in bf16, and what the low-precision products are compared with ("Scaling and Optimizing
+// Frontier Model Training", "MXFP8 expert kernels").  Operands are read as they lie in memory: W is K-major for the
+// forward and MN-major for dgrad, wgrad's operands are MN-major, so nothing is transposed, padded or copied.
+// Products and sums are kept in fp32 in tensor memory over the whole contraction, in steps of 16 in order, and rounded
+// once: there is no split, so a row's result depends neither on other rows nor on which form below runs.
+//
+// wgrad's contraction runs over the rows of one expert, and the block of 64 rows at an expert's end reaches into the
+// next expert's.  Those must read as zeros in both operands (0 times a NaN of another expert would be NaN), so the last
+// block comes in boxes of 8 rows, the group of 8 that holds the end in boxes of one row, and a box of rows that are not the
+// expert's is asked for behind the tensor's last row, where the tensor map fills in zeros.
+#include <algorithm>
+
+#include "gemm_tiles.cuh"
+
+namespace fme {
+
+namespace {
+
+constexpr int kThreadsBf = 384;
+constexpr int kEpiWarp0 = 4;
+constexpr int kStageK = 64;  // bf16 of the contraction in a stage: one 128-byte swizzle row
+constexpr int kStageBytesBf = kABytes + kBBytes;
+constexpr int kMaxStagesBf = 6;
+constexpr int kOutBlockBytes = 32 * 128;  // a warp's staging block: 32 rows of 128 bytes
+constexpr int kHalfMnBytes = kStageK * 128;  // 64 M or N values (128 bytes) of an MN-major stage
+
+enum class KindBf { kFwd, kDgrad, kWgrad };
+
+struct SharedBf {
+  uint64_t full[kMaxStagesBf];
+  uint64_t freed[kMaxStagesBf];  // the stage's MMAs are done (own CTA)
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint64_t peer_fills_bar;
+  uint32_t peer_fills;
+  uint32_t tmem_base;
+  int abort_flag;
+  int ok_flag;
+};
+
+// Instruction descriptor: fp32 accumulator (bit 4), bf16 operands (bits 7 and 10), the operands'
+// major-ness (bits 15, 16: 1 = MN-major), N / 8 and M / 16.
+constexpr uint32_t idesc_bf16(bool a_mn, bool b_mn, uint32_t m, uint32_t n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) |
+         ((m >> 4) << 24);
+}
+
+// One stage (64 of the contraction): four K = 16 steps, M = 256 over the pair, and the commit that frees the stage in
+// both CTAs.  kA, kB: distance of the steps in the operands' descriptors (16-byte units).
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void mma_stage_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate, uint64_t *freed) {
+  asm volatile(
+      "{\n\t.reg .pred z, o;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.u32 z, %8, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
+      "add.s64 a1, %1, %5;\n\tadd.s64 a2, %1, 2 * %5;\n\tadd.s64 a3, %1, 3 * %5;\n\t"
+      "add.s64 b1, %2, %6;\n\tadd.s64 b2, %2, 2 * %6;\n\tadd.s64 b3, %2, 3 * %6;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, z;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, o;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, o;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, o;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %7;\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(smem_u32(freed)), "n"(kA), "n"(kB), "h"(static_cast<uint16_t>(3)),
+      "r"(accumulate)
+      : "memory");
+}
+
+struct TileBf {
+  int32_t e;
+  int32_t nk;          // stages of the contraction
+  int32_t row0;        // this CTA's first output row: of all rows (fwd, dgrad) or of the expert's (wgrad)
+  int32_t rows_valid;  // of its 128
+  int32_t col0;        // first output column of the tile
+  int32_t p0, p1;      // wgrad: the expert's rows, the contraction
+};
+
+// Tiles and their counts are in 32 bits (checked on the host).
+template <KindBf K>
+__device__ __forceinline__ TileBf tile_bf(const LaunchBf16 &p, const Tables &s, uint32_t t, int rank) {
+  TileBf tl;
+  const uint32_t nb = (static_cast<uint32_t>(p.n) + kBN - 1) / kBN;
+  if constexpr (K == KindBf::kWgrad) {
+    const uint32_t per = (static_cast<uint32_t>(p.m) + kPairM - 1) / kPairM * nb;
+    const uint32_t order = t / per;
+    const uint32_t rem = t - order * per;
+    const uint32_t row = rem / nb;
+    tl.e = s.aux[order];
+    tl.p0 = s.off[tl.e];
+    tl.p1 = s.off[tl.e + 1];
+    tl.nk = (tl.p1 - tl.p0 + kStageK - 1) / kStageK;
+    tl.row0 = static_cast<int32_t>(row * kPairM + rank * kBM);
+    tl.rows_valid = min(kBM, static_cast<int32_t>(p.m) - tl.row0);
+    tl.col0 = static_cast<int32_t>((rem - row * nb) * kBN);
+  } else {
+    const uint32_t g = t / nb;
+    tl.col0 = static_cast<int32_t>((t - g * nb) * kBN);
+    tl.e = find_group(s.aux, p.num_experts, g);
+    const int32_t first = (static_cast<int32_t>(g) - s.aux[tl.e]) * kPairM + rank * kBM;
+    tl.row0 = s.off[tl.e] + first;
+    tl.rows_valid = min(kBM, s.off[tl.e + 1] - s.off[tl.e] - first);
+    tl.nk = static_cast<int32_t>((p.k + kStageK - 1) / kStageK);
+    tl.p0 = tl.p1 = 0;
+  }
+  return tl;
+}
+
+// A staged block (32 rows of 128 bytes, swizzled) to columns `col` on, by plain stores; with kAdd added to what is there
+// (one unfused add an element, all reads before the first write: they are in flight together).  Past the output's edge
+// nothing is written.
+template <typename T, bool kAdd>
+__device__ __forceinline__ void store_rows(T *y, int64_t ld, int64_t row0, int64_t col, int rows_valid, const uint8_t *blk,
+                                           int lane) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int j = lane & 7;
+  col += kPer * j;
+  if (col >= ld) return;
+  T *base = y + row0 * ld + col;
+  float4 old[8];
+  if (kAdd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      old[i] = r < rows_valid ? *reinterpret_cast<const float4 *>(base + r * ld) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    float4 v = *reinterpret_cast<const float4 *>(blk + r * 128 + 16 * (j ^ (r & 7)));
+    if (kAdd)
+      v = make_float4(__fadd_rn(old[i].x, v.x), __fadd_rn(old[i].y, v.y), __fadd_rn(old[i].z, v.z),
+                      __fadd_rn(old[i].w, v.w));
+    if (r < rows_valid) *reinterpret_cast<float4 *>(base + r * ld) = v;
+  }
+}
+
+template <KindBf K>
+__global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_constant__ LaunchBf16 p) {
+  constexpr bool kAmn = K == KindBf::kWgrad;
+  constexpr bool kBmn = K != KindBf::kFwd;
+  __shared__ SharedBf s;
+  extern __shared__ uint8_t dyn_smem[];
+  const uint32_t S = p.stages;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem_a = smem;
+  uint8_t *smem_b = smem_a + S * kABytes;
+  uint8_t *smem_out = smem + S * kStageBytesBf;
+  int32_t *gmem = reinterpret_cast<int32_t *>(smem_out + 8 * kOutBlockBytes);
+  const Tables tab{gmem, gmem + (p.num_experts + 1)};
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(pair::cta_rank());
+  const uint32_t pair_id = blockIdx.x >> 1;
+  const uint32_t pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 32) {
+    for (uint32_t i = 0; i < S; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.freed[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], kAccEmptyArrivals);
+    }
+    mbar_init(&s.drain, 1);
+    mbar_init(&s.peer_fills_bar, 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    prefetch_tensormap(&p.map_a);
+    prefetch_tensormap(&p.map_b);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    pair::tmem_alloc(&s.tmem_base, kTmemCols);
+    pair::tmem_relinquish();
+  }
+  start_next_kernel();  // its CTAs find room as these end
+  wait_for_previous_kernel();
+  // ---- tables (both CTAs of a pair see the same offsets and take the same way out)
+  if (warp == 0) {
+    const int32_t total = scan_groups(p.offsets, p.num_experts, p.rows, kPairM,
+                                      [&](int g, int32_t lo, int32_t, int32_t first) {
+                                        tab.off[g] = lo;
+                                        if (K != KindBf::kWgrad) tab.aux[g] = first;
+                                      });
+    if (lane == 0) {
+      tab.off[p.num_experts] = static_cast<int32_t>(p.rows);
+      if (K != KindBf::kWgrad) tab.aux[p.num_experts] = total;
+      s.ok_flag = total >= 0;
+    }
+  }
+  if constexpr (K == KindBf::kWgrad) {  // experts by decreasing work
+    __syncthreads();
+    if (s.ok_flag) {
+      for (int e = threadIdx.x; e < p.num_experts; e += kThreadsBf) {
+        const int32_t w = tab.off[e + 1] - tab.off[e];
+        int order = 0;
+        for (int f = 0; f < p.num_experts; ++f) {
+          const int32_t wf = tab.off[f + 1] - tab.off[f];
+          order += (wf > w) || (wf == w && f < e);
+        }
+        tab.aux[order] = e;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  pair::cluster_sync();  // both CTAs' barriers exist before any copy or arrive crosses the pair
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  volatile int *abort_flag = &s.abort_flag;
+  // A pair's tile of each round: one of every `pairs`.  wgrad's come with decreasing work, and every other round is
+  // walked backwards, so that a pair with a long tile gets a short one next.
+  auto tile_at = [&](uint32_t round) {
+    return round * pairs + (K == KindBf::kWgrad && (round & 1) ? pairs - 1 - pair_id : pair_id);
+  };
+  const uint32_t nb = static_cast<uint32_t>((p.n + kBN - 1) / kBN);
+  // malformed offsets: no tile, straight to the end
+  if (!s.ok_flag && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
+  const uint32_t total =
+      !s.ok_flag ? 0
+                 : (K == KindBf::kWgrad ? p.num_experts * static_cast<uint32_t>((p.m + kPairM - 1) / kPairM)
+                                        : tab.aux[p.num_experts]) *
+                       nb;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer (wgrad: the whole warp, as a block at
+    // an expert's end takes up to 60 copies)
+    if (K == KindBf::kWgrad || lane == 0) {
+      uint32_t stage = 0, phase = 1, filled = 0;
+      bool stop = false;
+      for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
+        const TileBf tl = tile_bf<K>(p, tab, t, rank);
+        const int32_t bcol = tl.col0 + rank * kHalfN;
+        for (int i = 0; i < tl.nk; ++i) {
+          stop = lane == 0 && !mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status);
+          if (K == KindBf::kWgrad) stop = warp_any(stop);
+          if (stop) break;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytesBf);
+          const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
+          uint8_t *a = smem_a + stage * kABytes, *b = smem_b + stage * kBBytes;
+          const int32_t k0 = i * kStageK;
+          if constexpr (K == KindBf::kWgrad) {
+            const int32_t row = tl.p0 + k0, left = tl.p1 - row;
+            if (left >= kStageK) {
+              if (lane < 4) {  // lanes 0, 1: A's two halves of 64 columns, 2, 3: B's
+                uint8_t *dst = (lane < 2 ? a : b) + (lane & 1) * kHalfMnBytes;
+                pair::tma_load_2d(dst, lane < 2 ? &p.map_a : &p.map_b, bar, (lane < 2 ? tl.row0 : bcol) + 64 * (lane & 1), row);
+              }
+            } else {  // lane = 8 (half of A or B) + group of 8 rows
+              const int32_t which = lane >> 3, grp = lane & 7;
+              uint8_t *dst = (which < 2 ? a : b) + (which & 1) * kHalfMnBytes;
+              const int32_t x = (which < 2 ? tl.row0 : bcol) + 64 * (which & 1);
+              const int32_t outside = static_cast<int32_t>(p.rows);
+              const int32_t split = left & 7 ? left >> 3 : 8;  // the group that holds the end
+              if (grp != split)
+                pair::tma_load_2d(dst + grp * 1024, which < 2 ? &p.map_a8 : &p.map_b8, bar, x,
+                                  8 * grp < left ? row + 8 * grp : outside);
+              if (split < 8)  // this lane's row of it
+                pair::tma_load_2d(dst + split * 1024 + grp * 128, which < 2 ? &p.map_a1 : &p.map_b1, bar, x,
+                                  8 * split + grp < left ? row + 8 * split + grp : outside);
+            }
+            __syncwarp();
+          } else {
+            pair::tma_load_2d(a, &p.map_a, bar, k0, tl.row0);
+            if constexpr (K == KindBf::kFwd) {
+              tma_load_3d_pair(b, &p.map_b, bar, k0, bcol, tl.e);
+            } else {
+              tma_load_3d_pair(b, &p.map_b, bar, bcol, k0, tl.e);
+              tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, k0, tl.e);
+            }
+          }
+          ++filled;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (lane == 0) {
+        const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
+        if (rank == 0) drain_pair_ring(s.full, S, filled, peer, kStageBytesBf);
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ------------------------------------------- MMA issuer (leader, whole warp)
+      constexpr uint32_t idesc = idesc_bf16(kAmn, kBmn, 256, 256);
+      const uint64_t a_desc = desc_sw128(smem_u32(smem_a), kAmn, kHalfMnBytes);
+      const uint64_t b_desc = desc_sw128(smem_u32(smem_b), kBmn, kHalfMnBytes);
+      uint32_t stage = 0, phase = 0, tiles = 0;
+      bool stop = false;
+      for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
+        const int nk = tile_bf<K>(p, tab, t, 0).nk;
+        if (nk == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const uint32_t b = tiles & 1;
+        stop = warp_any(!mbar_wait(&s.acc_empty[b], ((tiles >> 1) & 1) ^ 1, abort_flag, p.status));
+        for (int i = 0; i < nk && !stop; ++i) {
+          stop = warp_any(!mbar_wait(&s.full[stage], phase, abort_flag, p.status));
+          if (stop) break;
+          tc_fence_after();
+          // 16 of K: 32 bytes along a K-major row, 16 rows of an MN-major tile
+          if (elect_one()) {
+            mma_stage_pair<(kAmn ? 2048 : 32) / 16, (kBmn ? 2048 : 32) / 16>(
+                tmem + b * kBN, a_desc + stage * (kABytes / 16), b_desc + stage * (kBBytes / 16), idesc, i > 0,
+                &s.freed[stage]);
+            if (i == nk - 1) pair::commit_both(&s.acc_full[b]);
+          }
+          __syncwarp();
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        ++tiles;
+      }
+      __syncwarp();
+      if (elect_one()) {
+        pair::commit_local(&s.drain);
+        mbar_drain(&s.drain, 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ----------------------------------------------------------------- epilogue
+    const int ew = warp - kEpiWarp0;
+    const int q = warp & 3;    // tensor-memory lane quarter
+    const int half = ew >> 2;  // column half of the tile
+    uint8_t *blk = smem_out + ew * kOutBlockBytes;
+    const uint32_t leader_empty[2] = {pair::map_to_rank(&s.acc_empty[0], 0), pair::map_to_rank(&s.acc_empty[1], 0)};
+    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+    const int xs = lane & 7;  // the 128-byte swizzle of this lane's row
+    uint32_t tiles = 0;
+    bool stop = false;
+    for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
+      const TileBf tl = tile_bf<K>(p, tab, t, rank);
+      const int c0 = tl.col0 + half * 128;
+      const int warp_rows = tl.rows_valid - 32 * q;
+      const bool wanted = warp_rows > 0 && c0 < p.n;
+      const bool empty = K == KindBf::kWgrad && tl.nk == 0;
+      const uint32_t b = tiles & 1;
+      if (!empty) {
+        stop = warp_any(!mbar_wait(&s.acc_full[b], (tiles >> 1) & 1, abort_flag, p.status));
+        if (stop) break;
+        tc_fence_after();
+        ++tiles;
+      }
+      const int64_t out_row = (K == KindBf::kWgrad ? tl.e * p.m : int64_t(0)) + tl.row0 + 32 * q;
+      const bool fp32 = K == KindBf::kWgrad && p.out_fp32;
+      const bool add = fp32 && p.accumulate;
+      const int wide = fp32 ? 32 : 64;  // columns of a staging block
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair::arrive_remote_relaxed(leader_empty[b]);
+      };
+      if (!empty && !wanted) release();
+      if (!wanted || (empty && add)) continue;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[2][32];
+        if (!empty) {
+          tmem_ld_32x32(tq + b * kBN + 64 * c, v[0]);
+          tmem_ld_32x32(tq + b * kBN + 64 * c + 32, v[1]);
+          tmem_wait_ld_for(v[0]);
+          tmem_wait_ld_for(v[1]);
+          if (c == 1) release();  // registers hold the data
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0;
+        }
+        // one block of 64 bf16 columns, or two of 32 fp32
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !fp32) break;
+          const int col = c0 + 64 * c + 32 * h;
+          if (col >= p.n) break;
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          uint4 *row = reinterpret_cast<uint4 *>(blk + lane * 128);
+          if (fp32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              row[j ^ xs] = make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int at = 8 * (j & 3) + 2 * i;
+                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[j >> 2][at]), __uint_as_float(v[j >> 2][at + 1]));
+                w[i] = *reinterpret_cast<const uint32_t *>(&x);
+              }
+              row[j ^ xs] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          // A whole block leaves by a bulk store; rows cut by the expert's end or columns by the output's, and sums
+          // added to dW, by plain ones.
+          const bool bulk = !add && warp_rows >= 32 && col + wide <= p.n;
+          if (bulk) fence_proxy_async_shared();
+          __syncwarp();
+          if (bulk) {
+            if (lane == 0) {
+              tma_store_2d(&p.map_y, col, static_cast<int32_t>(out_row), blk);
+              bulk_commit();
+            }
+          } else {
+            if (add)
+              store_rows<float, true>(static_cast<float *>(p.y), p.n, out_row, col, warp_rows, blk, lane);
+            else if (fp32)
+              store_rows<float, false>(static_cast<float *>(p.y), p.n, out_row, col, warp_rows, blk, lane);
+            else
+              store_rows<__nv_bfloat16, false>(static_cast<__nv_bfloat16 *>(p.y), p.n, out_row, col, warp_rows, blk, lane);
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  pair::cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    pair::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------- forward, few rows an expert --
+// The same sums with the operands exchanged: an item is 128 rows of W_e (the MMA's M) and up to 64
+// of the expert's tokens (its N, in steps of 16), one CTA an item, two CTAs an SM.  With few tokens the time is that of
+// reading the weights once, and 256-row token tiles would leave all but a few rows of the MMAs
+// empty and put the weights on half as many SMs.  A sum's steps over k are those of the tiles above, in the same
+// order: a row's bits are the same in both forms.
+//   warp 0 producer, warp 1 MMA issuer, warps 2-5 epilogue (thread = row of W).
+constexpr int kFewTokens = 64;
+constexpr int kFewStages = 4;
+constexpr int kFewThreads = 192;
+constexpr int kFewBBytes = kFewTokens * 128;
+constexpr int kFewStageBytes = kABytes + kFewBBytes;
+constexpr uint32_t kFewTmemCols = 2 * kFewTokens;
+
+struct SharedFew {
+  uint64_t full[kFewStages];
+  uint64_t freed[kFewStages];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int ok_flag;
+};
+
+__device__ __forceinline__ void mma_stage_own(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate, uint64_t *freed) {
+  asm volatile(
+      "{\n\t.reg .pred z, o;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.u32 z, %5, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, o;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, o;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, o;\n\t"
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+      "}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(smem_u32(freed)), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_own(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+struct ItemFew {
+  int32_t e;
+  int32_t row0;    // first token row
+  int32_t tokens;  // 1 .. 64
+  int32_t n0;      // first row of W_e = output column
+};
+__device__ __forceinline__ ItemFew item_few(const LaunchBf16 &p, const Tables &s, uint32_t t) {
+  const uint32_t nb = (static_cast<uint32_t>(p.n) + kBM - 1) / kBM;
+  const uint32_t g = t / nb;
+  ItemFew it;
+  it.n0 = static_cast<int32_t>((t - g * nb) * kBM);
+  it.e = find_group(s.aux, p.num_experts, g);
+  const int32_t first = (static_cast<int32_t>(g) - s.aux[it.e]) * kFewTokens;
+  it.row0 = s.off[it.e] + first;
+  it.tokens = min(kFewTokens, s.off[it.e + 1] - s.off[it.e] - first);
+  return it;
+}
+
+__global__ void __launch_bounds__(kFewThreads, 2) gemm_bf16_few_kernel(const __grid_constant__ LaunchBf16 p) {
+  __shared__ SharedFew s;
+  extern __shared__ uint8_t dyn_smem[];
+  constexpr uint32_t S = kFewStages;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem_a = smem;
+  uint8_t *smem_b = smem_a + S * kABytes;
+  int32_t *gmem = reinterpret_cast<int32_t *>(smem + S * kFewStageBytes);
+  const Tables tab{gmem, gmem + (p.num_experts + 1)};
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem_base)),
+                 "r"(kFewTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (threadIdx.x == 64) {
+    for (uint32_t i = 0; i < S; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.freed[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 4);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    prefetch_tensormap(&p.map_a);
+    prefetch_tensormap(&p.map_b);
+  }
+  start_next_kernel();
+  wait_for_previous_kernel();
+  if (warp == 0) {
+    const int32_t total = scan_groups(p.offsets, p.num_experts, p.rows, kFewTokens,
+                                      [&](int g, int32_t lo, int32_t, int32_t first) {
+                                        tab.off[g] = lo;
+                                        tab.aux[g] = first;
+                                      });
+    if (lane == 0) {
+      tab.off[p.num_experts] = static_cast<int32_t>(p.rows);
+      tab.aux[p.num_experts] = total;
+      s.ok_flag = total >= 0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  volatile int *abort_flag = &s.abort_flag;
+  const int nk = static_cast<int>((p.k + kStageK - 1) / kStageK);
+  const uint32_t nb = static_cast<uint32_t>((p.n + kBM - 1) / kBM);
+  // malformed offsets: no item, straight to the end
+  const uint32_t total = s.ok_flag ? static_cast<uint32_t>(tab.aux[p.num_experts]) * nb : 0;
+  if (!s.ok_flag && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- producer
+      uint32_t stage = 0, filled = 0;
+      bool stop = false;
+      for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
+        const ItemFew it = item_few(p, tab, t);
+        const int groups = (it.tokens + 15) >> 4;
+        for (int i = 0; i < nk; ++i) {
+          if (!mbar_wait<true>(&s.freed[stage], ((filled / S) & 1) ^ 1, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&s.full[stage], kABytes + groups * 16 * 128);
+          tma_load_3d_own(smem_a + stage * kABytes, &p.map_a, &s.full[stage], i * kStageK, it.n0, it.e);
+          for (int j = 0; j < groups; ++j)
+            tma_load_2d_own(smem_b + stage * kFewBBytes + j * 16 * 128, &p.map_b, &s.full[stage], i * kStageK,
+                            it.row0 + 16 * j);
+          ++filled;
+          if (++stage == S) stage = 0;
+        }
+      }
+      // every copy has landed before the CTA can exit
+      for (uint32_t j = 0; j < S && j < filled; ++j) {
+        const uint32_t f = j + S * ((filled - 1 - j) / S);
+        mbar_drain(&s.full[j], (f / S) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------- MMA issuer (whole warp)
+    const uint64_t a_desc = desc_sw128(smem_u32(smem_a), false), b_desc = desc_sw128(smem_u32(smem_b), false);
+    uint32_t stage = 0, phase = 0, items = 0;
+    bool stop = false;
+    for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x, ++items) {
+      const uint32_t cols = (item_few(p, tab, t).tokens + 15) & ~15;
+      const uint32_t idesc = idesc_bf16(false, false, 128, cols);
+      const uint32_t b = items & 1;
+      stop = warp_any(!mbar_wait(&s.acc_empty[b], ((items >> 1) & 1) ^ 1, abort_flag, p.status));
+      for (int i = 0; i < nk && !stop; ++i) {
+        stop = warp_any(!mbar_wait(&s.full[stage], phase, abort_flag, p.status));
+        if (stop) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_stage_own(tmem + b * kFewTokens, a_desc + stage * (kABytes / 16), b_desc + stage * (kFewBBytes / 16), idesc,
+                        i > 0, &s.freed[stage]);
+          if (i == nk - 1) commit_own(&s.acc_full[b]);
+        }
+        __syncwarp();
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+    if (elect_one()) {
+      commit_own(&s.drain);
+      mbar_drain(&s.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // tensor-memory lane quarter
+    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t items = 0;
+    bool stop = false;
+    for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x, ++items) {
+      const ItemFew it = item_few(p, tab, t);
+      const uint32_t b = items & 1;
+      stop = warp_any(!mbar_wait(&s.acc_full[b], (items >> 1) & 1, abort_flag, p.status));
+      if (stop) break;
+      tc_fence_after();
+      const int64_t col = it.n0 + q * 32 + lane;
+      __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + static_cast<int64_t>(it.row0) * p.n + col;
+#pragma unroll
+      for (int c = 0; c < kFewTokens / 16; ++c) {
+        if (16 * c < it.tokens) {
+          uint32_t v[16];
+          tmem_ld_32x16(tq + b * kFewTokens + 16 * c, v);
+          tmem_wait_ld_for(v);
+          if (col < p.n) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (16 * c + j < it.tokens) y[(16 * c + j) * p.n] = __float2bfloat16_rn(__uint_as_float(v[j]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.acc_empty[b]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFewTmemCols) : "memory");
+}
+
+template <KindBf K>
+cudaError_t launch_bf(LaunchBf16 a) {
+  auto kernel = gemm_bf16_kernel<K>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
+  if (err != cudaSuccess) return err;
+  const int rest = 1024 + 8 * kOutBlockBytes + 8 * (a.num_experts + 1);
+  // as many stages as fit beside the expert tables
+  a.stages = std::min<int64_t>(kMaxStagesBf, (kGemmSmemLimit - rest) / kStageBytesBf);
+  const int64_t nb = (a.n + kBN - 1) / kBN;
+  const int64_t bound = K == KindBf::kWgrad ? a.num_experts * ((a.m + kPairM - 1) / kPairM) * nb
+                                            : (a.m / kPairM + std::min<int64_t>(a.num_experts, a.m)) * nb;
+  int64_t pairs = a.num_sms / 2;
+  if (bound < pairs) pairs = bound;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(kThreadsBf, 1, 1);
+  cfg.dynamicSmemBytes = rest + a.stages * kStageBytesBf;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+cudaError_t launch_few(const LaunchBf16 &a) {
+  const int smem = 1024 + kFewStages * kFewStageBytes + 8 * (a.num_experts + 1);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_shared(reinterpret_cast<const void *>(gemm_bf16_few_kernel), allowed);
+  if (err != cudaSuccess) return err;
+  const int64_t items = (a.m / kFewTokens + std::min<int64_t>(a.num_experts, a.m)) * ((a.n + kBM - 1) / kBM);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(2 * a.num_sms, items)), 1, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_bf16_few_kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_bf16_fwd(const LaunchBf16 &a) {
+  return bf16_few_rows(a.m, a.num_experts) ? launch_few(a) : launch_bf<KindBf::kFwd>(a);
+}
+cudaError_t launch_bf16_dgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kDgrad>(a); }
+cudaError_t launch_bf16_wgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kWgrad>(a); }
+
+}  // namespace fme

@@ -566,6 +566,33 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
                                            int32_t *dev_status, void *stream);
 
 /*
+ * grouped_gemm_fwd_bf16 -- Y[t, n] = sum_k x[t, k] w[e, n, k] for every row t of expert e, on bf16 operands (layers
+ * that stay in bf16, and what the low-precision products are compared with: "Scaling and Optimizing Frontier Model
+ * Training", "MXFP8 expert kernels").  Products and sums in fp32 on the tensor cores over the whole
+ * contraction, one rounding to bf16.  No split over k: a row's output does not depend on any other row, whatever the
+ * number of rows.
+ *
+ *   x         device bf16 [m x k], the rows grouped by expert (moe_permute)
+ *   w         device bf16 [num_experts][n][k]
+ *   offsets   device int32 [num_experts + 1], rows per expert, rising from 0 to m (otherwise FME_DEV_BAD_OFFSETS and y
+ *             is not written)
+ *   m, n, k   n and k multiples of 8, 8 .. 65536
+ *   y         device bf16 [m x n]
+ */
+fme_status grouped_gemm_fwd_bf16(const void *x, const void *w, const int32_t *offsets, int32_t num_experts, int64_t m,
+                                 int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream);
+
+/* grouped_gemm_dgrad_bf16 -- dX[t, :] = dY[t, :] W_e; dy bf16 [m x n], dx bf16 [m x k], w as the forward's. */
+fme_status grouped_gemm_dgrad_bf16(const void *dy, const void *w, const int32_t *offsets, int32_t num_experts, int64_t m,
+                                   int64_t n, int64_t k, void *dx, int32_t *dev_status, void *stream);
+
+/* grouped_gemm_wgrad_bf16 -- dW_e = dY_e^T X_e over the rows of expert e; dy bf16 [m x n], x bf16 [m x k], grouped with
+ * the same offsets, no padding between experts.  dw, dw_mode as grouped_gemm_wgrad_fp8_block128's: bf16, fp32, or added
+ * into fp32, one unfused add an element.  An expert with no rows gets zeros (nothing is added). */
+fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, const int32_t *offsets, int32_t num_experts,
+                                   int64_t n, int64_t k, void *dw, int32_t dw_mode, int32_t *dev_status, void *stream);
+
+/*
  * moe_gate -- the top_k experts of each token and their weights, from router logits.
  *
  * key[t, e] = fl32(logits[t, e] + bias[e]); ids[t, :] = the top_k largest keys, largest first,
