@@ -88,7 +88,7 @@ fme_status encode_map(const char *what, CUtensorMap *map, CUtensorMapDataType ty
   EncodeTiledFn fn;
   const fme_status st = get_encoder(&fn);
   if (st != FME_OK) return st;
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = CUDA_SUCCESS;
   for (int tries = 0; tries < 2; ++tries) {
     r = fn(map, type, rank, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
@@ -921,6 +921,20 @@ fme_status encode_bf16_weights(CUtensorMap *map, const void *base, uint64_t expe
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// MN-major operands, 64 rows x 128 columns: with whole groups of 64 columns, one box that gives them as two of 64 columns
+// one after the other ([experts][cols / 64][rows][64]); otherwise boxes of 64 columns, cut at the row's end.  `experts`
+// 0: a matrix without that dimension.
+fme_status encode_bf16_mn(CUtensorMap *map, bool *wide, const void *base, uint64_t experts, uint64_t rows, uint64_t cols) {
+  *wide = cols % 64 == 0;
+  if (!*wide)
+    return experts ? encode_bf16_weights(map, base, experts, rows, cols, 64) : encode_bf16_2d(map, base, rows, cols, 64);
+  cuuint64_t dims[4] = {64, rows, cols / 64, experts};
+  cuuint64_t strides[3] = {cols * 2, 128, rows * cols * 2};
+  cuuint32_t box[4] = {64, 64, 2, 1};
+  return encode_map(" (columns)", map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, experts ? 4 : 3, const_cast<void *>(base), dims,
+                    strides, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 // The forward (out = n columns, contraction k) and dgrad (out = k columns, contraction n).
 fme_status bf16_rows_gemm(bool dgrad, const void *a_rows, const void *w, const int32_t *offsets, int32_t num_experts,
                           int64_t m, int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream,
@@ -942,7 +956,9 @@ fme_status bf16_rows_gemm(bool dgrad, const void *a_rows, const void *w, const i
   const bool few = !dgrad && fme::bf16_few_rows(m, num_experts);
   CUtensorMap &rows_map = few ? a.map_b : a.map_a, &w_map = few ? a.map_a : a.map_b;
   if ((st = encode_bf16_2d(&rows_map, a_rows, m, a.k, few ? 16 : 128)) != FME_OK) return st;
-  if ((st = encode_bf16_weights(&w_map, w, num_experts, n, k, dgrad ? 64 : 128)) != FME_OK) return st;
+  st = dgrad ? encode_bf16_mn(&w_map, &a.wide_b, w, num_experts, n, k)
+             : encode_bf16_weights(&w_map, w, num_experts, n, k, 128);
+  if (st != FME_OK) return st;
   if ((st = encode_bf16_out(&a.map_y, y, a.n, m, OutBox::kWideBf16)) != FME_OK) return st;
   a.offsets = offsets;
   a.num_experts = num_experts;
@@ -986,15 +1002,12 @@ fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, con
   // without rows every expert is empty and the operands' maps are never used
   const void *abase = m ? dy : dw, *bbase = m ? x : dw;
   const int64_t extent = m ? m : 1;
-  if ((st = encode_bf16_2d(&a.map_a, abase, extent, n, 64)) != FME_OK ||
+  if ((st = encode_bf16_mn(&a.map_a, &a.wide_a, abase, 0, extent, n)) != FME_OK ||
       (st = encode_bf16_2d(&a.map_a8, abase, extent, n, 8)) != FME_OK ||
       (st = encode_bf16_2d(&a.map_a1, abase, extent, n, 1)) != FME_OK ||
-      (st = encode_bf16_2d(&a.map_b, bbase, extent, k, 64)) != FME_OK ||
+      (st = encode_bf16_mn(&a.map_b, &a.wide_b, bbase, 0, extent, k)) != FME_OK ||
       (st = encode_bf16_2d(&a.map_b8, bbase, extent, k, 8)) != FME_OK ||
       (st = encode_bf16_2d(&a.map_b1, bbase, extent, k, 1)) != FME_OK)
-    return st;
-  if ((st = encode_bf16_out(&a.map_y, dw, k, static_cast<uint64_t>(num_experts) * n,
-                            dw_mode == FME_DW_BF16 ? OutBox::kWideBf16 : OutBox::kWideFp32)) != FME_OK)
     return st;
   a.offsets = offsets;
   a.num_experts = num_experts;

@@ -175,13 +175,14 @@ cudaError_t launch_block128_wgrad(const LaunchBlock128 &a);
 struct LaunchBf16 {
   CUtensorMap map_a, map_b;                      // operands, 128-byte swizzle
   CUtensorMap map_a8, map_a1, map_b8, map_b1;    // wgrad: the same in boxes of 8 rows and of one
-  CUtensorMap map_y;                             // output, boxes of 32 rows x 128 bytes, 128-byte swizzle
+  CUtensorMap map_y;                             // output (not wgrad's), boxes of 32 rows x 128 bytes, 128-byte swizzle
   const int32_t *offsets;  // rows of each expert
   int32_t num_experts;
   int64_t rows;     // rows of all experts
   int64_t m, n, k;  // output rows (wgrad: of one expert) and columns; contraction (not wgrad)
   void *y;
   bool out_fp32, accumulate;  // wgrad
+  bool wide_a, wide_b;        // MN-major operands: the map gives 128 columns as two of 64 in one box
   int32_t *status;
   int num_sms;
   int stages;  // operand ring depth, set by the launcher
