@@ -480,16 +480,23 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
 // reading the weights once, and 256-row token tiles would leave all but a few rows of the MMAs
 // empty and put the weights on half as many SMs.  A sum's steps over k are those of the tiles above, in the same
 // order: a row's bits are the same in both forms.
-//   warp 0 producer, warp 1 MMA issuer, warps 2-5 epilogue (thread = row of W).
+//   warp 0 producer of W, warp 1 MMA issuer, warps 2-5 epilogue (thread = row of W), warp 6 producer of the tokens.
+// A stage holds 128 of k, as two halves of 64: what bounds a CTA that has an SM to itself is the producer's and the
+// issuer's way around their loops (4096 x 7168, one expert with one row, 32 CTAs: 28 us with 64 of k in nine stages, 21 with
+// 128 in four; 8 of 32 experts, 256 CTAs, 72.8 and 72.3).
 constexpr int kFewTokens = 64;
-constexpr int kFewStages = 9;
-constexpr int kFewThreads = 192;
-constexpr int kFewBBytes = kFewTokens * 128;
-constexpr int kFewStageBytes = kABytes + kFewBBytes;
+constexpr int kFewStages = 4;
+constexpr int kFewThreads = 224;
+constexpr int kFewTokenWarp = 6;
+constexpr int kFewHalfB = kFewTokens * 128;
+constexpr int kFewABytes = 2 * kABytes;
+constexpr int kFewBBytes = 2 * kFewHalfB;
+constexpr int kFewStageBytes = kFewABytes + kFewBBytes;
 constexpr uint32_t kFewTmemCols = 2 * kFewTokens;
 
 struct SharedFew {
-  uint64_t full[kFewStages];
+  uint64_t full[kFewStages];    // W's copies
+  uint64_t full_b[kFewStages];  // the tokens' copies
   uint64_t freed[kFewStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
@@ -499,20 +506,20 @@ struct SharedFew {
   int ok_flag;
 };
 
-__device__ __forceinline__ void mma_stage_own(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate, uint64_t *freed) {
+// 64 of the contraction: four K = 16 steps on one CTA (M = 128), both operands K-major.
+__device__ __forceinline__ void mma_half_own(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred z, o;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "setp.ne.u32 z, %5, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
+      "setp.ne.u32 z, %4, 0;\n\tsetp.eq.u32 o, 0, 0;\n\t"
       "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
       "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, z;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, o;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, o;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, o;\n\t"
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
       "}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(smem_u32(freed)), "r"(accumulate)
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void commit_own(uint64_t *bar) {
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
   constexpr uint32_t S = kFewStages;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   uint8_t *smem_a = smem;
-  uint8_t *smem_b = smem_a + S * kABytes;
+  uint8_t *smem_b = smem_a + S * kFewABytes;
   int32_t *gmem = reinterpret_cast<int32_t *>(smem + S * kFewStageBytes);
   const Tables tab{gmem, gmem + (p.num_experts + 1)};
   const int warp = threadIdx.x >> 5;
@@ -558,6 +565,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
   } else if (threadIdx.x == 64) {
     for (uint32_t i = 0; i < S; ++i) {
       mbar_init(&s.full[i], 1);
+      mbar_init(&s.full_b[i], 1);
       mbar_init(&s.freed[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -590,39 +598,73 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   volatile int *abort_flag = &s.abort_flag;
-  const int nk = static_cast<int>((p.k + kStageK - 1) / kStageK);
+  const int halves = static_cast<int>((p.k + kStageK - 1) / kStageK);
   const uint32_t nb = static_cast<uint32_t>((p.n + kBM - 1) / kBM);
   // malformed offsets: no item, straight to the end
   const uint32_t total = s.ok_flag ? static_cast<uint32_t>(tab.aux[p.num_experts]) * nb : 0;
   if (!s.ok_flag && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
 
+  // every copy of a producer has landed before the CTA can exit
+  auto drain = [](uint64_t *bars, uint32_t filled) {
+    for (uint32_t j = 0; j < S && j < filled; ++j) {
+      const uint32_t f = j + S * ((filled - 1 - j) / S);
+      mbar_drain(&bars[j], (f / S) & 1);
+    }
+  };
   if (warp == 0) {
     if (lane == 0) {
-      // -------------------------------------------------------------- producer
-      uint32_t stage = 0, filled = 0;
+      // ---------------------------------------------- producer of W
+      uint32_t stage = 0, phase = 1, filled = 0;
       bool stop = false;
       for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
         const ItemFew it = item_few(p, tab, t);
-        const int groups = (it.tokens + 15) >> 4;
-        for (int i = 0; i < nk; ++i) {
-          if (!mbar_wait<true>(&s.freed[stage], ((filled / S) & 1) ^ 1, abort_flag, p.status)) {
+        for (int i = 0; i < halves; i += 2) {
+          if (!mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status)) {
             stop = true;
             break;
           }
-          mbar_arrive_expect_tx(&s.full[stage], kABytes + groups * 16 * 128);
-          tma_load_3d_own(smem_a + stage * kABytes, &p.map_a, &s.full[stage], i * kStageK, it.n0, it.e);
-          for (int j = 0; j < groups; ++j)
-            tma_load_2d_own(smem_b + stage * kFewBBytes + j * 16 * 128, &p.map_b, &s.full[stage], i * kStageK,
-                            it.row0 + 16 * j);
+          uint8_t *a = smem_a + stage * kFewABytes;
+          const bool both = i + 1 < halves;
+          mbar_arrive_expect_tx(&s.full[stage], both ? 2 * kABytes : kABytes);
+          tma_load_3d_own(a, &p.map_a, &s.full[stage], i * kStageK, it.n0, it.e);
+          if (both) tma_load_3d_own(a + kABytes, &p.map_a, &s.full[stage], (i + 1) * kStageK, it.n0, it.e);
           ++filled;
-          if (++stage == S) stage = 0;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
-      // every copy has landed before the CTA can exit
-      for (uint32_t j = 0; j < S && j < filled; ++j) {
-        const uint32_t f = j + S * ((filled - 1 - j) / S);
-        mbar_drain(&s.full[j], (f / S) & 1);
+      drain(s.full, filled);
+    }
+  } else if (warp == kFewTokenWarp) {
+    if (lane == 0) {
+      // ---------------------------------------------- producer of the tokens
+      uint32_t stage = 0, phase = 1, filled = 0;
+      bool stop = false;
+      for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
+        const ItemFew it = item_few(p, tab, t);
+        const uint32_t bytes = ((it.tokens + 15) >> 4) * 16 * 128;  // of a half
+        for (int i = 0; i < halves; i += 2) {
+          if (!mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          uint8_t *b = smem_b + stage * kFewBBytes;
+          const bool both = i + 1 < halves;
+          mbar_arrive_expect_tx(&s.full_b[stage], both ? 2 * bytes : bytes);
+          for (int j = 0; j < it.tokens; j += 16) {
+            tma_load_2d_own(b + j * 128, &p.map_b, &s.full_b[stage], i * kStageK, it.row0 + j);
+            if (both) tma_load_2d_own(b + kFewHalfB + j * 128, &p.map_b, &s.full_b[stage], (i + 1) * kStageK, it.row0 + j);
+          }
+          ++filled;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
       }
+      drain(s.full_b, filled);
     }
   } else if (warp == 1) {
     // -------------------------------------------------- MMA issuer (whole warp)
@@ -634,14 +676,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
       const uint32_t idesc = idesc_bf16(false, false, 128, cols);
       const uint32_t b = items & 1;
       stop = warp_any(!mbar_wait(&s.acc_empty[b], ((items >> 1) & 1) ^ 1, abort_flag, p.status));
-      for (int i = 0; i < nk && !stop; ++i) {
-        stop = warp_any(!mbar_wait(&s.full[stage], phase, abort_flag, p.status));
+      for (int i = 0; i < halves && !stop; i += 2) {
+        stop = warp_any(!mbar_wait(&s.full[stage], phase, abort_flag, p.status) ||
+                        !mbar_wait(&s.full_b[stage], phase, abort_flag, p.status));
         if (stop) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_stage_own(tmem + b * kFewTokens, a_desc + stage * (kABytes / 16), b_desc + stage * (kFewBBytes / 16), idesc,
-                        i > 0, &s.freed[stage]);
-          if (i == nk - 1) commit_own(&s.acc_full[b]);
+          const uint64_t ad = a_desc + stage * (kFewABytes / 16), bd = b_desc + stage * (kFewBBytes / 16);
+          mma_half_own(tmem + b * kFewTokens, ad, bd, idesc, i > 0);
+          if (i + 1 < halves) mma_half_own(tmem + b * kFewTokens, ad + kABytes / 16, bd + kFewHalfB / 16, idesc, 1);
+          commit_own(&s.freed[stage]);
+          if (i + 2 >= halves) commit_own(&s.acc_full[b]);
         }
         __syncwarp();
         if (++stage == S) {
