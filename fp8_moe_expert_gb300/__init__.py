@@ -114,6 +114,13 @@ SYMBOLS = {
     "grouped_gemm_fwd_bf16": ("i32", ["p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
     "grouped_gemm_dgrad_bf16": ("i32", ["p", "p", "p", "i32", "i64", "i64", "i64", "p", "p", "p"]),
     "grouped_gemm_wgrad_bf16": ("i32", ["p", "p", "i64", "p", "i32", "i64", "i64", "p", "i32", "p", "p"]),
+    "grouped_gemv_nvfp4": ("i32", ["p", "i64", "p", "i32", "p", "p", "p", "p", "i32", "i64", "i64", "i64", "p", "p",
+                                   "p"]),
+    "grouped_gemv_nvfp4_swiglu": ("i32", ["p", "i64", "p", "i32", "p", "p", "p", "p", "i32", "i64", "i64", "i64", "p",
+                                          "p", "p"]),
+    "swiglu": ("i32", ["p", "i64", "i64", "p", "p"]),
+    "swiglu_backward": ("i32", ["p", "p", "i64", "i64", "p", "p"]),
+    "moe_permute": ("i32", ["p", "i64", "i64", "p", "i32", "p", "p", "p"]),
     "moe_gate": ("i32", ["p", "i32", "i64", "i32", "i32", "i32", "i32", "f32", "p", "p", "p", "p"]),
     "moe_gate_backward": ("i32", ["p", "i32", "p", "p", "i64", "i32", "i32", "i32", "i32", "f32", "p", "p", "p"]),
     "moe_balance_loss": ("i32", ["p", "i32", "p", "i64", "i32", "i32", "i32", "f32", "p", "i64", "p", "p", "p", "p",
@@ -659,6 +666,37 @@ def grouped_gemm_wgrad_bf16(dy, x, offsets, *, dw=None, dtype=None, accumulate=F
     (default) or float32; with accumulate the result is added into dw (float32)."""
     mode = _dw_mode("grouped_gemm_wgrad_bf16", dw, dtype, accumulate)
     return _bind().wgrad_bf16(dy, x, offsets, dw, mode, status, _raw(stream))
+
+
+def moe_permute(x, src_row, top_k, *, out=None, status=None, stream=None):
+    """The bf16 rows x[src_row // top_k] in grouped order -> out [tokens*top_k, n]; src_row int32 from moe_route.  Its
+    gradient is moe_combine of the rows' gradients with weights 1."""
+    return _bind().permute(x, src_row, top_k, out, status, _raw(stream))
+
+
+def swiglu(gate_up, *, h=None, stream=None):
+    """h [rows, inter] = silu(g) * u of gate_up [rows, 2*inter] = [g | u] (bf16): the h of swiglu_quantize_nvfp4."""
+    return _bind().swiglu(gate_up, h, _raw(stream))
+
+
+def swiglu_backward(gate_up, dh, *, d_gate_up=None, stream=None):
+    """The gradient of swiglu for dh [rows, inter] -> d_gate_up [rows, 2*inter] (bf16)."""
+    return _bind().swiglu_backward(gate_up, dh, d_gate_up, _raw(stream))
+
+
+# ------------------------------------------------- NVFP4 weights, few rows --
+def grouped_gemv_nvfp4(x, w_codes, w_sf, w_scale, offsets, *, src_row=None, top_k=1, y=None, status=None, stream=None):
+    """Y [m, n] (bf16) = X_e W_e^T per expert for few bf16 rows and NVFP4 weights: w_codes [E*n, k/2], w_sf and w_scale
+    [E*n] from quantize_nvfp4_pertoken of W [E*n, k] as one group; x [m, k], or with src_row (int32 [tokens*top_k], from
+    moe_route) the rows x[src_row // top_k] of x [tokens, k].  k is a multiple of 64."""
+    return _bind().gemv(x, w_codes, w_sf, w_scale, offsets, src_row, top_k, y, status, _raw(stream))
+
+
+def grouped_gemv_nvfp4_swiglu(x, w_codes, w_sf, w_scale, offsets, *, src_row=None, top_k=1, h=None, status=None,
+                              stream=None):
+    """grouped_gemv_nvfp4 of the gate/up weights with the activation: h [m, n/2] = silu(gate) * up (bf16), gate and up the
+    first and last n/2 rows of each expert's weights, not rounded in between.  n is a multiple of 256."""
+    return _bind().gemv_swiglu(x, w_codes, w_sf, w_scale, offsets, src_row, top_k, h, status, _raw(stream))
 
 
 # ------------------------------------------------------------------- router --

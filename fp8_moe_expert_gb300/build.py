@@ -25,8 +25,8 @@ BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quant_nvfp4.cu", "quant_mxfp8.cu", "gemm.cu", "gemm_nvfp4.cu", "route.cu",
            "quant_block128.cu", "gemm_block128.cu", "gemm_bf16.cu",
-           "gate.cu"]
-HEADERS = ["fme_device.cuh", "fme_launch.h", "gemm_common.cuh", "block128.cuh", "gemm_tiles.cuh"]
+           "gemv_nvfp4.cu", "activation.cu", "gate.cu"]
+HEADERS = ["fme_device.cuh", "fme_launch.h", "gemm_common.cuh", "block128.cuh", "gemm_tiles.cuh", "swiglu.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]

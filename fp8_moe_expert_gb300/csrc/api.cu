@@ -1023,6 +1023,113 @@ fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, con
   return err == cudaSuccess ? FME_OK : cuda_fail(err, "grouped_gemm_wgrad_bf16 launch");
 }
 
+// ----------------------------------------------- NVFP4 weights, few bf16 rows --
+namespace {
+
+fme_status gemv_nvfp4(bool swiglu, const void *x, int64_t x_rows, const int32_t *src_row, int32_t top_k,
+                      const uint8_t *w_codes, const uint8_t *w_sf, const float *w_scale, const int32_t *offsets,
+                      int32_t num_experts, int64_t m, int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream,
+                      const char *what) {
+  if (m < 0 || n < 0 || k < 0 || x_rows < 0 || check_groups(num_experts) != FME_OK) return FME_ERR_INVALID_ARGUMENT;
+  if (top_k < 1 || top_k > 64) return FME_ERR_INVALID_ARGUMENT;
+  if (x_rows > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (src_row ? m != x_rows * top_k : m != x_rows || top_k != 1) return FME_ERR_INVALID_ARGUMENT;
+  if (k % 64 != 0 || k < 64 || k > 8192 || n < 1 || n > 65536 || (swiglu && n % 256 != 0)) return FME_ERR_UNSUPPORTED_SHAPE;
+  // the number of items, of 8 rows and 32 weight rows at least, stays in 32 bits
+  if (m > (int64_t(1) << 31) - 1 - 256 || (m / 8 + num_experts) * ((n + 254) / 128) * 4 > (int64_t(1) << 31) - 1)
+    return FME_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets) return FME_ERR_INVALID_ARGUMENT;
+  if (m == 0) return FME_OK;
+  if (!x || !w_codes || !w_sf || !w_scale || !y) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(x) || !aligned16(src_row) || !aligned16(w_codes) || !aligned16(w_sf) || !aligned16(w_scale) ||
+      !aligned16(y) || !aligned16(offsets))
+    return FME_ERR_MISALIGNED;
+  fme::LaunchGemv a{};
+  fme_status st = current_device(&a.num_sms);
+  if (st != FME_OK) return st;
+  a.x = x;
+  a.x_rows = x_rows;
+  a.src_row = src_row;
+  a.top_k = top_k;
+  a.codes = w_codes;
+  a.sf = w_sf;
+  a.scale = w_scale;
+  a.offsets = offsets;
+  a.num_experts = num_experts;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  a.swiglu = swiglu;
+  a.y = y;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t err = fme::launch_gemv_nvfp4(a);
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, what);
+}
+
+}  // namespace
+
+fme_status grouped_gemv_nvfp4(const void *x, int64_t x_rows, const int32_t *src_row, int32_t top_k,
+                              const uint8_t *w_codes, const uint8_t *w_sf, const float *w_scale, const int32_t *offsets,
+                              int32_t num_experts, int64_t m, int64_t n, int64_t k, void *y, int32_t *dev_status,
+                              void *stream) {
+  return gemv_nvfp4(false, x, x_rows, src_row, top_k, w_codes, w_sf, w_scale, offsets, num_experts, m, n, k, y, dev_status,
+                    stream, "grouped_gemv_nvfp4 launch");
+}
+
+fme_status grouped_gemv_nvfp4_swiglu(const void *x, int64_t x_rows, const int32_t *src_row, int32_t top_k,
+                                     const uint8_t *w_codes, const uint8_t *w_sf, const float *w_scale,
+                                     const int32_t *offsets, int32_t num_experts, int64_t m, int64_t n, int64_t k, void *h,
+                                     int32_t *dev_status, void *stream) {
+  return gemv_nvfp4(true, x, x_rows, src_row, top_k, w_codes, w_sf, w_scale, offsets, num_experts, m, n, k, h, dev_status,
+                    stream, "grouped_gemv_nvfp4_swiglu launch");
+}
+
+// ------------------------------------------------- SwiGLU and grouping in bf16 --
+namespace {
+
+fme_status swiglu_bf16(const void *gate_up, const void *dh, bool backward, int64_t rows, int64_t inter, void *out,
+                       void *stream, const char *what) {
+  if (rows < 0 || inter < 0) return FME_ERR_INVALID_ARGUMENT;
+  if (inter < 8 || inter > 65536 || inter % 8 != 0 || rows > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (rows * (inter / 8) / 1024 > (int64_t(1) << 31) - 2) return FME_ERR_UNSUPPORTED_SHAPE;  // CTAs
+  if (rows == 0) return FME_OK;
+  if (!gate_up || !out || (backward && !dh)) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(gate_up) || !aligned16(dh) || !aligned16(out)) return FME_ERR_MISALIGNED;
+  int sms = 0;
+  fme_status st = current_device(&sms);
+  if (st != FME_OK) return st;
+  cudaError_t err = fme::launch_swiglu({gate_up, dh, rows, inter, out, static_cast<cudaStream_t>(stream)});
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, what);
+}
+
+}  // namespace
+
+fme_status swiglu(const void *gate_up, int64_t rows, int64_t inter, void *h, void *stream) {
+  return swiglu_bf16(gate_up, nullptr, false, rows, inter, h, stream, "swiglu launch");
+}
+
+fme_status swiglu_backward(const void *gate_up, const void *dh, int64_t rows, int64_t inter, void *d_gate_up,
+                           void *stream) {
+  return swiglu_bf16(gate_up, dh, true, rows, inter, d_gate_up, stream, "swiglu_backward launch");
+}
+
+fme_status moe_permute(const void *x, int64_t tokens, int64_t n, const int32_t *src_row, int32_t top_k, void *out,
+                       int32_t *dev_status, void *stream) {
+  if (tokens < 0 || n < 0 || top_k < 1 || top_k > 64) return FME_ERR_INVALID_ARGUMENT;
+  if (n < 8 || n > 65536 || n % 8 != 0 || tokens > ((int64_t(1) << 31) - 1) / top_k) return FME_ERR_UNSUPPORTED_SHAPE;
+  if (tokens * top_k * (n / 8) / 1024 > (int64_t(1) << 31) - 1 - 64) return FME_ERR_UNSUPPORTED_SHAPE;  // CTAs
+  if (tokens == 0) return FME_OK;
+  if (!x || !src_row || !out) return FME_ERR_INVALID_ARGUMENT;
+  if (!aligned16(x) || !aligned16(src_row) || !aligned16(out)) return FME_ERR_MISALIGNED;
+  int sms = 0;
+  fme_status st = current_device(&sms);
+  if (st != FME_OK) return st;
+  cudaError_t err =
+      fme::launch_permute({x, src_row, tokens, top_k, n, out, dev_status, static_cast<cudaStream_t>(stream)});
+  return err == cudaSuccess ? FME_OK : cuda_fail(err, "moe_permute launch");
+}
+
 // ------------------------------------------------------------------ router --
 namespace {
 

@@ -425,6 +425,87 @@ PyObject *wgrad_bf16(PyObject *const *a) {
   return one(a[3], dw);
 }
 
+// ------------------------------------------- NVFP4 weights, few rows; bf16 rows --
+// x, w_codes, w_sf, w_scale, offsets, src_row, top_k, y or h, status, stream
+template <bool kSwiglu>
+PyObject *gemv(PyObject *const *a) {
+  Call c{kSwiglu ? "grouped_gemv_nvfp4_swiglu" : "grouped_gemv_nvfp4"};
+  const Shape xs = dims(c, "x", a[0], 2);
+  const int64_t x_rows = xs[0], k = xs[1];
+  const int64_t w_rows = dims(c, "w_codes", a[1], 2)[0], e = dims(c, "offsets", a[4], 1)[0] - 1;
+  if (e < 1) throw Refused(std::string(c.where) + ": offsets must have at least 2 elements");
+  if (w_rows % e != 0)
+    throw Refused(std::string(c.where) + ": w_codes must have the same number of rows for each of the " + std::to_string(e) +
+                  " experts, got " + std::to_string(w_rows));
+  const int32_t experts = e > INT32_MAX ? INT32_MAX : static_cast<int32_t>(e);
+  const int64_t n = w_rows / e;
+  const int32_t top_k = integer32(a[6]);
+  const bool gather = a[5] != Py_None;
+  if (!gather && top_k != 1) throw Refused(std::string(c.where) + ": top_k goes with src_row");
+  const int64_t m = gather ? x_rows * top_k : x_rows;
+  const at::Tensor &x = input(c, "x", a[0], kBf16, {x_rows, k});
+  const at::Tensor &codes = input(c, "w_codes", a[1], kU8, {w_rows, k / 2});
+  const int64_t sf_bytes = fme_sf_bytes(w_rows, k, 16, 1);
+  const at::Tensor &sf = tensor(c, "w_sf", a[2]);
+  if (sf.numel() < sf_bytes)
+    throw Refused(std::string(c.where) + ": w_sf must have at least " + std::to_string(sf_bytes) + " bytes, got " +
+                  std::to_string(sf.numel()));
+  need(c, "w_sf", sf, kU8, sf.sizes());
+  const at::Tensor &scale = input(c, "w_scale", a[3], kF32, {w_rows});
+  const at::Tensor &off = input(c, "offsets", a[4], kI32, {e + 1});
+  const int32_t *src = gather ? ptr<int32_t>(input(c, "src_row", a[5], kI32, {m})) : nullptr;
+  int32_t *st = status_ptr(c, a[8]);
+  const OnStream on(c, a[9]);
+  const at::Tensor y = output(c, on, kSwiglu ? "h" : "y", a[7], kBf16, {m, kSwiglu ? n / 2 : n}, x);
+  call(c, [&] {
+    return (kSwiglu ? grouped_gemv_nvfp4_swiglu : grouped_gemv_nvfp4)(
+        ptr(x), x_rows, src, top_k, ptr<uint8_t>(codes), ptr<uint8_t>(sf), ptr<float>(scale), ptr<int32_t>(off), experts, m,
+        n, k, ptr(y), st, on.raw());
+  });
+  return one(a[7], y);
+}
+
+// gate_up, h, stream
+PyObject *act(PyObject *const *a) {
+  Call c{"swiglu"};
+  const Shape s = dims(c, "gate_up", a[0], 2);
+  const int64_t rows = s[0], inter = s[1] / 2;
+  const at::Tensor &gu = input(c, "gate_up", a[0], kBf16, {rows, 2 * inter});
+  const OnStream on(c, a[2]);
+  const at::Tensor h = output(c, on, "h", a[1], kBf16, {rows, inter}, gu);
+  call(c, [&] { return swiglu(ptr(gu), rows, inter, ptr(h), on.raw()); });
+  return one(a[1], h);
+}
+
+// gate_up, dh, d_gate_up, stream
+PyObject *act_backward(PyObject *const *a) {
+  Call c{"swiglu_backward"};
+  const Shape s = dims(c, "gate_up", a[0], 2);
+  const int64_t rows = s[0], inter = s[1] / 2;
+  const at::Tensor &gu = input(c, "gate_up", a[0], kBf16, {rows, 2 * inter});
+  const at::Tensor &dh = input(c, "dh", a[1], kBf16, {rows, inter});
+  const OnStream on(c, a[3]);
+  const at::Tensor d = output(c, on, "d_gate_up", a[2], kBf16, {rows, 2 * inter}, gu);
+  call(c, [&] { return swiglu_backward(ptr(gu), ptr(dh), rows, inter, ptr(d), on.raw()); });
+  return one(a[2], d);
+}
+
+// x, src_row, top_k, out, status, stream
+PyObject *permute(PyObject *const *a) {
+  Call c{"moe_permute"};
+  const Shape s = dims(c, "x", a[0], 2);
+  const int64_t tokens = s[0], n = s[1];
+  const int32_t top_k = integer32(a[2]);
+  const at::Tensor &x = input(c, "x", a[0], kBf16, {tokens, n});
+  if (top_k < 0) throw Refused(std::string(c.where) + ": top_k must not be negative");
+  const at::Tensor &src = input(c, "src_row", a[1], kI32, {tokens * top_k});
+  int32_t *st = status_ptr(c, a[4]);
+  const OnStream on(c, a[5]);
+  const at::Tensor out = output(c, on, "out", a[3], kBf16, {tokens * top_k, n}, x);
+  call(c, [&] { return moe_permute(ptr(x), tokens, n, ptr<int32_t>(src), top_k, ptr(out), st, on.raw()); });
+  return one(a[3], out);
+}
+
 // ---------------------------------------------------------------------- router --
 struct Logits {
   const at::Tensor &t;
@@ -608,6 +689,11 @@ PyMethodDef g_methods[] = {
     method<6, rows_gemm_bf16<false>>("fwd_bf16"),
     method<6, rows_gemm_bf16<true>>("dgrad_bf16"),
     method<7, wgrad_bf16>("wgrad_bf16"),
+    method<10, gemv<false>>("gemv"),
+    method<10, gemv<true>>("gemv_swiglu"),
+    method<3, act>("swiglu"),
+    method<4, act_backward>("swiglu_backward"),
+    method<6, permute>("permute"),
     method<9, gate>("gate"),
     method<9, gate_backward>("gate_backward"),
     method<12, balance_loss>("balance_loss"),

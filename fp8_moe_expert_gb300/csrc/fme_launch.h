@@ -200,6 +200,25 @@ cudaError_t launch_bf16_fwd(const LaunchBf16 &a);
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a);
 cudaError_t launch_bf16_wgrad(const LaunchBf16 &a);
 
+// Few bf16 rows times NVFP4 weights (gemv_nvfp4.cu).
+struct LaunchGemv {
+  const void *x;
+  int64_t x_rows;
+  const int32_t *src_row;  // or NULL
+  int32_t top_k;
+  const uint8_t *codes, *sf;
+  const float *scale;
+  const int32_t *offsets;
+  int32_t num_experts;
+  int64_t m, n, k;
+  bool swiglu;
+  void *y;
+  int32_t *status;
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_gemv_nvfp4(const LaunchGemv &a);
+
 // The router (gate.cu).
 struct LaunchGate {
   const void *logits;  // [tokens x num_experts], bf16 or fp32
@@ -245,6 +264,27 @@ cudaError_t launch_gate(const LaunchGate &a);
 cudaError_t launch_gate_backward(const LaunchGate &a);
 cudaError_t launch_balance_loss(const LaunchBalance &a);
 cudaError_t launch_balance_backward(const LaunchBalance &a);
+
+struct LaunchPermute {
+  const void *x;
+  const int32_t *src_row;
+  int64_t tokens;
+  int32_t top_k;
+  int64_t n;
+  void *out;
+  int32_t *status;
+  cudaStream_t stream;
+};
+cudaError_t launch_permute(const LaunchPermute &c);
+
+// SwiGLU in bf16 (activation.cu): the backward with dh.
+struct LaunchSwiglu {
+  const void *gate_up, *dh;
+  int64_t rows, inter;
+  void *out;
+  cudaStream_t stream;
+};
+cudaError_t launch_swiglu(const LaunchSwiglu &a);
 
 struct LaunchCombineBackward {
   const void *d_out, *y;

@@ -24,6 +24,7 @@
 
 #include "fme_device.cuh"
 #include "fme_launch.h"
+#include "swiglu.cuh"
 
 namespace fme {
 
@@ -183,19 +184,6 @@ constexpr int kNvSmemBudget = 220 * 1024;  // shared memory aimed for per SM
 // [G+1 group offsets][G+1 tile counts].
 __host__ __device__ __forceinline__ size_t nv_smem_bytes(int stages, int64_t row_bytes, int num_groups) {
   return static_cast<size_t>(stages) * (row_bytes + 8) + 8 * static_cast<size_t>(num_groups + 1);
-}
-
-// SwiGLU of two bf16 words: gate (g.lo, g.hi) and up (u.lo, u.hi) -> the bf16 word
-// (h.lo, h.hi), h = silu(g) * u rounded to bf16 (nearest even).
-__device__ __forceinline__ uint32_t swiglu_word(uint32_t g, uint32_t u) {
-  const float h0 = silu_times(__uint_as_float(g << 16), __uint_as_float(u << 16));
-  const float h1 = silu_times(__uint_as_float(g & 0xFFFF0000u), __uint_as_float(u & 0xFFFF0000u));
-  const __nv_bfloat162 h = __floats2bfloat162_rn(h0, h1);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ uint4 swiglu_uint4(const uint4 &g, const uint4 &u) {
-  return make_uint4(swiglu_word(g.x, u.x), swiglu_word(g.y, u.y), swiglu_word(g.z, u.z), swiglu_word(g.w, u.w));
 }
 
 // kSwiGLU: the row is produced from a gate/up row [g (k values) | u (k values)]

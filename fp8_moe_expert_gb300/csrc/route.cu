@@ -18,8 +18,7 @@
 //      counts to a per-expert running total in shared memory.
 // Ids outside [0, E) are reported (FME_DEV_BAD_INDEX), get row_of = -1 and take
 // no grouped row.
-#include "fme_device.cuh"
-#include "fme_launch.h"
+#include "block128.cuh"
 
 namespace fme {
 
@@ -245,6 +244,64 @@ cudaError_t launch_combine(const LaunchCombine &c) {
                                                    c.top_k, static_cast<uint32_t>(c.n), c.rows_y,
                                                    static_cast<uint16_t *>(c.out), c.status);
   return cudaGetLastError();
+}
+
+// moe_permute: out[r, :] = x[src_row[r] / top_k, :], the bf16 rows in grouped order.  Bound by memory.  A token's row is
+// read top_k times, at unrelated times, so the columns go in slabs whose part of x stays in L2: a CTA takes 1024 16-byte
+// pieces of a slab, four to a thread, and the slabs come one after the other.
+constexpr int kPermuteThreads = 256;
+constexpr int kPermutePieces = 4;
+
+__global__ void __launch_bounds__(kPermuteThreads) moe_permute_kernel(const uint16_t *x, const int32_t *src_row, int64_t rows,
+                                                                      int top_k, uint32_t n8, uint32_t slab8,
+                                                                      int64_t slab_ctas, uint16_t *out, int32_t *status) {
+  start_next_kernel();
+  wait_for_previous_kernel();
+  const uint32_t slab = static_cast<uint32_t>(blockIdx.x / slab_ctas);
+  const uint32_t c0 = slab * slab8, width = min(slab8, n8 - c0);
+  const int64_t base = (blockIdx.x - slab * slab_ctas) * (kPermuteThreads * kPermutePieces);
+  const int64_t row0 = base / width;
+  const uint32_t at0 = static_cast<uint32_t>(base - row0 * width);
+  uint4 v[kPermutePieces];
+  int64_t to[kPermutePieces];
+  const int64_t sources = rows;  // assignments
+#pragma unroll
+  for (int i = 0; i < kPermutePieces; ++i) {
+    const uint32_t at = at0 + threadIdx.x + i * kPermuteThreads;
+    const int64_t row = row0 + at / width;
+    const int64_t col = static_cast<int64_t>(c0 + at % width) * 8;
+    to[i] = -1;
+    if (row >= rows) continue;
+    int32_t a = src_row[row];
+    if (a < 0 || a >= sources) {
+      report(status, kDevBadIndex);
+      a = 0;
+    }
+    to[i] = row * n8 * 8 + col;
+    v[i] = *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(a / top_k) * n8 * 8 + col);
+  }
+#pragma unroll
+  for (int i = 0; i < kPermutePieces; ++i)
+    if (to[i] >= 0) __stcs(reinterpret_cast<uint4 *>(out + to[i]), v[i]);
+}
+
+cudaError_t launch_permute(const LaunchPermute &c) {
+  const int64_t rows = c.tokens * c.top_k;
+  const uint32_t n8 = static_cast<uint32_t>(c.n / 8);
+  // equal slabs of at most 2048 columns
+  const uint32_t slabs = (n8 + 255) / 256, slab8 = (n8 + slabs - 1) / slabs;
+  const int64_t slab_ctas = (rows * slab8 + kPermuteThreads * kPermutePieces - 1) / (kPermuteThreads * kPermutePieces);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(slab_ctas * slabs), 1, 1);
+  cfg.blockDim = dim3(kPermuteThreads, 1, 1);
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_permute_kernel, static_cast<const uint16_t *>(c.x), c.src_row, rows, c.top_k, n8,
+                            slab8, slab_ctas, static_cast<uint16_t *>(c.out), c.status);
 }
 
 // The gradient of moe_combine: for every assignment (t, k) with grouped row r = row_of[t, k],

@@ -593,6 +593,60 @@ fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, con
                                    int64_t n, int64_t k, void *dw, int32_t dw_mode, int32_t *dev_status, void *stream);
 
 /*
+ * grouped_gemv_nvfp4 -- products of few bf16 rows with NVFP4 weights, for decode steps:
+ *   y[t, j] = S[e, j] sum_i x'[t, i] c[e, j, i] sf[e, j, i / 16]   for every row t of expert e,
+ * c, sf and S the E2M1 codes, E4M3 block scales and fp32 row scales of the weights, x' the rows of x, gathered where
+ * src_row is given.  The activations are not quantized: only the weights' rounding is in the result ("Composer 2
+ * Technical Report", section 6.1, the NVFP4 variant, whose weights these are).  c sf is exact in bf16, products and sums
+ * are in fp32 on the tensor cores, S is applied in fp32, one rounding to bf16.  A row's result does not depend on any
+ * other row.  Any number of rows is computed; the weights are read again for every 8 to 32 rows of an expert, so that with
+ * many rows grouped_gemm_fwd_nvfp4 on quantized rows is the faster call.
+ *
+ *   x         device bf16 [x_rows x k]
+ *   src_row   device int32 [m] from moe_route: row t of the grouped rows is x[src_row[t] / top_k], m = x_rows * top_k.  An
+ *             index outside [0, m) sets FME_DEV_BAD_INDEX and reads row 0.  Or NULL: x holds the grouped rows,
+ *             m = x_rows, top_k = 1
+ *   w_codes, w_sf, w_scale  quantize_nvfp4_pertoken (or .._pertensor) of the weights [num_experts * n x k] as one group
+ *   offsets   device int32 [num_experts + 1], rows per expert, rising from 0 to m (otherwise FME_DEV_BAD_OFFSETS and y is
+ *             not written)
+ *   m, n, k   n 1 .. 65536; k a multiple of 64, 64 .. 8192
+ *   y         device bf16 [m x n]
+ */
+fme_status grouped_gemv_nvfp4(const void *x, int64_t x_rows, const int32_t *src_row, int32_t top_k,
+                              const uint8_t *w_codes, const uint8_t *w_sf, const float *w_scale, const int32_t *offsets,
+                              int32_t num_experts, int64_t m, int64_t n, int64_t k, void *y, int32_t *dev_status,
+                              void *stream);
+
+/* grouped_gemv_nvfp4_swiglu -- the gate/up projection's with the activation: h[t, j] = silu(g) u, g and u the unrounded
+ * fp32 outputs j and n / 2 + j of grouped_gemv_nvfp4, silu as in swiglu.  n a multiple of 256; h bf16 [m x n / 2]. */
+fme_status grouped_gemv_nvfp4_swiglu(const void *x, int64_t x_rows, const int32_t *src_row, int32_t top_k,
+                                     const uint8_t *w_codes, const uint8_t *w_sf, const float *w_scale,
+                                     const int32_t *offsets, int32_t num_experts, int64_t m, int64_t n, int64_t k, void *h,
+                                     int32_t *dev_status, void *stream);
+
+/*
+ * swiglu -- h = silu(g) * u, silu(v) = v / (1 + e^-v), of gate_up [rows x 2 inter] (bf16, a row is [g | u]), in fp32
+ * with a fast exponential and reciprocal (relative error a few 2^-17), rounded to bf16: bit for bit the h of
+ * swiglu_quantize_nvfp4, for layers that stay in bf16.  inter a multiple of 8, 8 .. 65536; h bf16 [rows x inter].
+ */
+fme_status swiglu(const void *gate_up, int64_t rows, int64_t inter, void *h, void *stream);
+
+/* swiglu_backward -- d(gate/up) bf16 [rows x 2 inter] from dh bf16 [rows x inter], as swiglu_backward_quantize_mxfp8
+ * forms its d_gate_up: dg = dh u sigma(g) (1 + g sigma(-g)), du = dh g sigma(g). */
+fme_status swiglu_backward(const void *gate_up, const void *dh, int64_t rows, int64_t inter, void *d_gate_up,
+                           void *stream);
+
+/*
+ * moe_permute -- the bf16 rows in grouped order: out[r, :] = x[src_row[r] / top_k, :] for r < tokens * top_k (src_row from
+ * moe_route).  An index outside [0, tokens * top_k) sets FME_DEV_BAD_INDEX and reads row 0.  Its gradient
+ * is moe_combine of the rows' gradients with weights 1.
+ *   x         device bf16 [tokens x n]; n a multiple of 8, 8 .. 65536; top_k 1 .. 64
+ *   out       device bf16 [tokens * top_k x n]
+ */
+fme_status moe_permute(const void *x, int64_t tokens, int64_t n, const int32_t *src_row, int32_t top_k, void *out,
+                       int32_t *dev_status, void *stream);
+
+/*
  * moe_gate -- the top_k experts of each token and their weights, from router logits.
  *
  * key[t, e] = fl32(logits[t, e] + bias[e]); ids[t, :] = the top_k largest keys, largest first,

@@ -1,0 +1,190 @@
+"""Products of few bf16 rows with NVFP4 weights against their 64-bit form.
+
+c sf is exact, the sums are in fp32: with s = sum |x| |w| each of at most k additions and the 8 of the partial sums loses
+2^-23 of s, the row scale's product 2^-24, and the output is rounded once (bf16, half a step 2^-8).  On small
+integers and scales that are powers of two every sum is exact."""
+import pytest
+import torch
+
+import fp8_moe_expert_gb300 as fme
+from tests import block128 as ref
+from tests import nvfp4w
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    fme.ensure_built()
+
+
+@pytest.fixture(autouse=True)
+def _nothing_cached():
+    torch.cuda.empty_cache()
+
+
+@pytest.fixture
+def status():
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    yield st
+    assert fme.read_device_status(st)[0] == 0
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def integers(shape, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randint(-2, 3, shape, generator=g, device=DEV).to(torch.bfloat16)
+
+
+def product64(x, w, off, n):
+    """(y, size) for grouped rows x and weights w [E n, k] in 64 bits."""
+    y = torch.zeros((x.shape[0], n), dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(y)
+    for e, (lo, hi) in enumerate(zip(off, off[1:])):
+        a, b = x[lo:hi].double(), w[e * n:(e + 1) * n].t()
+        y[lo:hi], size[lo:hi] = a @ b, a.abs() @ b.abs()
+    return y, size
+
+
+def sum_error(size, k):
+    return (k + 8 + 2) * 2.0 ** -23 * size
+
+
+# rows, experts, n, k: rows of the weights that fill no group of 128, experts that start inside one, a last chunk of 64
+SHAPES = [(1, 1, 1, 64), (1, 1, 128, 64), (1, 4, 256, 128), (3, 2, 130, 192), (8, 1, 100, 320), (9, 1, 7, 1024), (17, 3, 200, 1344),
+          (8, 8, 384, 7168), (40, 3, 1000, 512), (70, 2, 128, 8192), (130, 5, 264, 2048), (33, 200, 40, 192),
+          (2000, 1024, 8, 64)]
+
+
+@pytest.mark.parametrize("rows,experts,n,k", SHAPES)
+def test_product(rows, experts, n, k, status):
+    off = ref.split(rows, experts, rows + n)
+    w = ref.normal((experts * n, k), 0.05, 1)
+    w[::7] *= 1e-3
+    w[:, : k // 4] *= 30.0
+    codes, sf, scale = fme.quantize_nvfp4_pertoken(w, status=status)
+    x = ref.normal((rows, k), 1.0, 2)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32(off), status=status)
+    want, size = product64(x, nvfp4w.values(codes, sf, scale), off, n)
+    assert bool(((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + sum_error(size, k)).all())
+
+
+@pytest.mark.parametrize("rows,experts,n,k", SHAPES)
+def test_exact_sums(rows, experts, n, k, status):
+    off = ref.split(rows, experts, rows + n)
+    codes, sf, scale = nvfp4w.random_weights(experts * n, k, 3)
+    x = integers((rows, k), 4)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32(off), status=status)
+    want, _ = product64(x, nvfp4w.values(codes, sf, scale), off, n)
+    assert torch.equal(y, want.to(torch.bfloat16))
+
+
+def test_every_code_and_scale(status):
+    """One-hot rows pick single weights: every code under every finite scale, subnormal ones among them."""
+    k = 64
+    scales = torch.arange(0, 0x7F, dtype=torch.uint8, device=DEV)[:, None].expand(-1, k // 16).contiguous()
+    n = scales.shape[0]
+    one = torch.arange(16, dtype=torch.uint8, device=DEV)
+    codes = (one[0::2] + 16 * one[1::2]).repeat(4)[None, :].expand(n, -1).contiguous()  # k -> code k % 16
+    sf, scale = nvfp4w.tiled(scales), torch.full((n,), 0.5, device=DEV)
+    x = torch.eye(k, device=DEV).to(torch.bfloat16)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32([0, k]), status=status)
+    assert torch.equal(y.double(), nvfp4w.values(codes, sf, scale).t())
+
+
+@pytest.mark.parametrize("big", [2.0 ** 100, 2.0 ** -100])
+def test_large_and_small_rows(big, status):
+    n, k = 200, 256
+    codes, sf, scale = nvfp4w.random_weights(n, k, 5)
+    x = (integers((3, k), 6).float() * big).to(torch.bfloat16)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32([0, 3]), status=status)
+    want, _ = product64(x, nvfp4w.values(codes, sf, scale), [0, 3], n)
+    assert torch.equal(y.double(), want.to(torch.bfloat16).double())
+
+
+@pytest.mark.parametrize("tokens,top_k,experts,n,k", [(1, 8, 32, 256, 7168), (5, 2, 4, 512, 192), (16, 4, 4, 256, 1024),
+                                                      (40, 3, 5, 256, 320), (1, 1, 1, 256, 64)])
+def test_gathered_with_activation(tokens, top_k, experts, n, k, status):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    ids = torch.rand((tokens, experts), generator=g, device=DEV).argsort(dim=1)[:, :top_k].int().contiguous()
+    offsets, _, src = fme.moe_route(ids, experts, status=status)
+    w = ref.normal((experts * n, k), 0.05, 8)
+    codes, sf, scale = fme.quantize_nvfp4_pertoken(w, status=status)
+    x = ref.normal((tokens, k), 1.0, 9)
+    h = fme.grouped_gemv_nvfp4_swiglu(x, codes, sf, scale, offsets, src_row=src, top_k=top_k, status=status)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, offsets, src_row=src, top_k=top_k, status=status)
+    rows = x[src.long() // top_k]
+    assert torch.equal(y, fme.grouped_gemv_nvfp4(rows, codes, sf, scale, offsets, status=status))
+    want, size = product64(rows, nvfp4w.values(codes, sf, scale), offsets.tolist(), n)
+    gate, up = want.chunk(2, dim=1)
+    d_gate, d_up = sum_error(size, k).chunk(2, dim=1)
+    silu = torch.sigmoid(gate) * gate
+    # |silu'| <= 1.1; the fast exponential and reciprocal a few 2^-17
+    allowed = 1.1 * d_gate * (up.abs() + d_up) + silu.abs() * d_up + (2.0 ** -8 + 2.0 ** -14) * (silu * up).abs()
+    err = (h.double() - silu * up).abs()
+    assert bool((err <= 1.01 * allowed + 1e-30).all()), float((err - allowed).max())
+
+
+def test_a_rows_bits_do_not_depend_on_the_batch(status):
+    """Alone, among 8, 16 and more rows of an expert: the forms of 8, 16 and 32 rows."""
+    n, k = 512, 1344
+    codes, sf, scale = fme.quantize_nvfp4_pertoken(ref.normal((2 * n, k), 0.05, 1))
+    x = ref.normal((100, k), 1.0, 2)
+    for call in (fme.grouped_gemv_nvfp4, fme.grouped_gemv_nvfp4_swiglu):
+        whole = call(x, codes, sf, scale, i32([0, 37, 100]), status=status)
+        for lo, hi in ((0, 1), (3, 9), (5, 20), (0, 30)):
+            part = call(x[lo:hi].contiguous(), codes, sf, scale, i32([0, hi - lo, hi - lo]), status=status)
+            assert torch.equal(part, whole[lo:hi])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_rows_values_stay_its_own(bad, status):
+    n, k = 256, 192
+    codes, sf, scale = fme.quantize_nvfp4_pertoken(ref.normal((3 * n, k), 0.05, 1))
+    x = ref.normal((11, k), 1.0, 2)
+    off = i32([0, 4, 4, 11])
+    clean = fme.grouped_gemv_nvfp4(x, codes, sf, scale, off, status=status)
+    x[6, k - 1] = bad
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, off, status=status)
+    keep = [i for i in range(11) if i != 6]
+    assert torch.equal(y[keep], clean[keep]) and not bool(y[6].isfinite().all())
+
+
+def test_no_rows_and_malformed_offsets():
+    n, k = 128, 64
+    codes, sf, scale = nvfp4w.random_weights(2 * n, k, 1)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    empty = torch.empty((0, k), dtype=torch.bfloat16, device=DEV)
+    assert fme.grouped_gemv_nvfp4(empty, codes, sf, scale, i32([0, 0, 0]), status=st).shape == (0, n)
+    assert fme.read_device_status(st)[0] == 0
+    x = integers((5, k), 2)
+    for off in ([0, 6, 5], [1, 2, 5], [0, 2, 4], [0, -1, 5]):
+        st.zero_()
+        y = torch.full((5, n), 7.0, dtype=torch.bfloat16, device=DEV)
+        fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32(off), y=y, status=st)
+        assert fme.read_device_status(st)[0] == fme.ERR_DEVICE_BAD_OFFSETS and bool((y == 7.0).all())
+
+
+def test_gather_out_of_range_reads_row_0_and_is_reported():
+    n, k = 128, 64
+    codes, sf, scale = nvfp4w.random_weights(n, k, 1)
+    x = integers((3, k), 2)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32([0, 6]), src_row=i32([0, -1, 6, 5, 2, 1 << 30]), top_k=2, status=st)
+    assert fme.read_device_status(st)[0] == fme.ERR_DEVICE_BAD_INDEX
+    assert torch.equal(y, fme.grouped_gemv_nvfp4(x[[0, 0, 0, 2, 1, 0]], codes, sf, scale, i32([0, 6])))
+
+
+def test_nothing_outside_the_output_is_written(status):
+    rows, n, k = 13, 200, 128
+    codes, sf, scale = nvfp4w.random_weights(2 * n, k, 1)
+    whole = torch.full((rows * n + 2048,), 7.0, dtype=torch.bfloat16, device=DEV)
+    fme.grouped_gemv_nvfp4(integers((rows, k), 2), codes, sf, scale, i32([0, 5, rows]),
+                           y=whole[1024:1024 + rows * n].view(rows, n), status=status)
+    assert bool((whole[:1024] == 7.0).all()) and bool((whole[-1024:] == 7.0).all())
