@@ -215,6 +215,7 @@ struct LaunchGemv {
   void *y;
   int32_t *status;
   int num_sms;
+  int32_t x_tile, depth;  // set by the launcher
   cudaStream_t stream;
 };
 cudaError_t launch_gemv_nvfp4(const LaunchGemv &a);

@@ -132,7 +132,7 @@ def test_gathered_with_activation(tokens, top_k, experts, n, k, status):
 
 
 def test_a_rows_bits_do_not_depend_on_the_batch(status):
-    """Alone, among 8, 16 and more rows of an expert: the forms of 8, 16 and 32 rows."""
+    """Alone, and among more rows of an expert than are taken at a time."""
     n, k = 512, 1344
     codes, sf, scale = fme.quantize_nvfp4_pertoken(ref.normal((2 * n, k), 0.05, 1))
     x = ref.normal((100, k), 1.0, 2)
@@ -141,6 +141,40 @@ def test_a_rows_bits_do_not_depend_on_the_batch(status):
         for lo, hi in ((0, 1), (3, 9), (5, 20), (0, 30)):
             part = call(x[lo:hi].contiguous(), codes, sf, scale, i32([0, hi - lo, hi - lo]), status=status)
             assert torch.equal(part, whole[lo:hi])
+
+
+def within(y, want, size, k):
+    """Where no partial sum can leave fp32's range: one of terms of total size 2^127 and more (2^127 x 2 is an infinity
+    already) may overflow on the way to a sum that would not."""
+    fits = size < 2.0 ** 127
+    return bool(((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + sum_error(size, k))[fits].all())
+
+
+def test_rows_of_any_range(status):
+    """A row with values far apart is not exact in fp16: it takes its neighbours the other way, with their bits as they
+    were; and nothing of it is lost, weights of 0 at its large values among them."""
+    n, k = 256, 320
+    codes, sf, scale = nvfp4w.random_weights(n, k, 5)
+    x = integers((8, k), 6)
+    near = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32([0, 8]), status=status)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    for far in (2.0 ** 15, 2.0 ** 28, 2.0 ** 30, 2.0 ** 40, 2.0 ** 100, 2.0 ** 127):
+        y = x.clone()
+        y[3] = torch.where(torch.rand(k, generator=g, device=DEV) < 0.1, far, 2.0 ** -20).to(torch.bfloat16) * y[3]
+        got = fme.grouped_gemv_nvfp4(y, codes, sf, scale, i32([0, 8]), status=status)
+        keep = [0, 1, 2, 4, 5, 6, 7]
+        assert torch.equal(got[keep], near[keep])
+        want, size = product64(y, nvfp4w.values(codes, sf, scale), [0, 8], n)
+        assert within(got, want, size, k)
+        # one large value at a weight of 0 for every output, the rest small
+        c0 = codes.clone()
+        c0[:, 0] &= 0xF0
+        y[3] = 2.0 ** -20
+        y[3, 0] = far
+        got = fme.grouped_gemv_nvfp4(y, c0, sf, scale, i32([0, 8]), status=status)
+        want, size = product64(y, nvfp4w.values(c0, sf, scale), [0, 8], n)
+        assert within(got, want, size, k)
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
