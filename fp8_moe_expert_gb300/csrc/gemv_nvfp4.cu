@@ -25,9 +25,9 @@
 // layout keeps the scales of those four together), or, with SwiGLU, of two quarters of the gate rows and of the matching
 // up rows.  What a lane needs of a chunk, 16 bytes of codes a row and the scales, it copies itself into shared
 // memory, up to two chunks ahead and across the ends of units, and reads back: no barrier, no conflict, and the loads in
-// flight take no registers.  Two or eight warps share a unit, by the weights' sizes alone, each takes every second or
-// eighth chunk, and their sums are added in order: a sum's order depends on the weights' sizes alone, so a row's
-// bits do not depend on the other rows.
+// flight take no registers.  Two, four or eight warps share a unit, by how many there are.  The chunks of each residue mod 8
+// have a sum of their own, and the eight are added as a tree, ((0 + 4) + (2 + 6)) + ((1 + 5) + (3 + 7)), of which each warp
+// makes its branch: the order is the same however many warps share, so a row's bits do not depend on the other rows.
 //
 // A CTA an SM, 16 warps, takes consecutive units, mostly of the same up to 8 rows of x: those it brings into shared memory
 // once, converted, in the order in which the lanes read them.
@@ -48,6 +48,7 @@ constexpr int kChunk = 128;    // k of a warp's step
 constexpr int kGemvRows = 8;   // rows of x at a time
 constexpr int kRowsPad = 33;   // sums of a row of x in shared memory
 constexpr uint32_t kSlotBytes = 5 * 512;  // of a chunk: four rows' codes and their scales, 16 bytes a lane each
+constexpr int kSums = 8;                  // of every output: one of each residue of the chunks mod 8
 constexpr int kXPad = 64;                 // bytes between the rows of x, so that two of them cover all banks
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -152,6 +153,7 @@ struct Unit {
 template <bool kSwiglu, int kShare>
 __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __grid_constant__ LaunchGemv p) {
   constexpr int kGroups = kGemvWarps / kShare;
+  constexpr int kSets = kSums / kShare;  // of the eight sums, a warp's
   __shared__ SharedGemv s;
   extern __shared__ __align__(16) uint8_t dyn[];
   const int depth = p.depth;
@@ -291,11 +293,19 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       }
       src = static_cast<const uint16_t *>(p.x) + row * k;
       float top = 0.0f;
-      for (int c = slice * 32 + lane; c < k / 8; c += per_row * 32) {
-        float f[8];
-        unpack8(*reinterpret_cast<const uint4 *>(src + 8 * c), f);
+      for (int c = slice * 32 + lane; c < k / 8; c += 4 * per_row * 32) {
+        uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+        for (int b = 0; b < 4; ++b)
+          if (c + b * per_row * 32 < k / 8) v[b] = *reinterpret_cast<const uint4 *>(src + 8 * (c + b * per_row * 32));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (c + b * per_row * 32 >= k / 8) continue;
+          float f[8];
+          unpack8(v[b], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+        }
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
@@ -352,11 +362,10 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
     // ---- the units of this tile
     const uint32_t stop = min(end, (tile + 1) * per);
     for (; i < stop; i += kGroups) {
-      float acc[2][4] = {};
+      float acc[kSets][2][4] = {};
       auto sums = [&](auto half_tag) {
         constexpr bool kHalf = decltype(half_tag)::value;
-        uint32_t x_at = x_lane + share * (kChunk * 2);
-        for (int32_t c = share; c < chunks; c += kShare, x_at += kShare * kChunk * 2) {
+        auto add_chunk = [&](int32_t c, float(&to)[2][4]) {
           if (depth == 2)
             asm volatile("cp.async.wait_group 1;" ::: "memory");
           else
@@ -383,13 +392,18 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
               const uint4 &v = codes[q];
               decode8<kHalf>(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, sc[q][j >> 1], a[q]);
             }
-            const uint4 x = shared16(x_at + 64 * j);
+            const uint4 x = shared16(x_lane + c * (kChunk * 2) + 64 * j);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              mma_16816<kHalf>(acc[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
-              mma_16816<kHalf>(acc[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
+              mma_16816<kHalf>(to[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
+              mma_16816<kHalf>(to[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
             }
           }
+        };
+        for (int32_t c = share; c < chunks; c += kSums) {
+#pragma unroll
+          for (int i = 0; i < kSets; ++i)
+            if (c + i * kShare < chunks) add_chunk(c + i * kShare, acc[i]);
         }
       };
       if (wide)
@@ -397,12 +411,20 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       else
         sums(std::true_type{});
 
-      // ---- the warps' sums, in order
+      // ---- the eight sums: a warp's own, then the warps'
+      if constexpr (kSets > 1) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[0][m][j] = kSets == 2 ? acc[0][m][j] + acc[1][m][j]
+                                      : (acc[0][m][j] + acc[kSets / 2][m][j]) + (acc[1][m][j] + acc[kSets - 1][m][j]);
+      }
       float *to_part = part + warp * kGemvRows * kRowsPad;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to_part[(2 * t + (j & 1)) * kRowsPad + 8 * (2 * m + (j >> 1)) + g] = acc[m][j];
+        for (int j = 0; j < 4; ++j) to_part[(2 * t + (j & 1)) * kRowsPad + 8 * (2 * m + (j >> 1)) + g] = acc[0][m][j];
       auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kShare) : "memory"); };
       meet();
       const Unit it = unit_at(i, tile, e);
@@ -413,12 +435,18 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
         const int32_t row = weight_row(it, in >> 3, in & 7);
         if (!present(it, row)) continue;
         const float *from = theirs + tok * kRowsPad + in;
-        float v = 0.0f, up = 0.0f;
+        auto joined = [&](const float *at) {
+          float w[kShare];
 #pragma unroll
-        for (int w = 0; w < kShare; ++w) {
-          v += from[w * kGemvRows * kRowsPad];
-          if (kSwiglu) up += from[w * kGemvRows * kRowsPad + 16];
-        }
+          for (int j = 0; j < kShare; ++j) w[j] = at[j * kGemvRows * kRowsPad];
+#pragma unroll
+          for (int half = kShare / 2; half; half /= 2)
+#pragma unroll
+            for (int j = 0; j < half; ++j) w[j] += w[j + half];
+          return w[0];
+        };
+        float v = joined(from);
+        const float up = kSwiglu ? joined(from + 16) : 0.0f;
         const float back = wide ? 256.0f : s.back[tok];
         v = (v * back) * p.scale[row];
         if (kSwiglu) v = silu_times(v, (up * back) * p.scale[row + out_n]);
@@ -428,6 +456,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// An upper bound of a call's units.
+int64_t unit_bound(const LaunchGemv &a) {
+  const int64_t per = a.swiglu ? a.n / 256 * 8 : (a.n % 128 == 0 ? a.n / 128 : (a.n + 254) / 128) * 4;
+  return (a.m / kGemvRows + std::min<int64_t>(a.num_experts, a.m)) * per;
 }
 
 template <bool kSwiglu, int kShare>
@@ -442,12 +476,8 @@ cudaError_t launch_gemv(LaunchGemv a) {
   // two chunks of each warp where they fit beside x, else one
   constexpr int kSlots = kGemvWarps * static_cast<int>(kSlotBytes);
   a.depth = rest + 2 * kSlots <= 227 * 1024 - 256 ? 2 : 1;
-  const int64_t out_n = kSwiglu ? a.n / 2 : a.n;
-  const int64_t per = (a.n % 128 == 0 ? out_n / 128 : (a.n + 254) / 128) * (kSwiglu ? 8 : 4);
-  const int64_t units = (a.m / kGemvRows + std::min<int64_t>(a.num_experts, a.m)) * per;
   cudaLaunchConfig_t cfg = {};
-  constexpr int kGroups = kGemvWarps / kShare;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, (units + kGroups - 1) / kGroups)), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, unit_bound(a))), 1, 1);
   cfg.blockDim = dim3(kGemvThreads, 1, 1);
   cfg.dynamicSmemBytes = rest + a.depth * kSlots;
   cfg.stream = a.stream;
@@ -459,9 +489,15 @@ cudaError_t launch_gemv(LaunchGemv a) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// How many warps share a unit: the more units an SM gets, the fewer, as each meeting of warps costs.  Measured, us
+// with 8 / 4 / 2 warps: gate/up of 4096 x 7168 with SwiGLU, one expert with one row (0.8 units an SM) 9.5 / 11.1 / 15.8, two with
+// one each (1.7) 13.4 / 12.9 / 16.7, eight (7) 35.6 / 32.2 / 32.1; down projection of 7168 x 2048, one expert (1.5) 7.6 / 7.4 /
+// 7.8, four (6) 15.1 / 13.6 / 12.2, eight (12) 27.5 / 22.7 / 20.8.
 template <bool kSwiglu>
 cudaError_t launch_gemv(const LaunchGemv &a) {
-  return a.k > 2048 || a.n <= 4096 ? launch_gemv<kSwiglu, 8>(a) : launch_gemv<kSwiglu, 2>(a);
+  const int64_t units = unit_bound(a);
+  if (2 * units < 3 * a.num_sms) return launch_gemv<kSwiglu, 8>(a);
+  return a.k <= 2048 && units >= 4 * a.num_sms ? launch_gemv<kSwiglu, 2>(a) : launch_gemv<kSwiglu, 4>(a);
 }
 
 }  // namespace

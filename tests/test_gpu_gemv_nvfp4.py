@@ -177,6 +177,21 @@ def test_rows_of_any_range(status):
         assert within(got, want, size, k)
 
 
+def test_the_bits_with_two_four_and_eight_warps(status):
+    """One row alone and the same row among the rows of more and more experts, so that fewer warps share its sums."""
+    n, k = 2048, 1856
+    experts = 24
+    codes, sf, scale = fme.quantize_nvfp4_pertoken(ref.normal((experts * n, k), 0.05, 1))
+    x = ref.normal((2 * experts, k), 1.0, 2)
+    whole = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32([2 * e for e in range(experts + 1)]), status=status)
+    for e in (1, 2, 6, 13):
+        part = fme.grouped_gemv_nvfp4(x[:2 * e].contiguous(), codes, sf, scale,
+                                      i32([2 * min(i, e) for i in range(experts + 1)]), status=status)
+        assert torch.equal(part, whole[:2 * e])
+    one = fme.grouped_gemv_nvfp4(x[:1].contiguous(), codes, sf, scale, i32([0] + [1] * experts), status=status)
+    assert torch.equal(one, whole[:1])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_rows_values_stay_its_own(bad, status):
     n, k = 256, 192
