@@ -39,6 +39,7 @@ struct SharedBf {
   uint64_t acc_empty[2];
   uint64_t drain;
   uint64_t peer_fills_bar;
+  uint64_t end_go[kMaxStagesBf];  // wgrad: the stage, free and armed, is for a block at an expert's end
   uint32_t peer_fills;
   uint32_t tmem_base;
   int abort_flag;
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
     for (uint32_t i = 0; i < S; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.freed[i], 1);
+      mbar_init(&s.end_go[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.acc_full[i], 1);
@@ -248,53 +250,40 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
                        nb;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- producer (wgrad: the whole warp, as a block at
-    // an expert's end takes up to 60 copies)
-    if (K == KindBf::kWgrad || lane == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- producer
       uint32_t stage = 0, phase = 1, filled = 0;
       bool stop = false;
       for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
         const TileBf tl = tile_bf<K>(p, tab, t, rank);
         const int32_t bcol = tl.col0 + rank * kHalfN;
         for (int i = 0; i < tl.nk; ++i) {
-          stop = lane == 0 && !mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status);
-          if (K == KindBf::kWgrad) stop = warp_any(stop);
-          if (stop) break;
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytesBf);
+          if (!mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status)) {
+            stop = true;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytesBf);
           const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
           uint8_t *a = smem_a + stage * kABytes, *b = smem_b + stage * kBBytes;
           const int32_t k0 = i * kStageK;
           if constexpr (K == KindBf::kWgrad) {
-            const int32_t row = tl.p0 + k0, left = tl.p1 - row;
-            if (left >= kStageK) {
-              if (lane == 0) {
-                if (p.wide_a) {
-                  tma_load_3d_pair(a, &p.map_a, bar, 0, row, tl.row0 / 64);
-                } else {
-                  pair::tma_load_2d(a, &p.map_a, bar, tl.row0, row);
-                  pair::tma_load_2d(a + kHalfMnBytes, &p.map_a, bar, tl.row0 + 64, row);
-                }
-                if (p.wide_b) {
-                  tma_load_3d_pair(b, &p.map_b, bar, 0, row, bcol / 64);
-                } else {
-                  pair::tma_load_2d(b, &p.map_b, bar, bcol, row);
-                  pair::tma_load_2d(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, row);
-                }
+            const int32_t row = tl.p0 + k0;
+            if (tl.p1 - row < kStageK) {
+              mbar_arrive(&s.end_go[stage]);  // the last block: warp 2's
+            } else {
+              if (p.wide_a) {
+                tma_load_3d_pair(a, &p.map_a, bar, 0, row, tl.row0 / 64);
+              } else {
+                pair::tma_load_2d(a, &p.map_a, bar, tl.row0, row);
+                pair::tma_load_2d(a + kHalfMnBytes, &p.map_a, bar, tl.row0 + 64, row);
               }
-            } else {  // lane = 8 (half of A or B) + group of 8 rows
-              const int32_t which = lane >> 3, grp = lane & 7;
-              uint8_t *dst = (which < 2 ? a : b) + (which & 1) * kHalfMnBytes;
-              const int32_t x = (which < 2 ? tl.row0 : bcol) + 64 * (which & 1);
-              const int32_t outside = static_cast<int32_t>(p.rows);
-              const int32_t split = left & 7 ? left >> 3 : 8;  // the group that holds the end
-              if (grp != split)
-                pair::tma_load_2d(dst + grp * 1024, which < 2 ? &p.map_a8 : &p.map_b8, bar, x,
-                                  8 * grp < left ? row + 8 * grp : outside);
-              if (split < 8)  // this lane's row of it
-                pair::tma_load_2d(dst + split * 1024 + grp * 128, which < 2 ? &p.map_a1 : &p.map_b1, bar, x,
-                                  8 * split + grp < left ? row + 8 * split + grp : outside);
+              if (p.wide_b) {
+                tma_load_3d_pair(b, &p.map_b, bar, 0, row, bcol / 64);
+              } else {
+                pair::tma_load_2d(b, &p.map_b, bar, bcol, row);
+                pair::tma_load_2d(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, row);
+              }
             }
-            __syncwarp();
           } else {
             pair::tma_load_2d(a, &p.map_a, bar, k0, tl.row0);
             if constexpr (K == KindBf::kFwd) {
@@ -313,10 +302,35 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
           }
         }
       }
-      if (lane == 0) {
-        const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
-        if (rank == 0) drain_pair_ring(s.full, S, filled, peer, kStageBytesBf);
-      }
+      const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
+      if (rank == 0) drain_pair_ring(s.full, S, filled, peer, kStageBytesBf);
+    }
+  } else if (K == KindBf::kWgrad && warp == 2) {
+    // ------------------------------------------------ blocks at an expert's end (the whole warp: up to 60 copies).  The
+    // producer frees and arms their stages; it drains them too.  (In the producer itself a vote of the warp a
+    // stage cost 10%: 65536 x 4096 x 7168, 2.09 -> 1.97 ms without.)
+    uint32_t stage = 0, seen = 0;  // seen: a bit a stage, the parity of its end_go
+    for (uint32_t round = 0, t; (t = tile_at(round)) < total; ++round) {
+      const TileBf tl = tile_bf<K>(p, tab, t, rank);
+      stage = (stage + tl.nk) % S;  // of the tile's end
+      const int32_t left = (tl.p1 - tl.p0) % kStageK;
+      if (left == 0) continue;
+      const uint32_t at = stage == 0 ? S - 1 : stage - 1;
+      if (warp_any(!mbar_wait<true>(&s.end_go[at], (seen >> at) & 1, abort_flag, p.status))) break;
+      seen ^= 1u << at;
+      const uint32_t bar = pair::map_to_rank(&s.full[at], 0);
+      // lane = 8 (half of A or B) + group of 8 rows
+      const int32_t which = lane >> 3, grp = lane & 7;
+      uint8_t *dst = (which < 2 ? smem_a + at * kABytes : smem_b + at * kBBytes) + (which & 1) * kHalfMnBytes;
+      const int32_t x = (which < 2 ? tl.row0 : tl.col0 + rank * kHalfN) + 64 * (which & 1);
+      const int32_t row = tl.p1 - left, outside = static_cast<int32_t>(p.rows);
+      const int32_t split = left & 7 ? left >> 3 : 8;  // the group that holds the end
+      if (grp != split)
+        pair::tma_load_2d(dst + grp * 1024, which < 2 ? &p.map_a8 : &p.map_b8, bar, x, 8 * grp < left ? row + 8 * grp : outside);
+      if (split < 8)  // this lane's row of it
+        pair::tma_load_2d(dst + split * 1024 + grp * 128, which < 2 ? &p.map_a1 : &p.map_b1, bar, x,
+                          8 * split + grp < left ? row + 8 * split + grp : outside);
+      __syncwarp();
     }
   } else if (warp == 1) {
     if (rank == 0) {
