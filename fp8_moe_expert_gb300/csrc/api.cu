@@ -1026,6 +1026,16 @@ fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, con
 // ----------------------------------------------- NVFP4 weights, few bf16 rows --
 namespace {
 
+// Tiled scales as [groups of 128 rows][tiles][512 bytes], boxes of 4 tiles x the 128 bytes of 8 rows of each quarter, zero
+// fill past a row's last tile.
+fme_status encode_scale_tiles(CUtensorMap *map, const void *base, uint64_t groups, uint64_t tiles) {
+  cuuint64_t dims[3] = {512, tiles, groups};
+  cuuint64_t strides[2] = {512, tiles * 512};
+  cuuint32_t box[3] = {128, 4, 1};
+  return encode_map(" (scale tiles)", map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 fme_status gemv_nvfp4(bool swiglu, const void *x, int64_t x_rows, const int32_t *src_row, int32_t top_k,
                       const uint8_t *w_codes, const uint8_t *w_sf, const float *w_scale, const int32_t *offsets,
                       int32_t num_experts, int64_t m, int64_t n, int64_t k, void *y, int32_t *dev_status, void *stream,
@@ -1051,8 +1061,9 @@ fme_status gemv_nvfp4(bool swiglu, const void *x, int64_t x_rows, const int32_t 
   a.x_rows = x_rows;
   a.src_row = src_row;
   a.top_k = top_k;
-  a.codes = w_codes;
-  a.sf = w_sf;
+  const uint64_t w_rows = static_cast<uint64_t>(num_experts) * n;
+  if ((st = encode_u8_2d(&a.map_codes, w_codes, k / 2, w_rows, k / 2, 8)) != FME_OK) return st;
+  if ((st = encode_scale_tiles(&a.map_sf, w_sf, (w_rows + 127) / 128, k / 64)) != FME_OK) return st;
   a.scale = w_scale;
   a.offsets = offsets;
   a.num_experts = num_experts;

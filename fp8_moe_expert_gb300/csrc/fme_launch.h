@@ -202,11 +202,12 @@ cudaError_t launch_bf16_wgrad(const LaunchBf16 &a);
 
 // Few bf16 rows times NVFP4 weights (gemv_nvfp4.cu).
 struct LaunchGemv {
+  CUtensorMap map_codes;  // [weight rows x k / 2], boxes of 8 rows x 128 bytes, 128-byte swizzle
+  CUtensorMap map_sf;     // [groups of 128 rows][k / 64 tiles][512 bytes], boxes of 4 tiles x 128 bytes
   const void *x;
   int64_t x_rows;
   const int32_t *src_row;  // or NULL
   int32_t top_k;
-  const uint8_t *codes, *sf;
   const float *scale;
   const int32_t *offsets;
   int32_t num_experts;
@@ -215,7 +216,8 @@ struct LaunchGemv {
   void *y;
   int32_t *status;
   int num_sms;
-  int32_t x_tile, depth;  // set by the launcher
+  int32_t tile_rows;      // set by the launcher: rows of x at a time,
+  uint32_t shared_bytes;  // and what there is of shared memory
   cudaStream_t stream;
 };
 cudaError_t launch_gemv_nvfp4(const LaunchGemv &a);

@@ -20,23 +20,25 @@
 // Both multiply the same values but for a power of two, so the sums' bits are the same (as long as they are normal
 // numbers).
 //
-// Any order of k will do as long as both operands follow it.  A unit is 32 weight rows: lane (g, t) = (lane / 4, lane % 4)
-// of a warp takes 32 consecutive k of a chunk of 128 for four rows, g + 8 i of each quarter of a group of 128 (the tiled
-// layout keeps the scales of those four together), or, with SwiGLU, of two quarters of the gate rows and of the matching
-// up rows.  What a lane needs of a chunk, 16 bytes of codes a row and the scales, it copies itself into shared
-// memory, up to two chunks ahead and across the ends of units, and reads back: no barrier, no conflict, and the loads in
-// flight take no registers.  Two, four or eight warps share a unit, by how many there are.  The chunks of each residue mod 8
+// Any order of k will do as long as both operands follow it.  A unit is 32 weight rows: 8 of each quarter of a group of 128
+// (the tiled layout keeps the scales of rows 32 apart together), or, with SwiGLU, of two quarters of the gate rows
+// and of the matching up rows.  A warp's step is a chunk of 256 k of a unit: four boxes of 8 rows x 128 bytes of codes and the
+// tiles of scales come by bulk tensor copies into a ring of the warp's own, a step or two ahead and across the ends of units.
+// Lane (g, t) = (lane / 4, lane % 4) takes 32 consecutive k of each half chunk for one row of each box.
+//
+// Two, four or eight warps share a unit, by how many there are.  The chunks of each residue mod 8
 // have a sum of their own, and the eight are added as a tree, ((0 + 4) + (2 + 6)) + ((1 + 5) + (3 + 7)), of which each warp
 // makes its branch: the order is the same however many warps share, so a row's bits do not depend on the other rows.
 //
 // A CTA an SM, 16 warps, takes consecutive units, mostly of the same up to 8 rows of x: those it brings into shared memory
-// once, converted, in the order in which the lanes read them.
+// once, converted, in the order in which the lanes read them.  The most rows that any expert has decide how much of it
+// they take, and so how deep the rings are.
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <type_traits>
 
-#include "block128.cuh"
+#include "gemm_tiles.cuh"
 
 namespace fme {
 
@@ -44,10 +46,12 @@ namespace {
 
 constexpr int kGemvWarps = 16;
 constexpr int kGemvThreads = 32 * kGemvWarps;
-constexpr int kChunk = 128;    // k of a warp's step
-constexpr int kGemvRows = 8;   // rows of x at a time
+constexpr int kChunk = 256;    // k of a warp's step
+constexpr int kGemvRows = 8;   // rows of x at a time, at most
 constexpr int kRowsPad = 33;   // sums of a row of x in shared memory
-constexpr uint32_t kSlotBytes = 5 * 512;  // of a chunk: four rows' codes and their scales, 16 bytes a lane each
+constexpr uint32_t kBoxBytes = 8 * 128;    // 8 rows' codes of a chunk
+constexpr uint32_t kCodeBytes = 4 * kBoxBytes;
+constexpr uint32_t kTilesBytes = 4 * 128;  // scales of 8 rows of each quarter of a chunk
 constexpr int kSums = 8;                  // of every output: one of each residue of the chunks mod 8
 constexpr int kXPad = 64;                 // bytes between the rows of x, so that two of them cover all banks
 
@@ -114,16 +118,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 or 8 bytes from global into shared memory, zeros where `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ uint4 shared16(uint32_t src) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 shared8(uint32_t src) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(src) : "memory");
   return v;
 }
 
@@ -138,9 +140,12 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
 }
 
 struct SharedGemv {
+  uint64_t full[kGemvWarps][2];
   float amax[kGemvWarps];       // of a warp's part of a row of x
   float back[kGemvRows];        // 2^-s of each row's power of two
   int ok_flag;
+  int abort_flag;
+  int x_tile;  // rows of x of the largest tile
 };
 
 // A unit's place.  Weight rows, of all experts, are below 2^26.
@@ -154,31 +159,48 @@ template <bool kSwiglu, int kShare>
 __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __grid_constant__ LaunchGemv p) {
   constexpr int kGroups = kGemvWarps / kShare;
   constexpr int kSets = kSums / kShare;  // of the eight sums, a warp's
+  constexpr uint32_t kScaleBytes = (kSwiglu ? 2 : 1) * kTilesBytes;
   __shared__ SharedGemv s;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  const int depth = p.depth;
+  extern __shared__ uint8_t dyn_smem[];
+  uint8_t *dyn = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   const int32_t k = static_cast<int32_t>(p.k), n = static_cast<int32_t>(p.n);
   const int32_t chunks = (k + kChunk - 1) / kChunk;
   const uint32_t x_stride = chunks * kChunk * 2 + kXPad;  // bytes of a row of x
-  uint8_t *xs = dyn + kGemvWarps * depth * kSlotBytes;
-  float *part = reinterpret_cast<float *>(xs + p.x_tile * x_stride);  // [warp][row of x][weight row]
+  float *part = reinterpret_cast<float *>(dyn);           // [warp][row of x][weight row]
   int32_t *off = reinterpret_cast<int32_t *>(part + kGemvWarps * kGemvRows * kRowsPad);
   int32_t *first = off + (p.num_experts + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
+  // the row of a box that the lane takes: lanes of one phase of an access to shared memory read rows 4 apart, which the
+  // swizzle keeps in different banks
+  const int g = (lane >> 3) | (((lane >> 2) & 1) << 2), t = lane & 3;
   const int group = warp / kShare, share = warp % kShare;
+  if (lane == 0) {
+    mbar_init(&s.full[warp][0], 1);
+    mbar_init(&s.full[warp][1], 1);
+    if (warp == 0) {
+      s.abort_flag = 0;
+      prefetch_tensormap(&p.map_codes);
+      prefetch_tensormap(&p.map_sf);
+    }
+    fence_barrier_init();
+    fence_proxy_async_shared();
+  }
   start_next_kernel();
   wait_for_previous_kernel();
   if (warp == 0) {
-    const int32_t total = scan_groups(p.offsets, p.num_experts, p.m, kGemvRows,
-                                      [&](int e, int32_t lo, int32_t, int32_t unit) {
+    int32_t most = 0;
+    const int32_t total = scan_groups(p.offsets, p.num_experts, p.m, p.tile_rows,
+                                      [&](int e, int32_t lo, int32_t rows, int32_t unit) {
                                         off[e] = lo;
                                         first[e] = unit;
+                                        most = max(most, rows);
                                       });
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
     if (lane == 0) {
       off[p.num_experts] = static_cast<int32_t>(p.m);
       first[p.num_experts] = total;
       s.ok_flag = total >= 0;
+      s.x_tile = min(most, p.tile_rows);
     }
   }
   __syncthreads();
@@ -186,6 +208,13 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
     if (blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
     return;
   }
+  // the rows of x, then the rings in what is left: two chunks a warp where they fit, one otherwise
+  const uint32_t xs_off = (kGemvWarps * kGemvRows * kRowsPad * 4 + 8 * (p.num_experts + 1) + 15) & ~15u;
+  uint8_t *xs = dyn + xs_off;
+  const uint32_t ring_off = (xs_off + s.x_tile * x_stride + 1023) & ~1023u;
+  const int depth = ring_off + 2 * kGemvWarps * (kCodeBytes + kScaleBytes) <= p.shared_bytes ? 2 : 1;
+  uint8_t *codes_ring = dyn + ring_off + warp * depth * kCodeBytes;
+  uint8_t *scales_ring = dyn + ring_off + kGemvWarps * depth * kCodeBytes + warp * depth * kScaleBytes;
   // Groups of 128 weight rows (with SwiGLU: gate rows) that an expert's rows lie in, and the units of each.
   const int32_t out_n = kSwiglu ? n / 2 : n;
   const int32_t blocks = n % 128 == 0 ? out_n / 128 : (n + 254) / 128;
@@ -215,68 +244,51 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
   };
   auto present = [&](const Unit &it, int32_t row) { return row >= it.e * n && row < (it.e + 1) * n; };
 
-  // ---- copies of the weights: a cursor that runs `depth` chunks ahead of the sums
-  const uint8_t *code[4];
-  const uint8_t *scale[kSwiglu ? 2 : 1];
-  uint32_t copy_unit = begin + group;
+  // ---- copies of the weights, by lane 0: a cursor that runs `depth` chunks ahead of the sums
+  volatile int *abort_flag = &s.abort_flag;
+  uint32_t copy_unit = share < chunks ? begin + group : end, filled = 0;
   int32_t copy_c = share, copy_e = 0;
-  auto aim = [&] {  // the addresses of copy_unit's chunk copy_c
+  Unit copy{};
+  auto aim = [&] {
     const uint32_t tile = copy_unit / per;
     copy_e = expert_of(tile, copy_e);
-    const Unit it = unit_at(copy_unit, tile, copy_e);
-    const int32_t k0 = copy_c * kChunk + t * 32;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      int32_t row = weight_row(it, q, g);
-      if (!present(it, row)) row = it.e * n;  // another expert's or none: any row, its sums are not used
-      code[q] = p.codes + static_cast<int64_t>(row) * (k / 2) + k0 / 2;
-    }
-#pragma unroll
-    for (int h = 0; h < (kSwiglu ? 2 : 1); ++h) {
-      const int32_t row = weight_row(it, 2 * h, g);
-      const int64_t blk = min(row >> 7, ((it.e + 1) * n - 1) >> 7);
-      scale[h] = p.sf + (blk * (k >> 6) + (k0 >> 6)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4;
-    }
+    copy = unit_at(copy_unit, tile, copy_e);
   };
-  const uint32_t ring = smem_u32(dyn) + warp * (depth * kSlotBytes) + lane * 16;
-  auto copy_next = [&](uint32_t to) {
-    if (copy_unit < end) {
-      const uint32_t bytes = copy_c * kChunk + t * 32 < k ? 16u : 0u;
+  auto copy_next = [&](int slot) {
+    if (lane == 0 && copy_unit < end) {
+      uint64_t *bar = &s.full[warp][slot];
+      mbar_arrive_expect_tx(bar, kCodeBytes + kScaleBytes);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) copy16(to + q * 512, code[q], bytes);
-      if (kSwiglu) {
-        copy8(to + 4 * 512, scale[0], bytes >> 1);
-        copy8(to + 4 * 512 + 8, scale[kSwiglu ? 1 : 0], bytes >> 1);
-      } else {
-        copy16(to + 4 * 512, scale[0], bytes);
+      for (int q = 0; q < 4; ++q)
+        tma_load_2d_own(codes_ring + slot * kCodeBytes + q * kBoxBytes, &p.map_codes, bar, copy_c * (kChunk / 2),
+                        weight_row(copy, q, 0));
+#pragma unroll
+      for (int h = 0; h < (kSwiglu ? 2 : 1); ++h) {
+        const int32_t row = weight_row(copy, 2 * h, 0);
+        tma_load_3d_own(scales_ring + slot * kScaleBytes + h * kTilesBytes, &p.map_sf, bar, (row & 31) * 16,
+                        copy_c * (kChunk / 64), row >> 7);
       }
+      ++filled;
       copy_c += kShare;
-      if (copy_c < chunks) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) code[q] += kShare * (kChunk / 2);
-#pragma unroll
-        for (int h = 0; h < (kSwiglu ? 2 : 1); ++h) scale[h] += kShare * (kChunk / 64) * 512;
-      } else {
+      if (copy_c >= chunks) {
         copy_unit += kGroups;
         copy_c = share;
         if (copy_unit < end) aim();
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    __syncwarp();
   };
-  if (share >= chunks) copy_unit = end;  // no chunk for this warp
   if (copy_unit < end) aim();
-  copy_next(ring);
-  if (depth == 2) copy_next(ring + kSlotBytes);
-  uint32_t slot = 0;
+  for (int d = 0; d < depth; ++d) copy_next(d);
+  uint32_t used = 0;  // chunks so far
 
   const uint32_t xs_at = smem_u32(xs);
   int32_t e = 0;
   uint32_t i = begin + group;
   for (uint32_t tile = begin / per; tile * per < end; ++tile) {
     e = expert_of(tile, e);
-    const int32_t skip = (static_cast<int32_t>(tile) - first[e]) * kGemvRows;
-    const int32_t row0 = off[e] + skip, rows = min(kGemvRows, off[e + 1] - off[e] - skip);
+    const int32_t skip = (static_cast<int32_t>(tile) - first[e]) * p.tile_rows;
+    const int32_t row0 = off[e] + skip, rows = min(p.tile_rows, off[e + 1] - off[e] - skip);
 
     // ---- the tile's rows of x: the power of two of each, then their values in the order in which the lanes read them.
     // 16 / 2^j warps to a row.
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
     auto place = [&](bool half) {
       bool exact = true;
       for (int c = slice * 32 + lane; c < chunks * (kChunk / 8); c += per_row * 32) {
-        uint4 v = make_uint4(0, 0, 0, 0);  // behind k, in a last chunk of 64
+        uint4 v = make_uint4(0, 0, 0, 0);  // behind k
         if (c < k / 8) v = *reinterpret_cast<const uint4 *>(src + 8 * c);
         uint4 o;
         if (half) {
@@ -345,7 +357,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
           o = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                          __byte_perm(v.y, v.w, 0x7632));
         }
-        // piece c = 16 chunk + 4 t + j of the row goes where the lanes t = 0 .. 3 read their j-th side by side
+        // piece c = 16 half + 4 t + j of the row goes where the lanes t = 0 .. 3 read their j-th side by side
         const int at = (c & ~15) + 4 * (c & 3) + ((c >> 2) & 3);
         *reinterpret_cast<uint4 *>(xs + mine * x_stride + 16 * at) = o;
       }
@@ -357,46 +369,61 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       __syncthreads();
     }
     // (rows of x that are not there: the first, whose sums are not used)
-    const uint32_t x_lane = xs_at + (g < rows ? g : 0) * x_stride + t * 16;
+    const uint32_t x_lane = xs_at + (lane / 4 < rows ? lane / 4 : 0) * x_stride + t * 16;
 
     // ---- the units of this tile
     const uint32_t stop = min(end, (tile + 1) * per);
     for (; i < stop; i += kGroups) {
+      const Unit it = unit_at(i, tile, e);
+      const uint32_t quarters = kSwiglu ? (it.part & 1) * 8 : 0;  // SwiGLU: its two words of a row's four
       float acc[kSets][2][4] = {};
       auto sums = [&](auto half_tag) {
         constexpr bool kHalf = decltype(half_tag)::value;
         auto add_chunk = [&](int32_t c, float(&to)[2][4]) {
-          if (depth == 2)
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-          else
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-          const uint32_t from = ring + slot;
-          uint4 codes[4];
-          const uint4 w = shared16(from + 4 * 512);
+          const int slot = depth == 2 ? used & 1 : 0;
+          // (a wait that ran out: garbage from here on, which is not stored, and no more copies)
+          if (!mbar_wait(&s.full[warp][slot], (depth == 2 ? used >> 1 : used) & 1, abort_flag, p.status)) copy_unit = end;
+          __syncwarp();
+          ++used;
+          const uint32_t boxes = smem_u32(codes_ring) + slot * kCodeBytes + g * 128;
+          const uint32_t tiles = smem_u32(scales_ring) + slot * kScaleBytes + (t >> 1) * 128 + g * 16 + quarters;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) codes[q] = shared16(from + q * 512);
-          // the slot is read (loads return in order): its next chunk may be on its way
-          asm volatile("" ::"r"(codes[3].x), "r"(codes[3].w) : "memory");
-          copy_next(from);
-          if (depth == 2) slot = kSlotBytes - slot;
-          uint32_t sc[4][2];
-          decode_scales<kHalf>(w.x >> (16 * (t & 1)), sc[0]);
-          decode_scales<kHalf>(w.y >> (16 * (t & 1)), sc[1]);
-          decode_scales<kHalf>(w.z >> (16 * (t & 1)), sc[2]);
-          decode_scales<kHalf>(w.w >> (16 * (t & 1)), sc[3]);
+          for (int half = 0; half < 2; ++half) {
+            uint4 codes[4], w;  // w: the words of the four rows' scales
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 8 of the lane's 32 k
-            uint32_t a[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint4 &v = codes[q];
-              decode8<kHalf>(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, sc[q][j >> 1], a[q]);
+            for (int q = 0; q < 4; ++q) codes[q] = shared16(boxes + q * kBoxBytes + (((4 * half + t) ^ g) * 16));
+            if (kSwiglu) {
+              const uint2 gate = shared8(tiles + half * 256), up = shared8(tiles + half * 256 + kTilesBytes);
+              w = make_uint4(gate.x, gate.y, up.x, up.y);
+            } else {
+              w = shared16(tiles + half * 256);
             }
-            const uint4 x = shared16(x_lane + c * (kChunk * 2) + 64 * j);
+            if (half == 1) {  // all of the slot is read: its next chunk may be on its way
+              asm volatile("" ::"r"(codes[3].w), "r"(w.w) : "memory");
+              __syncwarp();
+              copy_next(slot);
+            }
+            const int32_t k0 = c * kChunk + half * 128;
+            if (k0 >= k) continue;
+            uint32_t sc[4][2];
+            decode_scales<kHalf>(w.x >> (16 * (t & 1)), sc[0]);
+            decode_scales<kHalf>(w.y >> (16 * (t & 1)), sc[1]);
+            decode_scales<kHalf>(w.z >> (16 * (t & 1)), sc[2]);
+            decode_scales<kHalf>(w.w >> (16 * (t & 1)), sc[3]);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              mma_16816<kHalf>(to[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
-              mma_16816<kHalf>(to[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
+            for (int j = 0; j < 4; ++j) {  // 8 of the lane's 32 k
+              uint32_t a[4][4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint4 &v = codes[q];
+                decode8<kHalf>(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, sc[q][j >> 1], a[q]);
+              }
+              const uint4 x = shared16(x_lane + k0 * 2 + 64 * j);
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                mma_16816<kHalf>(to[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
+                mma_16816<kHalf>(to[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
+              }
             }
           }
         };
@@ -427,10 +454,10 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
         for (int j = 0; j < 4; ++j) to_part[(2 * t + (j & 1)) * kRowsPad + 8 * (2 * m + (j >> 1)) + g] = acc[0][m][j];
       auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kShare) : "memory"); };
       meet();
-      const Unit it = unit_at(i, tile, e);
+      const bool stop = *abort_flag != 0;  // some warp's sums are garbage
       constexpr int kOut = kSwiglu ? 16 : 32;  // outputs of a row of x
       const float *theirs = part + group * kShare * kGemvRows * kRowsPad;
-      for (int o = share * 32 + lane; o < kOut * rows; o += 32 * kShare) {
+      for (int o = share * 32 + lane; o < kOut * rows && !stop; o += 32 * kShare) {
         const int tok = o / kOut, in = o % kOut;  // slot in / 8, lane row in % 8
         const int32_t row = weight_row(it, in >> 3, in & 7);
         if (!present(it, row)) continue;
@@ -455,13 +482,19 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       meet();
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  // A wait that ran out leaves copies behind: they land before the CTA can exit.
+  if (lane == 0)
+    for (uint32_t f = filled > static_cast<uint32_t>(depth) ? filled - depth : 0; f < filled; ++f)
+      mbar_drain(&s.full[warp][depth == 2 ? f & 1 : 0], (depth == 2 ? f >> 1 : f) & 1);
 }
+
+// Rows of x taken at a time: eight with 7168 of k are half of an SM's shared memory.
+int32_t gemv_tile_rows(int64_t k) { return k <= 7168 ? kGemvRows : kGemvRows / 2; }
 
 // An upper bound of a call's units.
 int64_t unit_bound(const LaunchGemv &a) {
   const int64_t per = a.swiglu ? a.n / 256 * 8 : (a.n % 128 == 0 ? a.n / 128 : (a.n + 254) / 128) * 4;
-  return (a.m / kGemvRows + std::min<int64_t>(a.num_experts, a.m)) * per;
+  return (a.m / gemv_tile_rows(a.k) + std::min<int64_t>(a.num_experts, a.m)) * per;
 }
 
 template <bool kSwiglu, int kShare>
@@ -470,16 +503,15 @@ cudaError_t launch_gemv(LaunchGemv a) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
   if (err != cudaSuccess) return err;
-  a.x_tile = static_cast<int32_t>(std::min<int64_t>(kGemvRows, a.m));
-  const int rest = a.x_tile * static_cast<int>((a.k + kChunk - 1) / kChunk * kChunk * 2 + kXPad) + kGemvWarps * kGemvRows * kRowsPad * 4 +
-                   8 * (a.num_experts + 1);
-  // two chunks of each warp where they fit beside x, else one
-  constexpr int kSlots = kGemvWarps * static_cast<int>(kSlotBytes);
-  a.depth = rest + 2 * kSlots <= 227 * 1024 - 256 ? 2 : 1;
+  a.tile_rows = gemv_tile_rows(a.k);
+  // all the shared memory of an SM: how it is used follows from the rows of the experts
+  cudaFuncAttributes f{};
+  if ((err = cudaFuncGetAttributes(&f, reinterpret_cast<const void *>(kernel))) != cudaSuccess) return err;
+  a.shared_bytes = 227 * 1024 - static_cast<uint32_t>(f.sharedSizeBytes) - 1024;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, unit_bound(a))), 1, 1);
   cfg.blockDim = dim3(kGemvThreads, 1, 1);
-  cfg.dynamicSmemBytes = rest + a.depth * kSlots;
+  cfg.dynamicSmemBytes = a.shared_bytes + 1024;
   cfg.stream = a.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
