@@ -505,9 +505,7 @@ cudaError_t launch_gemv(LaunchGemv a) {
   if (err != cudaSuccess) return err;
   a.tile_rows = gemv_tile_rows(a.k);
   // all the shared memory of an SM: how it is used follows from the rows of the experts
-  cudaFuncAttributes f{};
-  if ((err = cudaFuncGetAttributes(&f, reinterpret_cast<const void *>(kernel))) != cudaSuccess) return err;
-  a.shared_bytes = 227 * 1024 - static_cast<uint32_t>(f.sharedSizeBytes) - 1024;
+  a.shared_bytes = 226 * 1024 - (sizeof(SharedGemv) + 127) / 128 * 128;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, unit_bound(a))), 1, 1);
   cfg.blockDim = dim3(kGemvThreads, 1, 1);
@@ -521,15 +519,17 @@ cudaError_t launch_gemv(LaunchGemv a) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// How many warps share a unit: the more units an SM gets, the fewer, as each meeting of warps costs.  Measured, us
-// with 8 / 4 / 2 warps: gate/up of 4096 x 7168 with SwiGLU, one expert with one row (0.8 units an SM) 9.5 / 11.1 / 15.8, two with
-// one each (1.7) 13.4 / 12.9 / 16.7, eight (7) 35.6 / 32.2 / 32.1; down projection of 7168 x 2048, one expert (1.5) 7.6 / 7.4 /
-// 7.8, four (6) 15.1 / 13.6 / 12.2, eight (12) 27.5 / 22.7 / 20.8.
+// How many warps share a unit: eight while the SMs have few, then as few as the chunks of k make worth a meeting.  Measured,
+// us with 8 / 4 / 2 warps: gate/up of 4096 x 7168 with SwiGLU, one expert with one row (0.8 units an SM) 9.5 / 11.0 / 18.5, two
+// with one each (1.7) 12.8 / 13.4 / 19.2, four (3.4) 20.2 / 18.4 / 21.9, eight (7) 33.2 / 31.0 / 31.9, 32 (27) 102 / 98 / 98;
+// down projection of 7168 x 2048, one expert (1.5) 7.0 / 7.3 / 8.9, four (6) 13.8 / 13.1 / 12.0, 32 (47) 70 / 60 / 56; 8 experts
+// of 1000 x 1344 with 74 rows (4) 10.7 / 11.5 / 13.1.
 template <bool kSwiglu>
 cudaError_t launch_gemv(const LaunchGemv &a) {
   const int64_t units = unit_bound(a);
-  if (2 * units < 3 * a.num_sms) return launch_gemv<kSwiglu, 8>(a);
-  return a.k <= 2048 && units >= 4 * a.num_sms ? launch_gemv<kSwiglu, 2>(a) : launch_gemv<kSwiglu, 4>(a);
+  const bool short_k = a.k <= 2048;
+  if (units < (short_k ? 5 : 3) * a.num_sms) return launch_gemv<kSwiglu, 8>(a);
+  return short_k ? launch_gemv<kSwiglu, 2>(a) : launch_gemv<kSwiglu, 4>(a);
 }
 
 }  // namespace

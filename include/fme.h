@@ -599,8 +599,9 @@ fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, con
  * src_row is given.  The activations are not quantized: only the weights' rounding is in the result ("Composer 2
  * Technical Report", section 6.1, the NVFP4 variant, whose weights these are).  c sf is exact in bf16, products and sums
  * are in fp32 on the tensor cores, S is applied in fp32, one rounding to bf16.  A row's result does not depend on any
- * other row.  Any number of rows is computed; the weights are read again for every 8 to 32 rows of an expert, so that with
- * many rows grouped_gemm_fwd_nvfp4 on quantized rows is the faster call.
+ * other row (as long as its products are normal numbers of fp32).  Any number of rows is computed; the weights are read again
+ * for every 8 rows of an expert (4 with k above 7168), so that with many rows grouped_gemm_fwd_nvfp4 on
+ * quantized rows is the faster call.
  *
  *   x         device bf16 [x_rows x k]
  *   src_row   device int32 [m] from moe_route: row t of the grouped rows is x[src_row[t] / top_k], m = x_rows * top_k.  An

@@ -1,5 +1,6 @@
-"""The bf16 products' bounded waits in a build whose waits give up after 1 ns (as tests/test_gpu_block128_timeout.py).
-Every run must report FME_DEV_TIMEOUT or give the normal build's bits, each pair kernel must time out at least once, and the
+"""The bounded waits of the bf16 products and of those with NVFP4 weights in a build whose waits give up after 1 ns (as tests/test_gpu_block128_timeout.py).
+Every run must report FME_DEV_TIMEOUT or give the normal build's bits, each pair kernel must time out at least once (the others'
+waits may end within a poll), and the
 normal build's result afterwards must be unchanged.  No wait is made to hang: copies and MMAs in flight are awaited
 with a limit of their own."""
 import pytest
@@ -45,3 +46,16 @@ def test_wgrad(short_lib, first):  # noqa: F811
     check(lambda st: fme.grouped_gemm_wgrad_bf16(dy, x, off, dtype=torch.float32, status=st),
           lambda y, st, s: short_lib.grouped_gemm_wgrad_bf16(dy.data_ptr(), x.data_ptr(), m, off.data_ptr(), 2, N, N,
                                                              y.data_ptr(), fme.DW_FP32, st, s))
+
+
+@pytest.mark.parametrize("rows, k", [(5, 8192), (40, 2048)])
+def test_products_with_nvfp4_weights(short_lib, rows, k):  # noqa: F811
+    experts, n = 3, 2048
+    off = i32(0, rows // 2, rows // 2, rows)
+    codes, sf, scale = fme.quantize_nvfp4_pertoken(ref.normal((experts * n, k), 0.05, 1))
+    x = ref.normal((rows, k), 1.0, 2)
+    for name in ("grouped_gemv_nvfp4", "grouped_gemv_nvfp4_swiglu"):
+        check(lambda st: getattr(fme, name)(x, codes, sf, scale, off, status=st),
+              lambda y, st, s: getattr(short_lib, name)(x.data_ptr(), rows, None, 1, codes.data_ptr(), sf.data_ptr(),
+                                                        scale.data_ptr(), off.data_ptr(), experts, rows, n, k,
+                                                        y.data_ptr(), st, s), gives_up=False)
