@@ -953,7 +953,7 @@ fme_status bf16_rows_gemm(bool dgrad, const void *a_rows, const void *w, const i
   if (st != FME_OK) return st;
   a.k = dgrad ? n : k;
   a.n = dgrad ? k : n;
-  const bool few = !dgrad && fme::bf16_few_rows(m, num_experts);
+  const bool few = !dgrad && fme::bf16_few_rows(m, n, num_experts, a.num_sms);
   CUtensorMap &rows_map = few ? a.map_b : a.map_a, &w_map = few ? a.map_a : a.map_b;
   if ((st = encode_bf16_2d(&rows_map, a_rows, m, a.k, few ? 16 : 128)) != FME_OK) return st;
   st = dgrad ? encode_bf16_mn(&w_map, &a.wide_b, w, num_experts, n, k)

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 namespace fme {
@@ -189,12 +190,14 @@ struct LaunchBf16 {
   cudaStream_t stream;
 };
 // The forward takes its few-rows form (map_a = weights in 128-row boxes, map_b = tokens in 16-row
-// boxes) up to this many rows: there it reads the weights once, past it the token tiles of 64 read them again and again.
-// Measured, us (few rows / pairs): 32 experts of 4096 x 7168, 8 rows 91 / 107, 1536 rows 292 / 312, 2048 rows 300 / 312, 4096
-// rows 527 / 320; one expert, 1 row 33 / 42, 128 rows 46 / 44, 512 rows 83 / 46; 8 experts of 1048 x 1400, 400 rows 17 / 21,
-// 999 rows 17 / 19; 4 experts of 7168 x 2048, 256 rows 36 / 40, 512 rows 44 / 42.
-inline bool bf16_few_rows(int64_t m, int32_t num_experts) {
-  return m <= 16 + 48 * static_cast<int64_t>(num_experts);
+// boxes) up to this many rows: there it reads the weights once, past it the token tiles of 64 read them again and again.  It is
+// also taken while every item has an SM to itself.  Measured, us (few rows / pairs), even loads: 32 experts of 4096 x 7168, 1024
+// rows 270 / 293, 2048 rows 277 / 315, 3000 rows 370 / 324 (uneven loads fill more tiles: the border is at 48 rows an
+// expert); one expert, 16 rows 23 / 36, 256 rows 28 / 36, 384 rows 52 / 37; 8 experts of 1048 x 1400, 400 rows 11 / 14, 1400 rows
+// 18 / 15; 4 experts of 7168 x 2048, 256 rows 25 / 29, 768 rows 42 / 31.
+inline bool bf16_few_rows(int64_t m, int64_t n, int32_t num_experts, int num_sms) {
+  const int64_t tiles = num_experts == 1 ? (m + 63) / 64 : m / 64 + std::min<int64_t>(num_experts, m);
+  return m <= 16 + 48 * static_cast<int64_t>(num_experts) || tiles * ((n + 127) / 128) <= num_sms;
 }
 cudaError_t launch_bf16_fwd(const LaunchBf16 &a);
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a);

@@ -495,9 +495,10 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
 // empty and put the weights on half as many SMs.  A sum's steps over k are those of the tiles above, in the same
 // order: a row's bits are the same in both forms.
 //   warp 0 producer of W, warp 1 MMA issuer, warps 2-5 epilogue (thread = row of W), warp 6 producer of the tokens.
-// A stage holds 128 of k, as two halves of 64: what bounds a CTA that has an SM to itself is the producer's and the
-// issuer's way around their loops (4096 x 7168, one expert with one row, 32 CTAs: 28 us with 64 of k in nine stages, 21 with
-// 128 in four; 8 of 32 experts, 256 CTAs, 72.8 and 72.3).
+// A stage holds 128 of k, as two halves of 64: what bounds a CTA that has an SM to itself is the producers' and the
+// issuer's way around their loops (4096 x 7168, one expert with one row, 32 CTAs: 28.1 us with 64 of k in nine stages, 24.8
+// with 128 in four, 22.5 with a producer of its own for the tokens; with 64 rows 41, 39 and 28).  8 of 32 experts with a
+// row each, 256 items: 72.5 us, 6.5 TB/s of weights; all 32 experts 270 us.
 constexpr int kFewTokens = 64;
 constexpr int kFewStages = 4;
 constexpr int kFewThreads = 224;
@@ -807,7 +808,7 @@ cudaError_t launch_few(const LaunchBf16 &a) {
 }  // namespace
 
 cudaError_t launch_bf16_fwd(const LaunchBf16 &a) {
-  return bf16_few_rows(a.m, a.num_experts) ? launch_few(a) : launch_bf<KindBf::kFwd>(a);
+  return bf16_few_rows(a.m, a.n, a.num_experts, a.num_sms) ? launch_few(a) : launch_bf<KindBf::kFwd>(a);
 }
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kDgrad>(a); }
 cudaError_t launch_bf16_wgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kWgrad>(a); }

@@ -57,10 +57,12 @@ def forward64(x, w, off):
     return y, size
 
 
-# rows, experts, n, k: the first are in the form for few rows, the others in tiles
+# rows, experts, n, k: those of the first three lines are in the form for few rows, the others in tiles
 FORWARD = [(1, 1, 8, 8), (1, 4, 128, 64), (3, 2, 136, 72), (16, 1, 256, 200), (17, 3, 1048, 1400), (64, 1, 129 * 8, 512),
            (65, 1, 256, 64), (200, 40, 384, 328), (288, 1, 64, 64), (289, 1, 64, 64), (600, 2, 8, 16), (700, 3, 264, 24),
-           (1999, 8, 1048, 1400), (1500, 5, 520, 72), (4000, 7, 256, 512), (33100, 1024, 40, 136)]
+           (1500, 5, 520, 72), (4000, 7, 256, 512), (33100, 1024, 40, 136),
+           (1999, 8, 1048, 1400), (9000, 5, 520, 72), (9000, 7, 256, 512), (10000, 2, 8, 16), (15000, 1, 72, 8),
+           (60000, 1024, 40, 136)]
 
 
 @pytest.mark.parametrize("rows,experts,n,k", FORWARD)
@@ -129,22 +131,22 @@ def test_wgrad_added_into_fp32(rows, experts, n, k, status):
 
 def test_a_rows_bits_do_not_depend_on_the_batch(status):
     """One row alone, a few (the form for few rows) and the whole batch (tiles)."""
-    rows, experts, n, k = 900, 3, 392, 1352
-    off = [0, 500, 500, 900]
+    rows, experts, n, k = 6000, 3, 392, 1352
+    off = [0, 500, 500, 6000]
     x, w = ref.normal((rows, k), 1.0, 1), ref.normal((experts, n, k), 0.05, 2)
     y = fme.grouped_gemm_fwd_bf16(x, w, i32(off), status=status)
     few = fme.grouped_gemm_fwd_bf16(x[450:600].contiguous(), w, i32([0, 50, 50, 150]), status=status)
     assert torch.equal(few, y[450:600])
-    for r in (0, 499, 500, 899):
+    for r in (0, 499, 500, 899, 5999):
         e = 0 if r < 500 else 2
         one = fme.grouped_gemm_fwd_bf16(x[r:r + 1], w, i32([0] * (e + 1) + [1] * (experts - e)), status=status)
         assert torch.equal(one[0], y[r])
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_one_experts_values_do_not_reach_anothers(bad, status):
-    rows, n, k = 300, 136, 200
-    off = [0, 70, 70, 133, 300]
+@pytest.mark.parametrize("off", [[0, 70, 70, 133, 300], [0, 70, 70, 133, 9000]])
+def test_one_experts_values_do_not_reach_anothers(off, bad, status):
+    rows, n, k = off[-1], 136, 200
     dy, x, w = ref.normal((rows, n), 0.5, 1), ref.normal((rows, k), 0.5, 2), ref.normal((4, n, k), 0.05, 3)
     clean = (fme.grouped_gemm_wgrad_bf16(dy, x, i32(off), status=status),
              fme.grouped_gemm_dgrad_bf16(dy, w, i32(off), status=status),
@@ -164,11 +166,10 @@ def test_one_experts_values_do_not_reach_anothers(bad, status):
 
 @pytest.mark.parametrize("offsets", [[0, 5, 3, 300], [1, 5, 9, 300], [0, 5, 9, 299], [0, 5, 9, 301], [0, -5, 9, 300]])
 def test_malformed_offsets_are_reported_and_nothing_is_written(offsets):
-    rows, n, k = 300, 64, 72
+    rows, n, k = 30000, 64, 72
     dy, x, w = ref.normal((rows, n), 0.5, 1), ref.normal((rows, k), 0.5, 2), ref.normal((3, n, k), 0.05, 3)
-    for few in (False, True):
-        m = 40 if few else rows
-        off = i32([min(o, m) if o < 299 else o - rows + m for o in offsets])
+    for m in (rows, 40):  # in tiles, and the form for few rows
+        off = i32([o if o < 299 else o - 300 + m for o in offsets])
         for call, out in ((lambda st, o: fme.grouped_gemm_fwd_bf16(x[:m], w, off, y=o, status=st), (m, n)),
                           (lambda st, o: fme.grouped_gemm_dgrad_bf16(dy[:m], w, off, dx=o, status=st), (m, k)),
                           (lambda st, o: fme.grouped_gemm_wgrad_bf16(dy[:m], x[:m], off, dw=o, status=st), (3, n, k))):
@@ -179,8 +180,9 @@ def test_malformed_offsets_are_reported_and_nothing_is_written(offsets):
             assert bool((o == 7.0).all())
 
 
-def test_nothing_outside_the_outputs_is_written(status):
-    rows, experts, n, k = 333, 4, 1048, 88
+@pytest.mark.parametrize("rows", [333, 3333])
+def test_nothing_outside_the_outputs_is_written(rows, status):
+    experts, n, k = 4, 1048, 88
     off = i32(ref.split(rows, experts, 5))
     dy, x, w = ref.normal((rows, n), 0.5, 1), ref.normal((rows, k), 0.5, 2), ref.normal((experts, n, k), 0.05, 3)
 
@@ -205,9 +207,9 @@ def test_nothing_outside_the_outputs_is_written(status):
 
 def test_captured_and_replayed_with_other_loads(status):
     """A graph of the three products, replayed after the rows and their grouping changed."""
-    rows, experts, n, k = 700, 4, 136, 264
+    rows, experts, n, k = 9000, 4, 136, 264
     dy, x, w = ref.normal((rows, n), 0.5, 1), ref.normal((rows, k), 0.5, 2), ref.normal((experts, n, k), 0.05, 3)
-    off = i32([0, 100, 350, 350, 700])
+    off = i32([0, 100, 350, 350, 9000])
 
     def calls():
         return (fme.grouped_gemm_fwd_bf16(x, w, off, status=status), fme.grouped_gemm_dgrad_bf16(dy, w, off, status=status),
@@ -219,7 +221,7 @@ def test_captured_and_replayed_with_other_loads(status):
     with torch.cuda.graph(graph):
         out = calls()
     x.copy_(ref.normal((rows, k), 0.5, 7))
-    off.copy_(i32([0, 0, 1, 690, 700]))
+    off.copy_(i32([0, 0, 1, 8990, 9000]))
     for _ in range(2):
         for o in out:
             o.fill_(0)
@@ -229,8 +231,8 @@ def test_captured_and_replayed_with_other_loads(status):
 
 
 def test_on_a_stream_of_its_own(status):
-    rows, experts, n, k = 300, 3, 264, 520
-    off = i32([0, 120, 120, 300])
+    rows, experts, n, k = 9000, 3, 264, 520
+    off = i32([0, 120, 120, 9000])
     dy, x, w = ref.normal((rows, n), 0.5, 1), ref.normal((rows, k), 0.5, 2), ref.normal((experts, n, k), 0.05, 3)
     want = (fme.grouped_gemm_fwd_bf16(x, w, off), fme.grouped_gemm_dgrad_bf16(dy, w, off),
             fme.grouped_gemm_wgrad_bf16(dy, x, off))

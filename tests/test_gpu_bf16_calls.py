@@ -35,7 +35,7 @@ def calls(seed):
     """Calls of different inputs for each seed, as functions of the stream."""
     g = torch.Generator(device=DEV)
     g.manual_seed(seed)
-    tokens, top_k, experts, n, k = 150, 4, 6, 256, 384
+    tokens, top_k, experts, n, k = 3000, 4, 6, 256, 384
     ids = torch.rand((tokens, experts), generator=g, device=DEV).argsort(dim=1)[:, :top_k].int().contiguous()
     off, _, src = fme.moe_route(ids, experts)
     x, w = ref.normal((tokens, k), 1.0, seed), ref.normal((experts, n, k), 0.05, seed + 1)
@@ -103,7 +103,7 @@ def test_outputs_that_the_current_stream_still_reads(name):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("rows", [40, 1500])
+@pytest.mark.parametrize("rows", [40, 4000])
 def test_each_call_reads_what_the_call_before_wrote(rows):
     """A chain through the same buffers, many times, with other rows each time: the bits of a chain that waits after
     every call.  40 rows: the forward's form for few."""

@@ -18,7 +18,7 @@ def i32(*v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-@pytest.mark.parametrize("counts, pairs", [((200, 456), True), ((3, 40), False)])
+@pytest.mark.parametrize("counts, pairs", [((2000, 4560), True), ((3, 40), False)])
 def test_forward(short_lib, counts, pairs):  # noqa: F811
     m = sum(counts)
     off = i32(0, counts[0], m)

@@ -49,7 +49,7 @@ def reference(x, w_router, w_gate_up, w_down, ids, score, scale, top_k, alpha):
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
-@pytest.mark.parametrize("hidden,inter,experts,top_k,tokens", [(512, 256, 8, 2, 600), (400, 136, 5, 3, 77)])
+@pytest.mark.parametrize("hidden,inter,experts,top_k,tokens", [(512, 256, 8, 2, 600), (400, 136, 5, 3, 77), (256, 192, 4, 2, 9000)])
 def test_layer_against_fp32_autograd(example, score, hidden, inter, experts, top_k, tokens):
     layer = example.MoELayer(hidden, inter, experts, top_k, score=score, alpha=0.5, scale=2.0, seed=3)
     g = torch.Generator(device="cuda")
