@@ -1,7 +1,7 @@
 """GB300-native low-precision MoE expert path: NVFP4 per-token forward, MXFP8 backward.
 
 A thin binding over ``libfme.so`` (C ABI in ``include/fme.h``): ctypes, and a compiled
-module for the FP8 block-128 and router calls, whose host side would outlast
+module for the FP8 block-128, bf16, 4-bit and router calls, whose host side would outlast
 their kernels in Python.  Every step of the path runs in the library's CUDA
 kernels; the binding only turns torch tensors into pointers, allocates outputs
 with torch when the caller does not pass them, and turns status codes into

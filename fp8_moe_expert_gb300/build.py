@@ -112,7 +112,8 @@ def _without_binding(error: Exception) -> None:
     headers of Python and torch; its own calls raise until it is built, so an outdated one is taken away."""
     if os.path.exists(BINDING):
         os.remove(BINDING)
-    warnings.warn(f"the compiled binding was not built, the FP8 block-128 and router calls will raise: {error}",
+    warnings.warn(f"the compiled binding was not built, the FP8 block-128, bf16, 4-bit and router calls will "
+                  f"raise: {error}",
                   RuntimeWarning, stacklevel=3)
 
 

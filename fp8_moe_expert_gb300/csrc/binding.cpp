@@ -1,4 +1,4 @@
-// binding.cpp -- the Python side of the FP8 block-128, router and combine-gradient calls: checks
+// binding.cpp -- the Python side of the FP8 block-128, bf16, 4-bit, router and combine-gradient calls: checks
 // torch tensors, allocates the outputs that the caller does not bring, takes the current stream or the given one
 // and calls the C ABI (include/fme.h).
 //

@@ -10,6 +10,18 @@
 // Products and sums are kept in fp32 in tensor memory over the whole contraction, in steps of 16 in order, and rounded
 // once: there is no split, so a row's result depends neither on other rows nor on which form below runs.
 //
+// What bounds them.  A stage of 64 of the contraction takes a pair's M = 256, N = 256 MMAs 512 cycles; the 48 KB that
+// they read of an SM's shared memory and the 32 KB that the copies write there take 640 at 128 bytes a cycle, and 620 are
+// measured (without the copies the MMAs run at their rate).  65536 x 4096 x 7168, one expert: forward 1.95 ms,
+// 1.98 PFLOP/s, dgrad 1.96, wgrad 1.92; 32 experts of 2048 rows of 7168 x 2048: 0.99, 0.99 and 0.99 ms.  Kept up for
+// seconds, the power cap sets 1.61 PFLOP/s.  Tiles are 256 x 256 a pair, two accumulators in tensor memory, a ring of six
+// 32 KB stages.  12 warps a CTA:
+//   warp 0      producer: A and B by TMA, completing on the leader's barriers;
+//   warp 1      allocates tensor memory; in the leader issues the MMAs, a commit a stage frees it in both CTAs, one a tile
+//               hands the accumulator to both epilogues;
+//   warp 2      wgrad: the copies of blocks at an expert's end;
+//   warps 4-11  epilogue: 32 rows x 128 columns each, while the next tile's MMAs run.
+//
 // wgrad's contraction runs over the rows of one expert, and the block of 64 rows at an expert's end reaches into the
 // next expert's.  Those must read as zeros in both operands (0 times a NaN of another expert would be NaN), so the last
 // block comes in boxes of 8 rows, the group of 8 that holds the end in boxes of one row, and a box of rows that are not the
@@ -98,8 +110,8 @@ __device__ __forceinline__ TileBf tile_bf(const LaunchBf16 &p, const Tables &s, 
     tl.p1 = s.off[tl.e + 1];
     // Row by row of the expert's tiles.  Where its operands do not fit in L2 (64 MB as the border) the tiles worked on at
     // a time read each operand again from memory, the less the nearer they are to a square: bands of 8 tiles' height
-    // then, column by column (65536 rows, one expert of 4096 x 7168: 2.23 -> 2.09 ms; 32 experts of 2048 rows 2.18
-    // with bands, 2.14 without).
+    // then, column by column (65536 rows, one expert of 4096 x 7168: 2.19 -> 2.05 ms; 512 rows of each of 32 experts 0.63
+    // with bands, 0.61 without).
     uint32_t row, col;
     if (static_cast<int64_t>(tl.p1 - tl.p0) * (p.m + p.n) > (int64_t(64) << 19)) {
       const uint32_t band = rem / (8 * nb), in = rem - band * 8 * nb, high = min(8u, mb - 8 * band);
@@ -452,8 +464,8 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
             }
           }
           // A whole block leaves by a bulk store; rows cut by the expert's end or columns by the output's by plain ones.
-          // wgrad's leave by plain ones (fp32, 32 experts of 2048 rows: 1.135 ms, 1.150 by bulk stores; the forward is
-          // 0.5% slower by plain ones).
+          // wgrad's leave by plain ones (32 experts of 2048 rows, 7168 x 2048: 1.00 ms, 1.02 by bulk stores, fp32 1.07 and
+          // 1.09; the forward is 0.5% slower by plain ones).
           const bool bulk = K != KindBf::kWgrad && warp_rows >= 32 && col + wide <= p.n;
           if (bulk) fence_proxy_async_shared();
           __syncwarp();

@@ -18,7 +18,8 @@
 //         bits 8 .. 6 of each half, as bf16 the code's value times 2^-126 (its subnormal 0.5 a bf16 subnormal).  Times
 //         sf 2^118 it is c sf 2^-8.  13 integer operations and 4 products for 8 codes.
 // Both multiply the same values but for a power of two, so the sums' bits are the same (as long as they are normal
-// numbers).
+// numbers).  Gate/up of 4096 x 7168, 8 and all of 32 experts with a row each: 31 and 98 us (4.3 and 5.4 TB/s of weights), in
+// bf16 39 and 127.
 //
 // Any order of k will do as long as both operands follow it.  A unit is 32 weight rows: 8 of each quarter of a group of 128
 // (the tiled layout keeps the scales of rows 32 apart together), or, with SwiGLU, of two quarters of the gate rows
