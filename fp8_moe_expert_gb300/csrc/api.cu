@@ -1045,8 +1045,8 @@ fme_status gemv_nvfp4(bool swiglu, const void *x, int64_t x_rows, const int32_t 
   if (x_rows > (int64_t(1) << 31) - 1) return FME_ERR_UNSUPPORTED_SHAPE;
   if (src_row ? m != x_rows * top_k : m != x_rows || top_k != 1) return FME_ERR_INVALID_ARGUMENT;
   if (k % 64 != 0 || k < 64 || k > 8192 || n < 1 || n > 65536 || (swiglu && n % 256 != 0)) return FME_ERR_UNSUPPORTED_SHAPE;
-  // the number of items, of 8 rows and 32 weight rows at least, stays in 32 bits
-  if (m > (int64_t(1) << 31) - 1 - 256 || (m / 8 + num_experts) * ((n + 254) / 128) * 4 > (int64_t(1) << 31) - 1)
+  // the number of units, of 4 rows and 32 weight rows at least, stays in 32 bits
+  if (m > (int64_t(1) << 31) - 1 - 256 || (m / 4 + num_experts) * ((n + 254) / 128) * 4 > (int64_t(1) << 31) - 1)
     return FME_ERR_UNSUPPORTED_SHAPE;
   if (!offsets) return FME_ERR_INVALID_ARGUMENT;
   if (m == 0) return FME_OK;

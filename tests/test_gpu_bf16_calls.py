@@ -198,3 +198,55 @@ def test_captured_and_replayed(name):
         out.zero_()
         graph.replay()
         assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+def test_tensors_of_more_than_32_bits_of_elements():
+    """Outputs of 2.6e9 elements and weights of 4.3e9 bytes: rows at both ends and in the middle against 64 bits (small
+    integers: every sum is exact)."""
+    def ints(*shape):
+        return torch.randint(-2, 3, shape, device=DEV).to(torch.bfloat16)
+
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    torch.manual_seed(1)
+    m, n, k = 40000, 65536, 8
+    x, w, off = ints(m, k), ints(2, n, k), i32(0, 30000, m)
+    y = fme.grouped_gemm_fwd_bf16(x, w, off, status=st)
+    for r in (0, 29999, 30000, m - 1):
+        assert torch.equal(y[r], (x[r].double() @ w[int(r >= 30000)].double().t()).to(torch.bfloat16))
+    dx = fme.grouped_gemm_dgrad_bf16(y, w, off, status=st)  # rows of y past 2^31 elements
+    for r in (0, m - 1):
+        want = y[r].double() @ w[int(r >= 30000)].double()
+        size = y[r].double().abs() @ w[int(r >= 30000)].double().abs()
+        assert bool(((dx[r].double() - want).abs() <= 2.0 ** -8 * want.abs() + (n + 1) * 2.0 ** -23 * size).all())
+    g = fme.swiglu(y, h=torch.empty((m, n // 2), dtype=torch.bfloat16, device=DEV))
+    assert torch.equal(g[m - 1:], fme.swiglu(y[m - 1:].clone()))
+    d = fme.swiglu_backward(y, g)
+    assert torch.equal(d[m - 1:], fme.swiglu_backward(y[m - 1:].clone(), g[m - 1:].clone()))
+    del d, g
+    src = torch.arange(m - 1, -1, -1, dtype=torch.int32, device=DEV)
+    p = fme.moe_permute(y, src, 1, out=torch.empty_like(y), status=st)
+    assert torch.equal(p[0], y[m - 1]) and torch.equal(p[m - 1], y[0]) and torch.equal(p[30001], y[m - 30002])
+    del p, y
+    experts, n, k = 40, 8192, 8192
+    dy, x = ints(300, n), ints(300, k)
+    off = torch.tensor([0] * experts + [300], dtype=torch.int32, device=DEV)
+    off[1:experts] = 100
+    dw = fme.grouped_gemm_wgrad_bf16(dy, x, off, status=st)
+    assert torch.equal(dw[-1, -5:], (dy[100:, -5:].double().t() @ x[100:].double()).to(torch.bfloat16))
+    assert torch.equal(dw[0, :5], (dy[:100, :5].double().t() @ x[:100].double()).to(torch.bfloat16))
+    assert not bool(dw[1].any())
+    del dw
+    experts, n, k = 64, 16384, 8192
+    codes = torch.randint(0, 256, (experts * n, k // 2), dtype=torch.uint8, device=DEV)
+    sf = torch.full((experts * n * k // 16,), 0x38, dtype=torch.uint8, device=DEV)
+    scale = torch.ones(experts * n, device=DEV)
+    x = ints(3, k)
+    off = torch.tensor([0] * (experts - 1) + [1, 3], dtype=torch.int32, device=DEV)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, off, status=st)
+    from tests import nvfp4w
+
+    last = slice((experts - 1) * n, experts * n)
+    w = nvfp4w.values(codes[last][-512:], sf[:512 * k // 16], scale[:512])
+    assert torch.equal(y[1:, -512:], (x[1:].double() @ w.t()).to(torch.bfloat16))
+    assert fme.read_device_status(st)[0] == 0
