@@ -18,8 +18,8 @@
 //         bits 8 .. 6 of each half, as bf16 the code's value times 2^-126 (its subnormal 0.5 a bf16 subnormal).  Times
 //         sf 2^118 it is c sf 2^-8.  13 integer operations and 4 products for 8 codes.
 // Both multiply the same values but for a power of two, so the sums' bits are the same (as long as they are normal
-// numbers).  Gate/up of 4096 x 7168, 8 and all of 32 experts with a row each: 31 and 98 us (4.3 and 5.4 TB/s of weights), in
-// bf16 39 and 127.
+// numbers).  Gate/up of 4096 x 7168, 8 and all of 32 experts with a row each: 30 and 97 us (4.4 and 5.5 TB/s of weights), in
+// bf16 38 and 126.
 //
 // Any order of k will do as long as both operands follow it.  A unit is 32 weight rows: 8 of each quarter of a group of 128
 // (the tiled layout keeps the scales of rows 32 apart together), or, with SwiGLU, of two quarters of the gate rows
@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
   const int32_t k = static_cast<int32_t>(p.k), n = static_cast<int32_t>(p.n);
   const int32_t chunks = (k + kChunk - 1) / kChunk;
   const uint32_t x_stride = chunks * kChunk * 2 + kXPad;  // bytes of a row of x
-  float *part = reinterpret_cast<float *>(dyn);           // [warp][row of x][weight row]
-  int32_t *off = reinterpret_cast<int32_t *>(part + kGemvWarps * kGemvRows * kRowsPad);
+  int32_t *off = reinterpret_cast<int32_t *>(dyn);
   int32_t *first = off + (p.num_experts + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the row of a box that the lane takes: lanes of one phase of an access to shared memory read rows 4 apart, which the
@@ -209,11 +208,18 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
     if (blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
     return;
   }
-  // the rows of x, then the rings in what is left: two chunks a warp where they fit, one otherwise
-  const uint32_t xs_off = (kGemvWarps * kGemvRows * kRowsPad * 4 + 8 * (p.num_experts + 1) + 15) & ~15u;
-  uint8_t *xs = dyn + xs_off;
-  const uint32_t ring_off = (xs_off + s.x_tile * x_stride + 1023) & ~1023u;
-  const int depth = ring_off + 2 * kGemvWarps * (kCodeBytes + kScaleBytes) <= p.shared_bytes ? 2 : 1;
+  // the warps' sums, the rows of x, the rings: two chunks a warp and two buffers of sums where they fit
+  constexpr uint32_t kPartBytes = kGemvWarps * kGemvRows * kRowsPad * 4;
+  const uint32_t part_off = (8 * (p.num_experts + 1) + 15) & ~15u;
+  auto ring_at = [&](uint32_t parts) { return (part_off + parts * kPartBytes + s.x_tile * x_stride + 1023) & ~1023u; };
+  auto fits = [&](uint32_t chunks_ahead, uint32_t parts) {
+    return ring_at(parts) + chunks_ahead * kGemvWarps * (kCodeBytes + kScaleBytes) <= p.shared_bytes;
+  };
+  const int depth = fits(2, 1) ? 2 : 1;
+  const bool two_parts = fits(depth, 2);
+  float *part = reinterpret_cast<float *>(dyn + part_off);  // [buffer][warp][row of x][weight row]
+  uint8_t *xs = dyn + part_off + (two_parts ? 2 : 1) * kPartBytes;
+  const uint32_t ring_off = ring_at(two_parts ? 2 : 1);
   uint8_t *codes_ring = dyn + ring_off + warp * depth * kCodeBytes;
   uint8_t *scales_ring = dyn + ring_off + kGemvWarps * depth * kCodeBytes + warp * depth * kScaleBytes;
   // Groups of 128 weight rows (with SwiGLU: gate rows) that an expert's rows lie in, and the units of each.
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
 
   const uint32_t xs_at = smem_u32(xs);
   int32_t e = 0;
-  uint32_t i = begin + group;
+  uint32_t i = begin + group, turn = 0;
   for (uint32_t tile = begin / per; tile * per < end; ++tile) {
     e = expert_of(tile, e);
     const int32_t skip = (static_cast<int32_t>(tile) - first[e]) * p.tile_rows;
@@ -374,9 +380,16 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
 
     // ---- the units of this tile
     const uint32_t stop = min(end, (tile + 1) * per);
-    for (; i < stop; i += kGroups) {
+    for (; i < stop; i += kGroups, ++turn) {
       const Unit it = unit_at(i, tile, e);
       const uint32_t quarters = kSwiglu ? (it.part & 1) * 8 : 0;  // SwiGLU: its two words of a row's four
+      // the weight row whose outputs this lane will write, and its scales, on their way while the sums are made
+      constexpr int kOut = kSwiglu ? 16 : 32;  // outputs of a row of x
+      const int out = lane % kOut;             // slot out / 8, lane row out % 8
+      const int32_t out_row = weight_row(it, out >> 3, out & 7);
+      const bool writes = present(it, out_row);
+      const float scale = writes ? p.scale[out_row] : 0.0f;
+      const float up_scale = kSwiglu && writes ? p.scale[out_row + out_n] : 0.0f;
       float acc[kSets][2][4] = {};
       auto sums = [&](auto half_tag) {
         constexpr bool kHalf = decltype(half_tag)::value;
@@ -448,7 +461,10 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
             acc[0][m][j] = kSets == 2 ? acc[0][m][j] + acc[1][m][j]
                                       : (acc[0][m][j] + acc[kSets / 2][m][j]) + (acc[1][m][j] + acc[kSets - 1][m][j]);
       }
-      float *to_part = part + warp * kGemvRows * kRowsPad;
+      // With two buffers in turn a warp writes one again only after the others, done with it, have met once more: 56 -> 53 us
+      // for the down projection of all 32 experts.
+      float *sums_of = part + (two_parts ? turn & 1 : 0) * (kPartBytes / 4);
+      float *to_part = sums_of + warp * kGemvRows * kRowsPad;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -456,13 +472,9 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kShare) : "memory"); };
       meet();
       const bool stop = *abort_flag != 0;  // some warp's sums are garbage
-      constexpr int kOut = kSwiglu ? 16 : 32;  // outputs of a row of x
-      const float *theirs = part + group * kShare * kGemvRows * kRowsPad;
-      for (int o = share * 32 + lane; o < kOut * rows && !stop; o += 32 * kShare) {
-        const int tok = o / kOut, in = o % kOut;  // slot in / 8, lane row in % 8
-        const int32_t row = weight_row(it, in >> 3, in & 7);
-        if (!present(it, row)) continue;
-        const float *from = theirs + tok * kRowsPad + in;
+      const float *theirs = sums_of + group * kShare * kGemvRows * kRowsPad + out;
+      for (int tok = (share * 32 + lane) / kOut; tok < rows && writes && !stop; tok += 32 * kShare / kOut) {
+        const float *from = theirs + tok * kRowsPad;
         auto joined = [&](const float *at) {
           float w[kShare];
 #pragma unroll
@@ -476,11 +488,12 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
         float v = joined(from);
         const float up = kSwiglu ? joined(from + 16) : 0.0f;
         const float back = wide ? 256.0f : s.back[tok];
-        v = (v * back) * p.scale[row];
-        if (kSwiglu) v = silu_times(v, (up * back) * p.scale[row + out_n]);
-        static_cast<__nv_bfloat16 *>(p.y)[static_cast<int64_t>(row0 + tok) * out_n + (row - it.e * n)] = __float2bfloat16_rn(v);
+        v = (v * back) * scale;
+        if (kSwiglu) v = silu_times(v, (up * back) * up_scale);
+        static_cast<__nv_bfloat16 *>(p.y)[static_cast<int64_t>(row0 + tok) * out_n + (out_row - it.e * n)] =
+            __float2bfloat16_rn(v);
       }
-      meet();
+      if (!two_parts) meet();
     }
   }
   // A wait that ran out leaves copies behind: they land before the CTA can exit.
@@ -521,10 +534,10 @@ cudaError_t launch_gemv(LaunchGemv a) {
 }
 
 // How many warps share a unit: eight while the SMs have few, then as few as the chunks of k make worth a meeting.  Measured,
-// us with 8 / 4 / 2 warps: gate/up of 4096 x 7168 with SwiGLU, one expert with one row (0.8 units an SM) 9.5 / 11.0 / 18.5, two
-// with one each (1.7) 12.8 / 13.4 / 19.2, four (3.4) 20.2 / 18.4 / 21.9, eight (7) 33.2 / 31.0 / 31.9, 32 (27) 102 / 98 / 98;
-// down projection of 7168 x 2048, one expert (1.5) 7.0 / 7.3 / 8.9, four (6) 13.8 / 13.1 / 12.0, 32 (47) 70 / 60 / 56; 8 experts
-// of 1000 x 1344 with 74 rows (4) 10.7 / 11.5 / 13.1.
+// us with 8 / 4 / 2 warps: gate/up of 4096 x 7168 with SwiGLU, one expert with one row (0.8 units an SM) 9.3 / 10.9 / 18.6, two
+// with one each (1.7) 12.8 / 13.3 / 19.0, four (3.4) 19.9 / 18.4 / 21.8, eight (7) 31.5 / 29.8 / 30.7, 32 (27) 98 / 97 / 99;
+// down projection of 7168 x 2048, one expert (1.5) 6.8 / 7.0 / 8.8, four (6) 12.9 / 12.7 / 11.8, 32 (47) 62 / 54 / 53; 8 experts
+// of 1000 x 1344 with 74 rows (4) 10.8 / 11.2 / 12.7.
 template <bool kSwiglu>
 cudaError_t launch_gemv(const LaunchGemv &a) {
   const int64_t units = unit_bound(a);
