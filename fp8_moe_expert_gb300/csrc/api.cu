@@ -921,18 +921,34 @@ fme_status encode_bf16_weights(CUtensorMap *map, const void *base, uint64_t expe
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-// MN-major operands, 64 rows x 128 columns: with whole groups of 64 columns, one box that gives them as two of 64 columns
-// one after the other ([experts][cols / 64][rows][64]); otherwise boxes of 64 columns, cut at the row's end.  `experts`
-// 0: a matrix without that dimension.
+// MN-major weights, 64 rows x 128 columns: with whole groups of 64 columns, one box that gives them as two of 64 columns
+// one after the other ([experts][cols / 64][rows][64]); otherwise boxes of 64 columns, cut at the row's end.
 fme_status encode_bf16_mn(CUtensorMap *map, bool *wide, const void *base, uint64_t experts, uint64_t rows, uint64_t cols) {
   *wide = cols % 64 == 0;
-  if (!*wide)
-    return experts ? encode_bf16_weights(map, base, experts, rows, cols, 64) : encode_bf16_2d(map, base, rows, cols, 64);
+  if (!*wide) return encode_bf16_weights(map, base, experts, rows, cols, 64);
   cuuint64_t dims[4] = {64, rows, cols / 64, experts};
   cuuint64_t strides[3] = {cols * 2, 128, rows * cols * 2};
   cuuint32_t box[4] = {64, 64, 2, 1};
-  return encode_map(" (columns)", map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, experts ? 4 : 3, const_cast<void *>(base), dims,
-                    strides, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  return encode_map(" (columns)", map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// wgrad's operands, from 64 rows on: all windows of 64 rows of a matrix, window s its rows s .. s + 63 (from window to window
+// the stride is a row's), in the same boxes.  One that starts at row 64 - c of window s holds rows s + 64 - c .. s + 63 and
+// zeros behind them.
+fme_status encode_bf16_windows(CUtensorMap *map, bool *wide, const void *base, uint64_t rows, uint64_t cols) {
+  *wide = cols % 64 == 0;
+  cuuint64_t dims[4] = {64, 64, cols / 64, rows - 63};
+  cuuint64_t strides[3] = {cols * 2, 128, cols * 2};
+  cuuint32_t box[4] = {64, 64, 2, 1};
+  if (!*wide) {
+    dims[0] = cols;
+    dims[2] = rows - 63;
+    strides[1] = cols * 2;
+    box[2] = 1;
+  }
+  return encode_map(" (windows)", map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, *wide ? 4 : 3, const_cast<void *>(base), dims, strides,
+                    box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // The forward (out = n columns, contraction k) and dgrad (out = k columns, contraction n).
@@ -1002,12 +1018,13 @@ fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, con
   // without rows every expert is empty and the operands' maps are never used
   const void *abase = m ? dy : dw, *bbase = m ? x : dw;
   const int64_t extent = m ? m : 1;
-  if ((st = encode_bf16_mn(&a.map_a, &a.wide_a, abase, 0, extent, n)) != FME_OK ||
-      (st = encode_bf16_2d(&a.map_a8, abase, extent, n, 8)) != FME_OK ||
-      (st = encode_bf16_2d(&a.map_a1, abase, extent, n, 1)) != FME_OK ||
-      (st = encode_bf16_mn(&a.map_b, &a.wide_b, bbase, 0, extent, k)) != FME_OK ||
-      (st = encode_bf16_2d(&a.map_b8, bbase, extent, k, 8)) != FME_OK ||
-      (st = encode_bf16_2d(&a.map_b1, bbase, extent, k, 1)) != FME_OK)
+  if ((st = encode_bf16_2d(&a.early_a, abase, extent, n, 64)) != FME_OK ||
+      (st = encode_bf16_2d(&a.early_b, bbase, extent, k, 64)) != FME_OK)
+    return st;
+  a.map_a = a.early_a;  // with fewer rows than a window every block is an early one
+  a.map_b = a.early_b;
+  if (m >= 64 && ((st = encode_bf16_windows(&a.map_a, &a.wide_a, dy, m, n)) != FME_OK ||
+                  (st = encode_bf16_windows(&a.map_b, &a.wide_b, x, m, k)) != FME_OK))
     return st;
   a.offsets = offsets;
   a.num_experts = num_experts;

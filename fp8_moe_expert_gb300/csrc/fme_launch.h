@@ -174,9 +174,9 @@ cudaError_t launch_block128_wgrad(const LaunchBlock128 &a);
 
 // bf16 grouped GEMMs (gemm_bf16.cu).
 struct LaunchBf16 {
-  CUtensorMap map_a, map_b;                      // operands, 128-byte swizzle
-  CUtensorMap map_a8, map_a1, map_b8, map_b1;    // wgrad: the same in boxes of 8 rows and of one
-  CUtensorMap map_y;                             // output (not wgrad's), boxes of 32 rows x 128 bytes, 128-byte swizzle
+  CUtensorMap map_a, map_b;      // operands, 128-byte swizzle (wgrad: all windows of 64 rows; not with fewer rows)
+  CUtensorMap early_a, early_b;  // wgrad: the operands in boxes of 64 rows x 64 columns
+  CUtensorMap map_y;             // output (not wgrad's), boxes of 32 rows x 128 bytes, 128-byte swizzle
   const int32_t *offsets;  // rows of each expert
   int32_t num_experts;
   int64_t rows;     // rows of all experts

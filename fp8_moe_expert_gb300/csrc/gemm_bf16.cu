@@ -19,13 +19,16 @@
 //   warp 0      producer: A and B by TMA, completing on the leader's barriers;
 //   warp 1      allocates tensor memory; in the leader issues the MMAs, a commit a stage frees it in both CTAs, one a tile
 //               hands the accumulator to both epilogues;
-//   warp 2      wgrad: the copies of blocks at an expert's end;
+//   warp 2      wgrad: experts that end within the tensor's first 64 rows;
 //   warps 4-11  epilogue: 32 rows x 128 columns each, while the next tile's MMAs run.
 //
 // wgrad's contraction runs over the rows of one expert, and the block of 64 rows at an expert's end reaches into the
-// next expert's.  Those must read as zeros in both operands (0 times a NaN of another expert would be NaN), so the last
-// block comes in boxes of 8 rows, the group of 8 that holds the end in boxes of one row, and a box of rows that are not the
-// expert's is asked for behind the tensor's last row, where the tensor map fills in zeros.
+// next expert's.  Those must read as zeros in both operands (0 times a NaN of another expert would be NaN).  The operands' maps
+// are of all windows of 64 rows: a block is a window, and the last one, which starts inside the window that ends with the
+// expert, has nothing behind it, where the map fills in zeros.  Its MMAs stop at the K = 16 step that holds the end.
+// An end within the tensor's first 64 rows has no such window: there warp 2 of each CTA copies the block and writes the zeros (at
+// most 15 rows), and the leader's completes the stage.  Zeros written for every expert, or last blocks in copies of 8 rows and
+// of one, hold up each tile by 1 us: 500 rows of each of 32 experts of 7168 x 2048 442 and 396 us, by windows 318.
 #include <algorithm>
 
 #include "gemm_tiles.cuh"
@@ -51,8 +54,11 @@ struct SharedBf {
   uint64_t acc_empty[2];
   uint64_t drain;
   uint64_t peer_fills_bar;
-  uint64_t end_go[kMaxStagesBf];  // wgrad: the stage, free and armed, is for a block at an expert's end
+  uint64_t early_go[kMaxStagesBf];    // wgrad, blocks for warp 2: the stage is free,
+  uint64_t early_peer[kMaxStagesBf];  // the peer's half is there (the leader's),
+  uint64_t early_full;                // the copies have landed
   uint32_t peer_fills;
+  uint32_t peer_early;  // a bit a stage: the peer's latest fill is such a block
   uint32_t tmem_base;
   int abort_flag;
   int ok_flag;
@@ -84,6 +90,19 @@ __device__ __forceinline__ void mma_stage_pair(uint32_t d_tmem, uint64_t a_desc,
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(smem_u32(freed)), "n"(kA), "n"(kB), "h"(static_cast<uint16_t>(3)),
       "r"(accumulate)
       : "memory");
+}
+
+// The same of fewer steps.
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void mma_steps_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate, uint64_t *freed, int steps) {
+  for (int j = 0; j < steps; ++j)
+    asm volatile(
+        "{\n\t.reg .pred z;\n\tsetp.ne.u32 z, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, z;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc + j * kA), "l"(b_desc + j * kB), "r"(idesc), "r"(accumulate || j > 0 ? 1u : 0u)
+        : "memory");
+  pair::commit_both(freed);
 }
 
 struct TileBf {
@@ -192,7 +211,8 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
     for (uint32_t i = 0; i < S; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.freed[i], 1);
-      mbar_init(&s.end_go[i], 1);
+      mbar_init(&s.early_go[i], 1);
+      mbar_init(&s.early_peer[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.acc_full[i], 1);
@@ -201,6 +221,8 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
     mbar_init(&s.drain, 1);
     mbar_init(&s.peer_fills_bar, 1);
     s.abort_flag = 0;
+    mbar_init(&s.early_full, 1);
+    s.peer_early = 0;
     fence_barrier_init();
     fence_proxy_async_shared();
     prefetch_tensormap(&p.map_a);
@@ -265,6 +287,7 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
     if (lane == 0) {
       // ---------------------------------------------------------------- producer
       uint32_t stage = 0, phase = 1, filled = 0;
+      uint32_t early = 0;  // a bit a stage: its latest fill is warp 2's
       bool stop = false;
       for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
         const TileBf tl = tile_bf<K>(p, tab, t, rank);
@@ -274,38 +297,41 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
             stop = true;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytesBf);
-          const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
-          uint8_t *a = smem_a + stage * kABytes, *b = smem_b + stage * kBBytes;
-          const int32_t k0 = i * kStageK;
-          if constexpr (K == KindBf::kWgrad) {
-            const int32_t row = tl.p0 + k0;
-            if (tl.p1 - row < kStageK) {
-              mbar_arrive(&s.end_go[stage]);  // the last block: warp 2's
-            } else {
+          if (K == KindBf::kWgrad && tl.p1 < kStageK) {
+            mbar_arrive(&s.early_go[stage]);
+            early |= 1u << stage;
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytesBf);
+            const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
+            uint8_t *a = smem_a + stage * kABytes, *b = smem_b + stage * kBBytes;
+            const int32_t k0 = i * kStageK;
+            if constexpr (K == KindBf::kWgrad) {
+              // the window of 64 rows that starts here or ends with the expert
+              const int32_t window = min(tl.p0 + k0, tl.p1 - kStageK), from = tl.p0 + k0 - window;
               if (p.wide_a) {
-                tma_load_3d_pair(a, &p.map_a, bar, 0, row, tl.row0 / 64);
+                tma_load_4d_pair(a, &p.map_a, bar, 0, from, tl.row0 / 64, window);
               } else {
-                pair::tma_load_2d(a, &p.map_a, bar, tl.row0, row);
-                pair::tma_load_2d(a + kHalfMnBytes, &p.map_a, bar, tl.row0 + 64, row);
+                tma_load_3d_pair(a, &p.map_a, bar, tl.row0, from, window);
+                tma_load_3d_pair(a + kHalfMnBytes, &p.map_a, bar, tl.row0 + 64, from, window);
               }
               if (p.wide_b) {
-                tma_load_3d_pair(b, &p.map_b, bar, 0, row, bcol / 64);
+                tma_load_4d_pair(b, &p.map_b, bar, 0, from, bcol / 64, window);
               } else {
-                pair::tma_load_2d(b, &p.map_b, bar, bcol, row);
-                pair::tma_load_2d(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, row);
+                tma_load_3d_pair(b, &p.map_b, bar, bcol, from, window);
+                tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, from, window);
+              }
+            } else {
+              pair::tma_load_2d(a, &p.map_a, bar, k0, tl.row0);
+              if constexpr (K == KindBf::kFwd) {
+                tma_load_3d_pair(b, &p.map_b, bar, k0, bcol, tl.e);
+              } else if (p.wide_b) {
+                tma_load_4d_pair(b, &p.map_b, bar, 0, k0, bcol / 64, tl.e);
+              } else {
+                tma_load_3d_pair(b, &p.map_b, bar, bcol, k0, tl.e);
+                tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, k0, tl.e);
               }
             }
-          } else {
-            pair::tma_load_2d(a, &p.map_a, bar, k0, tl.row0);
-            if constexpr (K == KindBf::kFwd) {
-              tma_load_3d_pair(b, &p.map_b, bar, k0, bcol, tl.e);
-            } else if (p.wide_b) {
-              tma_load_4d_pair(b, &p.map_b, bar, 0, k0, bcol / 64, tl.e);
-            } else {
-              tma_load_3d_pair(b, &p.map_b, bar, bcol, k0, tl.e);
-              tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, k0, tl.e);
-            }
+            early &= ~(1u << stage);
           }
           ++filled;
           if (++stage == S) {
@@ -314,34 +340,60 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
           }
         }
       }
+      if (rank != 0) pair::st_remote_u32(pair::map_to_rank(&s.peer_early, 0), early);  // seen with the fills
       const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
-      if (rank == 0) drain_pair_ring(s.full, S, filled, peer, kStageBytesBf);
+      if (rank == 0)
+        drain_pair_ring(s.full, S, filled, peer, kStageBytesBf, early, *static_cast<volatile uint32_t *>(&s.peer_early));
     }
   } else if (K == KindBf::kWgrad && warp == 2) {
-    // ------------------------------------------------ blocks at an expert's end (the whole warp: up to 60 copies).  The
-    // producer frees and arms their stages; it drains them too.  (In the producer itself a vote of the warp a
-    // stage cost 10%: 65536 x 4096 x 7168, 2.09 -> 1.97 ms without.)
-    uint32_t stage = 0, seen = 0;  // seen: a bit a stage, the parity of its end_go
+    // ------------------------------------------------ blocks that end within the first 64 rows (a tile's only one)
+    uint32_t stage = 0, seen = 0, landed = 0;  // seen: a bit a stage, the parity of its early_go and early_peer
     for (uint32_t round = 0, t; (t = tile_at(round)) < total; ++round) {
       const TileBf tl = tile_bf<K>(p, tab, t, rank);
-      stage = (stage + tl.nk) % S;  // of the tile's end
-      const int32_t left = (tl.p1 - tl.p0) % kStageK;
-      if (left == 0) continue;
-      const uint32_t at = stage == 0 ? S - 1 : stage - 1;
-      if (warp_any(!mbar_wait<true>(&s.end_go[at], (seen >> at) & 1, abort_flag, p.status))) break;
+      const uint32_t at = stage;
+      stage = (stage + tl.nk) % S;
+      if (tl.nk == 0 || tl.p1 >= kStageK) continue;
+      const uint32_t parity = (seen >> at) & 1;
       seen ^= 1u << at;
-      const uint32_t bar = pair::map_to_rank(&s.full[at], 0);
-      // lane = 8 (half of A or B) + group of 8 rows
-      const int32_t which = lane >> 3, grp = lane & 7;
-      uint8_t *dst = (which < 2 ? smem_a + at * kABytes : smem_b + at * kBBytes) + (which & 1) * kHalfMnBytes;
-      const int32_t x = (which < 2 ? tl.row0 : tl.col0 + rank * kHalfN) + 64 * (which & 1);
-      const int32_t row = tl.p1 - left, outside = static_cast<int32_t>(p.rows);
-      const int32_t split = left & 7 ? left >> 3 : 8;  // the group that holds the end
-      if (grp != split)
-        pair::tma_load_2d(dst + grp * 1024, which < 2 ? &p.map_a8 : &p.map_b8, bar, x, 8 * grp < left ? row + 8 * grp : outside);
-      if (split < 8)  // this lane's row of it
-        pair::tma_load_2d(dst + split * 1024 + grp * 128, which < 2 ? &p.map_a1 : &p.map_b1, bar, x,
-                          8 * split + grp < left ? row + 8 * split + grp : outside);
+      if (warp_any(!mbar_wait<true>(&s.early_go[at], parity, abort_flag, p.status))) break;
+      uint8_t *a = smem_a + at * kABytes, *b = smem_b + at * kBBytes;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s.early_full, kStageBytesBf);
+        const uint32_t bar = pair::map_to_rank(&s.early_full, rank);
+        const int32_t bcol = tl.col0 + rank * kHalfN;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          pair::tma_load_2d(a + half * kHalfMnBytes, &p.early_a, bar, tl.row0 + 64 * half, tl.p0);
+          pair::tma_load_2d(b + half * kHalfMnBytes, &p.early_b, bar, bcol + 64 * half, tl.p0);
+        }
+      }
+      __syncwarp();
+      if (warp_any(!mbar_wait<true>(&s.early_full, landed, abort_flag, p.status))) {
+        mbar_drain(&s.early_full, landed);
+        break;
+      }
+      landed ^= 1;
+      const int32_t rows = tl.p1 - tl.p0;
+      a += rows * 128;
+      b += rows * 128;
+      for (int i = lane; i < (15 - (rows + 15) % 16) * 8; i += 32)  // 16 bytes of each half of A and B; the swizzle stays in a row
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          *reinterpret_cast<uint4 *>(a + half * kHalfMnBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(b + half * kHalfMnBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+        }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (rank != 0) {
+        if (lane == 0) pair::arrive_remote_release(pair::map_to_rank(&s.early_peer[at], 0));
+      } else {
+        if (warp_any(!pair::wait_acquire_cluster(&s.early_peer[at], parity, kWaitLimitNs))) {
+          *abort_flag = 1;
+          report(p.status, kDevTimeout);
+          break;
+        }
+        if (lane == 0) mbar_arrive(&s.full[at]);
+      }
       __syncwarp();
     }
   } else if (warp == 1) {
@@ -353,8 +405,10 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
       uint32_t stage = 0, phase = 0, tiles = 0;
       bool stop = false;
       for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
-        const int nk = tile_bf<K>(p, tab, t, 0).nk;
+        const TileBf tl = tile_bf<K>(p, tab, t, 0);
+        const int nk = tl.nk;
         if (nk == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const int left = K == KindBf::kWgrad ? (tl.p1 - tl.p0) % kStageK : 0;
         const uint32_t b = tiles & 1;
         stop = warp_any(!mbar_wait(&s.acc_empty[b], ((tiles >> 1) & 1) ^ 1, abort_flag, p.status));
         for (int i = 0; i < nk && !stop; ++i) {
@@ -363,9 +417,12 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
           tc_fence_after();
           // 16 of K: 32 bytes along a K-major row, 16 rows of an MN-major tile
           if (elect_one()) {
-            mma_stage_pair<(kAmn ? 2048 : 32) / 16, (kBmn ? 2048 : 32) / 16>(
-                tmem + b * kBN, a_desc + stage * (kABytes / 16), b_desc + stage * (kBBytes / 16), idesc, i > 0,
-                &s.freed[stage]);
+            constexpr uint32_t kA = (kAmn ? 2048 : 32) / 16, kB = (kBmn ? 2048 : 32) / 16;
+            const uint64_t a = a_desc + stage * (kABytes / 16), bd = b_desc + stage * (kBBytes / 16);
+            if (left != 0 && i == nk - 1)
+              mma_steps_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, i > 0, &s.freed[stage], (left + 15) / 16);
+            else
+              mma_stage_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, i > 0, &s.freed[stage]);
             if (i == nk - 1) pair::commit_both(&s.acc_full[b]);
           }
           __syncwarp();

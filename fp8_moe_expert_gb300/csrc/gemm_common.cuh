@@ -169,10 +169,14 @@ __device__ __forceinline__ Tile tile_at(const LaunchGemm &p, const Groups &s, in
 // the peer alone was never armed, so the leader arms it for the peer's bytes; a
 // fill issued by the leader alone waits for peer bytes that will never come, so
 // the leader counts them as arrived.  Each wait is bounded (kDrainLimitNs).
-__device__ inline void drain_pair_ring(uint64_t *bars, int S, uint32_t own, uint32_t peer, uint32_t peer_bytes) {
+// `own_skip`, `peer_skip`: a bit a stage, set where the latest fill's copies
+// complete on other barriers.
+__device__ inline void drain_pair_ring(uint64_t *bars, int S, uint32_t own, uint32_t peer, uint32_t peer_bytes,
+                                       uint32_t own_skip = 0, uint32_t peer_skip = 0) {
   const uint32_t last = own > peer ? own : peer;
   for (uint32_t j = 0; j < static_cast<uint32_t>(S) && j < last; ++j) {
     const uint32_t f = j + S * ((last - 1 - j) / S);  // latest fill of stage j
+    if (((f < own ? own_skip : peer_skip) >> j) & 1) continue;
     if (f >= own)
       mbar_arrive_expect_tx(&bars[j], peer_bytes);
     else if (f >= peer)

@@ -164,6 +164,25 @@ def test_one_experts_values_do_not_reach_anothers(off, bad, status):
         assert torch.equal(got[keep], want[keep]) and not bool(got[~keep].isfinite().any())
 
 
+@pytest.mark.parametrize("n,k", [(128, 320), (136, 200), (1088, 72)])
+def test_wgrad_ends_anywhere(n, k, status):
+    """Ends within the first 64 rows, each distance from a step of 16 and from a block of 64, NaN in every other expert's rows."""
+    sizes = [3, 13, 16, 15, 0, 17, 1, 47, 64, 63, 65, 1, 128, 79, 80, 81, 127, 200] + [64 + 3 * i for i in range(22)]
+    off = [0]
+    for s in sizes:
+        off.append(off[-1] + s)
+    dy, x = integers((off[-1], n), 1), integers((off[-1], k), 2)
+    want = wgrad64(dy, x, off)[0].to(torch.float32)
+    for odd in (0, 1):
+        a, b = dy.clone(), x.clone()
+        for e in range(odd, len(sizes), 2):
+            a[off[e]:off[e + 1]], b[off[e]:off[e + 1]] = float("nan"), float("inf")
+        dw = fme.grouped_gemm_wgrad_bf16(a, b, i32(off), dtype=torch.float32, status=status)
+        assert torch.equal(dw[1 - odd::2], want[1 - odd::2])
+        full = [e for e in range(odd, len(sizes), 2) if sizes[e]]
+        assert not bool(dw[full].isfinite().any())
+
+
 @pytest.mark.parametrize("offsets", [[0, 5, 3, 300], [1, 5, 9, 300], [0, 5, 9, 299], [0, 5, 9, 301], [0, -5, 9, 300]])
 def test_malformed_offsets_are_reported_and_nothing_is_written(offsets):
     rows, n, k = 30000, 64, 72

@@ -37,9 +37,9 @@ def test_dgrad(short_lib):  # noqa: F811
                                                              y.data_ptr(), st, s))
 
 
-@pytest.mark.parametrize("first", [128, 99])
+@pytest.mark.parametrize("first", [128, 99, 20])
 def test_wgrad(short_lib, first):  # noqa: F811
-    """With whole blocks, and with blocks that end inside: those have a producer of their own."""
+    """With whole blocks, with blocks that end inside, and with an end in the first 64 rows, which has a producer of its own."""
     off = i32(0, first, DEEP - 1)
     m = DEEP - 1
     dy, x = ref.normal((m, N), 1.0, 1), ref.normal((m, N), 0.02, 2)
