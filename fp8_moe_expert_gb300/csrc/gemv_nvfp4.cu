@@ -18,8 +18,8 @@
 //         bits 8 .. 6 of each half, as bf16 the code's value times 2^-126 (its subnormal 0.5 a bf16 subnormal).  Times
 //         sf 2^118 it is c sf 2^-8.  13 integer operations and 4 products for 8 codes.
 // Both multiply the same values but for a power of two, so the sums' bits are the same (as long as they are normal
-// numbers).  Gate/up of 4096 x 7168, 8 and all of 32 experts with a row each: 30 and 97 us (4.4 and 5.5 TB/s of weights), in
-// bf16 38 and 126.
+// numbers).  Gate/up of 4096 x 7168, 8 and all of 32 experts with a row each: 30 and 91 us (4.4 and 5.8 TB/s of weights), in
+// bf16 38 and 121.
 //
 // Any order of k will do as long as both operands follow it.  A unit is 32 weight rows: 8 of each quarter of a group of 128
 // (the tiled layout keeps the scales of rows 32 apart together), or, with SwiGLU, of two quarters of the gate rows
@@ -32,8 +32,8 @@
 // makes its branch: the order is the same however many warps share, so a row's bits do not depend on the other rows.
 //
 // A CTA an SM, 16 warps, takes consecutive units, mostly of the same up to 8 rows of x: those it brings into shared memory
-// once, converted, in the order in which the lanes read them.  The most rows that any expert has decide how much of it
-// they take, and so how deep the rings are.
+// once, converted, in the order in which the lanes read them, several experts' together where they fit.  The most rows that any
+// expert has decide how much of it they take, and so how deep the rings are.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -208,20 +208,19 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
     if (blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
     return;
   }
-  // the warps' sums, the rows of x, the rings: two chunks a warp and two buffers of sums where they fit
+  // the rings, the warps' sums, the rows of x: two chunks a warp and two buffers of sums where they fit beside the rows of the
+  // largest tile
   constexpr uint32_t kPartBytes = kGemvWarps * kGemvRows * kRowsPad * 4;
-  const uint32_t part_off = (8 * (p.num_experts + 1) + 15) & ~15u;
-  auto ring_at = [&](uint32_t parts) { return (part_off + parts * kPartBytes + s.x_tile * x_stride + 1023) & ~1023u; };
-  auto fits = [&](uint32_t chunks_ahead, uint32_t parts) {
-    return ring_at(parts) + chunks_ahead * kGemvWarps * (kCodeBytes + kScaleBytes) <= p.shared_bytes;
-  };
-  const int depth = fits(2, 1) ? 2 : 1;
-  const bool two_parts = fits(depth, 2);
-  float *part = reinterpret_cast<float *>(dyn + part_off);  // [buffer][warp][row of x][weight row]
-  uint8_t *xs = dyn + part_off + (two_parts ? 2 : 1) * kPartBytes;
-  const uint32_t ring_off = ring_at(two_parts ? 2 : 1);
+  constexpr uint32_t kRingBytes = kGemvWarps * (kCodeBytes + kScaleBytes);
+  const uint32_t ring_off = (8 * (p.num_experts + 1) + 1023) & ~1023u;
+  const uint32_t least = ring_off + kRingBytes + kPartBytes + s.x_tile * x_stride;
+  const int depth = least + kRingBytes <= p.shared_bytes ? 2 : 1;
+  const bool two_parts = least + (depth - 1) * kRingBytes + kPartBytes <= p.shared_bytes;
   uint8_t *codes_ring = dyn + ring_off + warp * depth * kCodeBytes;
   uint8_t *scales_ring = dyn + ring_off + kGemvWarps * depth * kCodeBytes + warp * depth * kScaleBytes;
+  float *part = reinterpret_cast<float *>(dyn + ring_off + depth * kRingBytes);  // [buffer][warp][row of x][weight row]
+  const uint32_t xs_off = ring_off + depth * kRingBytes + (two_parts ? 2 : 1) * kPartBytes;
+  uint8_t *xs = dyn + xs_off;
   // Groups of 128 weight rows (with SwiGLU: gate rows) that an expert's rows lie in, and the units of each.
   const int32_t out_n = kSwiglu ? n / 2 : n;
   const int32_t blocks = n % 128 == 0 ? out_n / 128 : (n + 254) / 128;
@@ -234,9 +233,10 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
 
   if (begin == end) return;
 
+  // The expert of a tile, from the expert of an earlier one.
   auto expert_of = [&](uint32_t tile, int32_t e) {
-    while (first[e + 1] <= static_cast<int32_t>(tile)) ++e;
-    return e;
+    if (first[e + 1] > static_cast<int32_t>(tile)) return e;
+    return e + 1 + find_group(first + e + 1, p.num_experts - e - 1, tile);
   };
   // Unit i of tile `tile` of expert e.
   auto unit_at = [&](uint32_t i, uint32_t tile, int32_t e) {
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
   // ---- copies of the weights, by lane 0: a cursor that runs `depth` chunks ahead of the sums
   volatile int *abort_flag = &s.abort_flag;
   uint32_t copy_unit = share < chunks ? begin + group : end, filled = 0;
-  int32_t copy_c = share, copy_e = 0;
+  int32_t e = find_group(first, p.num_experts, begin / per), copy_c = share, copy_e = e;
   Unit copy{};
   auto aim = [&] {
     const uint32_t tile = copy_unit / per;
@@ -290,14 +290,28 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
   uint32_t used = 0;  // chunks so far
 
   const uint32_t xs_at = smem_u32(xs);
-  int32_t e = 0;
+  // The rows of a tile of expert e.
+  auto row_of = [&](uint32_t tile, int32_t e) { return off[e] + (static_cast<int32_t>(tile) - first[e]) * p.tile_rows; };
+  auto row_end = [&](uint32_t tile, int32_t e) { return min(row_of(tile, e) + p.tile_rows, off[e + 1]); };
   uint32_t i = begin + group, turn = 0;
-  for (uint32_t tile = begin / per; tile * per < end; ++tile) {
+  for (uint32_t tile = begin / per, next; tile * per < end; tile = next) {
+    // ---- a pass: the tile and those behind it, as far as this CTA has units of them and there is room for their rows (their
+    // units then run side by side: 16 of 32 experts of 7168 x 2048 with a row each 30.0 us, one tile after the other 33.0)
     e = expert_of(tile, e);
-    const int32_t skip = (static_cast<int32_t>(tile) - first[e]) * p.tile_rows;
-    const int32_t row0 = off[e] + skip, rows = min(p.tile_rows, off[e + 1] - off[e] - skip);
+    const int32_t row0 = row_of(tile, e);
+    int32_t rows = row_end(tile, e) - row0;
+    next = tile + 1;
+    if (next * per < end) {
+      const int32_t room = min(kGemvRows, static_cast<int32_t>((p.shared_bytes - xs_off) / x_stride));
+      for (int32_t last_e = e; next * per < end; ++next) {
+        last_e = expert_of(next, last_e);
+        const int32_t more = row_end(next, last_e) - row0;
+        if (more > room) break;
+        rows = more;
+      }
+    }
 
-    // ---- the tile's rows of x: the power of two of each, then their values in the order in which the lanes read them.
+    // ---- its rows of x: the power of two of each, then their values in the order in which the lanes read them.
     // 16 / 2^j warps to a row.
     const int per_row = rows == 1 ? 16 : rows == 2 ? 8 : rows <= 4 ? 4 : 2;
     const int mine = warp / per_row, slice = warp % per_row;
@@ -330,7 +344,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
       if (lane == 0) s.amax[warp] = top;
     }
-    __syncthreads();  // also: the tile before is no longer read
+    __syncthreads();  // also: the pass before is no longer read
     float to = 1.0f;
     if (mine < rows) {
       float top = s.amax[mine * per_row];
@@ -378,122 +392,126 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
     // (rows of x that are not there: the first, whose sums are not used)
     const uint32_t x_lane = xs_at + (lane / 4 < rows ? lane / 4 : 0) * x_stride + t * 16;
 
-    // ---- the units of this tile
-    const uint32_t stop = min(end, (tile + 1) * per);
-    for (; i < stop; i += kGroups, ++turn) {
-      const Unit it = unit_at(i, tile, e);
-      const uint32_t quarters = kSwiglu ? (it.part & 1) * 8 : 0;  // SwiGLU: its two words of a row's four
-      // the weight row whose outputs this lane will write, and its scales, on their way while the sums are made
-      constexpr int kOut = kSwiglu ? 16 : 32;  // outputs of a row of x
-      const int out = lane % kOut;             // slot out / 8, lane row out % 8
-      const int32_t out_row = weight_row(it, out >> 3, out & 7);
-      const bool writes = present(it, out_row);
-      const float scale = writes ? p.scale[out_row] : 0.0f;
-      const float up_scale = kSwiglu && writes ? p.scale[out_row + out_n] : 0.0f;
-      float acc[kSets][2][4] = {};
-      auto sums = [&](auto half_tag) {
-        constexpr bool kHalf = decltype(half_tag)::value;
-        auto add_chunk = [&](int32_t c, float(&to)[2][4]) {
-          const int slot = depth == 2 ? used & 1 : 0;
-          // (a wait that ran out: garbage from here on, which is not stored, and no more copies)
-          if (!mbar_wait(&s.full[warp][slot], (depth == 2 ? used >> 1 : used) & 1, abort_flag, p.status)) copy_unit = end;
-          __syncwarp();
-          ++used;
-          const uint32_t boxes = smem_u32(codes_ring) + slot * kCodeBytes + g * 128;
-          const uint32_t tiles = smem_u32(scales_ring) + slot * kScaleBytes + (t >> 1) * 128 + g * 16 + quarters;
+    // ---- its units
+    for (uint32_t of = tile; of < next; ++of) {
+      e = expert_of(of, e);
+      const int32_t from_row = row_of(of, e) - row0, to_row = row_end(of, e) - row0;
+      const uint32_t stop = min(end, (of + 1) * per);
+      for (; i < stop; i += kGroups, ++turn) {
+        const Unit it = unit_at(i, of, e);
+        const uint32_t quarters = kSwiglu ? (it.part & 1) * 8 : 0;  // SwiGLU: its two words of a row's four
+        // the weight row whose outputs this lane will write, and its scales, on their way while the sums are made
+        constexpr int kOut = kSwiglu ? 16 : 32;  // outputs of a row of x
+        const int out = lane % kOut;             // slot out / 8, lane row out % 8
+        const int32_t out_row = weight_row(it, out >> 3, out & 7);
+        const bool writes = present(it, out_row);
+        const float scale = writes ? p.scale[out_row] : 0.0f;
+        const float up_scale = kSwiglu && writes ? p.scale[out_row + out_n] : 0.0f;
+        float acc[kSets][2][4] = {};
+        auto sums = [&](auto half_tag) {
+          constexpr bool kHalf = decltype(half_tag)::value;
+          auto add_chunk = [&](int32_t c, float(&to)[2][4]) {
+            const int slot = depth == 2 ? used & 1 : 0;
+            // (a wait that ran out: garbage from here on, which is not stored, and no more copies)
+            if (!mbar_wait(&s.full[warp][slot], (depth == 2 ? used >> 1 : used) & 1, abort_flag, p.status)) copy_unit = end;
+            __syncwarp();
+            ++used;
+            const uint32_t boxes = smem_u32(codes_ring) + slot * kCodeBytes + g * 128;
+            const uint32_t tiles = smem_u32(scales_ring) + slot * kScaleBytes + (t >> 1) * 128 + g * 16 + quarters;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint4 codes[4], w;  // w: the words of the four rows' scales
+            for (int half = 0; half < 2; ++half) {
+              uint4 codes[4], w;  // w: the words of the four rows' scales
 #pragma unroll
-            for (int q = 0; q < 4; ++q) codes[q] = shared16(boxes + q * kBoxBytes + (((4 * half + t) ^ g) * 16));
-            if (kSwiglu) {
-              const uint2 gate = shared8(tiles + half * 256), up = shared8(tiles + half * 256 + kTilesBytes);
-              w = make_uint4(gate.x, gate.y, up.x, up.y);
-            } else {
-              w = shared16(tiles + half * 256);
-            }
-            if (half == 1) {  // all of the slot is read: its next chunk may be on its way
-              asm volatile("" ::"r"(codes[3].w), "r"(w.w) : "memory");
-              __syncwarp();
-              copy_next(slot);
-            }
-            const int32_t k0 = c * kChunk + half * 128;
-            if (k0 >= k) continue;
-            uint32_t sc[4][2];
-            decode_scales<kHalf>(w.x >> (16 * (t & 1)), sc[0]);
-            decode_scales<kHalf>(w.y >> (16 * (t & 1)), sc[1]);
-            decode_scales<kHalf>(w.z >> (16 * (t & 1)), sc[2]);
-            decode_scales<kHalf>(w.w >> (16 * (t & 1)), sc[3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // 8 of the lane's 32 k
-              uint32_t a[4][4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint4 &v = codes[q];
-                decode8<kHalf>(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, sc[q][j >> 1], a[q]);
+              for (int q = 0; q < 4; ++q) codes[q] = shared16(boxes + q * kBoxBytes + (((4 * half + t) ^ g) * 16));
+              if (kSwiglu) {
+                const uint2 gate = shared8(tiles + half * 256), up = shared8(tiles + half * 256 + kTilesBytes);
+                w = make_uint4(gate.x, gate.y, up.x, up.y);
+              } else {
+                w = shared16(tiles + half * 256);
               }
-              const uint4 x = shared16(x_lane + k0 * 2 + 64 * j);
+              if (half == 1) {  // all of the slot is read: its next chunk may be on its way
+                asm volatile("" ::"r"(codes[3].w), "r"(w.w) : "memory");
+                __syncwarp();
+                copy_next(slot);
+              }
+              const int32_t k0 = c * kChunk + half * 128;
+              if (k0 >= k) continue;
+              uint32_t sc[4][2];
+              decode_scales<kHalf>(w.x >> (16 * (t & 1)), sc[0]);
+              decode_scales<kHalf>(w.y >> (16 * (t & 1)), sc[1]);
+              decode_scales<kHalf>(w.z >> (16 * (t & 1)), sc[2]);
+              decode_scales<kHalf>(w.w >> (16 * (t & 1)), sc[3]);
 #pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                mma_16816<kHalf>(to[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
-                mma_16816<kHalf>(to[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
+              for (int j = 0; j < 4; ++j) {  // 8 of the lane's 32 k
+                uint32_t a[4][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint4 &v = codes[q];
+                  decode8<kHalf>(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, sc[q][j >> 1], a[q]);
+                }
+                const uint4 x = shared16(x_lane + k0 * 2 + 64 * j);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                  mma_16816<kHalf>(to[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
+                  mma_16816<kHalf>(to[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
+                }
               }
             }
+          };
+          for (int32_t c = share; c < chunks; c += kSums) {
+#pragma unroll
+            for (int i = 0; i < kSets; ++i)
+              if (c + i * kShare < chunks) add_chunk(c + i * kShare, acc[i]);
           }
         };
-        for (int32_t c = share; c < chunks; c += kSums) {
-#pragma unroll
-          for (int i = 0; i < kSets; ++i)
-            if (c + i * kShare < chunks) add_chunk(c + i * kShare, acc[i]);
-        }
-      };
-      if (wide)
-        sums(std::false_type{});
-      else
-        sums(std::true_type{});
+        if (wide)
+          sums(std::false_type{});
+        else
+          sums(std::true_type{});
 
-      // ---- the eight sums: a warp's own, then the warps'
-      if constexpr (kSets > 1) {
+        // ---- the eight sums: a warp's own, then the warps'
+        if constexpr (kSets > 1) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[0][m][j] = kSets == 2 ? acc[0][m][j] + acc[1][m][j]
+                                        : (acc[0][m][j] + acc[kSets / 2][m][j]) + (acc[1][m][j] + acc[kSets - 1][m][j]);
+        }
+        // With two buffers in turn a warp writes one again only after the others, done with it, have met once more: 56 -> 53 us
+        // for the down projection of all 32 experts.
+        float *sums_of = part + (two_parts ? turn & 1 : 0) * (kPartBytes / 4);
+        float *to_part = sums_of + warp * kGemvRows * kRowsPad;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[0][m][j] = kSets == 2 ? acc[0][m][j] + acc[1][m][j]
-                                      : (acc[0][m][j] + acc[kSets / 2][m][j]) + (acc[1][m][j] + acc[kSets - 1][m][j]);
+          for (int j = 0; j < 4; ++j) to_part[(2 * t + (j & 1)) * kRowsPad + 8 * (2 * m + (j >> 1)) + g] = acc[0][m][j];
+        auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kShare) : "memory"); };
+        meet();
+        const bool stop = *abort_flag != 0;  // some warp's sums are garbage
+        const float *theirs = sums_of + group * kShare * kGemvRows * kRowsPad + out;
+        for (int tok = from_row + (share * 32 + lane) / kOut; tok < to_row && writes && !stop; tok += 32 * kShare / kOut) {
+          const float *from = theirs + tok * kRowsPad;
+          auto joined = [&](const float *at) {
+            float w[kShare];
+#pragma unroll
+            for (int j = 0; j < kShare; ++j) w[j] = at[j * kGemvRows * kRowsPad];
+#pragma unroll
+            for (int half = kShare / 2; half; half /= 2)
+#pragma unroll
+              for (int j = 0; j < half; ++j) w[j] += w[j + half];
+            return w[0];
+          };
+          float v = joined(from);
+          const float up = kSwiglu ? joined(from + 16) : 0.0f;
+          const float back = wide ? 256.0f : s.back[tok];
+          v = (v * back) * scale;
+          if (kSwiglu) v = silu_times(v, (up * back) * up_scale);
+          static_cast<__nv_bfloat16 *>(p.y)[static_cast<int64_t>(row0 + tok) * out_n + (out_row - it.e * n)] =
+              __float2bfloat16_rn(v);
+        }
+        if (!two_parts) meet();
       }
-      // With two buffers in turn a warp writes one again only after the others, done with it, have met once more: 56 -> 53 us
-      // for the down projection of all 32 experts.
-      float *sums_of = part + (two_parts ? turn & 1 : 0) * (kPartBytes / 4);
-      float *to_part = sums_of + warp * kGemvRows * kRowsPad;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) to_part[(2 * t + (j & 1)) * kRowsPad + 8 * (2 * m + (j >> 1)) + g] = acc[0][m][j];
-      auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kShare) : "memory"); };
-      meet();
-      const bool stop = *abort_flag != 0;  // some warp's sums are garbage
-      const float *theirs = sums_of + group * kShare * kGemvRows * kRowsPad + out;
-      for (int tok = (share * 32 + lane) / kOut; tok < rows && writes && !stop; tok += 32 * kShare / kOut) {
-        const float *from = theirs + tok * kRowsPad;
-        auto joined = [&](const float *at) {
-          float w[kShare];
-#pragma unroll
-          for (int j = 0; j < kShare; ++j) w[j] = at[j * kGemvRows * kRowsPad];
-#pragma unroll
-          for (int half = kShare / 2; half; half /= 2)
-#pragma unroll
-            for (int j = 0; j < half; ++j) w[j] += w[j + half];
-          return w[0];
-        };
-        float v = joined(from);
-        const float up = kSwiglu ? joined(from + 16) : 0.0f;
-        const float back = wide ? 256.0f : s.back[tok];
-        v = (v * back) * scale;
-        if (kSwiglu) v = silu_times(v, (up * back) * up_scale);
-        static_cast<__nv_bfloat16 *>(p.y)[static_cast<int64_t>(row0 + tok) * out_n + (out_row - it.e * n)] =
-            __float2bfloat16_rn(v);
-      }
-      if (!two_parts) meet();
     }
   }
   // A wait that ran out leaves copies behind: they land before the CTA can exit.
@@ -505,10 +523,11 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
 // Rows of x taken at a time: eight with 7168 of k are half of an SM's shared memory.
 int32_t gemv_tile_rows(int64_t k) { return k <= 7168 ? kGemvRows : kGemvRows / 2; }
 
-// An upper bound of a call's units.
+// An upper bound of a call's units: every expert with a row has a tile, and each further one takes as many rows as a tile.
 int64_t unit_bound(const LaunchGemv &a) {
   const int64_t per = a.swiglu ? a.n / 256 * 8 : (a.n % 128 == 0 ? a.n / 128 : (a.n + 254) / 128) * 4;
-  return (a.m / gemv_tile_rows(a.k) + std::min<int64_t>(a.num_experts, a.m)) * per;
+  const int64_t experts = std::min<int64_t>(a.num_experts, a.m);
+  return (experts + (a.m - experts) / gemv_tile_rows(a.k)) * per;
 }
 
 template <bool kSwiglu, int kShare>
@@ -533,17 +552,21 @@ cudaError_t launch_gemv(LaunchGemv a) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// How many warps share a unit: eight while the SMs have few, then as few as the chunks of k make worth a meeting.  Measured,
-// us with 8 / 4 / 2 warps: gate/up of 4096 x 7168 with SwiGLU, one expert with one row (0.8 units an SM) 9.3 / 10.9 / 18.6, two
-// with one each (1.7) 12.8 / 13.3 / 19.0, four (3.4) 19.9 / 18.4 / 21.8, eight (7) 31.5 / 29.8 / 30.7, 32 (27) 98 / 97 / 99;
-// down projection of 7168 x 2048, one expert (1.5) 6.8 / 7.0 / 8.8, four (6) 12.9 / 12.7 / 11.8, 32 (47) 62 / 54 / 53; 8 experts
-// of 1000 x 1344 with 74 rows (4) 10.8 / 11.2 / 12.7.
+// How many warps share a unit: eight while the SMs have few, four from two units an SM on; two where the chunks of k would leave
+// some of four without work and not of two.  Measured, us with 8 / 4 / 2 warps, experts with a row each: gate/up of 4096 x 7168
+// with SwiGLU, one (0.8 units an SM) 9.1 / 11.2 / 19.3, two (1.7) 11.6 / 13.2 / 19.7, three (2.5) 15.8 / 15.1 / 20.9, eight (7)
+// 31.6 / 30.0 / 31.0, 32 (27) 98 / 91 / 97; down projection of 7168 x 2048, one (1.5) 6.7 / 7.1 / 8.9, eight (12) 19.6 / 18.2 / 19.0,
+// 32 (47) 59 / 52 / 50, with 128 rows in all 63 / 57 / 59; 4096 x 1536, four (3.4) 8.7 / 8.5 / 8.4, 32 (27) 35 / 33 / 29; 4096 x
+// 2304, four 10.8 / 10.2 / 10.5, 32 50 / 44 / 40; 2048 x 512, eight (3.4) 7.5 / 6.7 / 6.2; 8 experts of 1000 x 1344 with 74 rows (2.7)
+// 11.2 / 11.8 / 13.8 (six chunks fill eight warps no worse than four).
 template <bool kSwiglu>
 cudaError_t launch_gemv(const LaunchGemv &a) {
-  const int64_t units = unit_bound(a);
-  const bool short_k = a.k <= 2048;
-  if (units < (short_k ? 5 : 3) * a.num_sms) return launch_gemv<kSwiglu, 8>(a);
-  return short_k ? launch_gemv<kSwiglu, 2>(a) : launch_gemv<kSwiglu, 4>(a);
+  const int64_t units = unit_bound(a), chunks = (a.k + kChunk - 1) / kChunk;
+  const bool uneven = chunks <= 10 && (chunks % 4 == 1 || chunks % 4 == 2);
+  const bool few = units < 5 * a.num_sms;
+  if (units < 2 * a.num_sms || (few && uneven && chunks > 4 && chunks < 8)) return launch_gemv<kSwiglu, 8>(a);
+  if (uneven && (!few || chunks <= 2)) return launch_gemv<kSwiglu, 2>(a);
+  return launch_gemv<kSwiglu, 4>(a);
 }
 
 }  // namespace

@@ -131,6 +131,33 @@ def test_gathered_with_activation(tokens, top_k, experts, n, k, status):
     assert bool((err <= 1.01 * allowed + 1e-30).all()), float((err - allowed).max())
 
 
+@pytest.mark.parametrize("experts,n,k", [(6, 1000, 1536), (40, 1000, 1536), (40, 1000, 2048), (12, 2048, 7168), (256, 512, 320),
+                                         (1024, 256, 64)])
+def test_experts_taken_together(experts, n, k, status):
+    """Units of several experts side by side, experts without rows and with more rows than fit between them, and every other
+    expert's rows NaN, infinite or of a range that only the other decoding takes."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(experts + k)
+    few = torch.randint(0, 3, (experts,), generator=g, device=DEV)
+    few[torch.randint(0, experts, (experts // 6 + 1,), generator=g, device=DEV)] = 9
+    off = [0] + few.cumsum(0).tolist()
+    codes, sf, scale = nvfp4w.random_weights(experts * n, k, 11)
+    x = integers((off[-1], k), 12)
+    y = fme.grouped_gemv_nvfp4(x, codes, sf, scale, i32(off), status=status)
+    want, _ = product64(x, nvfp4w.values(codes, sf, scale), off, n)
+    assert torch.equal(y, want.to(torch.bfloat16))
+    rows = torch.repeat_interleave(torch.arange(experts, device=DEV), few) % 2 == 1
+    for bad in (float("nan"), float("inf"), 2.0 ** -60):
+        other = x.clone()
+        other[rows, ::5] = bad
+        got = fme.grouped_gemv_nvfp4(other, codes, sf, scale, i32(off), status=status)
+        assert torch.equal(got[~rows], y[~rows])
+        if n % 256 == 0:
+            clean = fme.grouped_gemv_nvfp4_swiglu(x, codes, sf, scale, i32(off), status=status)
+            got = fme.grouped_gemv_nvfp4_swiglu(other, codes, sf, scale, i32(off), status=status)
+            assert torch.equal(got[~rows], clean[~rows])
+
+
 def test_a_rows_bits_do_not_depend_on_the_batch(status):
     """Alone, and among more rows of an expert than are taken at a time."""
     n, k = 512, 1344
