@@ -969,11 +969,12 @@ fme_status bf16_rows_gemm(bool dgrad, const void *a_rows, const void *w, const i
   if (st != FME_OK) return st;
   a.k = dgrad ? n : k;
   a.n = dgrad ? k : n;
-  const bool few = !dgrad && fme::bf16_few_rows(m, n, num_experts, a.num_sms);
+  a.few_halves = dgrad ? 0 : fme::bf16_few_halves(m, n, k, num_experts, a.num_sms);
+  const bool few = a.few_halves != 0;
   CUtensorMap &rows_map = few ? a.map_b : a.map_a, &w_map = few ? a.map_a : a.map_b;
   if ((st = encode_bf16_2d(&rows_map, a_rows, m, a.k, few ? 16 : 128)) != FME_OK) return st;
   st = dgrad ? encode_bf16_mn(&w_map, &a.wide_b, w, num_experts, n, k)
-             : encode_bf16_weights(&w_map, w, num_experts, n, k, 128);
+             : encode_bf16_weights(&w_map, w, num_experts, n, k, few ? 256 / a.few_halves : 128);
   if (st != FME_OK) return st;
   if ((st = encode_bf16_out(&a.map_y, y, a.n, m, OutBox::kWideBf16)) != FME_OK) return st;
   a.offsets = offsets;

@@ -183,21 +183,35 @@ struct LaunchBf16 {
   int64_t m, n, k;  // output rows (wgrad: of one expert) and columns; contraction (not wgrad)
   void *y;
   bool out_fp32, accumulate;  // wgrad
+  int few_halves;             // forward: bf16_few_halves
   bool wide_a, wide_b;        // MN-major operands: the map gives 128 columns as two of 64 in one box
   int32_t *status;
   int num_sms;
   int stages;  // operand ring depth, set by the launcher
   cudaStream_t stream;
 };
-// The forward takes its few-rows form (map_a = weights in 128-row boxes, map_b = tokens in 16-row
+// At most so many tiles of 64 tokens: each expert with a row has one, and 64 more rows make one more.
+inline int64_t bf16_few_tiles(int64_t m, int32_t num_experts) {
+  const int64_t experts = std::min<int64_t>(num_experts, m);
+  return experts + (m - experts) / 64;
+}
+// The forward takes its few-rows form (map_a = weights, map_b = tokens in 16-row
 // boxes) up to this many rows: there it reads the weights once, past it the token tiles of 64 read them again and again.  It is
 // also taken while every item has an SM to itself.  Measured, us (few rows / pairs), even loads: 32 experts of 4096 x 7168, 1024
 // rows 270 / 293, 2048 rows 277 / 315, 3000 rows 370 / 324 (uneven loads fill more tiles: the border is at 48 rows an
 // expert); one expert, 16 rows 23 / 36, 256 rows 28 / 36, 384 rows 52 / 37; 8 experts of 1048 x 1400, 400 rows 11 / 14, 1400 rows
 // 18 / 15; 4 experts of 7168 x 2048, 256 rows 25 / 29, 768 rows 42 / 31.
-inline bool bf16_few_rows(int64_t m, int64_t n, int32_t num_experts, int num_sms) {
-  const int64_t tiles = num_experts == 1 ? (m + 63) / 64 : m / 64 + std::min<int64_t>(num_experts, m);
-  return m <= 16 + 48 * static_cast<int64_t>(num_experts) || tiles * ((n + 127) / 128) <= num_sms;
+// Returns 0 where not; otherwise the blocks of 64 of k in a stage, 2, 4 or 8 for items of 128, 64 or 32 rows of W (the boxes of
+// map_a): the smaller ones while each has an SM to itself, and with a short k half of the SMs are left to the kernel behind,
+// which sets itself up there (1 us).  Measured, us (8 / 4 / 2 blocks): one expert of 4096 x 7168, 1 or 16 rows 16.6 / 18.7 / 23.0, 32
+// rows - / 19.4 / 23.6; of 7168 x 2048 (items of 64 rows: 112), one row - / 8.9 / 9.7; 4 experts of 1048 x 1400 with a row each
+// (132 items of 32) 8.1 / 7.0 / 8.0, 8 of them - / 9.1 / 8.4.
+inline int bf16_few_halves(int64_t m, int64_t n, int64_t k, int32_t num_experts, int num_sms) {
+  const int64_t tiles = bf16_few_tiles(m, num_experts);
+  auto alone = [&](int64_t rows, int sms) { return tiles * ((n + rows - 1) / rows) <= sms; };
+  if (m > 16 + 48 * static_cast<int64_t>(num_experts) && !alone(128, num_sms)) return 0;
+  if (m <= 16 && alone(32, k >= 4096 ? num_sms : num_sms / 2)) return 8;
+  return m <= 32 && alone(64, k >= 2048 ? num_sms : num_sms / 2) ? 4 : 2;
 }
 cudaError_t launch_bf16_fwd(const LaunchBf16 &a);
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a);

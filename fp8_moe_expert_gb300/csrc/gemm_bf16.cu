@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
 }
 
 // ------------------------------------------------- forward, few rows an expert --
-// The same sums with the operands exchanged: an item is 128 rows of W_e (the MMA's M) and up to 64
+// The same sums with the operands exchanged: an item is 128 rows of W_e (the MMA's M; or 64 or 32, below) and up to 64
 // of the expert's tokens (its N, in steps of 16), one CTA an item.  With few tokens the time is that of
 // reading the weights once, and 256-row token tiles would leave all but a few rows of the MMAs
 // empty and put the weights on half as many SMs.  A sum's steps over k are those of the tiles above, in the same
@@ -566,15 +566,18 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
 //   warp 0 producer of W, warp 1 MMA issuer, warps 2-5 epilogue (thread = row of W), warp 6 producer of the tokens.
 // A stage holds 128 of k, as two halves of 64: what bounds a CTA that has an SM to itself is the producers' and the
 // issuer's way around their loops (4096 x 7168, one expert with one row, 32 CTAs: 28.1 us with 64 of k in nine stages, 24.8
-// with 128 in four, 22.5 with a producer of its own for the tokens; with 64 rows 41, 39 and 28).  8 of 32 experts with a
+// with 128 in four, 23.0 with a producer of its own for the tokens; with 64 rows 41, 39 and 28).  8 of 32 experts with a
 // row each, 256 items: 72.5 us, 6.5 TB/s of weights; all 32 experts 270 us.
+// With few items of 128 rows most SMs would have none.  Up to 32 tokens in all an item may have 64 rows of W and a stage 256 of
+// k, up to 16 tokens 32 rows and 512: the stage's bytes are the same, kHalves blocks of 64 of k behind one another.  The
+// MMA's M stays 128: behind an item's rows it reads what lies there, and those rows of the accumulator are not read.  The one
+// expert with one row above: 16.6 us.
 constexpr int kFewTokens = 64;
 constexpr int kFewStages = 4;
 constexpr int kFewThreads = 224;
 constexpr int kFewTokenWarp = 6;
-constexpr int kFewHalfB = kFewTokens * 128;
 constexpr int kFewABytes = 2 * kABytes;
-constexpr int kFewBBytes = 2 * kFewHalfB;
+constexpr int kFewBBytes = 2 * kFewTokens * 128;
 constexpr int kFewStageBytes = kFewABytes + kFewBBytes;
 constexpr uint32_t kFewTmemCols = 2 * kFewTokens;
 
@@ -617,11 +620,12 @@ struct ItemFew {
   int32_t tokens;  // 1 .. 64
   int32_t n0;      // first row of W_e = output column
 };
+template <int kRows>
 __device__ __forceinline__ ItemFew item_few(const LaunchBf16 &p, const Tables &s, uint32_t t) {
-  const uint32_t nb = (static_cast<uint32_t>(p.n) + kBM - 1) / kBM;
+  const uint32_t nb = (static_cast<uint32_t>(p.n) + kRows - 1) / kRows;
   const uint32_t g = t / nb;
   ItemFew it;
-  it.n0 = static_cast<int32_t>((t - g * nb) * kBM);
+  it.n0 = static_cast<int32_t>((t - g * nb) * kRows);
   it.e = find_group(s.aux, p.num_experts, g);
   const int32_t first = (static_cast<int32_t>(g) - s.aux[it.e]) * kFewTokens;
   it.row0 = s.off[it.e] + first;
@@ -629,7 +633,10 @@ __device__ __forceinline__ ItemFew item_few(const LaunchBf16 &p, const Tables &s
   return it;
 }
 
+template <int kHalves>
 __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __grid_constant__ LaunchBf16 p) {
+  constexpr int kRows = 2 * kBM / kHalves;                // of W an item
+  constexpr int kHalfA = kFewABytes / kHalves, kHalfB = kFewBBytes / kHalves;
   __shared__ SharedFew s;
   extern __shared__ uint8_t dyn_smem[];
   constexpr uint32_t S = kFewStages;
@@ -683,7 +690,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
   const uint32_t tmem = s.tmem_base;
   volatile int *abort_flag = &s.abort_flag;
   const int halves = static_cast<int>((p.k + kStageK - 1) / kStageK);
-  const uint32_t nb = static_cast<uint32_t>((p.n + kBM - 1) / kBM);
+  const uint32_t nb = static_cast<uint32_t>((p.n + kRows - 1) / kRows);
   // malformed offsets: no item, straight to the end
   const uint32_t total = s.ok_flag ? static_cast<uint32_t>(tab.aux[p.num_experts]) * nb : 0;
   if (!s.ok_flag && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, kDevBadOffsets);
@@ -701,17 +708,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
       uint32_t stage = 0, phase = 1, filled = 0;
       bool stop = false;
       for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
-        const ItemFew it = item_few(p, tab, t);
-        for (int i = 0; i < halves; i += 2) {
+        const ItemFew it = item_few<kRows>(p, tab, t);
+        for (int i = 0; i < halves; i += kHalves) {
           if (!mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status)) {
             stop = true;
             break;
           }
           uint8_t *a = smem_a + stage * kFewABytes;
-          const bool both = i + 1 < halves;
-          mbar_arrive_expect_tx(&s.full[stage], both ? 2 * kABytes : kABytes);
-          tma_load_3d_own(a, &p.map_a, &s.full[stage], i * kStageK, it.n0, it.e);
-          if (both) tma_load_3d_own(a + kABytes, &p.map_a, &s.full[stage], (i + 1) * kStageK, it.n0, it.e);
+          mbar_arrive_expect_tx(&s.full[stage], min(kHalves, halves - i) * kHalfA);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            if (i + h < halves) tma_load_3d_own(a + h * kHalfA, &p.map_a, &s.full[stage], (i + h) * kStageK, it.n0, it.e);
           ++filled;
           if (++stage == S) {
             stage = 0;
@@ -727,20 +734,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
       uint32_t stage = 0, phase = 1, filled = 0;
       bool stop = false;
       for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x) {
-        const ItemFew it = item_few(p, tab, t);
+        const ItemFew it = item_few<kRows>(p, tab, t);
         const uint32_t bytes = ((it.tokens + 15) >> 4) * 16 * 128;  // of a half
-        for (int i = 0; i < halves; i += 2) {
+        for (int i = 0; i < halves; i += kHalves) {
           if (!mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status)) {
             stop = true;
             break;
           }
           uint8_t *b = smem_b + stage * kFewBBytes;
-          const bool both = i + 1 < halves;
-          mbar_arrive_expect_tx(&s.full_b[stage], both ? 2 * bytes : bytes);
-          for (int j = 0; j < it.tokens; j += 16) {
-            tma_load_2d_own(b + j * 128, &p.map_b, &s.full_b[stage], i * kStageK, it.row0 + j);
-            if (both) tma_load_2d_own(b + kFewHalfB + j * 128, &p.map_b, &s.full_b[stage], (i + 1) * kStageK, it.row0 + j);
-          }
+          mbar_arrive_expect_tx(&s.full_b[stage], min(kHalves, halves - i) * bytes);
+          for (int j = 0; j < it.tokens; j += 16)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              if (i + h < halves)
+                tma_load_2d_own(b + h * kHalfB + j * 128, &p.map_b, &s.full_b[stage], (i + h) * kStageK, it.row0 + j);
           ++filled;
           if (++stage == S) {
             stage = 0;
@@ -756,21 +763,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
     uint32_t stage = 0, phase = 0, items = 0;
     bool stop = false;
     for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x, ++items) {
-      const uint32_t cols = (item_few(p, tab, t).tokens + 15) & ~15;
+      const uint32_t cols = (item_few<kRows>(p, tab, t).tokens + 15) & ~15;
       const uint32_t idesc = idesc_bf16(false, false, 128, cols);
       const uint32_t b = items & 1;
       stop = warp_any(!mbar_wait(&s.acc_empty[b], ((items >> 1) & 1) ^ 1, abort_flag, p.status));
-      for (int i = 0; i < halves && !stop; i += 2) {
+      for (int i = 0; i < halves && !stop; i += kHalves) {
         stop = warp_any(!mbar_wait(&s.full[stage], phase, abort_flag, p.status) ||
                         !mbar_wait(&s.full_b[stage], phase, abort_flag, p.status));
         if (stop) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t ad = a_desc + stage * (kFewABytes / 16), bd = b_desc + stage * (kFewBBytes / 16);
-          mma_half_own(tmem + b * kFewTokens, ad, bd, idesc, i > 0);
-          if (i + 1 < halves) mma_half_own(tmem + b * kFewTokens, ad + kABytes / 16, bd + kFewHalfB / 16, idesc, 1);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h)
+            if (i + h < halves)
+              mma_half_own(tmem + b * kFewTokens, ad + h * (kHalfA / 16), bd + h * (kHalfB / 16), idesc, i + h > 0);
           commit_own(&s.freed[stage]);
-          if (i + 2 >= halves) commit_own(&s.acc_full[b]);
+          if (i + kHalves >= halves) commit_own(&s.acc_full[b]);
         }
         __syncwarp();
         if (++stage == S) {
@@ -792,7 +801,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
     uint32_t items = 0;
     bool stop = false;
     for (uint32_t t = blockIdx.x; t < total && !stop; t += gridDim.x, ++items) {
-      const ItemFew it = item_few(p, tab, t);
+      const ItemFew it = item_few<kRows>(p, tab, t);
       const uint32_t b = items & 1;
       stop = warp_any(!mbar_wait(&s.acc_full[b], (items >> 1) & 1, abort_flag, p.status));
       if (stop) break;
@@ -801,7 +810,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
       __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + static_cast<int64_t>(it.row0) * p.n + col;
 #pragma unroll
       for (int c = 0; c < kFewTokens / 16; ++c) {
-        if (16 * c < it.tokens) {
+        if (16 * c < it.tokens && q * 32 < kRows) {
           uint32_t v[16];
           tmem_ld_32x16(tq + b * kFewTokens + 16 * c, v);
           tmem_wait_ld_for(v);
@@ -855,12 +864,15 @@ cudaError_t launch_bf(LaunchBf16 a) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int kHalves>
 cudaError_t launch_few(const LaunchBf16 &a) {
   const int smem = 1024 + kFewStages * kFewStageBytes + 8 * (a.num_experts + 1);
+  auto kernel = gemm_bf16_few_kernel<kHalves>;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t err = allow_shared(reinterpret_cast<const void *>(gemm_bf16_few_kernel), allowed);
+  cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
   if (err != cudaSuccess) return err;
-  const int64_t items = (a.m / kFewTokens + std::min<int64_t>(a.num_experts, a.m)) * ((a.n + kBM - 1) / kBM);
+  constexpr int kRows = 2 * kBM / kHalves;
+  const int64_t items = bf16_few_tiles(a.m, a.num_experts) * ((a.n + kRows - 1) / kRows);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, items)), 1, 1);
   cfg.blockDim = dim3(kFewThreads, 1, 1);
@@ -871,13 +883,18 @@ cudaError_t launch_few(const LaunchBf16 &a) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_bf16_few_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
 
 cudaError_t launch_bf16_fwd(const LaunchBf16 &a) {
-  return bf16_few_rows(a.m, a.n, a.num_experts, a.num_sms) ? launch_few(a) : launch_bf<KindBf::kFwd>(a);
+  switch (a.few_halves) {
+    case 2: return launch_few<2>(a);
+    case 4: return launch_few<4>(a);
+    case 8: return launch_few<8>(a);
+    default: return launch_bf<KindBf::kFwd>(a);
+  }
 }
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kDgrad>(a); }
 cudaError_t launch_bf16_wgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kWgrad>(a); }

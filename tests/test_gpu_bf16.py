@@ -164,6 +164,19 @@ def test_one_experts_values_do_not_reach_anothers(off, bad, status):
         assert torch.equal(got[keep], want[keep]) and not bool(got[~keep].isfinite().any())
 
 
+@pytest.mark.parametrize("n", [40, 1000, 4096, 9000])
+@pytest.mark.parametrize("k", [64, 200, 520, 1400])
+def test_forward_of_few_rows_in_items_of_any_height(n, k, status):
+    """Items of 32, 64 and 128 rows of W, with blocks of 64 of k that do not fill a stage; a NaN row of W stays its own."""
+    for rows, experts in ((1, 1), (16, 1), (3, 5), (17, 1), (32, 2), (33, 1)):
+        off = ref.split(rows, experts, rows + n)
+        x, w = integers((rows, k), 1), integers((experts, n, k), 2)
+        w[:, 33 % n] = float("nan")
+        y = fme.grouped_gemm_fwd_bf16(x, w, i32(off), status=status)
+        want, _ = forward64(x, w, off)
+        assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.nan_to_num(), want.to(torch.bfloat16).nan_to_num())
+
+
 @pytest.mark.parametrize("n,k", [(128, 320), (136, 200), (1088, 72)])
 def test_wgrad_ends_anywhere(n, k, status):
     """Ends within the first 64 rows, each distance from a step of 16 and from a block of 64, NaN in every other expert's rows."""
