@@ -8,7 +8,10 @@
 // Frontier Model Training", "MXFP8 expert kernels").  Operands are read as they lie in memory: W is K-major for the
 // forward and MN-major for dgrad, wgrad's operands are MN-major, so nothing is transposed, padded or copied.
 // Products and sums are kept in fp32 in tensor memory over the whole contraction, in steps of 16 in order, and rounded
-// once: there is no split, so a row's result depends neither on other rows nor on which form below runs.
+// once: there is no split, so a row's result depends neither on other rows nor on which form below runs.  But each step
+// of the MMA cuts its sum towards zero, which adds up: relative error of dW over 4096, 20000 and 65536 rows of an expert 5e-6, 2e-5 and
+// 8e-5.  bf16 does not show that, fp32 does: there wgrad hands over a sum every 16 stages (1024 rows), and the epilogue's warps
+// add those up in registers, rounded to nearest: 8e-7, 8e-7 and 9e-7 (65536 rows, one expert of 4096 x 7168: 2.25 ms, without 2.09).
 //
 // What bounds them.  A stage of 64 of the contraction takes a pair's M = 256, N = 256 MMAs 512 cycles; the 48 KB that
 // they read of an SM's shared memory and the 32 KB that the copies write there take 640 at 128 bytes a cycle, and 620 are
@@ -43,6 +46,8 @@ constexpr int kStageK = 64;  // bf16 of the contraction in a stage: one 128-byte
 constexpr int kStageBytesBf = kABytes + kBBytes;
 constexpr int kMaxStagesBf = 6;
 constexpr int kOutBlockBytes = 32 * 128;  // a warp's staging block: 32 rows of 128 bytes
+constexpr int kSumStages = 16;  // kSum: stages of a sum in tensor memory, a power of two
+constexpr int kSumRegs = 216, kOtherRegs = 72;  // kSum: registers a thread of the epilogue's warps and of the others
 constexpr int kHalfMnBytes = kStageK * 128;  // 64 M or N values (128 bytes) of an MN-major stage
 
 enum class KindBf { kFwd, kDgrad, kWgrad };
@@ -187,7 +192,8 @@ __device__ __forceinline__ void store_rows(T *y, int64_t ld, int64_t row0, int64
   }
 }
 
-template <KindBf K>
+// kSum: wgrad into fp32, in sums of kSumStages.
+template <KindBf K, bool kSum>
 __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_constant__ LaunchBf16 p) {
   constexpr bool kAmn = K == KindBf::kWgrad;
   constexpr bool kBmn = K != KindBf::kFwd;
@@ -283,164 +289,174 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
                                         : tab.aux[p.num_experts]) *
                        nb;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- producer
-      uint32_t stage = 0, phase = 1, filled = 0;
-      uint32_t early = 0;  // a bit a stage: its latest fill is warp 2's
-      bool stop = false;
-      for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
-        const TileBf tl = tile_bf<K>(p, tab, t, rank);
-        const int32_t bcol = tl.col0 + rank * kHalfN;
-        for (int i = 0; i < tl.nk; ++i) {
-          if (!mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status)) {
-            stop = true;
-            break;
-          }
-          if (K == KindBf::kWgrad && tl.p1 < kStageK) {
-            mbar_arrive(&s.early_go[stage]);
-            early |= 1u << stage;
-          } else {
-            if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytesBf);
-            const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
-            uint8_t *a = smem_a + stage * kABytes, *b = smem_b + stage * kBBytes;
-            const int32_t k0 = i * kStageK;
-            if constexpr (K == KindBf::kWgrad) {
-              // the window of 64 rows that starts here or ends with the expert
-              const int32_t window = min(tl.p0 + k0, tl.p1 - kStageK), from = tl.p0 + k0 - window;
-              if (p.wide_a) {
-                tma_load_4d_pair(a, &p.map_a, bar, 0, from, tl.row0 / 64, window);
-              } else {
-                tma_load_3d_pair(a, &p.map_a, bar, tl.row0, from, window);
-                tma_load_3d_pair(a + kHalfMnBytes, &p.map_a, bar, tl.row0 + 64, from, window);
-              }
-              if (p.wide_b) {
-                tma_load_4d_pair(b, &p.map_b, bar, 0, from, bcol / 64, window);
-              } else {
-                tma_load_3d_pair(b, &p.map_b, bar, bcol, from, window);
-                tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, from, window);
-              }
-            } else {
-              pair::tma_load_2d(a, &p.map_a, bar, k0, tl.row0);
-              if constexpr (K == KindBf::kFwd) {
-                tma_load_3d_pair(b, &p.map_b, bar, k0, bcol, tl.e);
-              } else if (p.wide_b) {
-                tma_load_4d_pair(b, &p.map_b, bar, 0, k0, bcol / 64, tl.e);
-              } else {
-                tma_load_3d_pair(b, &p.map_b, bar, bcol, k0, tl.e);
-                tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, k0, tl.e);
-              }
-            }
-            early &= ~(1u << stage);
-          }
-          ++filled;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
-      if (rank != 0) pair::st_remote_u32(pair::map_to_rank(&s.peer_early, 0), early);  // seen with the fills
-      const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
-      if (rank == 0)
-        drain_pair_ring(s.full, S, filled, peer, kStageBytesBf, early, *static_cast<volatile uint32_t *>(&s.peer_early));
-    }
-  } else if (K == KindBf::kWgrad && warp == 2) {
-    // ------------------------------------------------ blocks that end within the first 64 rows (a tile's only one)
-    uint32_t stage = 0, seen = 0, landed = 0;  // seen: a bit a stage, the parity of its early_go and early_peer
-    for (uint32_t round = 0, t; (t = tile_at(round)) < total; ++round) {
-      const TileBf tl = tile_bf<K>(p, tab, t, rank);
-      const uint32_t at = stage;
-      stage = (stage + tl.nk) % S;
-      if (tl.nk == 0 || tl.p1 >= kStageK) continue;
-      const uint32_t parity = (seen >> at) & 1;
-      seen ^= 1u << at;
-      if (warp_any(!mbar_wait<true>(&s.early_go[at], parity, abort_flag, p.status))) break;
-      uint8_t *a = smem_a + at * kABytes, *b = smem_b + at * kBBytes;
+  if (warp < kEpiWarp0) {
+    // registers for the sums of the epilogue's warps, of what the launch has
+    if constexpr (kSum) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(&s.early_full, kStageBytesBf);
-        const uint32_t bar = pair::map_to_rank(&s.early_full, rank);
-        const int32_t bcol = tl.col0 + rank * kHalfN;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          pair::tma_load_2d(a + half * kHalfMnBytes, &p.early_a, bar, tl.row0 + 64 * half, tl.p0);
-          pair::tma_load_2d(b + half * kHalfMnBytes, &p.early_b, bar, bcol + 64 * half, tl.p0);
+        // ---------------------------------------------------------------- producer
+        uint32_t stage = 0, phase = 1, filled = 0;
+        uint32_t early = 0;  // a bit a stage: its latest fill is warp 2's
+        bool stop = false;
+        for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
+          const TileBf tl = tile_bf<K>(p, tab, t, rank);
+          const int32_t bcol = tl.col0 + rank * kHalfN;
+          for (int i = 0; i < tl.nk; ++i) {
+            if (!mbar_wait<true>(&s.freed[stage], phase, abort_flag, p.status)) {
+              stop = true;
+              break;
+            }
+            if (K == KindBf::kWgrad && tl.p1 < kStageK) {
+              mbar_arrive(&s.early_go[stage]);
+              early |= 1u << stage;
+            } else {
+              if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageBytesBf);
+              const uint32_t bar = pair::map_to_rank(&s.full[stage], 0);
+              uint8_t *a = smem_a + stage * kABytes, *b = smem_b + stage * kBBytes;
+              const int32_t k0 = i * kStageK;
+              if constexpr (K == KindBf::kWgrad) {
+                // the window of 64 rows that starts here or ends with the expert
+                const int32_t window = min(tl.p0 + k0, tl.p1 - kStageK), from = tl.p0 + k0 - window;
+                if (p.wide_a) {
+                  tma_load_4d_pair(a, &p.map_a, bar, 0, from, tl.row0 / 64, window);
+                } else {
+                  tma_load_3d_pair(a, &p.map_a, bar, tl.row0, from, window);
+                  tma_load_3d_pair(a + kHalfMnBytes, &p.map_a, bar, tl.row0 + 64, from, window);
+                }
+                if (p.wide_b) {
+                  tma_load_4d_pair(b, &p.map_b, bar, 0, from, bcol / 64, window);
+                } else {
+                  tma_load_3d_pair(b, &p.map_b, bar, bcol, from, window);
+                  tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, from, window);
+                }
+              } else {
+                pair::tma_load_2d(a, &p.map_a, bar, k0, tl.row0);
+                if constexpr (K == KindBf::kFwd) {
+                  tma_load_3d_pair(b, &p.map_b, bar, k0, bcol, tl.e);
+                } else if (p.wide_b) {
+                  tma_load_4d_pair(b, &p.map_b, bar, 0, k0, bcol / 64, tl.e);
+                } else {
+                  tma_load_3d_pair(b, &p.map_b, bar, bcol, k0, tl.e);
+                  tma_load_3d_pair(b + kHalfMnBytes, &p.map_b, bar, bcol + 64, k0, tl.e);
+                }
+              }
+              early &= ~(1u << stage);
+            }
+            ++filled;
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
         }
+        if (rank != 0) pair::st_remote_u32(pair::map_to_rank(&s.peer_early, 0), early);  // seen with the fills
+        const uint32_t peer = exchange_fills(rank, filled, &s.peer_fills, &s.peer_fills_bar, p.status);
+        if (rank == 0)
+          drain_pair_ring(s.full, S, filled, peer, kStageBytesBf, early, *static_cast<volatile uint32_t *>(&s.peer_early));
       }
-      __syncwarp();
-      if (warp_any(!mbar_wait<true>(&s.early_full, landed, abort_flag, p.status))) {
-        mbar_drain(&s.early_full, landed);
-        break;
-      }
-      landed ^= 1;
-      const int32_t rows = tl.p1 - tl.p0;
-      a += rows * 128;
-      b += rows * 128;
-      for (int i = lane; i < (15 - (rows + 15) % 16) * 8; i += 32)  // 16 bytes of each half of A and B; the swizzle stays in a row
+    } else if (K == KindBf::kWgrad && warp == 2) {
+      // ------------------------------------------------ blocks that end within the first 64 rows (a tile's only one)
+      uint32_t stage = 0, seen = 0, landed = 0;  // seen: a bit a stage, the parity of its early_go and early_peer
+      for (uint32_t round = 0, t; (t = tile_at(round)) < total; ++round) {
+        const TileBf tl = tile_bf<K>(p, tab, t, rank);
+        const uint32_t at = stage;
+        stage = (stage + tl.nk) % S;
+        if (tl.nk == 0 || tl.p1 >= kStageK) continue;
+        const uint32_t parity = (seen >> at) & 1;
+        seen ^= 1u << at;
+        if (warp_any(!mbar_wait<true>(&s.early_go[at], parity, abort_flag, p.status))) break;
+        uint8_t *a = smem_a + at * kABytes, *b = smem_b + at * kBBytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&s.early_full, kStageBytesBf);
+          const uint32_t bar = pair::map_to_rank(&s.early_full, rank);
+          const int32_t bcol = tl.col0 + rank * kHalfN;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          *reinterpret_cast<uint4 *>(a + half * kHalfMnBytes + 16 * i) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(b + half * kHalfMnBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+          for (int half = 0; half < 2; ++half) {
+            pair::tma_load_2d(a + half * kHalfMnBytes, &p.early_a, bar, tl.row0 + 64 * half, tl.p0);
+            pair::tma_load_2d(b + half * kHalfMnBytes, &p.early_b, bar, bcol + 64 * half, tl.p0);
+          }
         }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (rank != 0) {
-        if (lane == 0) pair::arrive_remote_release(pair::map_to_rank(&s.early_peer[at], 0));
-      } else {
-        if (warp_any(!pair::wait_acquire_cluster(&s.early_peer[at], parity, kWaitLimitNs))) {
-          *abort_flag = 1;
-          report(p.status, kDevTimeout);
+        __syncwarp();
+        if (warp_any(!mbar_wait<true>(&s.early_full, landed, abort_flag, p.status))) {
+          mbar_drain(&s.early_full, landed);
           break;
         }
-        if (lane == 0) mbar_arrive(&s.full[at]);
-      }
-      __syncwarp();
-    }
-  } else if (warp == 1) {
-    if (rank == 0) {
-      // ------------------------------------------- MMA issuer (leader, whole warp)
-      constexpr uint32_t idesc = idesc_bf16(kAmn, kBmn, 256, 256);
-      const uint64_t a_desc = desc_sw128(smem_u32(smem_a), kAmn, kHalfMnBytes);
-      const uint64_t b_desc = desc_sw128(smem_u32(smem_b), kBmn, kHalfMnBytes);
-      uint32_t stage = 0, phase = 0, tiles = 0;
-      bool stop = false;
-      for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
-        const TileBf tl = tile_bf<K>(p, tab, t, 0);
-        const int nk = tl.nk;
-        if (nk == 0) continue;  // an expert without rows: the epilogue writes zeros
-        const int left = K == KindBf::kWgrad ? (tl.p1 - tl.p0) % kStageK : 0;
-        const uint32_t b = tiles & 1;
-        stop = warp_any(!mbar_wait(&s.acc_empty[b], ((tiles >> 1) & 1) ^ 1, abort_flag, p.status));
-        for (int i = 0; i < nk && !stop; ++i) {
-          stop = warp_any(!mbar_wait(&s.full[stage], phase, abort_flag, p.status));
-          if (stop) break;
-          tc_fence_after();
-          // 16 of K: 32 bytes along a K-major row, 16 rows of an MN-major tile
-          if (elect_one()) {
-            constexpr uint32_t kA = (kAmn ? 2048 : 32) / 16, kB = (kBmn ? 2048 : 32) / 16;
-            const uint64_t a = a_desc + stage * (kABytes / 16), bd = b_desc + stage * (kBBytes / 16);
-            if (left != 0 && i == nk - 1)
-              mma_steps_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, i > 0, &s.freed[stage], (left + 15) / 16);
-            else
-              mma_stage_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, i > 0, &s.freed[stage]);
-            if (i == nk - 1) pair::commit_both(&s.acc_full[b]);
+        landed ^= 1;
+        const int32_t rows = tl.p1 - tl.p0;
+        a += rows * 128;
+        b += rows * 128;
+        for (int i = lane; i < (15 - (rows + 15) % 16) * 8; i += 32)  // 16 bytes of each half of A and B; the swizzle stays in a row
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            *reinterpret_cast<uint4 *>(a + half * kHalfMnBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(b + half * kHalfMnBytes + 16 * i) = make_uint4(0, 0, 0, 0);
           }
-          __syncwarp();
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (rank != 0) {
+          if (lane == 0) pair::arrive_remote_release(pair::map_to_rank(&s.early_peer[at], 0));
+        } else {
+          if (warp_any(!pair::wait_acquire_cluster(&s.early_peer[at], parity, kWaitLimitNs))) {
+            *abort_flag = 1;
+            report(p.status, kDevTimeout);
+            break;
+          }
+          if (lane == 0) mbar_arrive(&s.full[at]);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // ------------------------------------------- MMA issuer (leader, whole warp)
+        constexpr uint32_t idesc = idesc_bf16(kAmn, kBmn, 256, 256);
+        const uint64_t a_desc = desc_sw128(smem_u32(smem_a), kAmn, kHalfMnBytes);
+        const uint64_t b_desc = desc_sw128(smem_u32(smem_b), kBmn, kHalfMnBytes);
+        uint32_t stage = 0, phase = 0, tiles = 0;
+        bool stop = false;
+        for (uint32_t round = 0, t; (t = tile_at(round)) < total && !stop; ++round) {
+          const TileBf tl = tile_bf<K>(p, tab, t, 0);
+          const int nk = tl.nk;
+          if (nk == 0) continue;  // an expert without rows: the epilogue writes zeros
+          const int left = K == KindBf::kWgrad ? (tl.p1 - tl.p0) % kStageK : 0;
+          uint32_t b = 0;
+          for (int i = 0; i < nk && !stop; ++i) {
+            const int in = kSum ? i % kSumStages : i;  // the stage's place in its sum
+            if (in == 0) {
+              b = tiles & 1;
+              stop = warp_any(!mbar_wait(&s.acc_empty[b], ((tiles >> 1) & 1) ^ 1, abort_flag, p.status));
+              if (stop) break;
+              ++tiles;
+            }
+            stop = warp_any(!mbar_wait(&s.full[stage], phase, abort_flag, p.status));
+            if (stop) break;
+            tc_fence_after();
+            // 16 of K: 32 bytes along a K-major row, 16 rows of an MN-major tile
+            if (elect_one()) {
+              constexpr uint32_t kA = (kAmn ? 2048 : 32) / 16, kB = (kBmn ? 2048 : 32) / 16;
+              const uint64_t a = a_desc + stage * (kABytes / 16), bd = b_desc + stage * (kBBytes / 16);
+              if (left != 0 && i == nk - 1)
+                mma_steps_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, in > 0, &s.freed[stage], (left + 15) / 16);
+              else
+                mma_stage_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, in > 0, &s.freed[stage]);
+              if (i == nk - 1 || (kSum && in == kSumStages - 1)) pair::commit_both(&s.acc_full[b]);
+            }
+            __syncwarp();
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
-        ++tiles;
+        __syncwarp();
+        if (elect_one()) {
+          pair::commit_local(&s.drain);
+          mbar_drain(&s.drain, 0);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (elect_one()) {
-        pair::commit_local(&s.drain);
-        mbar_drain(&s.drain, 0);
-      }
-      __syncwarp();
     }
-  } else if (warp >= kEpiWarp0) {
+  } else {
+    if constexpr (kSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     // ----------------------------------------------------------------- epilogue
     const int ew = warp - kEpiWarp0;
     const int q = warp & 3;    // tensor-memory lane quarter
@@ -457,73 +473,134 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
       const int warp_rows = tl.rows_valid - 32 * q;
       const bool wanted = warp_rows > 0 && c0 < p.n;
       const bool empty = K == KindBf::kWgrad && tl.nk == 0;
-      const uint32_t b = tiles & 1;
       if (K == KindBf::kWgrad && p.accumulate && !empty && wanted) {
         // what the sums are added to is on its way into L2 while the MMAs run
         const float *at = static_cast<const float *>(p.y) + (static_cast<int64_t>(tl.e) * p.m + tl.row0 + 32 * q + lane) * p.n + c0;
         if (lane < warp_rows)
           for (int c = 0; c < 128 && c0 + c < p.n; c += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c));
       }
-      if (!empty) {
+      uint32_t b = 0;
+      auto next_sum = [&] {
+        b = tiles & 1;
         stop = warp_any(!mbar_wait(&s.acc_full[b], (tiles >> 1) & 1, abort_flag, p.status));
-        if (stop) break;
         tc_fence_after();
         ++tiles;
-      }
-      const int64_t out_row = (K == KindBf::kWgrad ? tl.e * p.m : int64_t(0)) + tl.row0 + 32 * q;
-      const bool fp32 = K == KindBf::kWgrad && p.out_fp32;
-      const bool add = fp32 && p.accumulate;
-      const int wide = fp32 ? 32 : 64;  // columns of a staging block
+      };
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) pair::arrive_remote_relaxed(leader_empty[b]);
       };
-      if (!empty && !wanted) release();
-      if (!wanted || (empty && add)) continue;
+      const int64_t out_row = (K == KindBf::kWgrad ? tl.e * p.m : int64_t(0)) + tl.row0 + 32 * q;
+      uint4 *row = reinterpret_cast<uint4 *>(blk + lane * 128);
+      auto pack = [](const uint32_t *v) {  // 8 values
+        uint32_t w[4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[2][32];
-        if (!empty) {
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          w[i] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      if constexpr (K == KindBf::kWgrad) {
+        const bool add = p.accumulate, fp32 = kSum || p.out_fp32;
+        // Columns 32 c on; blocks of 32 fp32 or 64 bf16 leave by plain stores (32 experts of 2048 rows, 7168 x 2048: 1.00 ms, 1.02
+        // by bulk stores, fp32 1.07 and 1.09).
+        auto put = [&](const uint32_t(&v)[32], int c) {
+          if (fp32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) row[j ^ xs] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) row[(4 * (c & 1) + j) ^ xs] = pack(v + 8 * j);
+            if ((c & 1) == 0) return;
+          }
+          __syncwarp();
+          float *y = static_cast<float *>(p.y);
+          if (add)
+            store_rows<float, true>(y, p.n, out_row, c0 + 32 * c, warp_rows, blk, lane);
+          else if (fp32)
+            store_rows<float, false>(y, p.n, out_row, c0 + 32 * c, warp_rows, blk, lane);
+          else
+            store_rows<__nv_bfloat16, false>(static_cast<__nv_bfloat16 *>(p.y), p.n, out_row, c0 + 32 * (c - 1), warp_rows, blk, lane);
+          __syncwarp();
+        };
+        if (kSum && tl.nk > kSumStages) {
+          float tot[128];
+#pragma unroll
+          for (int j = 0; j < 128; ++j) tot[j] = 0.0f;
+          for (int done = 0; done < tl.nk; done += kSumStages) {
+            next_sum();
+            if (stop) break;
+            if (wanted) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32(tq + b * kBN + 32 * c, v);
+                tmem_wait_ld_for(v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) tot[32 * c + j] += __uint_as_float(v[j]);
+              }
+            }
+            release();
+          }
+          if (stop) break;
+          if (!wanted) continue;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(tot[32 * c + j]);
+            put(v, c);
+          }
+        } else {
+          if (!empty) {
+            next_sum();
+            if (stop) break;
+            if (!wanted) release();
+          }
+          if (!wanted || (empty && add)) continue;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[2][32];
+            if (!empty) {
+              tmem_ld_32x32(tq + b * kBN + 64 * c, v[0]);
+              tmem_ld_32x32(tq + b * kBN + 64 * c + 32, v[1]);
+              tmem_wait_ld_for(v[0]);
+              tmem_wait_ld_for(v[1]);
+              if (c == 1) release();  // registers hold the data
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0;
+            }
+            put(v[0], 2 * c);
+            put(v[1], 2 * c + 1);
+          }
+        }
+      } else {
+        next_sum();
+        if (stop) break;
+        if (!wanted) {
+          release();
+          continue;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[2][32];
           tmem_ld_32x32(tq + b * kBN + 64 * c, v[0]);
           tmem_ld_32x32(tq + b * kBN + 64 * c + 32, v[1]);
           tmem_wait_ld_for(v[0]);
           tmem_wait_ld_for(v[1]);
           if (c == 1) release();  // registers hold the data
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0;
-        }
-        // one block of 64 bf16 columns, or two of 32 fp32
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1 && !fp32) break;
-          const int col = c0 + 64 * c + 32 * h;
+          const int col = c0 + 64 * c;
           if (col >= p.n) break;
           if (lane == 0) bulk_wait_read_all();
           __syncwarp();
-          uint4 *row = reinterpret_cast<uint4 *>(blk + lane * 128);
-          if (fp32) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              row[j ^ xs] = make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int at = 8 * (j & 3) + 2 * i;
-                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[j >> 2][at]), __uint_as_float(v[j >> 2][at + 1]));
-                w[i] = *reinterpret_cast<const uint32_t *>(&x);
-              }
-              row[j ^ xs] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          // A whole block leaves by a bulk store; rows cut by the expert's end or columns by the output's by plain ones.
-          // wgrad's leave by plain ones (32 experts of 2048 rows, 7168 x 2048: 1.00 ms, 1.02 by bulk stores, fp32 1.07 and
-          // 1.09; the forward is 0.5% slower by plain ones).
-          const bool bulk = K != KindBf::kWgrad && warp_rows >= 32 && col + wide <= p.n;
+          for (int j = 0; j < 8; ++j) row[j ^ xs] = pack(&v[j >> 2][8 * (j & 3)]);
+          // A whole block leaves by a bulk store (0.5% faster than by plain ones); rows cut by the expert's end or columns by
+          // the output's by plain ones.
+          const bool bulk = warp_rows >= 32 && col + 64 <= p.n;
           if (bulk) fence_proxy_async_shared();
           __syncwarp();
           if (bulk) {
@@ -532,12 +609,7 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
               bulk_commit();
             }
           } else {
-            if (add)
-              store_rows<float, true>(static_cast<float *>(p.y), p.n, out_row, col, warp_rows, blk, lane);
-            else if (fp32)
-              store_rows<float, false>(static_cast<float *>(p.y), p.n, out_row, col, warp_rows, blk, lane);
-            else
-              store_rows<__nv_bfloat16, false>(static_cast<__nv_bfloat16 *>(p.y), p.n, out_row, col, warp_rows, blk, lane);
+            store_rows<__nv_bfloat16, false>(static_cast<__nv_bfloat16 *>(p.y), p.n, out_row, col, warp_rows, blk, lane);
             __syncwarp();
           }
         }
@@ -833,12 +905,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFewTmemCols) : "memory");
 }
 
-template <KindBf K>
+template <KindBf K, bool kSum = false>
 cudaError_t launch_bf(LaunchBf16 a) {
-  auto kernel = gemm_bf16_kernel<K>;
+  auto kernel = gemm_bf16_kernel<K, kSum>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
   if (err != cudaSuccess) return err;
+  if (kSum) {  // what its warps ask for must be what the launch has: they would wait for more for ever
+    static const int regs = [&] {
+      cudaFuncAttributes attr;
+      return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
+    }();
+    if (regs * kThreadsBf < kSumRegs * (kThreadsBf - 32 * kEpiWarp0) + kOtherRegs * 32 * kEpiWarp0) return cudaErrorInvalidConfiguration;
+  }
   const int rest = 1024 + 8 * kOutBlockBytes + 8 * (a.num_experts + 1);
   // as many stages as fit beside the expert tables
   a.stages = std::min<int64_t>(kMaxStagesBf, (kGemmSmemLimit - rest) / kStageBytesBf);
@@ -897,6 +976,8 @@ cudaError_t launch_bf16_fwd(const LaunchBf16 &a) {
   }
 }
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kDgrad>(a); }
-cudaError_t launch_bf16_wgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kWgrad>(a); }
+cudaError_t launch_bf16_wgrad(const LaunchBf16 &a) {
+  return a.out_fp32 && a.rows > kSumStages * kStageK ? launch_bf<KindBf::kWgrad, true>(a) : launch_bf<KindBf::kWgrad>(a);
+}
 
 }  // namespace fme

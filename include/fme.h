@@ -588,7 +588,8 @@ fme_status grouped_gemm_dgrad_bf16(const void *dy, const void *w, const int32_t 
 
 /* grouped_gemm_wgrad_bf16 -- dW_e = dY_e^T X_e over the rows of expert e; dy bf16 [m x n], x bf16 [m x k], grouped with
  * the same offsets, no padding between experts.  dw, dw_mode as grouped_gemm_wgrad_fp8_block128's: bf16, fp32, or added
- * into fp32, one unfused add an element.  An expert with no rows gets zeros (nothing is added). */
+ * into fp32, one unfused add an element.  In fp32 the sums over 1024 rows each are added up in order, rounded to nearest.  An expert
+ * with no rows gets zeros (nothing is added). */
 fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, const int32_t *offsets, int32_t num_experts,
                                    int64_t n, int64_t k, void *dw, int32_t dw_mode, int32_t *dev_status, void *stream);
 

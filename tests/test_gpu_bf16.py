@@ -129,6 +129,23 @@ def test_wgrad_added_into_fp32(rows, experts, n, k, status):
     assert out is acc and torch.equal(acc, want)
 
 
+def test_long_wgrad_in_fp32_is_rounded_block_by_block(status):
+    """The sums of 1024 rows are exact here (products below 2^14), so the result is theirs, added in order in fp32."""
+    off, n, k = [0, 20000, 20037, 21061, 46661], 264, 136
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    dy, x = (torch.randint(0, 128, (off[-1], c), generator=g, device=DEV).to(torch.bfloat16) for c in (n, k))
+    want = torch.zeros((4, n, k), device=DEV)
+    for e, (lo, hi) in enumerate(zip(off, off[1:])):
+        for at in range(lo, hi, 1024):
+            to = min(at + 1024, hi)
+            want[e] += (dy[at:to].double().t() @ x[at:to].double()).float()
+    assert torch.equal(fme.grouped_gemm_wgrad_bf16(dy, x, i32(off), dtype=torch.float32, status=status), want)
+    old = torch.randn((4, n, k), device=DEV) * 1e6
+    out = fme.grouped_gemm_wgrad_bf16(dy, x, i32(off), dw=old.clone(), accumulate=True, status=status)
+    assert torch.equal(out, old + want)
+
+
 def test_a_rows_bits_do_not_depend_on_the_batch(status):
     """One row alone, a few (the form for few rows) and the whole batch (tiles)."""
     rows, experts, n, k = 6000, 3, 392, 1352

@@ -38,14 +38,17 @@ def test_dgrad(short_lib):  # noqa: F811
 
 
 @pytest.mark.parametrize("first", [128, 99, 20])
-def test_wgrad(short_lib, first):  # noqa: F811
-    """With whole blocks, with blocks that end inside, and with an end in the first 64 rows, which has a producer of its own."""
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_wgrad(short_lib, first, dtype):  # noqa: F811
+    """With whole blocks, with blocks that end inside, and with an end in the first 64 rows, which has a producer of its own.  (In fp32 a
+    sum is handed over every 16 stages, within a poll.)"""
     off = i32(0, first, DEEP - 1)
     m = DEEP - 1
     dy, x = ref.normal((m, N), 1.0, 1), ref.normal((m, N), 0.02, 2)
-    check(lambda st: fme.grouped_gemm_wgrad_bf16(dy, x, off, dtype=torch.float32, status=st),
+    check(lambda st: fme.grouped_gemm_wgrad_bf16(dy, x, off, dtype=dtype, status=st),
           lambda y, st, s: short_lib.grouped_gemm_wgrad_bf16(dy.data_ptr(), x.data_ptr(), m, off.data_ptr(), 2, N, N,
-                                                             y.data_ptr(), fme.DW_FP32, st, s))
+                                                             y.data_ptr(), fme.DW_FP32 if dtype == torch.float32 else fme.DW_BF16, st, s),
+          gives_up=dtype == torch.bfloat16)
 
 
 @pytest.mark.parametrize("rows, k", [(5, 8192), (40, 2048)])
