@@ -47,7 +47,6 @@ constexpr int kStageBytesBf = kABytes + kBBytes;
 constexpr int kMaxStagesBf = 6;
 constexpr int kOutBlockBytes = 32 * 128;  // a warp's staging block: 32 rows of 128 bytes
 constexpr int kSumStages = 16;  // kSum: stages of a sum in tensor memory, a power of two
-constexpr int kSumRegs = 216, kOtherRegs = 72;  // kSum: registers a thread of the epilogue's warps and of the others
 constexpr int kHalfMnBytes = kStageK * 128;  // 64 M or N values (128 bytes) of an MN-major stage
 
 enum class KindBf { kFwd, kDgrad, kWgrad };
@@ -160,6 +159,16 @@ __device__ __forceinline__ TileBf tile_bf(const LaunchBf16 &p, const Tables &s, 
     tl.p0 = tl.p1 = 0;
   }
   return tl;
+}
+
+// 32 lanes x 8 columns, and the wait for them.
+__device__ __forceinline__ void tmem_ld_32x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
 }
 
 // A staged block (32 rows of 128 bytes, swizzled) to columns `col` on, by plain stores; with kAdd added to what is there
@@ -290,8 +299,6 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
                        nb;
 
   if (warp < kEpiWarp0) {
-    // registers for the sums of the epilogue's warps, of what the launch has
-    if constexpr (kSum) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 0) {
       if (lane == 0) {
         // ---------------------------------------------------------------- producer
@@ -456,12 +463,12 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
       }
     }
   } else {
-    if constexpr (kSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     // ----------------------------------------------------------------- epilogue
     const int ew = warp - kEpiWarp0;
     const int q = warp & 3;    // tensor-memory lane quarter
     const int half = ew >> 2;  // column half of the tile
-    uint8_t *blk = smem_out + ew * kOutBlockBytes;
+    // from its 32-bit address: the compiler then keeps no 64-bit pointers through wgrad's sums, which have no registers to spare
+    uint8_t *blk = static_cast<uint8_t *>(__cvta_shared_to_generic(smem_u32(smem_out) + ew * kOutBlockBytes));
     const uint32_t leader_empty[2] = {pair::map_to_rank(&s.acc_empty[0], 0), pair::map_to_rank(&s.acc_empty[1], 0)};
     const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     const int xs = lane & 7;  // the 128-byte swizzle of this lane's row
@@ -534,12 +541,11 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
             if (stop) break;
             if (wanted) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32(tq + b * kBN + 32 * c, v);
-                tmem_wait_ld_for(v);
+              for (int c = 0; c < 16; ++c) {
+                uint32_t v[8];
+                tmem_ld_32x8(tq + b * kBN + 8 * c, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) tot[32 * c + j] += __uint_as_float(v[j]);
+                for (int j = 0; j < 8; ++j) tot[8 * c + j] += __uint_as_float(v[j]);
               }
             }
             release();
@@ -911,13 +917,6 @@ cudaError_t launch_bf(LaunchBf16 a) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t err = allow_shared(reinterpret_cast<const void *>(kernel), allowed);
   if (err != cudaSuccess) return err;
-  if (kSum) {  // what its warps ask for must be what the launch has: they would wait for more for ever
-    static const int regs = [&] {
-      cudaFuncAttributes attr;
-      return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
-    }();
-    if (regs * kThreadsBf < kSumRegs * (kThreadsBf - 32 * kEpiWarp0) + kOtherRegs * 32 * kEpiWarp0) return cudaErrorInvalidConfiguration;
-  }
   const int rest = 1024 + 8 * kOutBlockBytes + 8 * (a.num_experts + 1);
   // as many stages as fit beside the expert tables
   a.stages = std::min<int64_t>(kMaxStagesBf, (kGemmSmemLimit - rest) / kStageBytesBf);
