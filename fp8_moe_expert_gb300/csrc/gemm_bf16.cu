@@ -10,8 +10,10 @@
 // Products and sums are kept in fp32 in tensor memory over the whole contraction, in steps of 16 in order, and rounded
 // once: there is no split, so a row's result depends neither on other rows nor on which form below runs.  But each step
 // of the MMA cuts its sum towards zero, which adds up: relative error of dW over 4096, 20000 and 65536 rows of an expert 5e-6, 2e-5 and
-// 8e-5.  bf16 does not show that, fp32 does: there wgrad hands over a sum every 16 stages (1024 rows), and the epilogue's warps
-// add those up in registers, rounded to nearest: 8e-7, 8e-7 and 9e-7 (65536 rows, one expert of 4096 x 7168: 2.25 ms, without 2.09).
+// 8e-5 (4% of half a bf16 step).  fp32 shows that: there wgrad hands over a sum every 16 stages (1024 rows), and the
+// epilogue's warps add those up in registers, rounded to nearest: 8e-7, 8e-7 and 9e-7.  bf16 shows it past 65536 rows of an expert, where
+// it does the same every 1024 stages (sums of one sign over 2^25 rows 4% too small in one; the forward's and dgrad's
+// contractions end at 65536).
 //
 // What bounds them.  A stage of 64 of the contraction takes a pair's M = 256, N = 256 MMAs 512 cycles; the 48 KB that
 // they read of an SM's shared memory and the 32 KB that the copies write there take 640 at 128 bytes a cycle, and 620 are
@@ -46,7 +48,7 @@ constexpr int kStageK = 64;  // bf16 of the contraction in a stage: one 128-byte
 constexpr int kStageBytesBf = kABytes + kBBytes;
 constexpr int kMaxStagesBf = 6;
 constexpr int kOutBlockBytes = 32 * 128;  // a warp's staging block: 32 rows of 128 bytes
-constexpr int kSumStages = 16;  // kSum: stages of a sum in tensor memory, a power of two
+constexpr int kSumStages32 = 16, kSumStages16 = 1024;  // wgrad: stages of a sum in tensor memory, for fp32 and for bf16 dW
 constexpr int kHalfMnBytes = kStageK * 128;  // 64 M or N values (128 bytes) of an MN-major stage
 
 enum class KindBf { kFwd, kDgrad, kWgrad };
@@ -201,8 +203,8 @@ __device__ __forceinline__ void store_rows(T *y, int64_t ld, int64_t row0, int64
   }
 }
 
-// kSum: wgrad into fp32, in sums of kSumStages.
-template <KindBf K, bool kSum>
+// kSum: wgrad in sums of so many stages, a power of two (kSumStages32 into fp32, kSumStages16 into bf16); 0: in one.
+template <KindBf K, int kSum>
 __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_constant__ LaunchBf16 p) {
   constexpr bool kAmn = K == KindBf::kWgrad;
   constexpr bool kBmn = K != KindBf::kFwd;
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
           const int left = K == KindBf::kWgrad ? (tl.p1 - tl.p0) % kStageK : 0;
           uint32_t b = 0;
           for (int i = 0; i < nk && !stop; ++i) {
-            const int in = kSum ? i % kSumStages : i;  // the stage's place in its sum
+            const int in = kSum ? i % (kSum ? kSum : 1) : i;  // the stage's place in its sum
             if (in == 0) {
               b = tiles & 1;
               stop = warp_any(!mbar_wait(&s.acc_empty[b], ((tiles >> 1) & 1) ^ 1, abort_flag, p.status));
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
                 mma_steps_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, in > 0, &s.freed[stage], (left + 15) / 16);
               else
                 mma_stage_pair<kA, kB>(tmem + b * kBN, a, bd, idesc, in > 0, &s.freed[stage]);
-              if (i == nk - 1 || (kSum && in == kSumStages - 1)) pair::commit_both(&s.acc_full[b]);
+              if (i == nk - 1 || (kSum && in == kSum - 1)) pair::commit_both(&s.acc_full[b]);
             }
             __syncwarp();
             if (++stage == S) {
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
         return make_uint4(w[0], w[1], w[2], w[3]);
       };
       if constexpr (K == KindBf::kWgrad) {
-        const bool add = p.accumulate, fp32 = kSum || p.out_fp32;
+        const bool add = kSum != kSumStages16 && p.accumulate, fp32 = kSum ? kSum == kSumStages32 : p.out_fp32;
         // Columns 32 c on; blocks of 32 fp32 or 64 bf16 leave by plain stores (32 experts of 2048 rows, 7168 x 2048: 1.00 ms, 1.02
         // by bulk stores, fp32 1.07 and 1.09).
         auto put = [&](const uint32_t(&v)[32], int c) {
@@ -532,11 +534,11 @@ __global__ void __launch_bounds__(kThreadsBf, 1) gemm_bf16_kernel(const __grid_c
             store_rows<__nv_bfloat16, false>(static_cast<__nv_bfloat16 *>(p.y), p.n, out_row, c0 + 32 * (c - 1), warp_rows, blk, lane);
           __syncwarp();
         };
-        if (kSum && tl.nk > kSumStages) {
+        if (kSum && tl.nk > kSum) {
           float tot[128];
 #pragma unroll
           for (int j = 0; j < 128; ++j) tot[j] = 0.0f;
-          for (int done = 0; done < tl.nk; done += kSumStages) {
+          for (int done = 0; done < tl.nk; done += kSum) {
             next_sum();
             if (stop) break;
             if (wanted) {
@@ -911,7 +913,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) gemm_bf16_few_kernel(const __g
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFewTmemCols) : "memory");
 }
 
-template <KindBf K, bool kSum = false>
+template <KindBf K, int kSum = 0>
 cudaError_t launch_bf(LaunchBf16 a) {
   auto kernel = gemm_bf16_kernel<K, kSum>;
   static std::atomic<uint64_t> allowed{0};
@@ -976,7 +978,8 @@ cudaError_t launch_bf16_fwd(const LaunchBf16 &a) {
 }
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a) { return launch_bf<KindBf::kDgrad>(a); }
 cudaError_t launch_bf16_wgrad(const LaunchBf16 &a) {
-  return a.out_fp32 && a.rows > kSumStages * kStageK ? launch_bf<KindBf::kWgrad, true>(a) : launch_bf<KindBf::kWgrad>(a);
+  if (a.rows <= (a.out_fp32 ? kSumStages32 : kSumStages16) * kStageK) return launch_bf<KindBf::kWgrad>(a);
+  return a.out_fp32 ? launch_bf<KindBf::kWgrad, kSumStages32>(a) : launch_bf<KindBf::kWgrad, kSumStages16>(a);
 }
 
 }  // namespace fme

@@ -569,8 +569,9 @@ fme_status grouped_gemm_wgrad_fp8_block128(const uint8_t *dy_codes, const float 
  * grouped_gemm_fwd_bf16 -- Y[t, n] = sum_k x[t, k] w[e, n, k] for every row t of expert e, on bf16 operands (layers
  * that stay in bf16, and what the low-precision products are compared with: "Scaling and Optimizing Frontier Model
  * Training", "MXFP8 expert kernels").  Products and sums in fp32 on the tensor cores over the whole
- * contraction, one rounding to bf16.  No split over k: a row's output does not depend on any other row, whatever the
- * number of rows.
+ * contraction, one rounding to bf16.  Each step of 16 of the tensor cores cuts its sum towards zero: 8e-5 of it over a
+ * contraction of 65536, 4% of half a bf16 step.  No split over k: a row's output does not depend on any other row, whatever
+ * the number of rows.
  *
  *   x         device bf16 [m x k], the rows grouped by expert (moe_permute)
  *   w         device bf16 [num_experts][n][k]
@@ -588,8 +589,8 @@ fme_status grouped_gemm_dgrad_bf16(const void *dy, const void *w, const int32_t 
 
 /* grouped_gemm_wgrad_bf16 -- dW_e = dY_e^T X_e over the rows of expert e; dy bf16 [m x n], x bf16 [m x k], grouped with
  * the same offsets, no padding between experts.  dw, dw_mode as grouped_gemm_wgrad_fp8_block128's: bf16, fp32, or added
- * into fp32, one unfused add an element.  In fp32 the sums over 1024 rows each are added up in order, rounded to nearest.  An expert
- * with no rows gets zeros (nothing is added). */
+ * into fp32, one unfused add an element.  The sums over 65536 rows each (bf16; 1024 in fp32) are added up in order in fp32, rounded to
+ * nearest; within one the steps cut towards zero, as in the forward.  An expert with no rows gets zeros (nothing is added). */
 fme_status grouped_gemm_wgrad_bf16(const void *dy, const void *x, int64_t m, const int32_t *offsets, int32_t num_experts,
                                    int64_t n, int64_t k, void *dw, int32_t dw_mode, int32_t *dev_status, void *stream);
 
