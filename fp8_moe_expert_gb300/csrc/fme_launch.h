@@ -237,6 +237,31 @@ struct LaunchGemv {
   uint32_t shared_bytes;  // and what there is of shared memory
   cudaStream_t stream;
 };
+// Rows of x taken at a time, at most: eight with 7168 of k are half of an SM's shared memory.
+constexpr int kGemvRows = 8;
+inline int32_t gemv_tile_rows(int64_t k) { return k <= 7168 ? kGemvRows : kGemvRows / 2; }
+// An upper bound of a call's units: every expert with a row has a tile, and each further one takes as many rows as a tile.
+inline int64_t gemv_units(bool swiglu, int64_t m, int64_t n, int64_t k, int32_t num_experts) {
+  const int64_t per = swiglu ? n / 256 * 8 : (n % 128 == 0 ? n / 128 : (n + 254) / 128) * 4;
+  const int64_t experts = std::min<int64_t>(num_experts, m);
+  return (experts + (m - experts) / gemv_tile_rows(k)) * per;
+}
+// How many warps share a unit: eight while the SMs have few, four from two units an SM on; two where the chunks of 256 k would
+// leave some of four without work and not of two.  Measured, us with 8 / 4 / 2 warps, experts with a row each: gate/up of 4096 x 7168
+// with SwiGLU, one (0.8 units an SM) 9.1 / 11.2 / 19.3, two (1.7) 11.6 / 13.2 / 19.7, three (2.5) 15.8 / 15.1 / 20.9, eight (7)
+// 31.6 / 30.0 / 31.0, 32 (27) 98 / 91 / 97; down projection of 7168 x 2048, one (1.5) 6.7 / 7.1 / 8.9, eight (12) 19.6 / 18.2 / 19.0,
+// 32 (47) 59 / 52 / 50, with 128 rows in all 63 / 57 / 59; 4096 x 1536, four (3.4) 9.1 / 8.9 / 8.6, 32 (27) 35 / 33 / 29; 4096 x
+// 2304, four 10.8 / 10.2 / 10.5, 32 50 / 44 / 40; 2048 x 512, eight (3.4) 7.5 / 6.7 / 6.2.  Over 476 shapes (k 256 to 7168, 4 and 16
+// experts with a row each, 1 to 16 units an SM, with and without SwiGLU) the choice is 1% behind the fastest of the three on the
+// average, and 15% at most (13 chunks, five units an SM, where two warps would be it).  A rule of its own for five and six chunks
+// is not there: with two to five units an SM eight warps are behind four in all 28 of those shapes, though 74 rows of 8 experts of
+// 1000 x 1344 take 11.2 / 11.8 / 13.8.
+inline int gemv_share(int64_t units, int64_t k, int num_sms) {
+  if (units < 2 * num_sms) return 8;
+  const int64_t chunks = (k + 255) / 256;
+  const bool uneven = chunks <= 10 && (chunks % 4 == 1 || chunks % 4 == 2);
+  return uneven && (units >= 5 * num_sms || chunks <= 2) ? 2 : 4;
+}
 cudaError_t launch_gemv_nvfp4(const LaunchGemv &a);
 
 // The router (gate.cu).

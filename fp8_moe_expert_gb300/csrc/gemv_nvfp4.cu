@@ -48,7 +48,6 @@ namespace {
 constexpr int kGemvWarps = 16;
 constexpr int kGemvThreads = 32 * kGemvWarps;
 constexpr int kChunk = 256;    // k of a warp's step
-constexpr int kGemvRows = 8;   // rows of x at a time, at most
 constexpr int kRowsPad = 33;   // sums of a row of x in shared memory
 constexpr uint32_t kBoxBytes = 8 * 128;    // 8 rows' codes of a chunk
 constexpr uint32_t kCodeBytes = 4 * kBoxBytes;
@@ -520,16 +519,6 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       mbar_drain(&s.full[warp][depth == 2 ? f & 1 : 0], (depth == 2 ? f >> 1 : f) & 1);
 }
 
-// Rows of x taken at a time: eight with 7168 of k are half of an SM's shared memory.
-int32_t gemv_tile_rows(int64_t k) { return k <= 7168 ? kGemvRows : kGemvRows / 2; }
-
-// An upper bound of a call's units: every expert with a row has a tile, and each further one takes as many rows as a tile.
-int64_t unit_bound(const LaunchGemv &a) {
-  const int64_t per = a.swiglu ? a.n / 256 * 8 : (a.n % 128 == 0 ? a.n / 128 : (a.n + 254) / 128) * 4;
-  const int64_t experts = std::min<int64_t>(a.num_experts, a.m);
-  return (experts + (a.m - experts) / gemv_tile_rows(a.k)) * per;
-}
-
 template <bool kSwiglu, int kShare>
 cudaError_t launch_gemv(LaunchGemv a) {
   auto kernel = gemv_nvfp4_kernel<kSwiglu, kShare>;
@@ -540,7 +529,7 @@ cudaError_t launch_gemv(LaunchGemv a) {
   // all the shared memory of an SM: how it is used follows from the rows of the experts
   a.shared_bytes = 226 * 1024 - (sizeof(SharedGemv) + 127) / 128 * 128;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, unit_bound(a))), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.num_sms, gemv_units(a.swiglu, a.m, a.n, a.k, a.num_experts))), 1, 1);
   cfg.blockDim = dim3(kGemvThreads, 1, 1);
   cfg.dynamicSmemBytes = a.shared_bytes + 1024;
   cfg.stream = a.stream;
@@ -552,21 +541,13 @@ cudaError_t launch_gemv(LaunchGemv a) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// How many warps share a unit: eight while the SMs have few, four from two units an SM on; two where the chunks of k would leave
-// some of four without work and not of two.  Measured, us with 8 / 4 / 2 warps, experts with a row each: gate/up of 4096 x 7168
-// with SwiGLU, one (0.8 units an SM) 9.1 / 11.2 / 19.3, two (1.7) 11.6 / 13.2 / 19.7, three (2.5) 15.8 / 15.1 / 20.9, eight (7)
-// 31.6 / 30.0 / 31.0, 32 (27) 98 / 91 / 97; down projection of 7168 x 2048, one (1.5) 6.7 / 7.1 / 8.9, eight (12) 19.6 / 18.2 / 19.0,
-// 32 (47) 59 / 52 / 50, with 128 rows in all 63 / 57 / 59; 4096 x 1536, four (3.4) 8.7 / 8.5 / 8.4, 32 (27) 35 / 33 / 29; 4096 x
-// 2304, four 10.8 / 10.2 / 10.5, 32 50 / 44 / 40; 2048 x 512, eight (3.4) 7.5 / 6.7 / 6.2; 8 experts of 1000 x 1344 with 74 rows (2.7)
-// 11.2 / 11.8 / 13.8 (six chunks fill eight warps no worse than four).
 template <bool kSwiglu>
 cudaError_t launch_gemv(const LaunchGemv &a) {
-  const int64_t units = unit_bound(a), chunks = (a.k + kChunk - 1) / kChunk;
-  const bool uneven = chunks <= 10 && (chunks % 4 == 1 || chunks % 4 == 2);
-  const bool few = units < 5 * a.num_sms;
-  if (units < 2 * a.num_sms || (few && uneven && chunks > 4 && chunks < 8)) return launch_gemv<kSwiglu, 8>(a);
-  if (uneven && (!few || chunks <= 2)) return launch_gemv<kSwiglu, 2>(a);
-  return launch_gemv<kSwiglu, 4>(a);
+  switch (gemv_share(gemv_units(a.swiglu, a.m, a.n, a.k, a.num_experts), a.k, a.num_sms)) {
+    case 8: return launch_gemv<kSwiglu, 8>(a);
+    case 4: return launch_gemv<kSwiglu, 4>(a);
+    default: return launch_gemv<kSwiglu, 2>(a);
+  }
 }
 
 }  // namespace
