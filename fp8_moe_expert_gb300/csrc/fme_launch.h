@@ -198,20 +198,25 @@ inline int64_t bf16_few_tiles(int64_t m, int32_t num_experts) {
 // The forward takes its few-rows form (map_a = weights, map_b = tokens in 16-row
 // boxes) up to this many rows: there it reads the weights once, past it the token tiles of 64 read them again and again.  It is
 // also taken while every item has an SM to itself.  Measured, us (few rows / pairs), even loads: 32 experts of 4096 x 7168, 1024
-// rows 270 / 293, 2048 rows 277 / 315, 3000 rows 370 / 324 (uneven loads fill more tiles: the border is at 48 rows an
-// expert); one expert, 16 rows 23 / 36, 256 rows 28 / 36, 384 rows 52 / 37; 8 experts of 1048 x 1400, 400 rows 11 / 14, 1400 rows
-// 18 / 15; 4 experts of 7168 x 2048, 256 rows 25 / 29, 768 rows 42 / 31.
+// rows 270 / 293, 2048 rows 277 / 315, 3000 rows 370 / 324; one expert, 16 rows 23 / 36, 256 rows 28 / 36, 384 rows 52 / 37; 8 experts of
+// 1048 x 1400, 400 rows 11 / 14, 1400 rows 18 / 15; 4 experts of 7168 x 2048, 256 rows 25 / 29, 768 rows 42 / 31.  Where the pairs take
+// over depends on the loads, which the host does not know, more than on n and k.  Over eight shapes (n 512 to 9728, k 1024 to
+// 7168) and 1 to 32 experts, where the items are more than the SMs: with even loads the form for few rows is ahead in all 26
+// up to 64 rows an expert (there by 4 to 15%), the pairs in 25 from 80 on (by up to a third); with Zipf loads it is ahead in
+// all 17 at 16 rows an expert, in 17 of 20 at 32, 8 at 40, 5 at 48 and 3 at 64 (the pairs by up to 27%).  The border is between.
 // Returns 0 where not; otherwise the blocks of 64 of k in a stage, 2, 4 or 8 for items of 128, 64 or 32 rows of W (the boxes of
-// map_a): the smaller ones while each has an SM to itself, and with a short k half of the SMs are left to the kernel behind,
-// which sets itself up there (1 us).  Measured, us (8 / 4 / 2 blocks): one expert of 4096 x 7168, 1 or 16 rows 16.6 / 18.7 / 23.0, 32
-// rows - / 19.4 / 23.6; of 7168 x 2048 (items of 64 rows: 112), one row - / 8.9 / 9.7; 4 experts of 1048 x 1400 with a row each
-// (132 items of 32) 8.1 / 7.0 / 8.0, 8 of them - / 9.1 / 8.4.
+// map_a): the smaller ones while each has an SM to itself.  Items of 32 rows take more than half of the SMs only with a longer k:
+// the others are left to the kernel behind, which sets itself up there (1 us).  Measured, us (8 / 4 / 2 blocks): 4096 x 7168, one
+// expert, 1 or 16 rows 16.6 / 18.7 / 23.0, 32 rows - / 19.4 / 23.6; of seven shapes of 112 to 152 items of 32, with k 1536 and less
+// items of 64 are ahead by up to 10% (3584 x 512: 4.3 / 3.8), with 2048 and 2560 they differ by 4% at most, with 3584 and more items of
+// 32 are ahead in all (3584 x 4096: 11.0 / 11.9).  Of 13 shapes of 112 to 152 items of 64 they are ahead of 128 rows, or within 2%, for
+// every k from 512 to 7168 (7168 x 2048: 8.9 / 9.5; x 1024: 6.4 / 6.4).
 inline int bf16_few_halves(int64_t m, int64_t n, int64_t k, int32_t num_experts, int num_sms) {
   const int64_t tiles = bf16_few_tiles(m, num_experts);
   auto alone = [&](int64_t rows, int sms) { return tiles * ((n + rows - 1) / rows) <= sms; };
   if (m > 16 + 48 * static_cast<int64_t>(num_experts) && !alone(128, num_sms)) return 0;
-  if (m <= 16 && alone(32, k >= 4096 ? num_sms : num_sms / 2)) return 8;
-  return m <= 32 && alone(64, k >= 2048 ? num_sms : num_sms / 2) ? 4 : 2;
+  if (m <= 16 && alone(32, k >= 2560 ? num_sms : num_sms / 2)) return 8;
+  return m <= 32 && alone(64, num_sms) ? 4 : 2;
 }
 cudaError_t launch_bf16_fwd(const LaunchBf16 &a);
 cudaError_t launch_bf16_dgrad(const LaunchBf16 &a);
