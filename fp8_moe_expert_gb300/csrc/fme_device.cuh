@@ -22,7 +22,8 @@ constexpr int kMaxGroups = 1024;
 // may shorten it (-DFME_WAIT_LIMIT_NS=...) so that waits run out on purpose; the
 // waits that drain copies and MMAs already in flight before a CTA exits keep
 // their own, fixed limit (kDrainLimitNs), so the shortened build still lets
-// that work land.
+// that work land.  With -DFME_WAIT_ONE_LOOK a wait gives up at its first look at a
+// barrier that is not there yet: waits too short for any limit then run out too.
 #ifndef FME_WAIT_LIMIT_NS
 #define FME_WAIT_LIMIT_NS 2000000000ull
 #endif
@@ -125,12 +126,33 @@ __device__ __forceinline__ bool mbar_try_wait_suspend(uint64_t *bar, uint32_t pa
   return done != 0;
 }
 
+#ifdef FME_WAIT_ONE_LOOK
+// One look, which never suspends the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+#endif
+
 // Wait for the phase of `bar` with the given parity to complete.  Gives up when
 // *abort is set by another thread or after kWaitLimitNs; on a time-out it sets
 // *abort and reports kDevTimeout.  Returns true when the phase completed.
 template <bool kSuspend = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
                                           int32_t *status) {
+#ifdef FME_WAIT_ONE_LOOK
+  if (mbar_test_wait(bar, parity)) return true;
+  *abort = 1;
+  report(status, kDevTimeout);
+  return false;
+#else
   auto poll = [&] { return kSuspend ? mbar_try_wait_suspend(bar, parity) : mbar_try_wait(bar, parity); };
   if (poll()) return true;
   const uint64_t t0 = globaltimer();
@@ -144,6 +166,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
       return false;
     }
   }
+#endif
 }
 
 // Wait for the phase of `bar` with the given parity, up to kDrainLimitNs, with no
