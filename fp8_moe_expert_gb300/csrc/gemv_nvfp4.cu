@@ -13,10 +13,10 @@
 // N) the tensor work is small; decoding is what the SM spends its time on.  Two ways:
 //   fp16  4 conversions and 4 products for the 8 codes of a word.  x, times a power of two that brings its row's largest
 //         value to 2^14 .. 2^15, must be exact in fp16: a bf16 value is, down to 2^-29 of the largest;
-//   bf16  where it is not (a row with a wider range, infinities and NaN): two codes of a word lie 16 bits apart, one in each
-//         half.  A masked pair times (2^12 + 2^6) puts a code's sign into bit 15 and its exponent and mantissa into
-//         bits 8 .. 6 of each half, as bf16 the code's value times 2^-126 (its subnormal 0.5 a bf16 subnormal).  Times
-//         sf 2^118 it is c sf 2^-8.  13 integer operations and 4 products for 8 codes.
+//   bf16  where it is not (a row with a wider range or a NaN; one with an infinity is looked at unscaled): two codes of a
+//         word lie 16 bits apart, one in each half.  A masked pair times (2^12 + 2^6) puts a code's sign into bit 15 and its
+//         exponent and mantissa into bits 8 .. 6 of each half, as bf16 the code's value times 2^-126 (its subnormal 0.5 a bf16
+//         subnormal).  Times sf 2^118 it is c sf 2^-8.  13 integer operations and 4 products for 8 codes.
 // Both multiply the same values but for a power of two, so the sums' bits are the same (as long as they are normal
 // numbers).  Gate/up of 4096 x 7168, 8 and all of 32 experts with a row each: 30 and 91 us (4.4 and 5.8 TB/s of weights), in
 // bf16 38 and 121.
@@ -344,14 +344,14 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
       if (lane == 0) s.amax[warp] = top;
     }
     __syncthreads();  // also: the pass before is no longer read
-    float to = 1.0f;
+    float power = 1.0f;
     if (mine < rows) {
       float top = s.amax[mine * per_row];
       for (int j = 1; j < per_row; ++j) top = fmaxf(top, s.amax[mine * per_row + j]);
       // 2^s, s = 14 - the exponent of the largest, at most 120 (0 and infinity: any)
       const int exponent = static_cast<int>(__float_as_uint(top) >> 23);
       const int shift = exponent == 255 ? 0 : min(14 - (exponent - 127), 120);
-      to = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+      power = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
       if (slice == 0 && lane == 0) s.back[mine] = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
     }
     auto place = [&](bool half) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float lo = f[2 * j] * to, hi = f[2 * j + 1] * to;
+            const float lo = f[2 * j] * power, hi = f[2 * j + 1] * power;
             const __half2 h = __floats2half2_rn(lo, hi);
             const float2 b = __half22float2(h);
             exact = exact && b.x == lo && b.y == hi && (lo != 0.0f || f[2 * j] == 0.0f) && (hi != 0.0f || f[2 * j + 1] == 0.0f);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
         float acc[kSets][2][4] = {};
         auto sums = [&](auto half_tag) {
           constexpr bool kHalf = decltype(half_tag)::value;
-          auto add_chunk = [&](int32_t c, float(&to)[2][4]) {
+          auto add_chunk = [&](int32_t c, float(&sum)[2][4]) {
             const int slot = depth == 2 ? used & 1 : 0;
             // (a wait that ran out: garbage from here on, which is not stored, and no more copies)
             if (!mbar_wait(&s.full[warp][slot], (depth == 2 ? used >> 1 : used) & 1, abort_flag, p.status)) copy_unit = end;
@@ -451,16 +451,16 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
                 const uint4 x = shared16(x_lane + k0 * 2 + 64 * j);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                  mma_16816<kHalf>(to[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
-                  mma_16816<kHalf>(to[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
+                  mma_16816<kHalf>(sum[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], x.x, x.y);
+                  mma_16816<kHalf>(sum[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], x.z, x.w);
                 }
               }
             }
           };
           for (int32_t c = share; c < chunks; c += kSums) {
 #pragma unroll
-            for (int i = 0; i < kSets; ++i)
-              if (c + i * kShare < chunks) add_chunk(c + i * kShare, acc[i]);
+            for (int set = 0; set < kSets; ++set)
+              if (c + set * kShare < chunks) add_chunk(c + set * kShare, acc[set]);
           }
         };
         if (wide)
@@ -487,9 +487,9 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_nvfp4_kernel(const __gri
           for (int j = 0; j < 4; ++j) to_part[(2 * t + (j & 1)) * kRowsPad + 8 * (2 * m + (j >> 1)) + g] = acc[0][m][j];
         auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kShare) : "memory"); };
         meet();
-        const bool stop = *abort_flag != 0;  // some warp's sums are garbage
+        const bool garbage = *abort_flag != 0;  // some warp's sums
         const float *theirs = sums_of + group * kShare * kGemvRows * kRowsPad + out;
-        for (int tok = from_row + (share * 32 + lane) / kOut; tok < to_row && writes && !stop; tok += 32 * kShare / kOut) {
+        for (int tok = from_row + (share * 32 + lane) / kOut; tok < to_row && writes && !garbage; tok += 32 * kShare / kOut) {
           const float *from = theirs + tok * kRowsPad;
           auto joined = [&](const float *at) {
             float w[kShare];
