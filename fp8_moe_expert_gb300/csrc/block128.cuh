@@ -27,40 +27,49 @@ __device__ __forceinline__ void start_next_kernel() { asm volatile("griddepcontr
 // n rows takes ceil(n / unit) units; returns the total units, or -1 if the offsets
 // do not rise from 0 to rows (offsets NULL = one group of `rows`).  The whole warp
 // calls it; the table of 32 groups costs two loads and five shuffles, and the loads of 128 groups are in flight
-// together (256 experts: 0.7 us sooner than 32 by 32).  (Ordinary loads, see above.)
+// together (256 experts: 0.7 us sooner than 32 by 32).  Up to 32 groups go without that loop: every CTA of the quantizers
+// reads the table, and its instructions cost them 1.3% there (65536 x 7168 both ways, 32 groups 291 us, without 288).
+// (Ordinary loads, see above.)
 template <typename Fn>
 __device__ __forceinline__ int32_t scan_groups(const int32_t *offsets, int32_t num_groups, int64_t rows, int32_t unit,
                                                Fn fn) {
   const int lane = threadIdx.x & 31;
   int32_t base = 0;
   bool ok = true;
-  for (int g0 = 0; g0 < num_groups; g0 += 128) {
-    int32_t lo[4], hi[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int g = g0 + 32 * j + lane;
-      lo[j] = hi[j] = 0;
-      if (g < num_groups) {
-        lo[j] = offsets ? offsets[g] : 0;
-        hi[j] = offsets ? offsets[g + 1] : static_cast<int32_t>(rows);
-      }
+  auto load = [&](int g, int32_t &lo, int32_t &hi) {
+    lo = hi = 0;
+    if (g < num_groups) {
+      lo = offsets ? offsets[g] : 0;
+      hi = offsets ? offsets[g + 1] : static_cast<int32_t>(rows);
     }
+  };
+  auto groups32 = [&](int g, int32_t lo, int32_t hi) {
+    if (g < num_groups && (lo > hi || lo < 0 || hi > rows || (g == 0 && lo != 0) || (g == num_groups - 1 && hi != rows)))
+      ok = false;
+    const int32_t units = hi > lo ? (hi - lo - 1) / unit + 1 : 0;
+    int32_t incl = units;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (g0 + 32 * j >= num_groups) break;
-      const int g = g0 + 32 * j + lane;
-      if (g < num_groups && (lo[j] > hi[j] || lo[j] < 0 || hi[j] > rows || (g == 0 && lo[j] != 0) ||
-                             (g == num_groups - 1 && hi[j] != rows)))
-        ok = false;
-      const int32_t units = hi[j] > lo[j] ? (hi[j] - lo[j] - 1) / unit + 1 : 0;
-      int32_t incl = units;
+    for (int s = 1; s < 32; s <<= 1) {
+      const int32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, s);
+      if (lane >= s) incl += up;
+    }
+    if (g < num_groups) fn(g, lo, hi - lo, base + incl - units);
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  };
+  if (num_groups <= 32) {
+    int32_t lo, hi;
+    load(lane, lo, hi);
+    groups32(lane, lo, hi);
+  } else {
+    for (int g0 = 0; g0 < num_groups; g0 += 128) {
+      int32_t lo[4], hi[4];
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const int32_t up = __shfl_up_sync(0xFFFFFFFFu, incl, s);
-        if (lane >= s) incl += up;
+      for (int j = 0; j < 4; ++j) load(g0 + 32 * j + lane, lo[j], hi[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (g0 + 32 * j >= num_groups) break;
+        groups32(g0 + 32 * j + lane, lo[j], hi[j]);
       }
-      if (g < num_groups) fn(g, lo[j], hi[j] - lo[j], base + incl - units);
-      base += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
   }
   return __all_sync(0xFFFFFFFFu, ok) ? base : -1;
